@@ -124,7 +124,7 @@ def draw(rng):
 def _capacity(c):
     """Rows that any routing of the case fits into."""
     slots = c["tokens"] * c["top_k"]
-    return -(-(slots + min(slots, c["experts"]) * (c["m_aligned"] - 1)) // c["m_aligned"]) * c["m_aligned"]
+    return (slots + min(slots, c["experts"]) * (c["m_aligned"] - 1)) // c["m_aligned"] * c["m_aligned"]
 
 
 def _chosen(c, gen):
