@@ -104,7 +104,8 @@ typedef enum moegg_dtype {
   MOEGG_DT_E4M3 = 1,   /* OCP E4M3FN: A/B operands (MXFP8) or D/D_col outputs */
   MOEGG_DT_E2M1X2 = 2, /* packed OCP E2M1 pairs: A/B operands (MXFP4) */
   MOEGG_DT_BF16 = 3,   /* A/B operands (dense BF16 backend) or C / D outputs */
-  MOEGG_DT_E5M2 = 4    /* OCP E5M2: A/B operands (MXFP8, "Grouped GEMM + Quant", §Data Types) */
+  MOEGG_DT_E5M2 = 4,   /* OCP E5M2: A/B operands (MXFP8, "Grouped GEMM + Quant", §Data Types) */
+  MOEGG_DT_F32 = 5     /* fp32: layer operators only (router logits, linear's y and dw) */
 } moegg_dtype;
 
 typedef enum moegg_sf_layout {
@@ -132,19 +133,20 @@ typedef enum moegg_act {
                             of 32 columns, gate first, both clamped to [clamp_min, clamp_max]
                             ("Grouped GEMM + GLU + Hadamard", §Equations, GeGLU; the page's
                             constants are a = 1.702, offset = 1)                          */
-  MOEGG_ACT_DGEGLU = 6   /* dGeGLU backward: C_in pairs [gate_b|up_b], dC = [dgate_b|dup_b],
+  MOEGG_ACT_DGEGLU = 6,  /* dGeGLU backward: C_in pairs [gate_b|up_b], dC = [dgate_b|dup_b],
                             gate clamped above at clamp_max, up to [clamp_min, clamp_max],
                             dprob += row sums ("Grouped GEMM + dGLU", dGeGLU equations; the
                             page's defaults a = 1.702, offset = 1, clamps -7 / 7).  Output
                             formats as dSwiGLU (amax (L, 2) = [dgate, dup] blocks)        */
+  MOEGG_ACT_GELU = 7     /* y = z / 2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))): moegg_linear only */
 } moegg_act;
 
 /* Problem description (host struct). */
 typedef struct moegg_problem {
   int32_t num_groups;   /* L, 1..1024 ("Shapes and Divisibility": expert count <= 1024) */
   int32_t m_aligned;    /* group row alignment; multiple of 128 here                     */
-  int64_t valid_m;      /* rows of A == padded_offsets[L-1]; multiple of m_aligned,
-                           < 2^31 here                                                    */
+  int64_t valid_m;      /* rows of A == padded_offsets[L-1] (or more: rows behind the last
+                           group are left as they were); multiple of m_aligned, < 2^31 here */
   int32_t n;            /* GEMM N (rows of each expert's B); multiple of 32, <= 2^20 here
                            (64 for SwiGLU / GeGLU)                                        */
   int32_t k;            /* reduction length K; multiple of 128 bytes per row here (128
@@ -229,6 +231,178 @@ moegg_status moegg_check_offsets(const moegg_problem* problem, const int32_t* pa
  * overlapping.  Returns MOEGG_OK, MOEGG_ERROR_INVALID_VALUE,
  * MOEGG_ERROR_MISALIGNED or MOEGG_ERROR_LAUNCH. */
 moegg_status moegg_sf_to_kplanes(const uint8_t* src, uint8_t* dst, int64_t rows, int32_t k, void* stream);
+
+/* ==========================================================================
+ * Layer operators: what stands around the grouped product in an MoE layer.
+ * The router's choice, tokens sorted by expert and back, and the matrix
+ * product with bias, activation and residual, each with its gradient.
+ *
+ * They follow the conventions above: caller-owned dense row-major device
+ * tensors (16-byte aligned; vectors 4-byte aligned), no device allocation,
+ * asynchronous on `stream`, capturable (kernels only), every argument checked
+ * on the host before any HIP call.  Values in index tensors are device data:
+ * an index out of range is never followed (each function says what it counts
+ * as).  A workspace belongs to one call at a time: calls that may run at the
+ * same time (other streams, graphs replayed side by side) need their own.
+ * Results do not depend on the order in which workgroups run.
+ * ========================================================================== */
+
+typedef enum moegg_score {
+  MOEGG_SCORE_SOFTMAX = 0, /* p = softmax over the experts */
+  MOEGG_SCORE_SIGMOID = 1  /* p_e = 1 / (1 + exp(-logit_e)) */
+} moegg_score;
+
+typedef struct moegg_route_problem {
+  int64_t num_tokens;   /* T >= 0                                              */
+  int32_t num_experts;  /* E, 1..1024                                          */
+  int32_t top_k;        /* 1..min(E, 32)                                       */
+  int32_t dtype;        /* logits (and dlogits): BF16 | F32                    */
+  int32_t score;        /* moegg_score                                         */
+  int32_t renormalise;  /* weights divided by the sum of the chosen scores     */
+  float scale;          /* factor of the weights; finite                       */
+} moegg_route_problem;
+
+/* Router: the top_k experts of every token and their weights.
+ *   key_e   = logit_e, or p_e + bias_e (evaluated in 64 bits) where bias is given: the bias
+ *             (E, fp32) steers the choice and not the weights
+ *   ids     (T, top_k) int32: experts of the largest keys, largest first, ties to the lowest index
+ *   weights (T, top_k) fp32: scale p_j, or scale p_j / sum_i p_i over the chosen with renormalise
+ * Experts with a logit of -infinity or NaN (or a key of NaN or -infinity) are
+ * never chosen; where fewer than top_k remain, the ids that are left are -1
+ * with weight 0.  +infinity counts as the largest finite number.  A NaN logit
+ * makes the token's weights NaN where they come from a softmax over all
+ * experts (no renormalise), and has no other effect. */
+moegg_status moegg_route(const moegg_route_problem* problem, const void* logits, const float* bias, int32_t* ids,
+                         float* weights, void* stream);
+
+/* Gradient of moegg_route's weights: dlogits (T, E, dtype of the logits) from
+ * dweights (T, top_k) and the ids that moegg_route returned for these logits
+ * (ids outside 0..E-1 have no gradient; an id that appears twice in a token
+ * counts twice).  The choice itself, and so the bias, has no gradient. */
+moegg_status moegg_route_backward(const moegg_route_problem* problem, const void* logits, const int32_t* ids,
+                                  const float* dweights, void* dlogits, void* stream);
+
+typedef struct moegg_sort_problem {
+  int64_t num_tokens;   /* T >= 0                                              */
+  int32_t top_k;        /* slots per token, 1..32; slot t * top_k + j          */
+  int32_t num_experts;  /* L, 1..1024                                          */
+  int32_t m_aligned;    /* rows of an expert are padded to a multiple of this: 1..65536
+                           (128 or a multiple for moegg_run, 1 for moegg_linear) */
+  int64_t rows;         /* rows of the sorted tensors, >= moegg_sort_rows()    */
+} moegg_sort_problem;
+
+/* Rows that any routing of the problem's slots fits into (a multiple of
+ * m_aligned): rows is a host number, where the rows in use,
+ * padded_offsets[L-1], are known to the device alone.  -1 for an invalid
+ * problem or one with 2^31 rows or more.  moegg_run takes this number as
+ * valid_m: it works through the rows that padded_offsets names and leaves
+ * those behind the last expert as they were. */
+int64_t moegg_sort_rows(const moegg_sort_problem* problem);
+/* Bytes of workspace of moegg_sort (may be 0); -1 for an invalid problem. */
+int64_t moegg_sort_workspace(const moegg_sort_problem* problem);
+
+/* Slots sorted by expert, stable (an expert's rows in the order of their slots).
+ *   ids (T, top_k) int32; any value outside 0..L-1 drops the slot
+ *   padded_offsets (L) int32: end of every expert's padded rows (moegg_run's layout)
+ *   row_of (T, top_k) int32: the slot's row, -1 if dropped
+ *   slot_of (rows) int32: the row's slot, -1 for padding and for rows behind the last expert
+ *   weights (T, top_k) fp32 and prob (rows) fp32, both or neither: prob[row] = weights[slot], 0
+ *   where there is no slot (moegg_run's prob) */
+moegg_status moegg_sort(const moegg_sort_problem* problem, const int32_t* ids, const float* weights,
+                        int32_t* padded_offsets, int32_t* row_of, int32_t* slot_of, float* prob, void* workspace,
+                        int64_t workspace_bytes, void* stream);
+
+typedef struct moegg_exchange_problem {
+  int64_t num_tokens;   /* T >= 0                                              */
+  int64_t rows;         /* as sorted                                           */
+  int32_t top_k;
+  int32_t num_experts;  /* L                                                   */
+  int32_t width;        /* H: multiple of 8; of 128 for MX rows (256 for E2M1X2), <= 2^20 */
+  int32_t dtype;        /* of the rows written: BF16 | E4M3 | E5M2 | E2M1X2    */
+  int32_t sf_layout;    /* moegg_sf_layout of the scales of MX rows            */
+} moegg_exchange_problem;
+
+/* rows[row_of[t, j]] = x[t]: x (T, H) BF16; out (rows, H) in `dtype`, with E8M0
+ * scales in sf for the MX types: (rows, H/32), or (H/128, rows, 4) planes.
+ * These are moegg_run's A and SFA.  A block of 32 is scaled by the smallest
+ * power of two >= amax / q_max (448, 57344 or 6) and rounded to nearest even;
+ * a block of zeros has scale byte 0, a block with a NaN or an infinity has
+ * zero codes and scale byte 255 (NaN).  Padding rows inside the experts'
+ * rows become zero (scale byte 0); rows behind the last expert are left as
+ * they were. */
+moegg_status moegg_dispatch(const moegg_exchange_problem* problem, const void* x, const int32_t* row_of,
+                            const int32_t* slot_of, const int32_t* padded_offsets, void* out, uint8_t* sf,
+                            void* stream);
+
+/* y[t] = residual[t] + sum_j weights[t, j] rows_in[row_of[t, j]], summed in fp32
+ * in the order residual last, rounded once: rows_in (rows, H) BF16, weights
+ * (T, top_k) fp32 or NULL (ones), residual (T, H) BF16 or NULL, y (T, H) BF16
+ * (may be residual itself).  Dropped slots add nothing.  `dtype` must be BF16.
+ * Without weights this is also the gradient of moegg_dispatch. */
+moegg_status moegg_combine(const moegg_exchange_problem* problem, const void* rows_in, const int32_t* row_of,
+                           const float* weights, const void* residual, void* y, void* stream);
+
+/* Gradient of moegg_combine: out[row_of[t, j]] = weights[t, j] dy[t] in `dtype`
+ * (padding and rows behind the last expert as in moegg_dispatch), and, where
+ * dweights (T, top_k) is given, dweights[t, j] = sum_h dy[t, h] rows_in[row_of[t, j], h]
+ * (0 for a dropped slot); rows_in is needed for it and otherwise NULL.  out
+ * may not overlap rows_in.  The residual's gradient is dy itself. */
+moegg_status moegg_combine_backward(const moegg_exchange_problem* problem, const void* dy, const int32_t* row_of,
+                                    const int32_t* slot_of, const int32_t* padded_offsets, const void* rows_in,
+                                    const float* weights, void* out, uint8_t* sf, float* dweights, void* stream);
+
+/* values[slot] = rows_values[row_of[slot]] (0 for a dropped slot): fp32 numbers
+ * of the rows back in the order of the slots (moegg_run's dprob -> the gradient
+ * of the weights). */
+moegg_status moegg_unsort(const float* rows_values, const int32_t* row_of, float* values, int64_t num_slots,
+                          int64_t rows, void* stream);
+
+/* Matrix product with bias, activation and residual, dense or grouped.
+ *   z = x w_g^T + bias_g;  c = bf16(z);  y = act(z) + residual
+ * for the rows [offsets[g-1], offsets[g]) of group g (any nondecreasing ends,
+ * no alignment), or for all m rows where offsets is NULL (num_groups 1).
+ * act: NONE, SRELU (relu(z)^2), GELU, or SWIGLU on [X | G] pairs of 32 columns
+ * as in moegg_run (N_out = n / 2, else N_out = n).  Sums are fp32. */
+typedef struct moegg_linear_problem {
+  int64_t m;            /* rows, 0..2^31-1                                     */
+  int32_t n;            /* multiple of 8 (64 for SWIGLU), <= 2^20              */
+  int32_t k;            /* multiple of 8, <= 2^20                              */
+  int32_t num_groups;   /* 1..1024                                             */
+  int32_t act;          /* moegg_act                                           */
+  int32_t dtype;        /* y (forward) or dw (backward): BF16 | F32            */
+} moegg_linear_problem;
+
+typedef struct moegg_linear_args {
+  const void* x;          /* (m, k) BF16                                       */
+  const void* w;          /* (L, n, k) BF16                                    */
+  const float* bias;      /* (L, n) fp32 or NULL                  [forward]    */
+  const void* residual;   /* (m, N_out) BF16 or NULL              [forward]    */
+  const int32_t* offsets; /* (L) int32 group ends, or NULL                     */
+  void* y;                /* (m, N_out)                           [forward]    */
+  void* c;                /* (m, n) BF16: forward: written if not NULL; backward: read, unless act is NONE */
+  const void* dy;         /* (m, N_out) BF16                      [backward]   */
+  void* dx;               /* (m, k) BF16 or NULL                  [backward]   */
+  void* dw;               /* (L, n, k) or NULL                    [backward]   */
+  float* db;              /* (L, n) fp32 or NULL                  [backward]   */
+  void* workspace;        /* 16-byte aligned, moegg_linear*_workspace() bytes (NULL for 0) */
+  int64_t workspace_bytes;
+} moegg_linear_args;
+
+/* Workspace bytes of a forward / backward call; -1 for an invalid problem.
+ * The backward's depends on which of dx, dw and db are asked for (flags 1, 2, 4). */
+int64_t moegg_linear_workspace(const moegg_linear_problem* problem);
+int64_t moegg_linear_backward_workspace(const moegg_linear_problem* problem, int32_t want);
+
+/* Forward.  Rows behind the last group are left as they were.  m == 0:
+ * nothing is enqueued. */
+moegg_status moegg_linear(const moegg_linear_problem* problem, const moegg_linear_args* args, void* stream);
+
+/* Gradients: dz = dy act'(c), rounded to BF16 as the operand of both products;
+ * dx = dz w_g (rows behind the last group left as they were); dw_g = dz^T x
+ * and db_g = column sums of the unrounded dz over the group's rows (zero for
+ * an empty group; rows behind the last group are not read).  Whatever is NULL
+ * of dx, dw and db is not computed.  The residual's gradient is dy itself. */
+moegg_status moegg_linear_backward(const moegg_linear_problem* problem, const moegg_linear_args* args, void* stream);
 
 /* Output width N_out for a problem (N/2 SwiGLU / GeGLU, 2N dSwiGLU / dGeGLU, else N);
  * -1 if invalid act. */

@@ -11,7 +11,10 @@ The C ABI (include/moegg.h) is mirrored name for name:
 
 plus ``make_problem`` / ``make_args`` (fill the C structs from a problem dict
 and torch tensors' device pointers) and ``run`` / ``check`` (build the structs,
-call, raise ``MoeggError`` on a non-OK status).  Every step of the computation
+call, raise ``MoeggError`` on a non-OK status).  The layer operators
+around the grouped product (``route``, ``sort_tokens``, ``dispatch``,
+``combine``, ``linear`` and their gradients) are called with torch tensors
+and live in ``layer``.  Every step of the computation
 runs in the HIP library; this module never computes.  If ``libmoegg.so`` has
 not been built the first call raises ``RuntimeError``: there is no fallback.
 """
@@ -23,14 +26,17 @@ import os
 __all__ = ["MoeggError", "moegg_check", "moegg_run", "moegg_check_offsets", "moegg_n_out",
            "moegg_status_string", "moegg_last_error", "moegg_abi_version", "moegg_set_grid_limit", "make_problem",
            "make_args", "run", "check", "lib_path", "ABI_VERSION", "DTYPES", "ACTS", "STATUS", "SF_LAYOUTS",
-           "moegg_sf_to_kplanes", "sf_to_kplanes"]
+           "moegg_sf_to_kplanes", "sf_to_kplanes", "SCORES", "route", "route_backward", "SortPlan", "sort_tokens",
+           "sort_rows", "dispatch", "dispatch_backward", "combine", "combine_backward", "unsort", "linear",
+           "linear_backward"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libmoegg.so")
 
 ABI_VERSION = 5   # MOEGG_ABI_VERSION of the structs below
-DTYPES = {None: 0, "none": 0, "e4m3": 1, "e2m1x2": 2, "bf16": 3, "e5m2": 4}
-ACTS = {"none": 0, "swiglu": 1, "srelu": 2, "dswiglu": 3, "dsrelu": 4, "geglu": 5, "dgeglu": 6}
+DTYPES = {None: 0, "none": 0, "e4m3": 1, "e2m1x2": 2, "bf16": 3, "e5m2": 4, "f32": 5}
+ACTS = {"none": 0, "swiglu": 1, "srelu": 2, "dswiglu": 3, "dsrelu": 4, "geglu": 5, "dgeglu": 6, "gelu": 7}
+SCORES = {"softmax": 0, "sigmoid": 1}
 SF_LAYOUTS = {"row_major": 0, "kplanes": 1}
 STATUS = {0: "MOEGG_OK", 1: "MOEGG_ERROR_INVALID_VALUE", 2: "MOEGG_ERROR_MISALIGNED",
           3: "MOEGG_ERROR_NOT_SUPPORTED", 4: "MOEGG_ERROR_LAUNCH"}
@@ -52,6 +58,33 @@ class moegg_problem(ctypes.Structure):
 
 class moegg_args(ctypes.Structure):
     _fields_ = [(f, ctypes.c_void_p) for f in ARG_FIELDS]
+
+
+class moegg_route_problem(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int64), ("num_experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("score", ctypes.c_int32), ("renormalise", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class moegg_sort_problem(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int64), ("top_k", ctypes.c_int32), ("num_experts", ctypes.c_int32),
+                ("m_aligned", ctypes.c_int32), ("rows", ctypes.c_int64)]
+
+
+class moegg_exchange_problem(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int64), ("rows", ctypes.c_int64), ("top_k", ctypes.c_int32),
+                ("num_experts", ctypes.c_int32), ("width", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("sf_layout", ctypes.c_int32)]
+
+
+class moegg_linear_problem(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("num_groups", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class moegg_linear_args(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in ("x", "w", "bias", "residual", "offsets", "y", "c", "dy", "dx", "dw",
+                                               "db", "workspace")] + [("workspace_bytes", ctypes.c_int64)]
 
 
 class MoeggError(RuntimeError):
@@ -84,11 +117,34 @@ def _load():
         lib.moegg_sf_to_kplanes.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32,
                                             ctypes.c_void_p]
         lib.moegg_sf_to_kplanes.restype = ctypes.c_int
+        _declare_layer(lib)
         if lib.moegg_abi_version() != ABI_VERSION:
             raise RuntimeError(f"{lib_path} has ABI {lib.moegg_abi_version()}, these bindings "
                                f"expect {ABI_VERSION}: rebuild it with __graft_entry__.build()")
         _lib = lib
     return _lib
+
+
+def _declare_layer(lib) -> None:
+    """Signatures of the layer operators (called by ``layer``)."""
+    v, i64, i32, ref = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.POINTER
+    route, sort, exch = ref(moegg_route_problem), ref(moegg_sort_problem), ref(moegg_exchange_problem)
+    lin, lin_args = ref(moegg_linear_problem), ref(moegg_linear_args)
+    for name, args, res in (("moegg_route", [route] + [v] * 5, ctypes.c_int),
+                            ("moegg_route_backward", [route] + [v] * 5, ctypes.c_int),
+                            ("moegg_sort_rows", [sort], i64),
+                            ("moegg_sort_workspace", [sort], i64),
+                            ("moegg_sort", [sort] + [v] * 7 + [i64, v], ctypes.c_int),
+                            ("moegg_dispatch", [exch] + [v] * 7, ctypes.c_int),
+                            ("moegg_combine", [exch] + [v] * 6, ctypes.c_int),
+                            ("moegg_combine_backward", [exch] + [v] * 10, ctypes.c_int),
+                            ("moegg_unsort", [v, v, v, i64, i64, v], ctypes.c_int),
+                            ("moegg_linear_workspace", [lin], i64),
+                            ("moegg_linear_backward_workspace", [lin, i32], i64),
+                            ("moegg_linear", [lin, lin_args, v], ctypes.c_int),
+                            ("moegg_linear_backward", [lin, lin_args, v], ctypes.c_int)):
+        f = getattr(lib, name)
+        f.argtypes, f.restype = args, res
 
 
 # ---- the C functions, same names ----------------------------------------------
@@ -194,3 +250,8 @@ def run(problem: dict, tensors: dict, stream=None) -> None:
     st = moegg_run(make_problem(problem), make_args(tensors), _stream_handle(stream))
     if st != 0:
         raise MoeggError(st, moegg_last_error())
+
+
+# the layer operators (they use the names above)
+from .layer import (SortPlan, combine, combine_backward, dispatch, dispatch_backward, linear, linear_backward,  # noqa: E402
+                    route, route_backward, sort_rows, sort_tokens, unsort)

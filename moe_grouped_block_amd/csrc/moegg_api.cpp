@@ -12,6 +12,7 @@
 #include <cstring>
 #include <vector>
 
+#include "layer_internal.h"
 #include "moegg_internal.h"
 
 namespace {
@@ -173,6 +174,20 @@ moegg_status check_impl(const moegg_problem* pp, const moegg_args* ap) {
 }
 
 }  // namespace
+
+namespace moegg {
+
+moegg_status set_error(moegg_status st, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
+  va_end(ap);
+  return st;
+}
+
+void clear_error() { g_last_error[0] = '\0'; }
+
+}  // namespace moegg
 
 extern "C" {
 

@@ -1,0 +1,239 @@
+"""GPU tests of linear and its gradients against the float64 reference.
+Every bound is the one derived in layer_ref."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+mg = pytest.importorskip("moe_grouped_block_amd")
+import layer_ref as ref  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+ACTS = ["none", "swiglu", "srelu", "gelu"]
+
+
+def make(m, n, k, act, groups, seed, residual=False, empty=True):
+    gen = torch.Generator().manual_seed(seed)
+    x = torch.randn(m, k, generator=gen).to(torch.bfloat16)
+    w = (torch.randn(*((groups, n, k) if groups else (n, k)), generator=gen) / math.sqrt(k)).to(torch.bfloat16)
+    b = torch.randn(*((groups, n) if groups else (n,)), generator=gen) * 0.3
+    off = None
+    if groups:
+        cut = torch.sort(torch.randint(0, m + 1, (groups,), generator=gen)).values
+        cut[-1] = m
+        if empty and groups > 2:
+            cut[1] = cut[0]
+        off = torch.sort(cut).values.to(torch.int32)
+    n_out = n // 2 if act == "swiglu" else n
+    res = torch.randn(m, n_out, generator=gen).to(torch.bfloat16) if residual else None
+    return x, w, b, off, res, gen
+
+
+def cuda(t):
+    return None if t is None else t.cuda()
+
+
+def check_forward(m, n, k, act, groups, seed=1, residual=False, bias=True, dtype="bf16"):
+    x, w, b, off, res, _ = make(m, n, k, act, groups, seed, residual)
+    b = b if bias else None
+    print(f"[gpu-case] linear m={m} n={n} k={k} {act} groups={groups} residual={residual} {dtype}", flush=True)
+    y, c = mg.linear(x.cuda(), w.cuda(), bias=cuda(b), act=act, residual=cuda(res), offsets=cuda(off), save_c=True,
+                     dtype=dtype)
+    y2 = mg.linear(x.cuda(), w.cuda(), bias=cuda(b), act=act, residual=cuda(res), offsets=cuda(off), dtype=dtype)
+    assert torch.equal(y, y2)
+    r, z, mag = ref.linear(x, w, b, act, res, off)
+    zb = (k + 8) * ref.F32 * mag
+    assert ((c.cpu().double() - z).abs() <= zb * 1.01 + ref.BF16 * z.abs()).all()
+    bound = ref.linear_bound(z, mag, k, act, res, ref.BF16 if dtype == "bf16" else ref.F32)
+    bad = (y.cpu().double() - r).abs() > bound
+    assert not bad.any(), (int(bad.sum()), bad.nonzero()[:4])
+
+
+SHAPES = [(1, 64, 8), (1, 2816, 2048), (3, 128, 72), (5, 192, 1408), (16, 64, 264), (17, 320, 512), (33, 64, 2048),
+          (64, 256, 64), (100, 192, 136), (129, 1408, 200), (257, 320, 1000), (300, 576, 2056), (512, 512, 512)]
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("m,n,k", SHAPES)
+def test_forward(m, n, k, act):
+    check_forward(m, n, k, act, 0, seed=m + n)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 8, 8), (4, 24, 16), (40, 8, 2048), (130, 72, 1032), (260, 264, 328), (700, 1000, 504)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_forward_odd_widths(m, n, k, dtype):
+    check_forward(m, n, k, "none", 0, dtype=dtype)
+    check_forward(m, n, k, "gelu", 0, dtype=dtype, residual=True, bias=False)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_forward_residual(act, dtype):
+    for m, n, k in [(1, 128, 512), (19, 256, 264), (200, 320, 264), (600, 512, 320)]:
+        check_forward(m, n, k, act, 0, residual=True, dtype=dtype)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("m,n,k,groups", [(1, 64, 64, 3), (6, 128, 256, 64), (96, 192, 264, 64), (50, 64, 72, 1000),
+                                          (300, 320, 136, 5), (1000, 512, 512, 7), (2000, 192, 328, 64), (600, 256, 64, 1)])
+def test_forward_grouped(m, n, k, groups, act):
+    check_forward(m, n, k, act, groups, seed=m + groups, residual=groups % 2 == 1)
+
+
+def test_forward_long_sums():
+    for m in (2, 40, 300):
+        check_forward(m, 64, 16384, "none", 0)
+
+
+@pytest.mark.parametrize("m,n,k", [(4096, 2816, 2048), (16384, 64, 2048), (3000, 2048, 1408), (2500, 2560, 520)])
+def test_forward_large(m, n, k):
+    """Large products: against an fp64 product on the GPU."""
+    gen = torch.Generator(device="cuda").manual_seed(m)
+    x = torch.randn(m, k, generator=gen, device="cuda").to(torch.bfloat16)
+    w = (torch.randn(n, k, generator=gen, device="cuda") / math.sqrt(k)).to(torch.bfloat16)
+    b = torch.randn(n, generator=gen, device="cuda")
+    print(f"[gpu-case] linear large m={m} n={n} k={k}", flush=True)
+    for dtype, eps in (("bf16", ref.BF16), ("f32", ref.F32)):
+        y = mg.linear(x, w, bias=b, dtype=dtype)
+        z = x.double() @ w.double().t() + b.double()
+        mag = x.double().abs() @ w.double().abs().t() + b.double().abs()
+        assert ((y.double() - z).abs() <= (k + 8) * ref.F32 * mag + eps * z.abs()).all()
+
+
+def check_backward(m, n, k, act, groups, seed=1, dw_dtype="bf16", need=("dx", "dw", "db")):
+    x, w, _, off, _, gen = make(m, n, k, act, groups, seed)
+    n_out = n // 2 if act == "swiglu" else n
+    dy = torch.randn(m, n_out, generator=gen).to(torch.bfloat16)
+    c = (torch.randn(m, n, generator=gen) * 2).to(torch.bfloat16) if act != "none" else None
+    print(f"[gpu-case] linear backward m={m} n={n} k={k} {act} groups={groups} {dw_dtype} {need}", flush=True)
+    got = mg.linear_backward(dy.cuda(), x.cuda(), w.cuda(), c=cuda(c), act=act, offsets=cuda(off), need=need,
+                             dw_dtype=dw_dtype)
+    want = ref.linear_backward(dy, x, w, c, act, off)
+    for name, g in zip(("dx", "dw", "db"), got):
+        assert (g is None) == (name not in need)
+        if g is None:
+            continue
+        r, bound = want[name]
+        eps = ref.F32 if name == "db" or (name == "dw" and dw_dtype == "f32") else ref.BF16
+        bad = (g.cpu().double() - r).abs() > bound * (1 + eps) + eps * r.abs() + 1e-38
+        assert not bad.any(), (name, int(bad.sum()), bad.nonzero()[:4])
+    return got
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("m,n,k", [(1, 64, 8), (2, 192, 264), (17, 64, 2048), (100, 320, 136), (129, 1408, 200),
+                                   (300, 576, 1032), (600, 512, 512)])
+def test_backward(m, n, k, act):
+    check_backward(m, n, k, act, 0, seed=m + k)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 8, 8), (5, 24, 16), (70, 8, 1032), (333, 72, 264), (700, 1000, 504)])
+def test_backward_odd_widths(m, n, k):
+    check_backward(m, n, k, "none", 0, dw_dtype="f32")
+    check_backward(m, n, k, "gelu", 0)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("m,n,k,groups", [(1, 64, 64, 3), (6, 128, 256, 64), (96, 192, 264, 64), (300, 320, 136, 5),
+                                          (1000, 512, 512, 7), (2000, 192, 328, 64), (40, 64, 8, 300)])
+def test_backward_grouped(m, n, k, groups, act):
+    check_backward(m, n, k, act, groups, seed=m + groups, dw_dtype="f32" if groups == 5 else "bf16")
+
+
+@pytest.mark.parametrize("need", [("dx",), ("dw",), ("db",), ("dx", "db"), ("dw", "db")])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_backward_parts(need, act):
+    check_backward(150, 192, 136, act, 0, need=need)
+    check_backward(150, 192, 136, act, 4, need=need)
+
+
+def test_backward_long_sums():
+    """Weight gradients over many rows (the sum is split and joined)."""
+    check_backward(30011, 64, 72, "none", 0, dw_dtype="f32")
+    check_backward(30011, 64, 72, "swiglu", 3)
+
+
+@pytest.mark.parametrize("m,n,k", [(4096, 2816, 2048), (8000, 2048, 1408)])
+def test_backward_large(m, n, k):
+    gen = torch.Generator(device="cuda").manual_seed(m)
+    x = torch.randn(m, k, generator=gen, device="cuda").to(torch.bfloat16)
+    w = (torch.randn(n, k, generator=gen, device="cuda") / math.sqrt(k)).to(torch.bfloat16)
+    dy = torch.randn(m, n, generator=gen, device="cuda").to(torch.bfloat16)
+    print(f"[gpu-case] linear backward large m={m} n={n} k={k}", flush=True)
+    dx, dw, db = mg.linear_backward(dy, x, w, dw_dtype="f32")
+    d, xd, wd = dy.double(), x.double(), w.double()
+    for g, r, mag, terms, eps in ((dx, d @ wd, d.abs() @ wd.abs(), n, ref.BF16), (dw, d.t() @ xd, d.abs().t() @ xd.abs(), m, ref.F32),
+                                  (db, d.sum(0), d.abs().sum(0), m, ref.F32)):
+        assert ((g.double() - r).abs() <= (terms + 8) * ref.F32 * mag + eps * r.abs()).all()
+
+
+def test_rows_behind_the_last_group():
+    """They are neither written nor read."""
+    m, n, k, groups = 200, 128, 64, 3
+    x, w, b, _, _, gen = make(m, n, k, "none", groups, 5)
+    off = torch.tensor([40, 40, 150], dtype=torch.int32)
+    x[150:] = math.nan
+    dy = torch.randn(m, n, generator=gen).to(torch.bfloat16)
+    dy[150:] = math.nan
+    out = torch.full((m, n), 7.0, dtype=torch.bfloat16, device="cuda")
+    y = mg.linear(x.cuda(), w.cuda(), bias=b.cuda(), offsets=off.cuda(), out=out)
+    assert (y[150:] == 7.0).all() and torch.isfinite(y[:150]).all()
+    dx, dw, db = mg.linear_backward(dy.cuda(), x.cuda(), w.cuda(), offsets=off.cuda())
+    assert torch.isfinite(dx[:150]).all() and torch.isfinite(dw).all() and torch.isfinite(db).all()
+    assert (dw[1] == 0).all() and (db[1] == 0).all()              # the empty group
+
+
+def test_neighbours_do_not_leak():
+    """A group's infinities and NaN stay in its own rows and gradients."""
+    m, n, k, groups = 300, 128, 136, 4
+    x, w, b, _, _, gen = make(m, n, k, "none", groups, 6)
+    off = torch.tensor([70, 133, 222, 300], dtype=torch.int32)
+    dy = torch.randn(m, n, generator=gen).to(torch.bfloat16)
+    x[70:133], w[1], dy[70:133] = math.inf, math.nan, math.nan
+    y = mg.linear(x.cuda(), w.cuda(), bias=b.cuda(), offsets=off.cuda())
+    rest = torch.cat([torch.arange(70), torch.arange(133, 300)])
+    assert torch.isfinite(y[rest.cuda()]).all() and torch.isnan(y[70:133]).all()
+    dx, dw, db = mg.linear_backward(dy.cuda(), x.cuda(), w.cuda(), offsets=off.cuda())
+    assert torch.isfinite(dx[rest.cuda()]).all()
+    for g in (0, 2, 3):
+        assert torch.isfinite(dw[g]).all() and torch.isfinite(db[g]).all()
+
+
+def test_foreign_offsets_stay_inside():
+    """Offsets that decrease or leave the rows address nothing outside them."""
+    m, n, k, groups = 100, 64, 64, 5
+    x, w, b, _, _, gen = make(m, n, k, "none", groups, 7)
+    dy = torch.randn(m, n, generator=gen).to(torch.bfloat16)
+    for off in ([50, 20, 90, 60, 100], [-5, 30, 2 ** 31 - 1, 40, 100], [1000, 1000, 1000, 1000, 1000], [-1, -1, -1, -1, -1]):
+        o = torch.tensor(off, dtype=torch.int32).cuda()
+        y = mg.linear(x.cuda(), w.cuda(), bias=b.cuda(), offsets=o)
+        dx, dw, db = mg.linear_backward(dy.cuda(), x.cuda(), w.cuda(), offsets=o)
+        torch.cuda.synchronize()
+        assert y.shape == (m, n) and torch.isfinite(dw).all() and torch.isfinite(db).all()
+
+
+def test_activation_extremes():
+    """Pre-activations from -1e30 to 1e30 give the activation's limits, no NaN."""
+    for act in ("gelu", "swiglu", "srelu"):
+        v = torch.tensor([-1e30, -1e4, -50.0, -1.0, 0.0, 1.0, 50.0, 1e4], dtype=torch.float32)
+        x = v.to(torch.bfloat16).reshape(-1, 1).repeat(1, 8)
+        x[:, 1:] = 0
+        w = torch.zeros(64, 8, dtype=torch.bfloat16)
+        w[:, 0] = 1
+        y, c = mg.linear(x.cuda(), w.cuda(), act=act, save_c=True, dtype="f32")
+        r = ref.act(x[:, :1].double().repeat(1, 64), act)
+        assert torch.allclose(y.cpu().double(), r.clamp(max=3.4028234e38), rtol=1e-5, atol=1e-30)
+        dy = torch.ones(8, y.shape[1], dtype=torch.bfloat16)
+        dx, dw, db = mg.linear_backward(dy.cuda(), x.cuda(), w.cuda(), c=c, act=act)
+        fine = slice(1, None) if act != "srelu" else slice(0, None)
+        assert torch.isfinite(dx.float()[fine]).all() and torch.isfinite(db[0])
+
+
+def test_empty_rows():
+    w = torch.randn(3, 64, 64, device="cuda").to(torch.bfloat16)
+    x = torch.empty(0, 64, device="cuda", dtype=torch.bfloat16)
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    assert mg.linear(x, w, offsets=off).shape == (0, 64)
+    dx, dw, db = mg.linear_backward(x, x, w, offsets=off)
+    assert dx.shape == (0, 64) and (dw == 0).all() and (db == 0).all()
