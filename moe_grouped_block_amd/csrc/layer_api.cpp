@@ -185,6 +185,11 @@ moegg_status check_linear(const moegg_linear_problem* pp) {
     return set_error(MOEGG_ERROR_NOT_SUPPORTED, "n=%d k=%d: multiples of 8 needed", p.n, p.k);
   if (p.n > (1 << 20) || p.k > (1 << 20))
     return set_error(MOEGG_ERROR_NOT_SUPPORTED, "n=%d k=%d above 2^20", p.n, p.k);
+  // tiles of 128 x 64 at least, of y, dx and dw
+  const int64_t wide = (p.n > p.k ? p.n : p.k) / 64 + 1;
+  if ((p.m / 128 + p.num_groups + 1) * wide > INT32_MAX || p.num_groups * (p.n / 128 + 1) * int64_t{p.k / 64 + 1} > INT32_MAX)
+    return set_error(MOEGG_ERROR_NOT_SUPPORTED, "m=%lld n=%d k=%d num_groups=%d: above 2^31-1 tiles", (long long)p.m, p.n, p.k,
+                     p.num_groups);
   return MOEGG_OK;
 }
 

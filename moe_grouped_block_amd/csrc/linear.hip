@@ -8,252 +8,431 @@
 //
 // Group g owns rows [offsets[g-1], offsets[g]) (any numbers, no alignment);
 // without offsets there is one group of all rows.
-#include <hip/hip_runtime.h>
-
-#include "layer_internal.h"
+#include "linear_gemm.h"
 
 namespace moegg {
 namespace {
 
-typedef uint32_t v4u __attribute__((ext_vector_type(4)));
-typedef float v16f __attribute__((ext_vector_type(16)));
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+// ---------------------------------------------------------------------------
+// few rows: the weights are read once and nothing else matters
+// ---------------------------------------------------------------------------
+//
+// One workgroup computes 16 columns n for up to 16 rows of a group at a time.
+// Its 8 waves share r: each streams its part of the 16 weight rows from
+// global memory into registers (16 bytes a lane, 8 loads in flight) and
+// multiplies it with the rows of x by 16 x 16 x 32 MFMAs; the 8 partial sums
+// meet in LDS.
+constexpr int kFewThreads = 512;
+constexpr int kFewRows = 16;
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kGeluC = 0.7978845608028654f;    // sqrt(2 / pi)
-constexpr float kGeluA = 0.044715f;
-
-__device__ __forceinline__ float bf(uint16_t u) { return __uint_as_float(static_cast<uint32_t>(u) << 16); }
-__device__ __forceinline__ uint16_t to_bf(float f) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f)); }
-__device__ __forceinline__ float sigmoid(float x) {
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-x * kLog2e));
-}
-
-// gelu(z) = z / 2 (1 + tanh u) = z sigmoid(2 u), u = c (z + a z^3)
-__device__ __forceinline__ float act1(float z, int act) {
-  if (act == LIN_SRELU) {
-    const float r = fmaxf(z, 0.0f);
-    return r * r;
-  }
-  if (act == LIN_GELU) return z * sigmoid(2.0f * kGeluC * z * (1.0f + kGeluA * z * z));
-  return z;
-}
-__device__ __forceinline__ float dact1(float z, int act) {
-  if (act == LIN_SRELU) return 2.0f * fmaxf(z, 0.0f);
-  if (act == LIN_GELU) {
-    z = fminf(fmaxf(z, -30.0f), 30.0f);          // s is 0 or 1 there: keeps 0 times z^3 from becoming NaN
-    const float s = sigmoid(2.0f * kGeluC * z * (1.0f + kGeluA * z * z));
-    return s + z * s * (1.0f - s) * 2.0f * kGeluC * (1.0f + 3.0f * kGeluA * z * z);
-  }
-  return 1.0f;
-}
-
-// Rows [begin, end) of group g, inside [0, m] whatever the offsets hold.
-__device__ __forceinline__ void group_rows(const LinearArgs& a, int g, int64_t& begin, int64_t& end) {
-  begin = 0;
-  end = a.m;
-  if (a.offsets) {
-    begin = g ? a.offsets[g - 1] : 0;
-    end = a.offsets[g];
-    begin = min(max(begin, int64_t{0}), a.m);
-    end = min(max(end, begin), a.m);
-  }
-}
-
-// Row tile `mt` of the groups' tiles of BM rows (a tile holds rows of one
-// group): group, first row, end of the group's rows; false past the last.
-template <int BM>
-__device__ __forceinline__ bool find_tile(const LinearArgs& a, int64_t mt, int& g, int64_t& row0, int64_t& end) {
-  if (!a.offsets) {
-    g = 0;
-    row0 = mt * BM;
-    end = a.m;
-    return row0 < end;
-  }
-  int64_t before = 0;
-  for (g = 0; g < a.groups; ++g) {
-    int64_t b;
-    group_rows(a, g, b, end);
-    const int64_t tiles = (end - b + BM - 1) / BM;
-    if (mt < before + tiles) {
-      row0 = b + (mt - before) * BM;
-      return true;
+__global__ __launch_bounds__(kFewThreads, 2) void linear_few_rows_kernel(LinearArgs a) {
+  constexpr int NW = kFewThreads / 64, U = 8;
+  __shared__ float part[NW][16][17];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int l16 = lane & 15, q = lane >> 4;
+  const int g = blockIdx.y;
+  int64_t begin, end;
+  group_rows(a, g, begin, end);
+  const bool pair = a.act == LIN_SWIGLU;
+  // weight row of index i: SwiGLU takes 8 linear columns and their 8 gates
+  const int n0 = blockIdx.x * 16;
+  auto column = [&](int i) {
+    if (!pair) return n0 + i;
+    const int j = blockIdx.x * 8 + (i & 7);                 // output column
+    return (j >> 5) * 64 + (j & 31) + (i & 8) * 4;
+  };
+  const int n_w = min(column(l16), a.n - 1);
+  const uint16_t* const wrow = a.w + (static_cast<int64_t>(g) * a.n + n_w) * a.k;
+  const int steps = (a.k + 31) / 32;
+  const int s0 = steps * wave / NW, s1 = steps * (wave + 1) / NW;
+  const int n_out = pair ? a.n / 2 : a.n;
+  typedef float v4f4 __attribute__((ext_vector_type(4)));
+  for (int64_t m0 = begin; m0 < end; m0 += kFewRows) {
+    const int rows = static_cast<int>(min(end - m0, int64_t{kFewRows}));
+    const uint16_t* const xrow = a.x + (m0 + min(l16, rows - 1)) * a.k;
+    v4f4 acc{};
+    for (int s = s0; s < s1; s += U) {
+      v4u vw[U], vx[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int r = (s + u) * 32 + q * 8;
+        vw[u] = v4u{};
+        vx[u] = v4u{};
+        if (s + u < s1 && r < a.k) {
+          vw[u] = *reinterpret_cast<const v4u*>(wrow + r);
+          vx[u] = *reinterpret_cast<const v4u*>(xrow + r);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, vw[u]), __builtin_bit_cast(v8bf, vx[u]), acc,
+                                                      0, 0, 0);
     }
-    before += tiles;
+    // lane: row l16, weight rows 4 q + [0, 4)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) part[wave][l16][4 * q + e] = acc[e];
+    __syncthreads();
+    if (threadIdx.x < 256) {
+      const int i = threadIdx.x & 15, row = threadIdx.x >> 4;
+      const int n = column(i);
+      if (row < rows && n < a.n) {
+        const int64_t m = m0 + row;
+        float z = 0.0f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) z += part[w][row][i];
+        if (a.bias) z += a.bias[static_cast<int64_t>(g) * a.n + n];
+        if (a.c) a.c[m * a.n + n] = static_cast<uint16_t>(bf16x2(z, 0.0f));
+        float y = z;
+        bool store = true;
+        int ycol = n;
+        if (pair) {
+          float gate = 0.0f;
+          const int ng = n + 32;
+          store = i < 8;
+          if (store) {
+#pragma unroll
+            for (int w = 0; w < NW; ++w) gate += part[w][row][i + 8];
+            if (a.bias) gate += a.bias[static_cast<int64_t>(g) * a.n + ng];
+          }
+          y = z * (gate * sigmoid_f(gate));
+          ycol = blockIdx.x * 8 + i;
+        } else if (a.act == LIN_GELU) {
+          y = gelu_f(z);
+        } else if (a.act == LIN_SRELU) {
+          const float v = fmaxf(z, 0.0f);
+          y = v * v;
+        }
+        if (store) {
+          if (a.residual) y += bf_lo(a.residual[m * n_out + ycol]);
+          if (a.out_f32) static_cast<float*>(a.y)[m * n_out + ycol] = y;
+          else static_cast<uint16_t*>(a.y)[m * n_out + ycol] = static_cast<uint16_t>(bf16x2(y, 0.0f));
+        }
+      }
+    }
+    __syncthreads();
   }
-  return false;
 }
 
-// acc[j] += P(p0 + wave's 32 rows, r) Q(q0 + 32 j + row, r) over r in [r0, r1).
-// An operand is contiguous along r (element (i, r) at i ld + r) or along i
-// (at r ld + i); rows from `n` on and r from r1 on count as zero.
-constexpr int kBM = 128, kBN = 64, kBK = 32, kPitch = kBK + 8;
-template <bool ALONG_I, int ROWS>
-__device__ __forceinline__ void stage(uint16_t (*lds)[kPitch], const uint16_t* src, int64_t ld, int64_t i0, int64_t n,
-                                      int64_t r0, int64_t r1) {
-  if constexpr (!ALONG_I) {
-    for (int p = threadIdx.x; p < ROWS * (kBK / 8); p += 256) {
-      const int i = p / (kBK / 8), c = p % (kBK / 8) * 8;
-      v4u u{};
-      if (i0 + i < n && r0 + c < r1) u = *reinterpret_cast<const v4u*>(src + (i0 + i) * ld + r0 + c);
-      *reinterpret_cast<v4u*>(&lds[i][c]) = u;
+// ---------------------------------------------------------------------------
+// joins of a split r
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ v4f sum_parts(const float* at, int64_t stride, int parts) {
+  v4f s = *reinterpret_cast<const v4f*>(at);
+  for (int p = 1; p < parts; ++p) s += *reinterpret_cast<const v4f*>(at + p * stride);
+  return s;
+}
+
+__device__ __forceinline__ void store4(void* base, bool f32, int64_t i, v4f v) {
+  if (f32) *reinterpret_cast<v4f*>(static_cast<float*>(base) + i) = v;
+  else *reinterpret_cast<v2u*>(static_cast<uint16_t*>(base) + i) = v2u{bf16x2(v.x, v.y), bf16x2(v.z, v.w)};
+}
+
+// dx or dw: 4 numbers a thread.
+__global__ __launch_bounds__(256) void linear_join_kernel(const float* partial, int64_t count, int parts, void* out, bool f32) {
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (i < count) store4(out, f32, i, sum_parts(partial + i, count, parts));
+}
+
+// Forward (one group): 4 columns of z a thread, or 4 of each half of a pair.
+__global__ __launch_bounds__(256) void linear_join_forward_kernel(LinearArgs a, int parts) {
+  const bool pair = a.act == LIN_SWIGLU;
+  const int n_out = pair ? a.n / 2 : a.n, per_row = n_out / 4;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t m = i / per_row;
+  if (m >= a.m) return;
+  const int ycol = static_cast<int>(i - m * per_row) * 4;
+  const int n = pair ? (ycol >> 5) * 64 + (ycol & 31) : ycol;
+  const int64_t stride = a.m * a.n;
+  auto z_of = [&](int col) __attribute__((always_inline)) {
+    v4f z = sum_parts(a.partial + m * a.n + col, stride, parts);
+    if (a.bias) z += *reinterpret_cast<const v4f_any*>(a.bias + col);
+    if (a.c) store4(a.c, false, m * a.n + col, z);
+    return z;
+  };
+  v4f z = z_of(n);
+  if (pair) {
+    const v4f gate = z_of(n + 32);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) z[e] = z[e] * (gate[e] * sigmoid_f(gate[e]));
+  } else if (a.act == LIN_GELU) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) z[e] = gelu_f(z[e]);
+  } else if (a.act == LIN_SRELU) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float v = fmaxf(z[e], 0.0f);
+      z[e] = v * v;
+    }
+  }
+  if (a.residual) {
+    const v2u u = *reinterpret_cast<const v2u*>(a.residual + m * n_out + ycol);
+    z += v4f{bf_lo(u.x), bf_hi(u.x), bf_lo(u.y), bf_hi(u.y)};
+  }
+  store4(a.y, a.out_f32, m * n_out + ycol, z);
+}
+
+// ---------------------------------------------------------------------------
+// dz and db
+// ---------------------------------------------------------------------------
+//
+// One pass over dy and c: dz in bf16, and the column sums of the unrounded
+// dz over tiles of kDzRows rows of one group, summed per group afterwards.
+constexpr int kDzRows = 128;
+
+__device__ __forceinline__ void unpack8(v4u u, float* f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = bf_lo(u[i]);
+    f[2 * i + 1] = bf_hi(u[i]);
+  }
+}
+__device__ __forceinline__ v4u pack8(const float* f) {
+  return v4u{bf16x2(f[0], f[1]), bf16x2(f[2], f[3]), bf16x2(f[4], f[5]), bf16x2(f[6], f[7])};
+}
+
+// 32 threads run along 256 columns of dy, 8 rows at a time.
+__global__ __launch_bounds__(256) void linear_dz_kernel(LinearArgs a, uint16_t* dz, float* sums) {
+  __shared__ float red[8][32][17];
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, lane = threadIdx.x & 63;
+  int g;
+  int64_t row0, end;
+  if (!find_row_tile<kDzRows>(a, blockIdx.x, lane, g, row0, end)) return;
+  const bool pair = a.act == LIN_SWIGLU;
+  const int n_out = pair ? a.n / 2 : a.n;
+  const int col = (blockIdx.y * 32 + tx) * 8;                  // of dy
+  const int n = pair ? (col >> 5) * 64 + (col & 31) : col;     // of dz (and n + 32 of a pair)
+  float s[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s[i] = 0.0f;
+  if (col < n_out) {
+    for (int64_t m = row0 + ty; m < min(row0 + kDzRows, end); m += 8) {
+      float d[8], v[8];
+      unpack8(*reinterpret_cast<const v4u*>(a.dy + m * n_out + col), d);
+      if (pair) {
+        float x[8], q[8], w[8];
+        unpack8(*reinterpret_cast<const v4u*>(a.c + m * a.n + n), x);
+        unpack8(*reinterpret_cast<const v4u*>(a.c + m * a.n + n + 32), q);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float sg = sigmoid_f(q[i]);
+          v[i] = d[i] * (q[i] * sg);
+          w[i] = d[i] * (x[i] * sg) * (1.0f + q[i] * (1.0f - sg));
+          s[i] += v[i];
+          s[8 + i] += w[i];
+        }
+        if (dz) *reinterpret_cast<v4u*>(dz + m * a.n + n + 32) = pack8(w);
+      } else {
+        if (a.act != LIN_NONE) {
+          float z[8];
+          unpack8(*reinterpret_cast<const v4u*>(a.c + m * a.n + n), z);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (a.act == LIN_SRELU) {
+              v[i] = d[i] * (2.0f * fmaxf(z[i], 0.0f));
+            } else {
+              // past 30 s is 0 or 1: keeps 0 times z^3 from becoming NaN
+              const float c = fminf(fmaxf(z[i], -30.0f), 30.0f);
+              const float sg = sigmoid_f(2.0f * kGeluC * c * (1.0f + kGeluA * c * c));
+              v[i] = d[i] * (sg + c * sg * (1.0f - sg) * (2.0f * kGeluC) * (1.0f + 3.0f * kGeluA * c * c));
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = d[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] += v[i];
+      }
+      if (dz) *reinterpret_cast<v4u*>(dz + m * a.n + n) = pack8(v);
+    }
+  }
+  if (!sums) return;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) red[ty][tx][i] = s[i];
+  __syncthreads();
+  // 32 x 16 sums, two a thread
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = (threadIdx.x & 7) + 8 * h, t = threadIdx.x >> 3;
+    const int c = (blockIdx.y * 32 + t) * 8;
+    if (c >= n_out || (h && !pair)) continue;
+    float v = 0.0f;
+#pragma unroll
+    for (int y = 0; y < 8; ++y) v += red[y][t][i];
+    const int at = pair ? (c >> 5) * 64 + (c & 31) + (i & 7) + 32 * h : c + (i & 7);
+    sums[static_cast<int64_t>(blockIdx.x) * a.n + at] = v;
+  }
+}
+
+__global__ __launch_bounds__(256) void linear_db_kernel(LinearArgs a, const float* sums) {
+  __shared__ float red[4][64];
+  const int lane = threadIdx.x & 63, q = threadIdx.x >> 6, g = blockIdx.y;
+  // tiles of the groups before g, and of g
+  int before = 0, mine = 0;
+  if (a.offsets) {
+    for (int i = lane; i <= g; i += 64) {
+      int64_t b, e;
+      group_rows(a, i, b, e);
+      const int t = static_cast<int>((e - b + kDzRows - 1) / kDzRows);
+      if (i < g) before += t;
+      else mine = t;
+    }
+    for (int d = 32; d; d >>= 1) {
+      before += __shfl_xor(before, d);
+      mine += __shfl_xor(mine, d);
     }
   } else {
-    for (int p = threadIdx.x; p < kBK * (ROWS / 8); p += 256) {
-      const int r = p / (ROWS / 8), c = p % (ROWS / 8) * 8;
-      v4u u{};
-      if (r0 + r < r1 && i0 + c < n) u = *reinterpret_cast<const v4u*>(src + (r0 + r) * ld + i0 + c);
-      for (int q = 0; q < 8; ++q) lds[c + q][r] = static_cast<uint16_t>(u[q / 2] >> (16 * (q & 1)));
-    }
+    mine = static_cast<int>((a.m + kDzRows - 1) / kDzRows);
   }
-}
-template <bool P_ALONG_I, bool Q_ALONG_I>
-__device__ __forceinline__ void product(const uint16_t* p, int64_t ldp, int64_t p0, int64_t np, const uint16_t* q,
-                                        int64_t ldq, int64_t q0, int64_t nq, int64_t r0, int64_t r1, v16f* acc) {
-  __shared__ __attribute__((aligned(16))) uint16_t sp[kBM][kPitch], sq[kBN][kPitch];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l32 = lane & 31, hi = lane >> 5;
-  for (int64_t r = r0; r < r1; r += kBK) {
-    __syncthreads();
-    stage<P_ALONG_I, kBM>(sp, p, ldp, p0, np, r, r1);
-    stage<Q_ALONG_I, kBN>(sq, q, ldq, q0, nq, r, r1);
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < kBK; kk += 16) {
-      const v8bf fp = *reinterpret_cast<const v8bf*>(&sp[wave * 32 + l32][kk + 8 * hi]);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const v8bf fq = *reinterpret_cast<const v8bf*>(&sq[32 * j + l32][kk + 8 * hi]);
-        acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fq, fp, acc[j], 0, 0, 0);
-      }
-    }
-  }
-}
-// Accumulator element v of lane l: P row l % 32, Q row 8 (v / 4) + 4 (l / 32) + v % 4.
-__device__ __forceinline__ int q_row(int v) { return 8 * (v / 4) + 4 * ((threadIdx.x >> 5) & 1) + v % 4; }
-
-__global__ __launch_bounds__(256) void linear_kernel(LinearArgs a) {
-  int g;
-  int64_t row0, end;
-  if (!find_tile<kBM>(a, blockIdx.y, g, row0, end)) return;
-  const int n0 = blockIdx.x * kBN;
-  v16f acc[2] = {};
-  product<false, false>(a.x, a.k, row0, end, a.w + static_cast<int64_t>(g) * a.n * a.k, a.k, n0, a.n, 0, a.k, acc);
-  const int64_t m = row0 + (threadIdx.x >> 6) * 32 + (threadIdx.x & 31);
-  if (m >= end) return;
-  const int n_out = a.act == LIN_SWIGLU ? a.n / 2 : a.n;
-  for (int j = 0; j < 2; ++j)
-    for (int v = 0; v < 16; ++v) {
-      const int n = n0 + 32 * j + q_row(v);
-      if (n >= a.n) continue;
-      if (a.bias) acc[j][v] += a.bias[static_cast<int64_t>(g) * a.n + n];
-      if (a.c) a.c[m * a.n + n] = to_bf(acc[j][v]);
-    }
-  for (int j = 0; j < 2; ++j)
-    for (int v = 0; v < 16; ++v) {
-      int n = n0 + 32 * j + q_row(v);
-      if (n >= a.n) continue;
-      float y;
-      if (a.act == LIN_SWIGLU) {
-        if (j) continue;
-        y = acc[0][v] * (acc[1][v] * sigmoid(acc[1][v]));
-        n = n0 / 2 + q_row(v);
-      } else {
-        y = act1(acc[j][v], a.act);
-      }
-      if (a.residual) y += bf(a.residual[m * n_out + n]);
-      if (a.out_f32) static_cast<float*>(a.y)[m * n_out + n] = y;
-      else static_cast<uint16_t*>(a.y)[m * n_out + n] = to_bf(y);
-    }
-}
-
-// dz of row m, column n, in fp32.
-__device__ __forceinline__ float dz_at(const LinearArgs& a, int64_t m, int n) {
-  if (a.act == LIN_NONE) return bf(a.dy[m * a.n + n]);
-  if (a.act == LIN_SWIGLU) {
-    const int pair = n / 64, i = n % 32;
-    const float d = bf(a.dy[m * (a.n / 2) + pair * 32 + i]);
-    const float x = bf(a.c[m * a.n + pair * 64 + i]), q = bf(a.c[m * a.n + pair * 64 + 32 + i]);
-    const float s = sigmoid(q);
-    return n % 64 < 32 ? d * (q * s) : d * (x * s) * (1.0f + q * (1.0f - s));
-  }
-  return bf(a.dy[m * a.n + n]) * dact1(bf(a.c[m * a.n + n]), a.act);
-}
-__global__ __launch_bounds__(256) void dz_kernel(LinearArgs a, uint16_t* dz) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i < a.m * a.n) dz[i] = to_bf(dz_at(a, i / a.n, static_cast<int>(i % a.n)));
-}
-__global__ __launch_bounds__(256) void db_kernel(LinearArgs a) {
-  __shared__ float part[4][64];
-  const int n = blockIdx.x * 64 + (threadIdx.x & 63), q = threadIdx.x >> 6, g = blockIdx.y;
-  int64_t begin, end;
-  group_rows(a, g, begin, end);
-  float sum = 0.0f;
+  const int n = blockIdx.x * 64 + lane;
+  float s = 0.0f;
   if (n < a.n)
-    for (int64_t m = begin + q; m < end; m += 4) sum += dz_at(a, m, n);
-  part[q][threadIdx.x & 63] = sum;
+    for (int t = q; t < mine; t += 4) s += sums[static_cast<int64_t>(before + t) * a.n + n];
+  red[q][lane] = s;
   __syncthreads();
-  if (q == 0 && n < a.n) a.db[static_cast<int64_t>(g) * a.n + n] = (part[0][threadIdx.x] + part[1][threadIdx.x]) + (part[2][threadIdx.x] + part[3][threadIdx.x]);
-}
-__global__ __launch_bounds__(256) void dx_kernel(LinearArgs a, const uint16_t* dz) {
-  int g;
-  int64_t row0, end;
-  if (!find_tile<kBM>(a, blockIdx.y, g, row0, end)) return;
-  const int k0 = blockIdx.x * kBN;
-  v16f acc[2] = {};
-  product<false, true>(dz, a.n, row0, end, a.w + static_cast<int64_t>(g) * a.n * a.k, a.k, k0, a.k, 0, a.n, acc);
-  const int64_t m = row0 + (threadIdx.x >> 6) * 32 + (threadIdx.x & 31);
-  if (m >= end) return;
-  for (int j = 0; j < 2; ++j)
-    for (int v = 0; v < 16; ++v) {
-      const int k = k0 + 32 * j + q_row(v);
-      if (k < a.k) a.dx[m * a.k + k] = to_bf(acc[j][v]);
-    }
-}
-__global__ __launch_bounds__(256) void dw_kernel(LinearArgs a, const uint16_t* dz) {
-  const int g = blockIdx.z;
-  int64_t begin, end;
-  group_rows(a, g, begin, end);
-  const int n0 = blockIdx.y * kBM, k0 = blockIdx.x * kBN;
-  v16f acc[2] = {};
-  product<true, true>(dz, a.n, n0, a.n, a.x, a.k, k0, a.k, begin, end, acc);
-  const int n = n0 + (threadIdx.x >> 6) * 32 + (threadIdx.x & 31);
-  if (n >= a.n) return;
-  for (int j = 0; j < 2; ++j)
-    for (int v = 0; v < 16; ++v) {
-      const int k = k0 + 32 * j + q_row(v);
-      if (k >= a.k) continue;
-      const int64_t at = (static_cast<int64_t>(g) * a.n + n) * a.k + k;
-      if (a.out_f32) static_cast<float*>(a.dw)[at] = acc[j][v];
-      else static_cast<uint16_t*>(a.dw)[at] = to_bf(acc[j][v]);
-    }
+  if (q == 0 && n < a.n) a.db[static_cast<int64_t>(g) * a.n + n] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
 }
 
-unsigned div_up(int64_t a, int64_t b) { return static_cast<unsigned>((a + b - 1) / b); }
-unsigned row_tiles(const LinearArgs& a) { return div_up(a.m, kBM) + (a.offsets ? a.groups : 0); }
+// ---------------------------------------------------------------------------
+// choices
+// ---------------------------------------------------------------------------
+
+int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return div_up(a, b) * b; }
+
+// Row tiles of all groups at most.
+int64_t row_tiles(const LinearArgs& a, int64_t bm) { return div_up(a.m, bm) + (a.groups > 1 ? a.groups - 1 : 0); }
+
+enum Shape : int { SHAPE_256 = 0, SHAPE_128 = 1, SHAPE_64 = 2 };
+struct Plan {
+  Shape shape;
+  int parts;          // of r
+  int64_t tiles;      // workgroups per part
+};
+
+Plan choose(int64_t tiles256, int64_t tiles128, int64_t tiles64, int64_t cols, int64_t r, bool splittable) {
+  Plan p;
+  if (cols <= 64) p = {SHAPE_64, 1, tiles64};
+  else if (tiles256 >= 160) p = {SHAPE_256, 1, tiles256};
+  else p = {SHAPE_128, 1, tiles128};
+  if (splittable && p.shape != SHAPE_256) {
+    const int64_t most = div_up(r, 4 * kR);              // at least 4 steps a part
+    const int64_t fill = 512 / p.tiles;
+    p.parts = static_cast<int>(fill < 1 ? 1 : fill < most ? fill : most);
+    if (p.parts > 64) p.parts = 64;
+  }
+  return p;
+}
+// Split only without offsets: the join goes over all rows.  (The workspace is
+// sized without knowing them, so never too small.)
+Plan plan_rows(const LinearArgs& a, int64_t cols, int64_t r) {
+  return choose(row_tiles(a, 256) * div_up(cols, 256), row_tiles(a, 128) * div_up(cols, 128),
+                row_tiles(a, 128) * div_up(cols, 64), cols, r, a.groups == 1 && !a.offsets);
+}
+Plan plan_dw(const LinearArgs& a) {
+  Plan p = choose(a.groups * div_up(a.n, 256) * div_up(a.k, 256), a.groups * div_up(a.n, 128) * div_up(a.k, 128),
+                  a.groups * div_up(a.n, 128) * div_up(a.k, 64), a.k, a.m, a.groups == 1);
+  return p;
+}
+bool few_rows(const LinearArgs& a) { return a.m <= 16 * static_cast<int64_t>(a.groups); }
+
+template <int MODE, bool SPLIT>
+void launch_shape(const LinearArgs& a, const Plan& p, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(p.tiles), static_cast<unsigned>(p.parts));
+  switch (p.shape) {
+    case SHAPE_256: hipLaunchKernelGGL((linear_tile_kernel<MODE, 256, 256, 2, 4, SPLIT>), grid, dim3(512), 0, s, a, p.parts); break;
+    case SHAPE_128: hipLaunchKernelGGL((linear_tile_kernel<MODE, 128, 128, 2, 2, SPLIT>), grid, dim3(256), 0, s, a, p.parts); break;
+    case SHAPE_64: hipLaunchKernelGGL((linear_tile_kernel<MODE, 128, 64, 4, 1, SPLIT>), grid, dim3(256), 0, s, a, p.parts); break;
+  }
+}
+template <int MODE>
+hipError_t launch_tiles(const LinearArgs& a, const Plan& p, int64_t count, hipStream_t s) {
+  if (p.parts == 1) {
+    launch_shape<MODE, false>(a, p, s);
+    return hipGetLastError();
+  }
+  launch_shape<MODE, true>(a, p, s);
+  if (MODE == MODE_FORWARD)
+    hipLaunchKernelGGL(linear_join_forward_kernel, dim3(static_cast<unsigned>(div_up(count / (a.act == LIN_SWIGLU ? 2 : 1), 1024))),
+                       dim3(256), 0, s, a, p.parts);
+  else
+    hipLaunchKernelGGL(linear_join_kernel, dim3(static_cast<unsigned>(div_up(count, 1024))), dim3(256), 0, s, a.partial, count,
+                       p.parts, MODE == MODE_DX ? static_cast<void*>(a.dx) : a.dw, MODE == MODE_DW && a.out_f32);
+  return hipGetLastError();
+}
+
+int64_t partial_bytes(const Plan& p, int64_t count) { return p.parts > 1 ? p.parts * count * 4 : 0; }
+
+// Workspace of the backward: dz, the column sums of the row tiles, and the
+// parts of dx and dw (one after the other in the same place).
+struct BackwardWorkspace {
+  int64_t dz, sums, partial, total;
+};
+BackwardWorkspace backward_workspace(const LinearArgs& a, bool dx, bool dw, bool db) {
+  BackwardWorkspace w{};
+  int64_t at = 0;
+  w.dz = at;
+  if (a.act != LIN_NONE && (dx || dw)) at += round_up(a.m * a.n * 2, 256);
+  w.sums = at;
+  if (db) at += round_up(row_tiles(a, kDzRows) * a.n * 4, 256);
+  w.partial = at;
+  int64_t most = 0;
+  if (dx && a.m) most = partial_bytes(plan_rows(a, a.k, a.n), a.m * a.k);
+  if (dw) {
+    const int64_t b = partial_bytes(plan_dw(a), static_cast<int64_t>(a.groups) * a.n * a.k);
+    most = b > most ? b : most;
+  }
+  w.total = at + most;
+  return w;
+}
 
 }  // namespace
 
-int64_t linear_workspace(const LinearArgs&) { return 0; }
-int64_t linear_backward_workspace(const LinearArgs& a, bool dx, bool dw, bool) {
-  return a.act != LIN_NONE && (dx || dw) ? a.m * a.n * 2 : 0;
+int64_t linear_workspace(const LinearArgs& a) {
+  if (a.m == 0 || few_rows(a)) return 0;
+  return partial_bytes(plan_rows(a, a.n, a.k), a.m * a.n);
+}
+int64_t linear_backward_workspace(const LinearArgs& a, bool dx, bool dw, bool db) {
+  return backward_workspace(a, dx, dw, db).total;
 }
 
-hipError_t launch_linear(const LinearArgs& a, hipStream_t s) {
+hipError_t launch_linear(const LinearArgs& args, hipStream_t s) {
+  LinearArgs a = args;
   if (a.m == 0) return hipSuccess;
-  hipLaunchKernelGGL(linear_kernel, dim3(div_up(a.n, kBN), row_tiles(a)), dim3(256), 0, s, a);
-  return hipGetLastError();
+  if (few_rows(a)) {
+    hipLaunchKernelGGL(linear_few_rows_kernel, dim3(static_cast<unsigned>(div_up(a.n, 16)), static_cast<unsigned>(a.groups)),
+                       dim3(kFewThreads), 0, s, a);
+    return hipGetLastError();
+  }
+  a.partial = static_cast<float*>(a.workspace);
+  return launch_tiles<MODE_FORWARD>(a, plan_rows(a, a.n, a.k), a.m * a.n, s);
 }
 
-hipError_t launch_linear_backward(const LinearArgs& a, hipStream_t s) {
-  const uint16_t* dz = a.dy;
-  if (a.act != LIN_NONE && a.m && (a.dx || a.dw)) {
-    dz = static_cast<uint16_t*>(a.workspace);
-    hipLaunchKernelGGL(dz_kernel, dim3(div_up(a.m * a.n, 256)), dim3(256), 0, s, a, static_cast<uint16_t*>(a.workspace));
+hipError_t launch_linear_backward(const LinearArgs& args, hipStream_t s) {
+  LinearArgs a = args;
+  const BackwardWorkspace w = backward_workspace(a, a.dx, a.dw, a.db);
+  uint8_t* const ws = static_cast<uint8_t*>(a.workspace);
+  const bool make_dz = a.act != LIN_NONE && (a.dx || a.dw) && a.m;
+  uint16_t* const dz = make_dz ? reinterpret_cast<uint16_t*>(ws + w.dz) : nullptr;
+  float* const sums = a.db ? reinterpret_cast<float*>(ws + w.sums) : nullptr;
+  a.dz = make_dz ? dz : a.dy;
+  a.partial = reinterpret_cast<float*>(ws + w.partial);
+  hipError_t e = hipSuccess;
+  if ((make_dz || a.db) && a.m) {
+    const int n_out = a.act == LIN_SWIGLU ? a.n / 2 : a.n;
+    hipLaunchKernelGGL(linear_dz_kernel, dim3(static_cast<unsigned>(row_tiles(a, kDzRows)), static_cast<unsigned>(div_up(n_out, 256))),
+                       dim3(256), 0, s, a, dz, sums);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  if (a.db) hipLaunchKernelGGL(db_kernel, dim3(div_up(a.n, 64), a.groups), dim3(256), 0, s, a);
-  if (a.dx && a.m) hipLaunchKernelGGL(dx_kernel, dim3(div_up(a.k, kBN), row_tiles(a)), dim3(256), 0, s, a, dz);
-  if (a.dw) hipLaunchKernelGGL(dw_kernel, dim3(div_up(a.k, kBN), div_up(a.n, kBM), a.groups), dim3(256), 0, s, a, dz);
-  return hipGetLastError();
+  if (a.db) {
+    hipLaunchKernelGGL(linear_db_kernel, dim3(static_cast<unsigned>(div_up(a.n, 64)), static_cast<unsigned>(a.groups)), dim3(256), 0,
+                       s, a, sums);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (a.dx && a.m && (e = launch_tiles<MODE_DX>(a, plan_rows(a, a.k, a.n), a.m * a.k, s)) != hipSuccess) return e;
+  if (a.dw && (e = launch_tiles<MODE_DW>(a, plan_dw(a), static_cast<int64_t>(a.groups) * a.n * a.k, s)) != hipSuccess) return e;
+  return e;
 }
 
 }  // namespace moegg

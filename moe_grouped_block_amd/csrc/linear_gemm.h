@@ -1,0 +1,507 @@
+// The tile kernel of linear and its gradients (BF16 operands, fp32 sums).
+//
+//   out(p, q) = sum over r of P(p, r) Q(q, r)
+//
+//   forward   P = x rows (m),   Q = w rows (n),    r = k   both contiguous along r
+//   dx        P = dz rows (m),  Q = w columns (k), r = n   Q contiguous along q
+//   dw        P = dz columns (n), Q = x columns (k), r = m   both contiguous along p / q
+//
+// One workgroup computes a BP x BQ tile in steps of 64 r.  Each step's two
+// operand tiles come into LDS by direct global -> LDS loads of 16 bytes a lane,
+// two stages deep.  An operand contiguous along r lies in LDS as rows of 64 r
+// (128 bytes) and is read with 16-byte reads; one contiguous along its rows
+// lies as 64 lines of its rows and is read with the transposing 8-byte reads
+// (ds_read_b64_tr_b16: 16 lanes read 4 lines of 16 elements, and each gets
+// one column's 4), so no operand is ever transposed in memory.  Both images are swizzled in 16-byte
+// chunks so that a read's lanes meet all banks once.
+//
+// The Q tile is the matrix instruction's first operand: a lane then holds
+// one row p of the output and runs of 4 contiguous columns.
+#pragma once
+
+#include "grouped_gemm.h"
+#include "layer_internal.h"
+
+namespace moegg {
+namespace {
+
+constexpr int kR = 64;                 // r per step
+
+// What a lane reads past the end of r: zeros.
+__device__ const uint32_t kZeros[4] = {0, 0, 0, 0};
+
+// Swizzle of line r of an image whose lines hold CH 16-byte chunks: the slot
+// of chunk c is c ^ line_swizzle(r).  A transposing read covers 4 lines of 64
+// bytes in 32 lanes; lines are 256 bytes or more apart in multiples of the 64
+// banks (CH >= 16), or half of that (CH = 8).
+template <int CH>
+__device__ __forceinline__ int line_swizzle(int r) {
+  return (CH >= 16 ? (r & 3) << 2 : ((r >> 1) & 1) << 2) ^ (((r >> 3) & 1) << 1);
+}
+
+// One operand's tile of ROWS rows: staging and fragments.
+template <bool ALONG_R, int ROWS, int NW>
+struct TileOperand {
+  static constexpr int BYTES = ROWS * kR * 2;
+  static constexpr int NI = BYTES / 1024 / NW;     // 1 KB loads per wave and step
+  static constexpr int CH = ROWS / 8;              // chunks per line (rows contiguous)
+  static_assert(NI * NW * 1024 == BYTES, "tile split over the waves");
+  const uint8_t* base;                             // wave-uniform: the step's first byte
+  uint32_t off[NI];                                // per lane
+  int64_t advance;                                 // bytes per step
+
+  // Image row (ALONG_R) or line of load j, and its source chunk.
+  __device__ static __forceinline__ int image_row(int wave, int j, int lane) {
+    return ALONG_R ? (wave * NI + j) * 8 + (lane >> 3) : ((wave * NI + j) * 64 + lane) / CH;
+  }
+  __device__ static __forceinline__ int image_chunk(int wave, int j, int lane) {
+    const int r = image_row(wave, j, lane);
+    return ALONG_R ? (lane & 7) ^ ((r >> 1) & 7) : (lane % CH) ^ line_swizzle<CH>(r);
+  }
+  // Tile of rows [i0, i0 + ROWS) of `n`, from r0 on; rows past the last one
+  // repeat it (their results are not stored).
+  __device__ __forceinline__ void init(const uint16_t* src, int64_t ld, int64_t i0, int64_t n, int64_t r0, int wave,
+                                       int lane) {
+    if constexpr (ALONG_R) {
+      base = reinterpret_cast<const uint8_t*>(src + i0 * ld + r0);
+      advance = kR * 2;
+      const int last = static_cast<int>(min(n - i0, int64_t{ROWS})) - 1;
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+        off[j] = static_cast<uint32_t>(min(image_row(wave, j, lane), last)) * static_cast<uint32_t>(ld * 2) +
+                 image_chunk(wave, j, lane) * 16;
+    } else {
+      base = reinterpret_cast<const uint8_t*>(src + r0 * ld + i0);
+      advance = kR * ld * 2;
+      const int last = (static_cast<int>(min(n - i0, int64_t{ROWS})) >> 3) - 1;
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+        off[j] = static_cast<uint32_t>(image_row(wave, j, lane)) * static_cast<uint32_t>(ld * 2) +
+                 min(image_chunk(wave, j, lane), last) * 16;
+    }
+  }
+  __device__ __forceinline__ void load(uint8_t* lds, int wave, int j) const {
+    dma16(at(base, off[j]), lds + (wave * NI + j) * 1024);
+  }
+  // The last step of a ragged r: `left` of its 64 r exist.
+  __device__ __forceinline__ void load_tail(uint8_t* lds, int wave, int lane, int j, int left) const {
+    const int r = ALONG_R ? image_chunk(wave, j, lane) * 8 : image_row(wave, j, lane);
+    const uint8_t* src = r < left ? at(base, off[j]) : reinterpret_cast<const uint8_t*>(kZeros);
+    dma16(src, lds + (wave * NI + j) * 1024);
+  }
+
+  // Per-lane byte offset of the fragments of the 32 rows from tb on.
+  __device__ static __forceinline__ uint32_t frag_base(int tb, int lane) {
+    if constexpr (ALONG_R) {
+      return (tb + (lane & 31)) * (kR * 2);
+    } else {
+      const int q = lane >> 4;
+      const int line = (q >> 1) * 8 + ((lane >> 2) & 3);
+      const int chunk = tb / 8 + (q & 1) * 2 + ((lane & 3) >> 1);
+      return line * (ROWS * 2) + (chunk ^ line_swizzle<CH>(line)) * 16 + (lane & 1) * 8;
+    }
+  }
+  // Fragment of window kk (16 r): lane l holds row tb + l % 32, r 8 (l / 32) + [0, 8).
+  __device__ static __forceinline__ v8bf frag(const uint8_t* lds, uint32_t fb, int kk, int lane) {
+    if constexpr (ALONG_R) {
+      const int sw = ((lane & 31) >> 1) & 7;
+      return *reinterpret_cast<const v8bf*>(lds + fb + (((2 * kk + (lane >> 5)) ^ sw) * 16));
+    } else {
+      typedef short v4s __attribute__((ext_vector_type(4)));
+      typedef short v8s __attribute__((ext_vector_type(8)));
+      typedef __attribute__((address_space(3))) v4s lds4;
+      lds4* const p = (lds4*)(lds + fb + kk * (16 * ROWS * 2));
+      const v4s a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p);
+      const v4s b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p + ROWS);     // 4 lines on (8 bytes a step)
+      return __builtin_bit_cast(v8bf, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+  }
+};
+
+enum LinearMode : int { MODE_FORWARD = 0, MODE_DX = 1, MODE_DW = 2 };
+
+// Rows [begin, end) of group g, inside [0, m] whatever the offsets hold.
+__device__ __forceinline__ void group_rows(const LinearArgs& a, int g, int64_t& begin, int64_t& end) {
+  begin = 0;
+  end = a.m;
+  if (a.offsets) {
+    begin = g ? a.offsets[g - 1] : 0;
+    end = a.offsets[g];
+    begin = min(max(begin, int64_t{0}), a.m);
+    end = min(max(end, begin), a.m);
+  }
+}
+
+// Tiles of BM rows of every group (a tile holds rows of one group); the
+// groups run along the lanes, 64 at a time.
+template <int BM>
+__device__ __forceinline__ int count_row_tiles(const LinearArgs& a, int lane) {
+  if (!a.offsets) return static_cast<int>((a.m + BM - 1) / BM);
+  int sum = 0;
+  for (int g = lane; g < a.groups; g += 64) {
+    int64_t b, e;
+    group_rows(a, g, b, e);
+    sum += static_cast<int>((e - b + BM - 1) / BM);
+  }
+  for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+  return __builtin_amdgcn_readfirstlane(sum);
+}
+// Row tile mt: its group, first row and the end of the group's rows.
+template <int BM>
+__device__ __forceinline__ bool find_row_tile(const LinearArgs& a, int mt, int lane, int& g, int64_t& row0, int64_t& end) {
+  if (!a.offsets) {
+    g = 0;
+    row0 = static_cast<int64_t>(mt) * BM;
+    end = a.m;
+    return row0 < end;
+  }
+  int before = 0;
+  for (int g0 = 0; g0 < a.groups; g0 += 64) {
+    int64_t b = 0, e = 0;
+    if (g0 + lane < a.groups) group_rows(a, g0 + lane, b, e);
+    const int tiles = static_cast<int>((e - b + BM - 1) / BM);
+    int scan = tiles;
+    for (int d = 1; d < 64; d <<= 1) {
+      const int y = __shfl_up(scan, d);
+      if (lane >= d) scan += y;
+    }
+    const uint64_t past = __ballot(before + scan > mt);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      g = __builtin_amdgcn_readfirstlane(g0 + l);
+      const int first = before + __builtin_amdgcn_readlane(scan, l) - __builtin_amdgcn_readlane(tiles, l);
+      const int bl = __builtin_amdgcn_readlane(static_cast<int>(b), l);
+      row0 = bl + static_cast<int64_t>(mt - first) * BM;
+      end = __builtin_amdgcn_readlane(static_cast<int>(e), l);
+      return true;
+    }
+    before += __builtin_amdgcn_readlane(scan, 63);
+  }
+  return false;
+}
+
+// Workgroup w of `total` tiles -> tile.  Workgroups go round-robin over the 8
+// XCDs (each with its own L2), so each pass of 256 gives every XCD 32
+// consecutive tiles (the last pass an eighth of what is left).
+__device__ __forceinline__ int tile_of_workgroup(int w, int total) {
+  const int pass = w & ~255, rem = min(total - pass, 256), i = w - pass;
+  const int xcd = i & 7, j = i >> 3;
+  return pass + xcd * (rem >> 3) + min(xcd, rem & 7) + j;
+}
+// Tile -> (row tile, column tile): bands of 8 row tiles, rows fastest, so that
+// consecutive tiles share operands.
+__device__ __forceinline__ void tile_position(int t, int rows, int cols, int& rt, int& ct) {
+  const int band = t / (8 * cols), in = t - band * 8 * cols;
+  const int height = min(8, rows - 8 * band);
+  ct = in / height;
+  rt = 8 * band + in - ct * height;
+}
+
+// 16-byte aligned or not, 4 floats.
+typedef float v4f_any __attribute__((ext_vector_type(4), aligned(4)));
+
+// Rows of a 32-row block of output through the wave's LDS scratch, in whole
+// W-byte segments: lane (row l32, half hi) holds bytes [32 b + 16 hi, + 16) of
+// its row in q[b].  Rows from `rows` on and bytes from `valid` on are not stored.
+template <int W>
+__device__ __forceinline__ void store_block(uint8_t* base, int64_t pitch, const v4u* q, uint8_t* lds, int lane, int rows,
+                                            int valid) {
+  constexpr int CPR = W / 16;
+  auto slot = [](int r, int c) __attribute__((always_inline)) {
+    return W == 128 ? c ^ ((r >> 1) & 7) : c ^ ((r >> 2) & 3);
+  };
+  const int l32 = lane & 31, hi = lane >> 5;
+  wave_sync_lds();
+#pragma unroll
+  for (int b = 0; b < W / 32; ++b) *reinterpret_cast<v4u*>(lds + l32 * W + slot(l32, 2 * b + hi) * 16) = q[b];
+  wave_sync_lds();
+  const int c = lane % CPR;
+  v4u v[W / 32];
+#pragma unroll
+  for (int k = 0; k < W / 32; ++k) {
+    const int r = k * (64 / CPR) + lane / CPR;
+    v[k] = *reinterpret_cast<const v4u*>(lds + r * W + slot(r, c) * 16);
+  }
+#pragma unroll
+  for (int k = 0; k < W / 32; ++k) {
+    const int r = k * (64 / CPR) + lane / CPR;
+    if (r < rows && c * 16 < valid) *reinterpret_cast<v4u*>(base + r * pitch + c * 16) = v[k];
+  }
+  wave_sync_lds();
+}
+
+// gelu(z) = z / 2 (1 + tanh u) = z sigmoid(2 u), u = c (z + a z^3)
+constexpr float kGeluC = 0.7978845608028654f;    // sqrt(2 / pi)
+constexpr float kGeluA = 0.044715f;
+__device__ __forceinline__ float gelu_f(float z) {
+  return z * sigmoid_f(2.0f * kGeluC * z * (1.0f + kGeluA * z * z));
+}
+__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+
+// The tile kernel.  SPLIT: blockIdx.y is a part of r, and the sums go to
+// the workspace, (parts, rows of the output, columns) fp32.
+template <int MODE, int BP, int BQ, int WP, int WQ, bool SPLIT>
+__global__ __launch_bounds__(64 * WP * WQ, 2) void linear_tile_kernel(LinearArgs a, int parts) {
+  constexpr int NW = WP * WQ, TM = BP / WP / 32, TN = BQ / WQ / 32;
+  using TP = TileOperand<MODE != MODE_DW, BP, NW>;
+  using TQ = TileOperand<MODE == MODE_FORWARD, BQ, NW>;
+  static_assert(TN == 2, "a wave's columns are one pair of 32-column blocks");
+  // one array per stage and operand: the compiler then sees that a stage's
+  // loads do not touch what is being read
+  __shared__ __attribute__((aligned(16))) uint8_t sP0[TP::BYTES], sP1[TP::BYTES], sQ0[TQ::BYTES], sQ1[TQ::BYTES];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wp = wave / WQ, wq = wave % WQ;
+
+  // ---- the tile ----
+  const int cols = MODE == MODE_FORWARD ? a.n : a.k;       // columns of the output
+  const int col_tiles = (cols + BQ - 1) / BQ;
+  int g;
+  int64_t row0, row_end, r0 = 0, r1;
+  int col0;
+  if constexpr (MODE == MODE_DW) {
+    const int row_tiles = (a.n + BP - 1) / BP;
+    const int t = tile_of_workgroup(blockIdx.x, gridDim.x);
+    g = t / (row_tiles * col_tiles);
+    int rt, ct;
+    tile_position(t - g * row_tiles * col_tiles, row_tiles, col_tiles, rt, ct);
+    row0 = static_cast<int64_t>(rt) * BP;
+    row_end = a.n;
+    col0 = ct * BQ;
+    group_rows(a, g, r0, r1);
+  } else {
+    const int row_tiles = count_row_tiles<BP>(a, lane);
+    const int total = row_tiles * col_tiles;
+    if (static_cast<int>(blockIdx.x) >= total) return;
+    int rt, ct;
+    tile_position(tile_of_workgroup(blockIdx.x, total), row_tiles, col_tiles, rt, ct);
+    if (!find_row_tile<BP>(a, rt, lane, g, row0, row_end)) return;
+    col0 = ct * BQ;
+    r1 = MODE == MODE_FORWARD ? a.k : a.n;
+  }
+  if constexpr (SPLIT) {
+    const int64_t steps = (r1 - r0 + kR - 1) / kR;
+    const int64_t lo = steps * blockIdx.y / parts, hi = steps * (blockIdx.y + 1) / parts;
+    r1 = min(r1, r0 + hi * kR);
+    r0 += lo * kR;
+  }
+  const int64_t wg = static_cast<int64_t>(g) * a.n * a.k;
+  TP p;
+  TQ q;
+  if constexpr (MODE == MODE_FORWARD) {
+    p.init(a.x, a.k, row0, row_end, r0, wave, lane);
+    q.init(a.w + wg, a.k, col0, a.n, r0, wave, lane);
+  } else if constexpr (MODE == MODE_DX) {
+    p.init(a.dz, a.n, row0, row_end, r0, wave, lane);
+    q.init(a.w + wg, a.k, col0, a.k, r0, wave, lane);
+  } else {
+    p.init(a.dz, a.n, row0, a.n, r0, wave, lane);
+    q.init(a.x, a.k, col0, a.k, r0, wave, lane);
+  }
+  uint32_t fp[TM], fq[TN];
+#pragma unroll
+  for (int t = 0; t < TM; ++t) fp[t] = TP::frag_base(wp * (TM * 32) + t * 32, lane);
+#pragma unroll
+  for (int t = 0; t < TN; ++t) fq[t] = TQ::frag_base(wq * (TN * 32) + t * 32, lane);
+
+  // ---- the sum ----
+  v16f acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = v16f{};
+  const int64_t span = r1 - r0;
+  const int steps = static_cast<int>((span + kR - 1) / kR);
+  const int tail = static_cast<int>(span - static_cast<int64_t>(steps - 1) * kR);   // r of the last step
+  auto issue = [&](int s, uint8_t* lp, uint8_t* lq) __attribute__((always_inline)) {
+    if (s == steps - 1 && tail < kR) {
+#pragma unroll
+      for (int j = 0; j < TP::NI; ++j) p.load_tail(lp, wave, lane, j, tail);
+#pragma unroll
+      for (int j = 0; j < TQ::NI; ++j) q.load_tail(lq, wave, lane, j, tail);
+    } else {
+#pragma unroll
+      for (int j = 0; j < TP::NI; ++j) p.load(lp, wave, j);
+#pragma unroll
+      for (int j = 0; j < TQ::NI; ++j) q.load(lq, wave, j);
+    }
+    p.base += p.advance;
+    q.base += q.advance;
+  };
+  auto compute = [&](const uint8_t* lp, const uint8_t* lq) __attribute__((always_inline)) {
+#pragma unroll
+    for (int kk = 0; kk < kR / 16; ++kk) {
+      v8bf vq[TN];
+#pragma unroll
+      for (int j = 0; j < TN; ++j) vq[j] = TQ::frag(lq, fq[j], kk, lane);
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        const v8bf vp = TP::frag(lp, fp[i], kk, lane);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vq[j], vp, acc[i][j], 0, 0, 0);
+      }
+    }
+  };
+  auto arrive = [&]() __attribute__((always_inline)) {
+    wait_vmcnt<0>();
+    __syncthreads();
+  };
+  if (steps > 0) {
+    issue(0, sP0, sQ0);
+    arrive();
+    for (int s = 0; s < steps; s += 2) {
+      if (s + 1 < steps) issue(s + 1, sP1, sQ1);
+      compute(sP0, sQ0);
+      arrive();
+      if (s + 1 >= steps) break;
+      if (s + 2 < steps) issue(s + 2, sP0, sQ0);
+      compute(sP1, sQ1);
+      arrive();
+    }
+  }
+
+  // ---- the output ----
+  uint8_t* const scratch = (wave & 1 ? sP1 : sP0) + (wave >> 1) * 4096;
+  static_assert(TP::BYTES >= (NW + 1) / 2 * 4096, "scratch of the waves");
+  const int l32 = lane & 31, hi = lane >> 5;
+  const int ncol = col0 + wq * 64;                          // the wave's first column
+  if (ncol >= cols) return;
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int64_t rb = row0 + wp * (TM * 32) + i * 32;      // first row of the block
+    const int rows = static_cast<int>(min(row_end - rb, int64_t{32}));
+    if (rows <= 0) break;
+    if constexpr (SPLIT) {
+      const int64_t out_rows = MODE == MODE_DW ? static_cast<int64_t>(a.groups) * a.n : a.m;
+      const int64_t r = (MODE == MODE_DW ? static_cast<int64_t>(g) * a.n : 0) + rb;
+      float* const base = a.partial + (blockIdx.y * out_rows + r) * cols + ncol;
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        v4u v[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          v[b] = v4u{__float_as_uint(acc[i][j][4 * b]), __float_as_uint(acc[i][j][4 * b + 1]),
+                     __float_as_uint(acc[i][j][4 * b + 2]), __float_as_uint(acc[i][j][4 * b + 3])};
+        store_block<128>(reinterpret_cast<uint8_t*>(base + 32 * j), static_cast<int64_t>(cols) * 4, v, scratch, lane, rows,
+                         (cols - ncol - 32 * j) * 4);
+      }
+    } else if constexpr (MODE != MODE_FORWARD) {
+      const int64_t r = (MODE == MODE_DW ? static_cast<int64_t>(g) * a.n : 0) + rb;
+      if (MODE == MODE_DW && a.out_f32) {
+        float* const base = static_cast<float*>(a.dw) + r * cols + ncol;
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          v4u v[4];
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            v[b] = v4u{__float_as_uint(acc[i][j][4 * b]), __float_as_uint(acc[i][j][4 * b + 1]),
+                       __float_as_uint(acc[i][j][4 * b + 2]), __float_as_uint(acc[i][j][4 * b + 3])};
+          store_block<128>(reinterpret_cast<uint8_t*>(base + 32 * j), static_cast<int64_t>(cols) * 4, v, scratch, lane, rows,
+                           (cols - ncol - 32 * j) * 4);
+        }
+      } else {
+        uint16_t* const base = (MODE == MODE_DW ? static_cast<uint16_t*>(a.dw) : a.dx) + r * cols + ncol;
+        v4u v[4];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          float f[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) f[e] = acc[i][j][e];
+          bf16_pieces(f, v + 2 * j);
+        }
+        store_block<128>(reinterpret_cast<uint8_t*>(base), static_cast<int64_t>(cols) * 2, v, scratch, lane, rows,
+                         (cols - ncol) * 2);
+      }
+    } else {
+      // z = sum + bias, c = bf16(z)
+      float z[TN][16];
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const int n = ncol + 32 * j + 8 * b + 4 * hi;
+          v4f_any v{};
+          if (a.bias && n < a.n) v = *reinterpret_cast<const v4f_any*>(a.bias + static_cast<int64_t>(g) * a.n + n);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) z[j][4 * b + e] = acc[i][j][4 * b + e] + v[e];
+        }
+      if (a.c) {
+        v4u v[4];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) bf16_pieces(z[j], v + 2 * j);
+        store_block<128>(reinterpret_cast<uint8_t*>(a.c + rb * a.n + ncol), static_cast<int64_t>(a.n) * 2, v, scratch, lane,
+                         rows, (a.n - ncol) * 2);
+      }
+      // y = act(z): TO blocks of 32 columns from column ycol on
+      const bool pair = a.act == LIN_SWIGLU;
+      const int n_out = pair ? a.n / 2 : a.n, ycol = pair ? ncol / 2 : ncol;
+      if (pair) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) z[0][e] = z[0][e] * (z[1][e] * sigmoid_f(z[1][e]));
+      } else if (a.act == LIN_GELU) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) z[j][e] = gelu_f(z[j][e]);
+      } else if (a.act == LIN_SRELU) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float v = fmaxf(z[j][e], 0.0f);
+            z[j][e] = v * v;
+          }
+      }
+      if (a.residual) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          if (j && pair) break;
+          v4u u[2];
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const int n = ycol + 32 * j + 16 * b + 8 * hi;
+            u[b] = v4u{};
+            if (n < n_out && l32 < rows) u[b] = *reinterpret_cast<const v4u*>(a.residual + (rb + l32) * n_out + n);
+          }
+          v2u w[4];
+          unpack_bf16(u, w);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            z[j][4 * b] += bf_lo(w[b].x);
+            z[j][4 * b + 1] += bf_hi(w[b].x);
+            z[j][4 * b + 2] += bf_lo(w[b].y);
+            z[j][4 * b + 3] += bf_hi(w[b].y);
+          }
+        }
+      }
+      if (a.out_f32) {
+        float* const base = static_cast<float*>(a.y) + rb * n_out + ycol;
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          if (j && pair) break;
+          v4u v[4];
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            v[b] = v4u{__float_as_uint(z[j][4 * b]), __float_as_uint(z[j][4 * b + 1]), __float_as_uint(z[j][4 * b + 2]),
+                       __float_as_uint(z[j][4 * b + 3])};
+          store_block<128>(reinterpret_cast<uint8_t*>(base + 32 * j), static_cast<int64_t>(n_out) * 4, v, scratch, lane, rows,
+                           (n_out - ycol - 32 * j) * 4);
+        }
+      } else {
+        uint8_t* const base = reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(a.y) + rb * n_out + ycol);
+        v4u v[4];
+        bf16_pieces(z[0], v);
+        if (pair) {
+          store_block<64>(base, static_cast<int64_t>(n_out) * 2, v, scratch, lane, rows, 64);
+        } else {
+          bf16_pieces(z[1], v + 2);
+          store_block<128>(base, static_cast<int64_t>(n_out) * 2, v, scratch, lane, rows, (n_out - ycol) * 2);
+        }
+      }
+    }
+  }
+}
+
+}  // namespace
+}  // namespace moegg
