@@ -364,7 +364,7 @@ moegg_status moegg_unsort(const float* rows_values, const int32_t* row_of, float
  * act: NONE, SRELU (relu(z)^2), GELU, or SWIGLU on [X | G] pairs of 32 columns
  * as in moegg_run (N_out = n / 2, else N_out = n).  Sums are fp32. */
 typedef struct moegg_linear_problem {
-  int64_t m;            /* rows, 0..2^31-1                                     */
+  int64_t m;            /* rows, 0..2^31-1024                                  */
   int32_t n;            /* multiple of 8 (64 for SWIGLU), <= 2^20              */
   int32_t k;            /* multiple of 8, <= 2^20                              */
   int32_t num_groups;   /* 1..1024                                             */

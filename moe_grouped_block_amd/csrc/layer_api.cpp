@@ -171,7 +171,8 @@ moegg_status check_linear(const moegg_linear_problem* pp) {
   if (!pp) return set_error(MOEGG_ERROR_INVALID_VALUE, "problem must be non-NULL");
   const moegg_linear_problem& p = *pp;
   if (p.m < 0) return set_error(MOEGG_ERROR_INVALID_VALUE, "m=%lld negative", (long long)p.m);
-  if (p.m > INT32_MAX) return set_error(MOEGG_ERROR_NOT_SUPPORTED, "m=%lld above 2^31-1", (long long)p.m);
+  // (the kernels count r, which may be m, in 32 bits up to two steps past its end)
+  if (p.m > INT32_MAX - 1023) return set_error(MOEGG_ERROR_NOT_SUPPORTED, "m=%lld above 2^31-1024", (long long)p.m);
   if (p.n <= 0 || p.k <= 0) return set_error(MOEGG_ERROR_INVALID_VALUE, "n=%d k=%d must be positive", p.n, p.k);
   if (p.num_groups < 1 || p.num_groups > moegg::kMaxExperts)
     return set_error(MOEGG_ERROR_INVALID_VALUE, "num_groups=%d outside 1..%d", p.num_groups, moegg::kMaxExperts);

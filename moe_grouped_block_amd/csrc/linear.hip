@@ -341,7 +341,7 @@ template <int MODE, bool SPLIT>
 void launch_shape(const LinearArgs& a, const Plan& p, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(p.tiles), static_cast<unsigned>(p.parts));
   switch (p.shape) {
-    case SHAPE_256: hipLaunchKernelGGL((linear_tile_kernel<MODE, 256, 256, 2, 4, SPLIT>), grid, dim3(512), 0, s, a, p.parts); break;
+    case SHAPE_256: hipLaunchKernelGGL((linear_pingpong_kernel<MODE, SPLIT>), grid, dim3(512), 0, s, a, p.parts); break;
     case SHAPE_128: hipLaunchKernelGGL((linear_tile_kernel<MODE, 128, 128, 2, 2, SPLIT>), grid, dim3(256), 0, s, a, p.parts); break;
     case SHAPE_64: hipLaunchKernelGGL((linear_tile_kernel<MODE, 128, 64, 4, 1, SPLIT>), grid, dim3(256), 0, s, a, p.parts); break;
   }

@@ -39,8 +39,9 @@ __device__ __forceinline__ int line_swizzle(int r) {
   return (CH >= 16 ? (r & 3) << 2 : ((r >> 1) & 1) << 2) ^ (((r >> 3) & 1) << 1);
 }
 
-// One operand's tile of ROWS rows: staging and fragments.
-template <bool ALONG_R, int ROWS, int NW>
+// One operand's tile of ROWS rows: staging and fragments.  With HALF 0 or 1
+// the 128 image rows are the ones of a 256-row tile whose bit 6 is HALF.
+template <bool ALONG_R, int ROWS, int NW, int HALF = -1>
 struct TileOperand {
   static constexpr int BYTES = ROWS * kR * 2;
   static constexpr int NI = BYTES / 1024 / NW;     // 1 KB loads per wave and step
@@ -58,26 +59,30 @@ struct TileOperand {
     const int r = image_row(wave, j, lane);
     return ALONG_R ? (lane & 7) ^ ((r >> 1) & 7) : (lane % CH) ^ line_swizzle<CH>(r);
   }
-  // Tile of rows [i0, i0 + ROWS) of `n`, from r0 on; rows past the last one
+  // Tile row of image row i.
+  __device__ static __forceinline__ int tile_row(int i) {
+    return HALF < 0 ? i : (i & 63) | (i & 64) << 1 | HALF << 6;
+  }
+  // Tile of rows from i0 on (up to n), from r0 on; rows past the last one
   // repeat it (their results are not stored).
   __device__ __forceinline__ void init(const uint16_t* src, int64_t ld, int64_t i0, int64_t n, int64_t r0, int wave,
                                        int lane) {
     if constexpr (ALONG_R) {
       base = reinterpret_cast<const uint8_t*>(src + i0 * ld + r0);
       advance = kR * 2;
-      const int last = static_cast<int>(min(n - i0, int64_t{ROWS})) - 1;
+      const int last = static_cast<int>(min(n - i0, int64_t{256})) - 1;
 #pragma unroll
       for (int j = 0; j < NI; ++j)
-        off[j] = static_cast<uint32_t>(min(image_row(wave, j, lane), last)) * static_cast<uint32_t>(ld * 2) +
+        off[j] = static_cast<uint32_t>(min(tile_row(image_row(wave, j, lane)), last)) * static_cast<uint32_t>(ld * 2) +
                  image_chunk(wave, j, lane) * 16;
     } else {
       base = reinterpret_cast<const uint8_t*>(src + r0 * ld + i0);
       advance = kR * ld * 2;
-      const int last = (static_cast<int>(min(n - i0, int64_t{ROWS})) >> 3) - 1;
+      const int last = static_cast<int>(min(n - i0, int64_t{256})) - 8;
 #pragma unroll
       for (int j = 0; j < NI; ++j)
         off[j] = static_cast<uint32_t>(image_row(wave, j, lane)) * static_cast<uint32_t>(ld * 2) +
-                 min(image_chunk(wave, j, lane), last) * 16;
+                 min(tile_row(image_chunk(wave, j, lane) * 8), last) * 2;
     }
   }
   __device__ __forceinline__ void load(uint8_t* lds, int wave, int j) const {
@@ -239,137 +244,60 @@ __device__ __forceinline__ float gelu_f(float z) {
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
 
-// The tile kernel.  SPLIT: blockIdx.y is a part of r, and the sums go to
-// the workspace, (parts, rows of the output, columns) fp32.
-template <int MODE, int BP, int BQ, int WP, int WQ, bool SPLIT>
-__global__ __launch_bounds__(64 * WP * WQ, 2) void linear_tile_kernel(LinearArgs a, int parts) {
-  constexpr int NW = WP * WQ, TM = BP / WP / 32, TN = BQ / WQ / 32;
-  using TP = TileOperand<MODE != MODE_DW, BP, NW>;
-  using TQ = TileOperand<MODE == MODE_FORWARD, BQ, NW>;
-  static_assert(TN == 2, "a wave's columns are one pair of 32-column blocks");
-  // one array per stage and operand: the compiler then sees that a stage's
-  // loads do not touch what is being read
-  __shared__ __attribute__((aligned(16))) uint8_t sP0[TP::BYTES], sP1[TP::BYTES], sQ0[TQ::BYTES], sQ1[TQ::BYTES];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wp = wave / WQ, wq = wave % WQ;
+// What a workgroup computes: rows [row0, row_end) (up to its tile's), columns
+// from col0 on, r in [r0, r1), of group g.
+struct LinearTile {
+  int g, col0;
+  int64_t row0, row_end, r0, r1;
+};
 
-  // ---- the tile ----
-  const int cols = MODE == MODE_FORWARD ? a.n : a.k;       // columns of the output
-  const int col_tiles = (cols + BQ - 1) / BQ;
-  int g;
-  int64_t row0, row_end, r0 = 0, r1;
-  int col0;
+template <int MODE>
+__device__ __forceinline__ int out_columns(const LinearArgs& a) { return MODE == MODE_FORWARD ? a.n : a.k; }
+
+// blockIdx.x is the tile; SPLIT: blockIdx.y is a part of r.
+template <int MODE, int BP, int BQ, bool SPLIT>
+__device__ __forceinline__ bool locate(const LinearArgs& a, int parts, int lane, LinearTile& t) {
+  const int col_tiles = (out_columns<MODE>(a) + BQ - 1) / BQ;
+  int rt, ct;
+  t.r0 = 0;
   if constexpr (MODE == MODE_DW) {
     const int row_tiles = (a.n + BP - 1) / BP;
-    const int t = tile_of_workgroup(blockIdx.x, gridDim.x);
-    g = t / (row_tiles * col_tiles);
-    int rt, ct;
-    tile_position(t - g * row_tiles * col_tiles, row_tiles, col_tiles, rt, ct);
-    row0 = static_cast<int64_t>(rt) * BP;
-    row_end = a.n;
-    col0 = ct * BQ;
-    group_rows(a, g, r0, r1);
+    const int i = tile_of_workgroup(blockIdx.x, gridDim.x);
+    t.g = i / (row_tiles * col_tiles);
+    tile_position(i - t.g * row_tiles * col_tiles, row_tiles, col_tiles, rt, ct);
+    t.row0 = static_cast<int64_t>(rt) * BP;
+    t.row_end = a.n;
+    group_rows(a, t.g, t.r0, t.r1);
   } else {
     const int row_tiles = count_row_tiles<BP>(a, lane);
     const int total = row_tiles * col_tiles;
-    if (static_cast<int>(blockIdx.x) >= total) return;
-    int rt, ct;
+    if (static_cast<int>(blockIdx.x) >= total) return false;
     tile_position(tile_of_workgroup(blockIdx.x, total), row_tiles, col_tiles, rt, ct);
-    if (!find_row_tile<BP>(a, rt, lane, g, row0, row_end)) return;
-    col0 = ct * BQ;
-    r1 = MODE == MODE_FORWARD ? a.k : a.n;
+    if (!find_row_tile<BP>(a, rt, lane, t.g, t.row0, t.row_end)) return false;
+    t.r1 = MODE == MODE_FORWARD ? a.k : a.n;
   }
+  t.col0 = ct * BQ;
   if constexpr (SPLIT) {
-    const int64_t steps = (r1 - r0 + kR - 1) / kR;
+    const int64_t steps = (t.r1 - t.r0 + kR - 1) / kR;
     const int64_t lo = steps * blockIdx.y / parts, hi = steps * (blockIdx.y + 1) / parts;
-    r1 = min(r1, r0 + hi * kR);
-    r0 += lo * kR;
+    t.r1 = min(t.r1, t.r0 + hi * kR);
+    t.r0 += lo * kR;
   }
-  const int64_t wg = static_cast<int64_t>(g) * a.n * a.k;
-  TP p;
-  TQ q;
-  if constexpr (MODE == MODE_FORWARD) {
-    p.init(a.x, a.k, row0, row_end, r0, wave, lane);
-    q.init(a.w + wg, a.k, col0, a.n, r0, wave, lane);
-  } else if constexpr (MODE == MODE_DX) {
-    p.init(a.dz, a.n, row0, row_end, r0, wave, lane);
-    q.init(a.w + wg, a.k, col0, a.k, r0, wave, lane);
-  } else {
-    p.init(a.dz, a.n, row0, a.n, r0, wave, lane);
-    q.init(a.x, a.k, col0, a.k, r0, wave, lane);
-  }
-  uint32_t fp[TM], fq[TN];
-#pragma unroll
-  for (int t = 0; t < TM; ++t) fp[t] = TP::frag_base(wp * (TM * 32) + t * 32, lane);
-#pragma unroll
-  for (int t = 0; t < TN; ++t) fq[t] = TQ::frag_base(wq * (TN * 32) + t * 32, lane);
+  return true;
+}
 
-  // ---- the sum ----
-  v16f acc[TM][TN];
-#pragma unroll
-  for (int i = 0; i < TM; ++i)
-#pragma unroll
-    for (int j = 0; j < TN; ++j) acc[i][j] = v16f{};
-  const int64_t span = r1 - r0;
-  const int steps = static_cast<int>((span + kR - 1) / kR);
-  const int tail = static_cast<int>(span - static_cast<int64_t>(steps - 1) * kR);   // r of the last step
-  auto issue = [&](int s, uint8_t* lp, uint8_t* lq) __attribute__((always_inline)) {
-    if (s == steps - 1 && tail < kR) {
-#pragma unroll
-      for (int j = 0; j < TP::NI; ++j) p.load_tail(lp, wave, lane, j, tail);
-#pragma unroll
-      for (int j = 0; j < TQ::NI; ++j) q.load_tail(lq, wave, lane, j, tail);
-    } else {
-#pragma unroll
-      for (int j = 0; j < TP::NI; ++j) p.load(lp, wave, j);
-#pragma unroll
-      for (int j = 0; j < TQ::NI; ++j) q.load(lq, wave, j);
-    }
-    p.base += p.advance;
-    q.base += q.advance;
-  };
-  auto compute = [&](const uint8_t* lp, const uint8_t* lq) __attribute__((always_inline)) {
-#pragma unroll
-    for (int kk = 0; kk < kR / 16; ++kk) {
-      v8bf vq[TN];
-#pragma unroll
-      for (int j = 0; j < TN; ++j) vq[j] = TQ::frag(lq, fq[j], kk, lane);
-#pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        const v8bf vp = TP::frag(lp, fp[i], kk, lane);
-#pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vq[j], vp, acc[i][j], 0, 0, 0);
-      }
-    }
-  };
-  auto arrive = [&]() __attribute__((always_inline)) {
-    wait_vmcnt<0>();
-    __syncthreads();
-  };
-  if (steps > 0) {
-    issue(0, sP0, sQ0);
-    arrive();
-    for (int s = 0; s < steps; s += 2) {
-      if (s + 1 < steps) issue(s + 1, sP1, sQ1);
-      compute(sP0, sQ0);
-      arrive();
-      if (s + 1 >= steps) break;
-      if (s + 2 < steps) issue(s + 2, sP0, sQ0);
-      compute(sP1, sQ1);
-      arrive();
-    }
-  }
-
-  // ---- the output ----
-  uint8_t* const scratch = (wave & 1 ? sP1 : sP0) + (wave >> 1) * 4096;
-  static_assert(TP::BYTES >= (NW + 1) / 2 * 4096, "scratch of the waves");
+// A wave's accumulators to memory: rows [row, row + 32 TM) of group g up to
+// row_end, 64 columns from ncol on, through 4 KB of LDS scratch.  SPLIT: to
+// the workspace, (parts, rows of the output, columns) fp32.
+template <int MODE, bool SPLIT, int TM, int TN>
+__device__ __forceinline__ void store_output(const LinearArgs& a, v16f (&acc)[TM][TN], int g, int64_t row, int64_t row_end,
+                                             int ncol, uint8_t* scratch, int lane) {
   const int l32 = lane & 31, hi = lane >> 5;
-  const int ncol = col0 + wq * 64;                          // the wave's first column
+  const int cols = out_columns<MODE>(a);
   if (ncol >= cols) return;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
-    const int64_t rb = row0 + wp * (TM * 32) + i * 32;      // first row of the block
+    const int64_t rb = row + i * 32;                        // first row of the block
     const int rows = static_cast<int>(min(row_end - rb, int64_t{32}));
     if (rows <= 0) break;
     if constexpr (SPLIT) {
@@ -501,6 +429,283 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void linear_tile_kernel(LinearArgs
       }
     }
   }
+}
+
+// The tile kernel.  SPLIT: blockIdx.y is a part of r, and the sums go to
+// the workspace, (parts, rows of the output, columns) fp32.
+template <int MODE, int BP, int BQ, int WP, int WQ, bool SPLIT>
+__global__ __launch_bounds__(64 * WP * WQ, 2) void linear_tile_kernel(LinearArgs a, int parts) {
+  constexpr int NW = WP * WQ, TM = BP / WP / 32, TN = BQ / WQ / 32;
+  using TP = TileOperand<MODE != MODE_DW, BP, NW>;
+  using TQ = TileOperand<MODE == MODE_FORWARD, BQ, NW>;
+  static_assert(TN == 2, "a wave's columns are one pair of 32-column blocks");
+  // one array per stage and operand: the compiler then sees that a stage's
+  // loads do not touch what is being read
+  __shared__ __attribute__((aligned(16))) uint8_t sP0[TP::BYTES], sP1[TP::BYTES], sQ0[TQ::BYTES], sQ1[TQ::BYTES];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wp = wave / WQ, wq = wave % WQ;
+
+  LinearTile t;
+  if (!locate<MODE, BP, BQ, SPLIT>(a, parts, lane, t)) return;
+  const int64_t wg = static_cast<int64_t>(t.g) * a.n * a.k;
+  TP p;
+  TQ q;
+  if constexpr (MODE == MODE_FORWARD) {
+    p.init(a.x, a.k, t.row0, t.row_end, t.r0, wave, lane);
+    q.init(a.w + wg, a.k, t.col0, a.n, t.r0, wave, lane);
+  } else if constexpr (MODE == MODE_DX) {
+    p.init(a.dz, a.n, t.row0, t.row_end, t.r0, wave, lane);
+    q.init(a.w + wg, a.k, t.col0, a.k, t.r0, wave, lane);
+  } else {
+    p.init(a.dz, a.n, t.row0, a.n, t.r0, wave, lane);
+    q.init(a.x, a.k, t.col0, a.k, t.r0, wave, lane);
+  }
+  uint32_t fp[TM], fq[TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i) fp[i] = TP::frag_base(wp * (TM * 32) + i * 32, lane);
+#pragma unroll
+  for (int j = 0; j < TN; ++j) fq[j] = TQ::frag_base(wq * (TN * 32) + j * 32, lane);
+
+  // ---- the sum ----
+  v16f acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = v16f{};
+  const int64_t span = t.r1 - t.r0;
+  const int steps = static_cast<int>((span + kR - 1) / kR);
+  const int tail = static_cast<int>(span - static_cast<int64_t>(steps - 1) * kR);   // r of the last step
+  auto issue = [&](int s, uint8_t* lp, uint8_t* lq) __attribute__((always_inline)) {
+    if (s >= steps - 1 && (s >= steps || tail < kR)) {
+      const int left = s < steps ? tail : 0;
+#pragma unroll
+      for (int j = 0; j < TP::NI; ++j) p.load_tail(lp, wave, lane, j, left);
+#pragma unroll
+      for (int j = 0; j < TQ::NI; ++j) q.load_tail(lq, wave, lane, j, left);
+    } else {
+#pragma unroll
+      for (int j = 0; j < TP::NI; ++j) p.load(lp, wave, j);
+#pragma unroll
+      for (int j = 0; j < TQ::NI; ++j) q.load(lq, wave, j);
+    }
+    p.base += p.advance;
+    q.base += q.advance;
+  };
+  auto compute = [&](const uint8_t* lp, const uint8_t* lq) __attribute__((always_inline)) {
+#pragma unroll
+    for (int kk = 0; kk < kR / 16; ++kk) {
+      v8bf vq[TN];
+#pragma unroll
+      for (int j = 0; j < TN; ++j) vq[j] = TQ::frag(lq, fq[j], kk, lane);
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        const v8bf vp = TP::frag(lp, fp[i], kk, lane);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vq[j], vp, acc[i][j], 0, 0, 0);
+      }
+    }
+  };
+  auto arrive = [&]() __attribute__((always_inline)) {
+    wait_vmcnt<0>();
+    __syncthreads();
+  };
+  // Steps go in pairs, so that the loop has one exit and names its buffers
+  // statically; an odd last step is followed by one of zeros.
+  if (steps > 0) {
+    issue(0, sP0, sQ0);
+    arrive();
+    for (int s = 0; s < steps; s += 2) {
+      issue(s + 1, sP1, sQ1);
+      compute(sP0, sQ0);
+      arrive();
+      if (s + 2 < steps) issue(s + 2, sP0, sQ0);
+      compute(sP1, sQ1);
+      arrive();
+    }
+  }
+
+  // ---- the output ----
+  uint8_t* const scratch = (wave & 1 ? sP1 : sP0) + (wave >> 1) * 4096;
+  static_assert(TP::BYTES >= (NW + 1) / 2 * 4096, "scratch of the waves");
+  store_output<MODE, SPLIT>(a, acc, t.g, t.row0 + wp * (TM * 32), t.row_end, t.col0 + wq * 64, scratch, lane);
+}
+
+// The 256 x 256 tile on the ping-pong schedule of the grouped product (8
+// waves, 2 along p x 4 along q, each 128 x 64).  A step is four clusters: M0
+// reads the fragments of Q and of the wave's first two P blocks, C0 runs their
+// MFMAs, M1 reads the other two P blocks, C1 runs theirs.  The two waves of a
+// SIMD (w and w + 4) run one cluster apart, so one issues MFMAs while the
+// other reads LDS.  P lies in two images (its rows with bit 6 clear and set),
+// so that a stage comes in two sets: Q and the low half of P, free again after
+// M0, and the high half of P, free after M1.  Stage s + 2's first set is
+// issued in M1(s) and C1(s), its second in C0(s + 1); a set has about four
+// clusters to land and is waited for one cluster and barrier before its use.
+// Steps past the last read zeros, so the steps go in pairs with one exit and
+// every wave has the same loads in flight.
+template <int MODE, bool SPLIT>
+__global__ __launch_bounds__(512, 1) void linear_pingpong_kernel(LinearArgs a, int parts) {
+  constexpr bool PR = MODE != MODE_DW, QR = MODE == MODE_FORWARD;
+  using TL = TileOperand<PR, 128, 8, 0>;
+  using TH = TileOperand<PR, 128, 8, 1>;
+  using TQ = TileOperand<QR, 256, 8>;
+  constexpr int N_EA = TL::NI, N_EB = TQ::NI, N_EARLY = N_EA + N_EB, N_LATE = TH::NI;
+  static_assert(N_EA == 2 && N_EB == 4 && N_LATE == 2, "loads per wave and step");
+  __shared__ __attribute__((aligned(16))) uint8_t sL0[TL::BYTES], sL1[TL::BYTES], sH0[TH::BYTES], sH1[TH::BYTES];
+  __shared__ __attribute__((aligned(16))) uint8_t sQ0[TQ::BYTES], sQ1[TQ::BYTES];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wp = wave >> 2, wq = wave & 3;
+
+  LinearTile t;
+  if (!locate<MODE, 256, 256, SPLIT>(a, parts, lane, t)) return;
+  const int64_t wg = static_cast<int64_t>(t.g) * a.n * a.k;
+  TL pl;
+  TH ph;
+  TQ q;
+  {
+    const uint16_t* const src = MODE == MODE_FORWARD ? a.x : a.dz;
+    const int64_t ld = MODE == MODE_FORWARD ? a.k : a.n, n = MODE == MODE_DW ? a.n : t.row_end;
+    pl.init(src, ld, t.row0, n, t.r0, wave, lane);
+    ph.init(src, ld, t.row0, n, t.r0, wave, lane);
+    q.init(MODE == MODE_DW ? a.x : a.w + wg, a.k, t.col0, MODE == MODE_FORWARD ? a.n : a.k, t.r0, wave, lane);
+  }
+  v16f acc[4][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) acc[i][j] = v16f{};
+
+  const int span = static_cast<int>(t.r1 - t.r0);
+  const int full = span / kR;
+  struct Stage {
+    uint8_t *l, *h, *q;
+  };
+  const Stage st0{sL0, sH0, sQ0}, st1{sL1, sH1, sQ1};
+  // loads of stage s (in order per operand: the bases run along); ANY: a
+  // stage that is ragged or past the end
+  auto issue_l = [&](auto any, int s, const Stage& d) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < N_EA; ++j)
+      if constexpr (decltype(any)::value) pl.load_tail(d.l, wave, lane, j, span - s * kR);
+      else pl.load(d.l, wave, j);
+    pl.base += pl.advance;
+  };
+  auto issue_q = [&](auto any, int s, const Stage& d, int j) __attribute__((always_inline)) {
+    if constexpr (decltype(any)::value) q.load_tail(d.q, wave, lane, j, span - s * kR);
+    else q.load(d.q, wave, j);
+    if (j == N_EB - 1) q.base += q.advance;
+  };
+  auto issue_h = [&](auto any, int s, const Stage& d, int j) __attribute__((always_inline)) {
+    if constexpr (decltype(any)::value) ph.load_tail(d.h, wave, lane, j, span - s * kR);
+    else ph.load(d.h, wave, j);
+    if (j == N_LATE - 1) ph.base += ph.advance;
+  };
+  auto sync = []() __attribute__((always_inline)) {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  typedef v4u Frags[4];       // one 32-row block, the step's four windows
+  auto settle = [](Frags& f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) asm volatile("" : "+v"(f[k]));
+  };
+  auto pin = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) asm volatile("" : "+v"(acc[i][j]));
+  };
+  auto mma = [&](int i0, const Frags* fp, const Frags* fq, auto&& hook) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          acc[i0 + i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, fq[j][k]),
+                                                                   __builtin_bit_cast(v8bf, fp[i][k]), acc[i0 + i][j], 0, 0, 0);
+          hook(k * 4 + i * 2 + j);
+        }
+  };
+  // step s out of `st`; `other`: the other buffer
+  auto step = [&](auto any, int s, const Stage& st, const Stage& other) __attribute__((always_inline)) {
+    // lane addresses are rebuilt from an opaque lane id rather than kept live
+    int l0 = lane;
+    asm volatile("" : "+v"(l0));
+    Frags fq[2], fp[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t b = TQ::frag_base(wq * 64 + j * 32, l0);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) fq[j][k] = __builtin_bit_cast(v4u, TQ::frag(st.q, b, k, l0));
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t b = TL::frag_base(wp * 64 + i * 32, l0);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) fp[i][k] = __builtin_bit_cast(v4u, TL::frag(st.l, b, k, l0));
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) settle(fq[j]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) settle(fp[i]);
+    wait_vmcnt<N_EARLY>();                       // this step's second set
+    sync();
+    mma(0, fp, fq, [&](int m) __attribute__((always_inline)) {
+      if (m % 8 == 0) issue_h(any, s + 1, other, m / 8);
+    });
+    pin();
+    sync();
+    int l1 = lane;
+    asm volatile("" : "+v"(l1));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t b = TH::frag_base(wp * 64 + i * 32, l1);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) fp[i][k] = __builtin_bit_cast(v4u, TH::frag(st.h, b, k, l1));
+    }
+    issue_l(any, s + 2, st);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) settle(fp[i]);
+    wait_vmcnt<N_LATE + N_EA>();                 // the next step's first set
+    sync();
+    mma(2, fp, fq, [&](int m) __attribute__((always_inline)) {
+      if (m % 4 == 0) issue_q(any, s + 2, st, m / 4);
+    });
+    pin();
+    sync();
+  };
+  if (span > 0) {
+    const std::true_type any{};
+    const std::false_type plain{};
+    issue_l(any, 0, st0);
+#pragma unroll
+    for (int j = 0; j < N_EB; ++j) issue_q(any, 0, st0, j);
+#pragma unroll
+    for (int j = 0; j < N_LATE; ++j) issue_h(any, 0, st0, j);
+    issue_l(any, 1, st1);
+#pragma unroll
+    for (int j = 0; j < N_EB; ++j) issue_q(any, 1, st1, j);
+    wait_vmcnt<N_LATE + N_EARLY>();
+    sync();
+    if (wp) sync();
+    int s = 0;
+    for (; s + 3 < full; s += 2) {
+      step(plain, s, st0, st1);
+      step(plain, s + 1, st1, st0);
+    }
+    for (; s * kR < span; s += 2) {
+      step(any, s, st0, st1);
+      step(any, s + 1, st1, st0);
+    }
+    wait_vmcnt<0>();
+    if (!wp) sync();
+    sync();
+  }
+  uint8_t* const scratch = (wave < 4 ? sL0 : sL1) + (wave & 3) * 4096;
+  store_output<MODE, SPLIT>(a, acc, t.g, t.row0 + wp * 128, t.row_end, t.col0 + wq * 64, scratch, lane);
 }
 
 }  // namespace
