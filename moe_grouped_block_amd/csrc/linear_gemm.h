@@ -95,32 +95,47 @@ struct TileOperand {
     dma16(src, lds + (wave * NI + j) * 1024);
   }
 
-  // Per-lane byte offset of the fragments of the 32 rows from tb on.
-  __device__ static __forceinline__ uint32_t frag_base(int tb, int lane) {
-    if constexpr (ALONG_R) {
-      return (tb + (lane & 31)) * (kR * 2);
-    } else {
-      const int q = lane >> 4;
-      const int line = (q >> 1) * 8 + ((lane >> 2) & 3);
-      const int chunk = tb / 8 + (q & 1) * 2 + ((lane & 3) >> 1);
-      return line * (ROWS * 2) + (chunk ^ line_swizzle<CH>(line)) * 16 + (lane & 1) * 8;
+  // Per-lane byte offsets of the fragments of B blocks of 32 rows from tb on,
+  // B a power of two and tb a multiple of 32 B.  Along r an offset belongs to a
+  // window of 16 r and the block is a constant more; along the rows it is the
+  // other way round (the swizzle does not move with the window).
+  template <int B>
+  struct Frags {
+    static constexpr int N = ALONG_R ? 4 : B;
+    uint32_t off[N];
+    __device__ __forceinline__ void init(int tb, int lane) {
+      if constexpr (ALONG_R) {
+        const int row = tb + (lane & 31), sw = (row >> 1) & 7;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) off[k] = row * (kR * 2) + (((2 * k + (lane >> 5)) ^ sw) * 16);
+      } else {
+        const int q = lane >> 4, line = (q >> 1) * 8 + ((lane >> 2) & 3);
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+          const int chunk = tb / 8 + 4 * b + (q & 1) * 2 + ((lane & 3) >> 1);
+          off[b] = line * (ROWS * 2) + (chunk ^ line_swizzle<CH>(line)) * 16 + (lane & 1) * 8;
+        }
+      }
     }
-  }
-  // Fragment of window kk (16 r): lane l holds row tb + l % 32, r 8 (l / 32) + [0, 8).
-  __device__ static __forceinline__ v8bf frag(const uint8_t* lds, uint32_t fb, int kk, int lane) {
-    if constexpr (ALONG_R) {
-      const int sw = ((lane & 31) >> 1) & 7;
-      return *reinterpret_cast<const v8bf*>(lds + fb + (((2 * kk + (lane >> 5)) ^ sw) * 16));
-    } else {
-      typedef short v4s __attribute__((ext_vector_type(4)));
-      typedef short v8s __attribute__((ext_vector_type(8)));
-      typedef __attribute__((address_space(3))) v4s lds4;
-      lds4* const p = (lds4*)(lds + fb + kk * (16 * ROWS * 2));
-      const v4s a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p);
-      const v4s b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p + ROWS);     // 4 lines on (8 bytes a step)
-      return __builtin_bit_cast(v8bf, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+    // computed once, not again at every use
+    __device__ __forceinline__ void keep() {
+#pragma unroll
+      for (int i = 0; i < N; ++i) asm volatile("" : "+v"(off[i]));
     }
-  }
+    // Block b, window k: lane l holds row tb + 32 b + l % 32, r 16 k + 8 (l / 32) + [0, 8).
+    __device__ __forceinline__ v4u read(const uint8_t* lds, int b, int k) const {
+      if constexpr (ALONG_R) {
+        return *reinterpret_cast<const v4u*>(lds + off[k] + b * (32 * kR * 2));
+      } else {
+        typedef short v4s __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) v4s lds4;
+        lds4* const p = (lds4*)(lds + off[b] + k * (16 * ROWS * 2));
+        const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p);
+        const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p + ROWS);     // 4 lines on (8 bytes a step)
+        return __builtin_bit_cast(v4u, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+      }
+    }
+  };
 };
 
 enum LinearMode : int { MODE_FORWARD = 0, MODE_DX = 1, MODE_DW = 2 };
@@ -461,11 +476,10 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void linear_tile_kernel(LinearArgs
     p.init(a.dz, a.n, t.row0, a.n, t.r0, wave, lane);
     q.init(a.x, a.k, t.col0, a.k, t.r0, wave, lane);
   }
-  uint32_t fp[TM], fq[TN];
-#pragma unroll
-  for (int i = 0; i < TM; ++i) fp[i] = TP::frag_base(wp * (TM * 32) + i * 32, lane);
-#pragma unroll
-  for (int j = 0; j < TN; ++j) fq[j] = TQ::frag_base(wq * (TN * 32) + j * 32, lane);
+  typename TP::template Frags<TM> fp;
+  typename TQ::template Frags<TN> fq;
+  fp.init(wp * (TM * 32), lane);
+  fq.init(wq * (TN * 32), lane);
 
   // ---- the sum ----
   v16f acc[TM][TN];
@@ -497,10 +511,10 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void linear_tile_kernel(LinearArgs
     for (int kk = 0; kk < kR / 16; ++kk) {
       v8bf vq[TN];
 #pragma unroll
-      for (int j = 0; j < TN; ++j) vq[j] = TQ::frag(lq, fq[j], kk, lane);
+      for (int j = 0; j < TN; ++j) vq[j] = __builtin_bit_cast(v8bf, fq.read(lq, j, kk));
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
-        const v8bf vp = TP::frag(lp, fp[i], kk, lane);
+        const v8bf vp = __builtin_bit_cast(v8bf, fp.read(lp, i, kk));
 #pragma unroll
         for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vq[j], vp, acc[i][j], 0, 0, 0);
       }
@@ -570,6 +584,12 @@ __global__ __launch_bounds__(512, 1) void linear_pingpong_kernel(LinearArgs a, i
     ph.init(src, ld, t.row0, n, t.r0, wave, lane);
     q.init(MODE == MODE_DW ? a.x : a.w + wg, a.k, t.col0, MODE == MODE_FORWARD ? a.n : a.k, t.r0, wave, lane);
   }
+  typename TL::template Frags<2> ap;            // both halves of P lie alike
+  typename TQ::template Frags<2> aq;
+  ap.init(wp * 64, lane);
+  aq.init(wq * 64, lane);
+  ap.keep();
+  aq.keep();
   v16f acc[4][2];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -606,8 +626,8 @@ __global__ __launch_bounds__(512, 1) void linear_pingpong_kernel(LinearArgs a, i
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
   };
-  typedef v4u Frags[4];       // one 32-row block, the step's four windows
-  auto settle = [](Frags& f) __attribute__((always_inline)) {
+  typedef v4u Window[4];      // one 32-row block, the step's four windows
+  auto settle = [](Window& f) __attribute__((always_inline)) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) asm volatile("" : "+v"(f[k]));
   };
@@ -617,7 +637,7 @@ __global__ __launch_bounds__(512, 1) void linear_pingpong_kernel(LinearArgs a, i
 #pragma unroll
       for (int j = 0; j < 2; ++j) asm volatile("" : "+v"(acc[i][j]));
   };
-  auto mma = [&](int i0, const Frags* fp, const Frags* fq, auto&& hook) __attribute__((always_inline)) {
+  auto mma = [&](int i0, const Window* fp, const Window* fq, auto&& hook) __attribute__((always_inline)) {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -631,22 +651,15 @@ __global__ __launch_bounds__(512, 1) void linear_pingpong_kernel(LinearArgs a, i
   };
   // step s out of `st`; `other`: the other buffer
   auto step = [&](auto any, int s, const Stage& st, const Stage& other) __attribute__((always_inline)) {
-    // lane addresses are rebuilt from an opaque lane id rather than kept live
-    int l0 = lane;
-    asm volatile("" : "+v"(l0));
-    Frags fq[2], fp[2];
+    Window fq[2], fp[2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t b = TQ::frag_base(wq * 64 + j * 32, l0);
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) fq[j][k] = __builtin_bit_cast(v4u, TQ::frag(st.q, b, k, l0));
-    }
+      for (int k = 0; k < 4; ++k) fq[j][k] = aq.read(st.q, j, k);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t b = TL::frag_base(wp * 64 + i * 32, l0);
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) fp[i][k] = __builtin_bit_cast(v4u, TL::frag(st.l, b, k, l0));
-    }
+      for (int k = 0; k < 4; ++k) fp[i][k] = ap.read(st.l, i, k);
 #pragma unroll
     for (int j = 0; j < 2; ++j) settle(fq[j]);
 #pragma unroll
@@ -658,14 +671,10 @@ __global__ __launch_bounds__(512, 1) void linear_pingpong_kernel(LinearArgs a, i
     });
     pin();
     sync();
-    int l1 = lane;
-    asm volatile("" : "+v"(l1));
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t b = TH::frag_base(wp * 64 + i * 32, l1);
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) fp[i][k] = __builtin_bit_cast(v4u, TH::frag(st.h, b, k, l1));
-    }
+      for (int k = 0; k < 4; ++k) fp[i][k] = ap.read(st.h, i, k);
     issue_l(any, s + 2, st);
 #pragma unroll
     for (int i = 0; i < 2; ++i) settle(fp[i]);
