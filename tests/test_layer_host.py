@@ -220,7 +220,7 @@ def test_front_refuses_host_tensors_and_wrong_types():
     with pytest.raises(ValueError, match="need"):
         mg.linear_backward(x, x, x, need=("dy",))
     with pytest.raises(TypeError, match="SortPlan"):
-        mg.layer._exchange_problem(None, 64, "bf16", "row_major", None)
+        mg.layer._plan_pointers(None, 0)
     with pytest.raises(ValueError, match="score"):
         mg.layer._code(mg.SCORES, "relu", "score")
 
