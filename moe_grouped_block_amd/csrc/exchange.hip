@@ -53,15 +53,23 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
 // (block, wave, position) runs in slot order and the sort is stable:
 //   row = start of the expert + its slots in blocks before b
 //         + its slots in the block's waves before w + rank inside the wave
+// Every block sums the counts of all blocks itself (they are small and in
+// L2), all threads at once: no block waits for another.
 __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
   constexpr int NW = kSortThreads / 64;
   __shared__ int32_t count[NW][kMaxExperts];    // a wave's slots per expert, then its next row
-  __shared__ int32_t base[kMaxExperts];         // first row of the expert, then + rows of the blocks before
+  __shared__ int32_t base[kMaxExperts];         // slots of the expert in the blocks before
   __shared__ int32_t total[kMaxExperts];        // slots of the expert in all blocks
+  __shared__ int32_t finish[kMaxExperts];       // end of the expert's padded rows
   __shared__ int32_t wsum[NW];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int E = a.experts, nb = gridDim.x, b = blockIdx.x;
-  for (int i = tid; i < NW * kMaxExperts; i += kSortThreads) (&count[0][0])[i] = 0;
+  for (int e = tid; e < E; e += kSortThreads) {
+    base[e] = 0;
+    total[e] = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) count[w][e] = 0;
+  }
   __syncthreads();
   const int64_t beg = static_cast<int64_t>(b) * a.chunk;
   const int64_t end = min(beg + a.chunk, a.slots);
@@ -71,23 +79,33 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
     const int e = expert_of(a, i);
     if (e >= 0) atomicAdd(&count[wave][e], 1);
   }
-  __syncthreads();
-  // per expert: its slots before this block and in all blocks
-  for (int e = tid; e < E; e += kSortThreads) {
-    int before = 0, all = 0;
-    if (nb > 1) {
-      for (int q = 0; q < nb; ++q) {
-        const int h = a.hist[q * E + e];
-        before += q < b ? h : 0;
-        all += h;
+  if (nb > 1) {
+    // threads = (group of blocks, expert); sums of whole numbers, so their
+    // order does not matter
+    const int lanes = E < kSortThreads ? E : kSortThreads, groups = kSortThreads / lanes;
+    const int q0 = tid / lanes, e0 = tid % lanes;
+    if (q0 < groups)
+      for (int e = e0; e < E; e += lanes) {
+        int before = 0, all = 0;
+#pragma unroll 8
+        for (int q = q0; q < nb; q += groups) {
+          const int h = a.hist[q * E + e];
+          before += q < b ? h : 0;
+          all += h;
+        }
+        atomicAdd(&base[e], before);
+        atomicAdd(&total[e], all);
       }
-    } else {
+    __syncthreads();
+  } else {
+    __syncthreads();
+    for (int e = tid; e < E; e += kSortThreads) {
+      int all = 0;
       for (int w = 0; w < NW; ++w) all += count[w][e];
+      total[e] = all;
     }
-    base[e] = before;
-    total[e] = all;
+    __syncthreads();
   }
-  __syncthreads();
   // padded starts: a scan over the experts, kSortThreads at a time
   int carry = 0;
   for (int e0 = 0; e0 < E; e0 += kSortThreads) {
@@ -106,17 +124,11 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
       if (w < wave) add += wsum[w];
       carry += wsum[w];
     }
-    const int finish = add + scan;              // end of expert e's rows
     if (e < E) {
-      const int start = finish - padded;
-      if (b == 0) a.padded_offsets[e] = finish;
-      // padding rows of the experts, dealt out over the blocks
-      if (e % nb == b)
-        for (int64_t r = start + all; r < min(static_cast<int64_t>(finish), a.rows); ++r) {
-          a.slot_of[r] = -1;
-          if (a.prob) a.prob[r] = 0.0f;
-        }
-      int at = start + base[e];
+      finish[e] = add + scan;
+      if (b == 0) a.padded_offsets[e] = add + scan;
+      int at = add + scan - padded + base[e];
+      total[e] += add + scan - padded;          // first padding row
       for (int w = 0; w < NW; ++w) {
         const int c = count[w][e];
         count[w][e] = at;
@@ -125,7 +137,13 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
     }
     __syncthreads();
   }
-  // rows behind the last expert
+  // padding rows of the experts, dealt out over the blocks, and rows behind
+  // the last expert
+  for (int e = b; e < E; e += nb)
+    for (int64_t r = total[e] + tid; r < min(static_cast<int64_t>(finish[e]), a.rows); r += kSortThreads) {
+      a.slot_of[r] = -1;
+      if (a.prob) a.prob[r] = 0.0f;
+    }
   for (int64_t r = carry + static_cast<int64_t>(b) * kSortThreads + tid; r < a.rows;
        r += static_cast<int64_t>(nb) * kSortThreads) {
     a.slot_of[r] = -1;
@@ -196,62 +214,111 @@ __device__ __forceinline__ uint32_t mx_byte(uint32_t amax) {
   return static_cast<uint32_t>(byte < 0 ? 0 : byte);
 }
 
-// One wave's share of a row in an MX format: lane l holds columns 8 l + [0, 8)
-// of a 512-column chunk; a block of 32 is 4 lanes, a scale word (128 columns)
-// a 16-lane row.  Returns the lane's scale byte's word (all 16 lanes alike);
-// codes: 8 bytes, or 4 of E2M1.
+// MX rows: lane l holds columns 16 l + [0, 16) of a 1024-column chunk; a block
+// of 32 is 2 lanes, a scale word (128 columns) 8.
+
+// A block's amax (fp32 bits) in its lanes -> its scale byte; the scale word of
+// the lane's 128 columns (all 8 lanes alike).
 template <int KIND>
-__device__ __forceinline__ uint32_t mx_codes(const float* v, v2u& codes) {
-  uint32_t amax = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7FFFFFFFu);   // NaN bits are the largest
+__device__ __forceinline__ uint32_t mx_scale(uint32_t amax, uint32_t& word) {
   amax = max(amax, dpp_u<0xB1>(amax));
-  amax = max(amax, dpp_u<0x4E>(amax));
   uint32_t byte;
   if constexpr (KIND == ROW_E4M3) byte = mx_byte<8, 6>(amax);
   else if constexpr (KIND == ROW_E5M2) byte = mx_byte<15, 6>(amax);
   else byte = mx_byte<2, 4>(amax);
-  // 2^(127 - byte), exact (2^-126 for 253, 2^-127 for 254); zero codes in a NaN block
-  const float inv = byte == 255u ? 0.0f : byte == 254u ? __uint_as_float(0x00400000u) : __uint_as_float((254u - byte) << 23);
-  float q[8];
+  word = byte << (8 * ((threadIdx.x >> 1) & 3));
+  word |= dpp_u<0x4E>(word);        // lanes 2 apart: two bytes
+  word |= dpp_u<0x141>(word);       // mirrored halves of 8: all four
+  return byte;
+}
+
+// The scaled conversions divide by the power of two given as fp32 (2^-127 is
+// its subnormal) and round to nearest even.
+typedef short v2s __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ float mx_factor(uint32_t byte) { return __uint_as_float(byte ? byte << 23 : 0x00400000u); }
+
+// 16 bf16 (two 16-byte pieces) -> codes: 16 bytes, or 8 of E2M1; zeros in a
+// block that holds a NaN or an infinity.
+template <int KIND>
+__device__ __forceinline__ uint32_t mx_from_bf16(v4u a, v4u b, v4u& codes) {
+  typedef uint16_t v2h __attribute__((ext_vector_type(2)));
+  typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+  const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  v2h m = __builtin_bit_cast(v2h, u[0] & 0x7FFF7FFFu);       // magnitudes; NaN bits are the largest
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = byte == 255u ? 0.0f : v[i] * inv;
-  if constexpr (KIND == ROW_E4M3) {
-    int a = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
-    a = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], a, true);
-    int b = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);
-    b = __builtin_amdgcn_cvt_pk_fp8_f32(q[6], q[7], b, true);
-    codes = v2u{static_cast<uint32_t>(a), static_cast<uint32_t>(b)};
-  } else if constexpr (KIND == ROW_E5M2) {
-    int a = __builtin_amdgcn_cvt_pk_bf8_f32(q[0], q[1], 0, false);
-    a = __builtin_amdgcn_cvt_pk_bf8_f32(q[2], q[3], a, true);
-    int b = __builtin_amdgcn_cvt_pk_bf8_f32(q[4], q[5], 0, false);
-    b = __builtin_amdgcn_cvt_pk_bf8_f32(q[6], q[7], b, true);
-    codes = v2u{static_cast<uint32_t>(a), static_cast<uint32_t>(b)};
-  } else {
-    uint32_t a = 0;
-    a = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(a, q[0], q[1], 1.0f, 0);
-    a = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(a, q[2], q[3], 1.0f, 1);
-    a = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(a, q[4], q[5], 1.0f, 2);
-    a = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(a, q[6], q[7], 1.0f, 3);
-    codes = v2u{a, 0u};
+  for (int i = 1; i < 8; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(v2h, u[i] & 0x7FFF7FFFu));
+  uint32_t word;
+  const uint32_t byte = mx_scale<KIND>(static_cast<uint32_t>(max(m.x, m.y)) << 16, word);
+  const float f = mx_factor(byte);
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const v2b x = __builtin_bit_cast(v2b, u[2 * i]), y = __builtin_bit_cast(v2b, u[2 * i + 1]);
+    if constexpr (KIND == ROW_E4M3) {
+      v2s c = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(v2s{0, 0}, x, f, false);
+      w[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(c, y, f, true));
+    } else if constexpr (KIND == ROW_E5M2) {
+      v2s c = __builtin_amdgcn_cvt_scalef32_pk_bf8_bf16(v2s{0, 0}, x, f, false);
+      w[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf8_bf16(c, y, f, true));
+    } else if (i & 1) {
+      w[i / 2] = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w[i / 2], x, f, 2);
+      w[i / 2] = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w[i / 2], y, f, 3);
+    } else {
+      w[i / 2] = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w[i / 2], x, f, 0);
+      w[i / 2] = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w[i / 2], y, f, 1);
+    }
   }
-  uint32_t word = byte << (8 * ((threadIdx.x >> 2) & 3));
-  word |= dpp_u<0x124>(word);       // row_ror 4
-  word |= dpp_u<0x128>(word);       // row_ror 8
+  const uint32_t keep = byte == 255u ? 0u : 0xFFFFFFFFu;
+  codes = v4u{w[0] & keep, w[1] & keep, w[2] & keep, w[3] & keep};
   return word;
 }
 
-// Store lane `lane`'s 8 columns (col .. col + 8) of a row.
+// The same from 16 fp32.
 template <int KIND>
-__device__ __forceinline__ void store_row(const ExchangeArgs& a, int64_t row, int col, int lane, v4u bf, v2u codes,
-                                          uint32_t word) {
+__device__ __forceinline__ uint32_t mx_from_f32(const float* v, v4u& codes) {
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  uint32_t word;
+  const uint32_t byte = mx_scale<KIND>(amax, word);
+  const float f = mx_factor(byte);
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float* const q = v + 4 * i;
+    if constexpr (KIND == ROW_E4M3) {
+      v2s c = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(v2s{0, 0}, q[0], q[1], f, false);
+      w[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(c, q[2], q[3], f, true));
+    } else if constexpr (KIND == ROW_E5M2) {
+      v2s c = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(v2s{0, 0}, q[0], q[1], f, false);
+      w[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(c, q[2], q[3], f, true));
+    } else if (i & 1) {
+      w[i / 2] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[i / 2], q[0], q[1], f, 2);
+      w[i / 2] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[i / 2], q[2], q[3], f, 3);
+    } else {
+      w[i / 2] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[i / 2], q[0], q[1], f, 0);
+      w[i / 2] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[i / 2], q[2], q[3], f, 1);
+    }
+  }
+  const uint32_t keep = byte == 255u ? 0u : 0xFFFFFFFFu;
+  codes = v4u{w[0] & keep, w[1] & keep, w[2] & keep, w[3] & keep};
+  return word;
+}
+
+// Columns of a row that a wave holds at a time, and a lane's part of them.
+template <int KIND>
+constexpr int kLaneCols = KIND == ROW_BF16 ? 8 : 16;
+
+// A lane's columns of a row (from col on): BF16 bits in q, or codes in q and
+// the scale word.
+template <int KIND>
+__device__ __forceinline__ void store_row(const ExchangeArgs& a, int64_t row, int col, int lane, v4u q, uint32_t word) {
   if constexpr (KIND == ROW_BF16) {
-    *reinterpret_cast<v4u*>(a.rows_out + (row * a.width + col) * 2) = bf;
+    *reinterpret_cast<v4u*>(a.rows_out + (row * a.width + col) * 2) = q;
   } else {
-    if constexpr (KIND == ROW_E2M1) *reinterpret_cast<uint32_t*>(a.rows_out + (row * a.width + col) / 2) = codes.x;
-    else *reinterpret_cast<v2u*>(a.rows_out + row * a.width + col) = codes;
-    if ((lane & 15) == 0) {
+    if constexpr (KIND == ROW_E2M1) *reinterpret_cast<v2u*>(a.rows_out + (row * a.width + col) / 2) = v2u{q.x, q.y};
+    else *reinterpret_cast<v4u*>(a.rows_out + row * a.width + col) = q;
+    if ((lane & 7) == 0) {
       const int64_t w = col >> 7;
       uint32_t* const s = reinterpret_cast<uint32_t*>(a.scales);
       s[a.kplanes ? w * a.rows + row : row * (a.width >> 7) + w] = word;
@@ -259,18 +326,30 @@ __device__ __forceinline__ void store_row(const ExchangeArgs& a, int64_t row, in
   }
 }
 
-// Zero the padding rows among rows [64 q, 64 q + 64) (one wave).
+// Zero the padding rows among rows [kPadRows q, kPadRows (q + 1)) (one wave).
+// These waves come first in a launch and take few rows each: with 64 rows a
+// wave, behind the tokens' waves, the last of them ended 10 us after all
+// others.
+constexpr int kPadRows = 16;
 template <int KIND>
 __device__ __forceinline__ void zero_padding(const ExchangeArgs& a, int64_t q, int lane) {
   const int64_t last = a.offsets[a.experts - 1];
   const int64_t end = last < a.rows ? last : a.rows;
-  const int64_t r = 64 * q + lane;
-  uint64_t pad = __ballot(r < end && a.slot_of[r < a.rows ? r : 0] < 0);
+  const int64_t r = kPadRows * q + lane;
+  uint64_t pad = __ballot(lane < kPadRows && r < end && a.slot_of[r < end ? r : 0] < 0);
   while (pad) {
-    const int64_t row = 64 * q + __builtin_ctzll(pad);
+    const int64_t row = kPadRows * q + __builtin_ctzll(pad);
     pad &= pad - 1;
-    for (int col = lane * 8; col < a.width; col += 512) store_row<KIND>(a, row, col, lane, v4u{}, v2u{}, 0u);
+    for (int col = lane * kLaneCols<KIND>; col < a.width; col += 64 * kLaneCols<KIND>)
+      store_row<KIND>(a, row, col, lane, v4u{}, 0u);
   }
+}
+
+// This wave's number among the launch's waves of 4 a workgroup, in scalar
+// registers: what is the same for a wave (its token's rows and weights) then
+// comes by scalar loads.
+__device__ __forceinline__ int64_t wave_number() {
+  return static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 }
 
 // Row of slot s, or -1.
@@ -279,61 +358,87 @@ __device__ __forceinline__ int64_t row_at(const ExchangeArgs& a, int64_t s) {
   return r >= 0 && r < a.rows ? r : -1;
 }
 
-// dispatch: one wave for 512 columns of a token; the waves behind them zero
-// the padding.
-template <int KIND>
-__global__ __launch_bounds__(256) void dispatch_kernel(ExchangeArgs a, int64_t token_waves) {
-  const int lane = threadIdx.x & 63;
-  const int64_t wave = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  if (wave >= token_waves) {
-    const int64_t q = wave - token_waves;
-    if (64 * q < a.rows) zero_padding<KIND>(a, q, lane);
-    return;
-  }
-  const int chunks = (a.width + 511) / 512;
-  const int64_t t = wave / chunks;
-  const int col = static_cast<int>(wave - t * chunks) * 512 + lane * 8;
-  const bool in = col < a.width;
-  v4u u{};
-  if (in) u = *reinterpret_cast<const v4u*>(a.x + t * a.width + col);
-  v2u codes{};
-  uint32_t word = 0;
-  if constexpr (KIND != ROW_BF16) {
-    const float v[8] = {lo(u.x), hi(u.x), lo(u.y), hi(u.y), lo(u.z), hi(u.z), lo(u.w), hi(u.w)};
-    word = mx_codes<KIND>(v, codes);
-  }
-  for (int j = 0; j < a.top_k; ++j) {
-    const int64_t row = row_at(a, t * a.top_k + j);
-    if (row >= 0 && in) store_row<KIND>(a, row, col, lane, u, codes, word);
+__device__ __forceinline__ void unpack(v4u u, float* v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = lo(u[i]);
+    v[2 * i + 1] = hi(u[i]);
   }
 }
 
-// combine: one wave for 512 columns of a token.
-__global__ __launch_bounds__(256) void combine_kernel(ExchangeArgs a) {
+// dispatch: one wave for 512 columns of a token (1024 of an MX row), read
+// and brought to the rows' format once.
+template <int KIND>
+__global__ __launch_bounds__(256) void dispatch_kernel(ExchangeArgs a, int64_t pad_waves) {
+  constexpr int C = kLaneCols<KIND>;
   const int lane = threadIdx.x & 63;
-  const int64_t wave = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  int64_t wave = wave_number();
+  if (wave < pad_waves) {
+    zero_padding<KIND>(a, wave, lane);
+    return;
+  }
+  wave -= pad_waves;
+  const int chunks = (a.width + 64 * C - 1) / (64 * C);
+  const int64_t t = wave / chunks;
+  if (t >= a.tokens) return;
+  const int col = static_cast<int>(wave - t * chunks) * 64 * C + lane * C;
+  const bool in = col < a.width;
+  v4u u{};
+  uint32_t word = 0;
+  const v4u* const src = reinterpret_cast<const v4u*>(a.x + t * a.width + col);
+  if (in) u = src[0];
+  if constexpr (KIND != ROW_BF16) {
+    v4u u1{};
+    if (in) u1 = src[1];
+    word = mx_from_bf16<KIND>(u, u1, u);
+  }
+  for (int j = 0; j < a.top_k; ++j) {
+    const int64_t row = row_at(a, t * a.top_k + j);
+    if (row >= 0 && in) store_row<KIND>(a, row, col, lane, u, word);
+  }
+}
+
+// combine: one wave for 512 columns of a token, the gathers of eight rows in
+// flight at once.
+__global__ __launch_bounds__(256) void combine_kernel(ExchangeArgs a) {
+  constexpr int U = 8;
+  const int lane = threadIdx.x & 63;
+  const int64_t wave = wave_number();
   const int chunks = (a.width + 511) / 512;
   const int64_t t = wave / chunks;
   const int col = static_cast<int>(wave - t * chunks) * 512 + lane * 8;
   if (t >= a.tokens || col >= a.width) return;
+  v4u res{};
+  if (a.residual) res = *reinterpret_cast<const v4u*>(a.residual + t * a.width + col);
   float v[8] = {};
-  for (int j = 0; j < a.top_k; ++j) {
-    const int64_t row = row_at(a, t * a.top_k + j);
-    if (row < 0) continue;
-    const float w = a.weights ? a.weights[t * a.top_k + j] : 1.0f;
-    const v4u u = *reinterpret_cast<const v4u*>(a.rows_in + row * a.width + col);
+  for (int j0 = 0; j0 < a.top_k; j0 += U) {
+    v4u u[U];
+    float w[U];
+    bool there[U];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = fmaf(w, lo(u[i]), v[2 * i]);
-      v[2 * i + 1] = fmaf(w, hi(u[i]), v[2 * i + 1]);
+    for (int i = 0; i < U; ++i) {
+      const int j = min(j0 + i, a.top_k - 1);
+      const int64_t row = row_at(a, t * a.top_k + j);
+      there[i] = row >= 0 && j0 + i < a.top_k;
+      w[i] = a.weights ? a.weights[t * a.top_k + j] : 1.0f;
+      u[i] = v4u{};
+      if (there[i]) u[i] = *reinterpret_cast<const v4u*>(a.rows_in + row * a.width + col);
     }
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (there[i]) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          v[2 * q] = fmaf(w[i], lo(u[i][q]), v[2 * q]);
+          v[2 * q + 1] = fmaf(w[i], hi(u[i][q]), v[2 * q + 1]);
+        }
+      }
   }
   if (a.residual) {
-    const v4u u = *reinterpret_cast<const v4u*>(a.residual + t * a.width + col);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] += lo(u[i]);
-      v[2 * i + 1] += hi(u[i]);
+    for (int q = 0; q < 4; ++q) {
+      v[2 * q] += lo(res[q]);
+      v[2 * q + 1] += hi(res[q]);
     }
   }
   *reinterpret_cast<v4u*>(a.y + t * a.width + col) =
@@ -347,49 +452,71 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // backward of combine: one wave for a token (the dot products run over the
-// whole row); the waves behind them zero the padding of drows.
+// whole row), kSame rows of it at once, so that dy is read once for them.
 template <int KIND>
-__global__ __launch_bounds__(256) void combine_backward_kernel(ExchangeArgs a) {
+__global__ __launch_bounds__(256) void combine_backward_kernel(ExchangeArgs a, int64_t pad_waves) {
+  constexpr int C = kLaneCols<KIND>, kSame = KIND == ROW_BF16 ? 4 : 2;
   const int lane = threadIdx.x & 63;
-  const int64_t wave = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  if (wave >= a.tokens) {
-    const int64_t q = wave - a.tokens;
-    if (64 * q < a.rows) zero_padding<KIND>(a, q, lane);
+  const int64_t wave = wave_number();
+  if (wave < pad_waves) {
+    zero_padding<KIND>(a, wave, lane);
     return;
   }
-  const int64_t t = wave;
-  for (int j = 0; j < a.top_k; ++j) {
-    const int64_t slot = t * a.top_k + j, row = row_at(a, slot);
-    const float w = a.weights ? a.weights[slot] : 1.0f;
-    float dot = 0.0f;
-    if (row >= 0) {
-      for (int c0 = 0; c0 < a.width; c0 += 512) {
-        const int col = c0 + lane * 8;
-        const bool in = col < a.width;
-        v4u u{}, r{};
-        if (in) u = *reinterpret_cast<const v4u*>(a.x + t * a.width + col);
-        if (in && a.dweights) r = *reinterpret_cast<const v4u*>(a.rows_in + row * a.width + col);
-        float v[8];
+  const int64_t t = wave - pad_waves;
+  if (t >= a.tokens) return;
+  for (int j0 = 0; j0 < a.top_k; j0 += kSame) {
+    int64_t row[kSame];
+    float w[kSame], dot[kSame];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          dot = fmaf(lo(u[i]), lo(r[i]), dot);
-          dot = fmaf(hi(u[i]), hi(r[i]), dot);
-          v[2 * i] = w * lo(u[i]);
-          v[2 * i + 1] = w * hi(u[i]);
+    for (int i = 0; i < kSame; ++i) {
+      const int64_t slot = t * a.top_k + min(j0 + i, a.top_k - 1);
+      row[i] = j0 + i < a.top_k ? row_at(a, slot) : -1;
+      w[i] = a.weights ? a.weights[slot] : 1.0f;
+      dot[i] = 0.0f;
+    }
+    for (int c0 = 0; c0 < a.width; c0 += 64 * C) {
+      const int col = c0 + lane * C;
+      const bool in = col < a.width;
+      v4u d[C / 8], r[kSame][C / 8];
+#pragma unroll
+      for (int h = 0; h < C / 8; ++h) {
+        d[h] = v4u{};
+        if (in) d[h] = reinterpret_cast<const v4u*>(a.x + t * a.width + col)[h];
+#pragma unroll
+        for (int i = 0; i < kSame; ++i) {
+          r[i][h] = v4u{};
+          if (in && a.dweights && row[i] >= 0) r[i][h] = reinterpret_cast<const v4u*>(a.rows_in + row[i] * a.width + col)[h];
         }
-        v2u codes{};
+      }
+      float dv[C];
+#pragma unroll
+      for (int h = 0; h < C / 8; ++h) unpack(d[h], dv + 8 * h);
+#pragma unroll
+      for (int i = 0; i < kSame; ++i) {
+        if (row[i] < 0) continue;
+        float v[C];
+#pragma unroll
+        for (int h = 0; h < C / 8; ++h) unpack(r[i][h], v + 8 * h);
+#pragma unroll
+        for (int e = 0; e < C; ++e) {
+          dot[i] = fmaf(dv[e], v[e], dot[i]);
+          v[e] = w[i] * dv[e];
+        }
+        v4u q{};
         uint32_t word = 0;
-        v4u bf{};
         if constexpr (KIND == ROW_BF16)
-          bf = v4u{bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7])};
+          q = v4u{bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7])};
         else
-          word = mx_codes<KIND>(v, codes);
-        if (in) store_row<KIND>(a, row, col, lane, bf, codes, word);
+          word = mx_from_f32<KIND>(v, q);
+        if (in) store_row<KIND>(a, row[i], col, lane, q, word);
       }
     }
     if (a.dweights) {
-      dot = wave_sum(dot);
-      if (lane == 0) a.dweights[slot] = dot;
+#pragma unroll
+      for (int i = 0; i < kSame; ++i) {
+        const float s = wave_sum(dot[i]);
+        if (lane == 0 && j0 + i < a.top_k) a.dweights[t * a.top_k + j0 + i] = row[i] >= 0 ? s : 0.0f;
+      }
     }
   }
 }
@@ -432,11 +559,13 @@ hipError_t launch_sort(const SortArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_dispatch(const ExchangeArgs& a, hipStream_t s) {
-  const int64_t token_waves = a.tokens * ((a.width + 511) / 512);
-  const unsigned blocks = blocks_of(token_waves + (a.rows + 63) / 64);
+  const int cols = a.kind == ROW_BF16 ? 512 : 1024;
+  const int64_t token_waves = a.tokens * ((a.width + cols - 1) / cols);
+  const int64_t pad_waves = (a.rows + kPadRows - 1) / kPadRows;
+  const unsigned blocks = blocks_of(token_waves + pad_waves);
   if (!blocks) return hipErrorInvalidValue;
   return by_kind(a.kind, [&](auto c) {
-    hipLaunchKernelGGL((dispatch_kernel<decltype(c)::value>), dim3(blocks), dim3(256), 0, s, a, token_waves);
+    hipLaunchKernelGGL((dispatch_kernel<decltype(c)::value>), dim3(blocks), dim3(256), 0, s, a, pad_waves);
     return hipGetLastError();
   });
 }
@@ -449,10 +578,11 @@ hipError_t launch_combine(const ExchangeArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_combine_backward(const ExchangeArgs& a, hipStream_t s) {
-  const unsigned blocks = blocks_of(a.tokens + (a.rows + 63) / 64);
+  const int64_t pad_waves = (a.rows + kPadRows - 1) / kPadRows;
+  const unsigned blocks = blocks_of(a.tokens + pad_waves);
   if (!blocks) return hipErrorInvalidValue;
   return by_kind(a.kind, [&](auto c) {
-    hipLaunchKernelGGL((combine_backward_kernel<decltype(c)::value>), dim3(blocks), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((combine_backward_kernel<decltype(c)::value>), dim3(blocks), dim3(256), 0, s, a, pad_waves);
     return hipGetLastError();
   });
 }

@@ -54,16 +54,17 @@ struct SortArgs {
   int32_t blocks;           // sort_blocks(slots)
   int32_t chunk;            // slots per block
 };
-// Slots per block and block count of the sort: one block while the slots fit
-// into one, then blocks of kSortChunk, and longer ones past 256 blocks (each
-// block sums the counts of all blocks before it).
+// Slots per block and block count of the sort: one block (and one launch) up
+// to kSortOne slots, then blocks of kSortChunk, and longer ones past 256 blocks
+// (each block sums the counts of all blocks).
 constexpr int kSortThreads = 512;
-constexpr int kSortChunk = 2048;
+constexpr int kSortOne = 4096;
+constexpr int kSortChunk = 1024;
 constexpr int kSortMaxBlocks = 256;
 inline int32_t sort_chunk(int64_t slots) {
-  const int64_t even = (slots + kSortMaxBlocks - 1) / kSortMaxBlocks;
-  const int64_t c = even > kSortChunk ? (even + kSortThreads - 1) / kSortThreads * kSortThreads : kSortChunk;
-  return static_cast<int32_t>(c);
+  const int64_t even = slots <= kSortOne ? slots : (slots + kSortMaxBlocks - 1) / kSortMaxBlocks;
+  const int64_t least = slots <= kSortOne ? 1 : kSortChunk;
+  return static_cast<int32_t>(((even > least ? even : least) + kSortThreads - 1) / kSortThreads * kSortThreads);
 }
 inline int32_t sort_blocks(int64_t slots) {
   const int64_t c = sort_chunk(slots);

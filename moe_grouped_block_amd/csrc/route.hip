@@ -139,127 +139,278 @@ struct Row {
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
-// The weights of the chosen logits l[0..k) (identical in all of a token's
-// lanes, -inf where there is none).  `top` and `total`: the softmax's
-// maximum and sum over all experts (not renormalised).
+// A token's lanes all belong to one wave: what one of them put into LDS is
+// there for the others once the compiler keeps the order (the LDS runs a
+// wave's accesses in order).
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Choices j = lane, lane + LPT, ... are a lane's own: at most JPL of them.
+template <int LPT>
+constexpr int kJpl = (kMaxTopK + LPT - 1) / LPT;
+
+// The weights of the chosen logits (l[i]: choice lane + i LPT, -inf where
+// there is none).  `top` and `total`: the softmax's maximum and sum over all
+// experts (not renormalised).
 // Renormalised, the softmax is one over the chosen experts alone, and the
 // sigmoid's ratio is formed from u_j = p_j exp(-m'), m' = min(0, max l):
 // u_j = 1 / (exp(m') + exp(m' - l_j)), which does not underflow when every
 // chosen score does.
-template <typename Get, typename Put>
-__device__ __forceinline__ void chosen_weights(const RouteArgs& a, float top, float total, Get&& logit, Put&& put) {
-  const int k = a.top_k;
-  float m = kNegInf;
-  for (int j = 0; j < k; ++j) m = fmaxf(m, logit(j));
+template <int LPT>
+__device__ __forceinline__ void chosen_weights(const RouteArgs& a, float top, float total, const float* l, float* w) {
+  constexpr int JPL = kJpl<LPT>;
   if (a.renormalise) {
+    float m = l[0];
+#pragma unroll
+    for (int i = 1; i < JPL; ++i) m = fmaxf(m, l[i]);
+    m = lanes_max<LPT>(m);
     const float mm = a.softmax ? m : fminf(m, 0.0f);
-    auto u = [&](float l) {
-      if (l == kNegInf) return 0.0f;
-      return a.softmax ? expf(l - mm) : 1.0f / (expf(mm) + expf(mm - l));
-    };
+    const float em = a.softmax ? 0.0f : expf(mm);
     float sum = 0.0f;
-    for (int j = 0; j < k; ++j) sum += u(logit(j));
+#pragma unroll
+    for (int i = 0; i < JPL; ++i) {
+      const float e = a.softmax ? expf(l[i] - mm) : 1.0f / (em + expf(mm - l[i]));
+      w[i] = l[i] == kNegInf ? 0.0f : e;
+      sum += w[i];
+    }
+    sum = lanes_sum<LPT>(sum);
     const float r = sum > 0.0f ? a.scale / sum : 0.0f;
-    for (int j = 0; j < k; ++j) put(j, u(logit(j)) * r);
+#pragma unroll
+    for (int i = 0; i < JPL; ++i) w[i] *= r;
   } else {
-    for (int j = 0; j < k; ++j) {
-      const float l = logit(j);
-      put(j, l == kNegInf ? 0.0f : a.scale * (a.softmax ? expf(l - top) / total : sigmoid(l)));
+#pragma unroll
+    for (int i = 0; i < JPL; ++i) {
+      const float p = a.softmax ? expf(l[i] - top) / total : sigmoid(l[i]);
+      w[i] = l[i] == kNegInf ? 0.0f : a.scale * p;
     }
   }
 }
 
 // ---- forward ---------------------------------------------------------------
 
+// The `rounds` largest keys of a token (-inf: cannot be chosen), largest
+// first, ties to the lowest expert: its ids[], logits[] and, where wanted,
+// keys[].  A round: the largest key of the token's lanes, the first expert
+// that has it, which is taken out.
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
+template <typename R, int LPT, int EPL, int V, typename Key>
+__device__ __forceinline__ void choose(Key* key, const float* x, int rounds, int lane, int* ids, float* logits, Key* keys) {
+  constexpr Key none = -static_cast<Key>(__builtin_inff());
+  for (int j = 0; j < rounds; ++j) {
+    Key best = key[0];
+#pragma unroll
+    for (int q = 1; q < EPL; ++q) best = larger(best, key[q]);
+    steps<LPT>([&](auto c) { best = larger(best, partner<decltype(c)::value>(best)); });
+    int at = 0x7FFFFFFF;
+#pragma unroll
+    for (int q = EPL - 1; q >= 0; --q) at = key[q] == best ? R::expert(lane, q / V, q % V) : at;
+    int first = at;
+    steps<LPT>([&](auto c) {
+      first = min(first, static_cast<int>(partner<decltype(c)::value>(static_cast<uint32_t>(first))));
+    });
+    if (at == first) {                       // one lane: the expert's own
+      float logit = kNegInf;
+#pragma unroll
+      for (int q = 0; q < EPL; ++q) {
+        const bool it = R::expert(lane, q / V, q % V) == first;
+        logit = it ? x[q] : logit;
+        key[q] = it ? none : key[q];
+      }
+      const bool there = best > none;
+      ids[j] = there ? first : -1;
+      logits[j] = there ? logit : kNegInf;
+      if (keys) keys[j] = best;
+    }
+  }
+}
+
+// e^x by the exponential unit, for sums and keys with bounds of their own.
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.4426950408889634f); }
+
+// With a bias the keys are sums of two numbers of different size, whose
+// order can hang on bits that fp32 does not have.  They are formed in fp32
+// first, with kSpare choices more than asked for.  Where two neighbours in
+// that order are nearer than the error of both, and not made of the same
+// numbers (whose sums are equal in any precision), the choices up to the next
+// clear gap are put into the order of their keys in 64 bits, one key a lane;
+// where no gap follows, the wave's tokens are chosen again with all keys in 64
+// bits.  Measured, 16381 tokens, 256 experts, sigmoid: 64 bits for every token
+// 30 us, this form 17 us.
+constexpr int kSpare = 2;
+constexpr int kSlots = kMaxTopK + kSpare;
+
 template <bool BF16, int LPT, int EPL, int V, bool BIAS>
 __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
   using R = Row<BF16, LPT, EPL, V>;
-  using Key = std::conditional_t<BIAS, double, float>;
-  constexpr int TPB = 256 / LPT;
-  __shared__ float chosen[TPB][kMaxTopK];
+  constexpr int TPB = 256 / LPT, JPL = kJpl<LPT>;
+  __shared__ float s_logit[TPB][kSlots];
+  __shared__ int s_id[TPB][kSlots];
+  __shared__ float s_key[BIAS ? TPB : 1][kSlots];
+  __shared__ int s_flag[BIAS ? TPB : 1][kSlots];
+  __shared__ double s_exact[BIAS ? TPB : 1][kSlots];
   const int lane = threadIdx.x % LPT, slot = threadIdx.x / LPT;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * TPB + slot;
   const bool live = t < a.tokens;               // idle lanes repeat the last token and store nothing
   const int64_t row = live ? t : a.tokens - 1;
+  const int k = a.top_k;
   float x[EPL];
   R::load(a.logits, row, a.experts, lane, x);
 
-  float top = kNegInf, total = 1.0f;
-#pragma unroll
-  for (int j = 0; j < EPL; ++j) top = fmaxf(top, x[j]);
-  top = lanes_max<LPT>(top);
-  const float shift = top == kNegInf ? 0.0f : top;
+  float top = 0.0f, total = 1.0f;
   if (a.softmax) {
+    top = x[0];
+#pragma unroll
+    for (int j = 1; j < EPL; ++j) top = fmaxf(top, x[j]);
+    top = lanes_max<LPT>(fmaxf(top, kNegInf));   // (a token of NaN: -inf)
+    if (top == kNegInf) top = 0.0f;
     total = 0.0f;
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) total += expf(x[j] - shift);
+    for (int j = 0; j < EPL; ++j) total += fast_exp(x[j] - top);
     total = lanes_sum<LPT>(total);
   }
 
-  // keys: the logit, or score + bias in 64 bits (the choice hangs on the
-  // last bits of a sum of two numbers of different size)
-  Key key[EPL];
-  if constexpr (BIAS) {
-    double dt = 0.0;
-    if (a.softmax) {
-#pragma unroll
-      for (int j = 0; j < EPL; ++j) {
-        key[j] = exp(static_cast<double>(x[j]) - shift);
-        dt += x[j] == x[j] ? key[j] : 0.0;
-      }
-      dt = 1.0 / lanes_sum<LPT>(dt);
-    }
-#pragma unroll
-    for (int i = 0; i < R::NI; ++i)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int j = i * V + v, e = R::expert(lane, i, v);
-        const double p = a.softmax ? key[j] * dt : 1.0 / (1.0 + exp(-static_cast<double>(x[j])));
-        const double b = e < a.experts ? static_cast<double>(a.bias[e]) : 0.0;
-        const double q = p + b;
-        key[j] = x[j] > kNegInf && q > -__builtin_inf() ? q : -__builtin_inf();   // NaN: false
-      }
-  } else {
+  float key[EPL];
+  if constexpr (!BIAS) {
 #pragma unroll
     for (int j = 0; j < EPL; ++j) key[j] = x[j] > kNegInf ? x[j] : kNegInf;
-  }
-
-  for (int j = 0; j < a.top_k; ++j) {
-    // best of this lane (the lowest expert first: ties keep it), then of the token's lanes
-    Key best = key[0];
-    int at = R::expert(lane, 0, 0);
-    float logit = x[0];
+    choose<R, LPT, EPL, V, float>(key, x, k, lane, s_id[slot], s_logit[slot], nullptr);
+    wave_sync();
+  } else {
+    // a NaN in the softmax's sum leaves the choice among the others
+    float valid = total;
+    if (a.softmax && __any(!(total == total))) {
+      valid = 0.0f;
 #pragma unroll
-    for (int q = 1; q < EPL; ++q)
-      if (key[q] > best) {
-        best = key[q];
-        at = R::expert(lane, q / V, q % V);
-        logit = x[q];
-      }
-    steps<LPT>([&](auto c) {
-      constexpr int S = decltype(c)::value;
-      const Key ob = partner<S>(best);
-      const int oa = static_cast<int>(partner<S>(static_cast<uint32_t>(at)));
-      const float ol = partner<S>(logit);
-      if (ob > best || (ob == best && oa < at)) {
-        best = ob;
-        at = oa;
-        logit = ol;
-      }
-    });
-    const bool there = best > -static_cast<Key>(__builtin_inf());
+      for (int j = 0; j < EPL; ++j) valid += x[j] == x[j] ? fast_exp(x[j] - top) : 0.0f;
+      valid = lanes_sum<LPT>(valid);
+    }
+    const float rt = 1.0f / valid;
 #pragma unroll
-    for (int q = 0; q < EPL; ++q)
-      if (R::expert(lane, q / V, q % V) == at) key[q] = -static_cast<Key>(__builtin_inf());
-    if (lane == 0) {
-      if (live) a.ids[t * a.top_k + j] = there ? at : -1;
-      chosen[slot][j] = there ? logit : kNegInf;
+    for (int i = 0; i < R::NI; ++i) {
+      typedef float vec __attribute__((ext_vector_type(V), aligned(4)));
+      const int e = R::expert(lane, i, 0);
+      const vec bv = *reinterpret_cast<const vec*>(a.bias + (e < a.experts ? e : 0));   // (whole groups of V exist)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int j = i * V + v;
+        const float b = bv[v];
+        const float p = a.softmax ? fast_exp(x[j] - top) * rt : __builtin_amdgcn_rcpf(1.0f + fast_exp(-x[j]));
+        const float q = p + b;
+        key[j] = x[j] > kNegInf && q > kNegInf ? q : kNegInf;    // NaN: false
+      }
+    }
+    const int cand = min(k + kSpare, a.experts);
+    choose<R, LPT, EPL, V, float>(key, x, cand, lane, s_id[slot], s_logit[slot], s_key[slot]);
+    float rest = key[0];
+#pragma unroll
+    for (int q = 1; q < EPL; ++q) rest = fmaxf(rest, key[q]);
+    rest = lanes_max<LPT>(rest);                   // the best that is left
+    wave_sync();
+    // Choice j against the next: 0 clear, 1 the same numbers, 2 in doubt.  A key
+    // is off by a rounding of its sum and by p's error: p <= 1, its exponential's
+    // argument (p |x| < 0.4), the unit's last places and a sum of up to 16 + 6
+    // terms, below 50 2^-24.
+    constexpr float kP = 2.0f * 50.0f * 5.9604645e-8f, kSum = 2.4e-7f;
+    bool maybe = false;
+    for (int j = lane; j < cand; j += LPT) {
+      const float k0 = s_key[slot][j], k1 = j + 1 < cand ? s_key[slot][j + 1] : rest;
+      int f = 0;
+      if (k1 > kNegInf && !(k0 - k1 > kP + kSum * (fabsf(k0) + fabsf(k1)))) {
+        f = 2;
+        if (j + 1 < cand && s_logit[slot][j] == s_logit[slot][j + 1] &&
+            a.bias[s_id[slot][j]] == a.bias[s_id[slot][j + 1]])
+          f = 1;
+      }
+      s_flag[slot][j] = f;
+      maybe |= f && j < k;
+    }
+    wave_sync();
+    if (__any(maybe)) {
+      int m = k;                                   // choices up to the next clear gap
+      while (m < cand && s_flag[slot][m - 1]) ++m;
+      const bool open = s_flag[slot][m - 1] != 0;
+      bool doubt = false;
+      for (int j = 0; j < m; ++j) doubt |= s_flag[slot][j] == 2;
+      if (__any(doubt)) {
+        const bool all = __any(doubt && open);
+        double exact[EPL];
+        double dt = 1.0;
+        if (a.softmax || all) {
+          double sum = 0.0;
+#pragma unroll
+          for (int j = 0; j < EPL; ++j) {
+            exact[j] = a.softmax ? exp(static_cast<double>(x[j]) - top) : 1.0 / (1.0 + exp(-static_cast<double>(x[j])));
+            sum += x[j] == x[j] ? exact[j] : 0.0;
+          }
+          if (a.softmax) dt = 1.0 / lanes_sum<LPT>(sum);
+        }
+        if (all) {
+#pragma unroll
+          for (int j = 0; j < EPL; ++j) {
+            const int e = R::expert(lane, j / V, j % V);
+            const double q = exact[j] * dt + a.bias[e < a.experts ? e : 0];
+            exact[j] = x[j] > kNegInf && q > -__builtin_inf() ? q : -__builtin_inf();
+          }
+          choose<R, LPT, EPL, V, double>(exact, x, k, lane, s_id[slot], s_logit[slot], nullptr);
+        } else {
+          constexpr int N = (kSlots + LPT - 1) / LPT;
+          double mine[N];
+          int id[N], rank[N];
+          float lg[N];
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const int j = lane + i * LPT;
+            id[i] = j < m ? s_id[slot][j] : -1;
+            lg[i] = j < m ? s_logit[slot][j] : kNegInf;
+            mine[i] = 0.0;
+            if (id[i] >= 0) {
+              const double l = lg[i];
+              mine[i] = (a.softmax ? exp(l - top) * dt : 1.0 / (1.0 + exp(-l))) + a.bias[id[i]];
+              s_exact[slot][j] = mine[i];
+            }
+          }
+          wave_sync();
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            rank[i] = 0;
+            for (int j = 0; j < m; ++j) {
+              const double o = s_exact[slot][j];
+              const int oid = s_id[slot][j];
+              if (oid >= 0 && (o > mine[i] || (o == mine[i] && oid < id[i]))) ++rank[i];
+            }
+          }
+          wave_sync();
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (id[i] >= 0) {
+              s_id[slot][rank[i]] = id[i];
+              s_logit[slot][rank[i]] = lg[i];
+            }
+        }
+        wave_sync();
+      }
     }
   }
-  __syncthreads();
-  if (lane == 0 && live)
-    chosen_weights(a, shift, total, [&](int j) { return chosen[slot][j]; },
-                   [&](int j, float w) { a.weights[t * a.top_k + j] = w; });
+
+  float l[JPL], w[JPL];
+#pragma unroll
+  for (int i = 0; i < JPL; ++i) {
+    const int j = lane + i * LPT;
+    l[i] = j < k ? s_logit[slot][j] : kNegInf;
+  }
+  chosen_weights<LPT>(a, top, total, l, w);
+#pragma unroll
+  for (int i = 0; i < JPL; ++i) {
+    const int j = lane + i * LPT;
+    if (live && j < k) {
+      a.ids[t * k + j] = s_id[slot][j];
+      a.weights[t * k + j] = w[i];
+    }
+  }
 }
 
 // ---- backward --------------------------------------------------------------
@@ -272,8 +423,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
 template <bool BF16, int LPT, int EPL, int V>
 __global__ __launch_bounds__(256) void route_backward_kernel(RouteArgs a) {
   using R = Row<BF16, LPT, EPL, V>;
-  constexpr int TPB = 256 / LPT;
-  __shared__ float s_l[TPB][kMaxTopK], s_w[TPB][kMaxTopK];
+  constexpr int TPB = 256 / LPT, JPL = kJpl<LPT>;
   __shared__ float s_d[TPB][kMaxTopK];
   __shared__ int s_id[TPB][kMaxTopK];
   const int lane = threadIdx.x % LPT, slot = threadIdx.x / LPT;
@@ -281,69 +431,72 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteArgs a) {
   const bool live = t < a.tokens;
   const int64_t row = live ? t : a.tokens - 1;
   const int k = a.top_k;
-  for (int j = lane; j < k; j += LPT) {
-    int id = a.ids[row * k + j];
-    if (id < 0 || id >= a.experts) id = -1;
-    float l = kNegInf;
-    if (id >= 0) {
-      l = BF16 ? from_bf16(static_cast<const uint16_t*>(a.logits)[row * a.experts + id])
-               : static_cast<const float*>(a.logits)[row * a.experts + id];
-      l = l > kMaxF ? kMaxF : l;
+  float l[JPL], g[JPL], w[JPL];
+  int id[JPL];
+#pragma unroll
+  for (int i = 0; i < JPL; ++i) {
+    const int j = lane + i * LPT;
+    id[i] = j < k ? a.ids[row * k + j] : -1;
+    if (id[i] < 0 || id[i] >= a.experts) id[i] = -1;
+    l[i] = kNegInf;
+    g[i] = 0.0f;
+    if (id[i] >= 0) {
+      l[i] = BF16 ? from_bf16(static_cast<const uint16_t*>(a.logits)[row * a.experts + id[i]])
+                  : static_cast<const float*>(a.logits)[row * a.experts + id[i]];
+      l[i] = l[i] > kMaxF ? kMaxF : l[i];
+      g[i] = a.dweights[row * k + j];
     }
-    s_id[slot][j] = id;
-    s_l[slot][j] = l;
-    s_d[slot][j] = id >= 0 ? a.dweights[row * k + j] : 0.0f;
   }
   float x[EPL];
   float top = 0.0f, total = 1.0f;
   const bool full = a.softmax && !a.renormalise;      // every expert has a gradient
   if (full) {
     R::load(a.logits, row, a.experts, lane, x);
-    top = kNegInf;
+    top = x[0];
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) top = fmaxf(top, x[j]);
-    top = lanes_max<LPT>(top);
+    for (int j = 1; j < EPL; ++j) top = fmaxf(top, x[j]);
+    top = lanes_max<LPT>(fmaxf(top, kNegInf));
     if (top == kNegInf) top = 0.0f;
     total = 0.0f;
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) total += expf(x[j] - top);
+    for (int j = 0; j < EPL; ++j) total += fast_exp(x[j] - top);
     total = lanes_sum<LPT>(total);
   }
-  __syncthreads();
-  // every lane forms the same k numbers; lane 0 keeps them
+  chosen_weights<LPT>(a, top, total, l, w);
   float dot = 0.0f;
-  chosen_weights(a, top, total, [&](int j) { return s_l[slot][j]; },
-                 [&](int j, float w) {
-                   dot += s_d[slot][j] * w;
-                   if (lane == 0) s_w[slot][j] = w;
-                 });
-  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < JPL; ++i) dot += g[i] * w[i];
+  dot = lanes_sum<LPT>(dot);
   if (a.renormalise) dot = a.scale != 0.0f ? dot / a.scale : 0.0f;
-  for (int j = lane; j < k; j += LPT) {
-    const float g = s_d[slot][j], w = s_w[slot][j];
+#pragma unroll
+  for (int i = 0; i < JPL; ++i) {
+    const int j = lane + i * LPT;
     float d;
     if (a.renormalise) {
-      d = w * (g - dot);
-      if (!a.softmax) d *= sigmoid(-s_l[slot][j]);
+      d = w[i] * (g[i] - dot);
+      if (!a.softmax) d *= sigmoid(-l[i]);
     } else {
-      d = a.softmax ? g * a.scale : g * w * sigmoid(-s_l[slot][j]);
+      d = a.softmax ? g[i] * a.scale : g[i] * w[i] * sigmoid(-l[i]);
     }
-    s_d[slot][j] = s_id[slot][j] >= 0 ? d : 0.0f;
+    if (j < k) {
+      s_id[slot][j] = id[i];
+      s_d[slot][j] = id[i] >= 0 ? d : 0.0f;
+    }
   }
-  __syncthreads();
+  wave_sync();
   float out[EPL];
 #pragma unroll
   for (int q = 0; q < EPL; ++q) out[q] = 0.0f;
   for (int j = 0; j < k; ++j) {
-    const int id = s_id[slot][j];
+    const int e = s_id[slot][j];
     const float d = s_d[slot][j];
 #pragma unroll
-    for (int q = 0; q < EPL; ++q) out[q] += R::expert(lane, q / V, q % V) == id ? d : 0.0f;
+    for (int q = 0; q < EPL; ++q) out[q] += R::expert(lane, q / V, q % V) == e ? d : 0.0f;
   }
   if (full) {
     const float r = total > 0.0f ? 1.0f / total : (total == 0.0f ? 0.0f : total);   // NaN stays
 #pragma unroll
-    for (int q = 0; q < EPL; ++q) out[q] = expf(x[q] - top) * r * (out[q] - dot);
+    for (int q = 0; q < EPL; ++q) out[q] = fast_exp(x[q] - top) * r * (out[q] - dot);
   }
   if (live) R::store(a.dlogits, t, a.experts, lane, out);
 }
