@@ -117,59 +117,68 @@ __global__ __launch_bounds__(kFewThreads, 2) void linear_few_rows_kernel(LinearA
 // joins of a split r
 // ---------------------------------------------------------------------------
 
-__device__ __forceinline__ v4f sum_parts(const float* at, int64_t stride, int parts) {
-  v4f s = *reinterpret_cast<const v4f*>(at);
-  for (int p = 1; p < parts; ++p) s += *reinterpret_cast<const v4f*>(at + p * stride);
-  return s;
-}
-
 __device__ __forceinline__ void store4(void* base, bool f32, int64_t i, v4f v) {
   if (f32) *reinterpret_cast<v4f*>(static_cast<float*>(base) + i) = v;
   else *reinterpret_cast<v2u*>(static_cast<uint16_t*>(base) + i) = v2u{bf16x2(v.x, v.y), bf16x2(v.z, v.w)};
 }
 
-// dx or dw: 4 numbers a thread.
-__global__ __launch_bounds__(256) void linear_join_kernel(const float* partial, int64_t count, int parts, void* out, bool f32) {
-  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
-  if (i < count) store4(out, f32, i, sum_parts(partial + i, count, parts));
-}
-
-// Forward (one group): 4 columns of z a thread, or 4 of each half of a pair.
-__global__ __launch_bounds__(256) void linear_join_forward_kernel(LinearArgs a, int parts) {
-  const bool pair = a.act == LIN_SWIGLU;
-  const int n_out = pair ? a.n / 2 : a.n, per_row = n_out / 4;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t m = i / per_row;
-  if (m >= a.m) return;
-  const int ycol = static_cast<int>(i - m * per_row) * 4;
-  const int n = pair ? (ycol >> 5) * 64 + (ycol & 31) : ycol;
-  const int64_t stride = a.m * a.n;
-  auto z_of = [&](int col) __attribute__((always_inline)) {
-    v4f z = sum_parts(a.partial + m * a.n + col, stride, parts);
-    if (a.bias) z += *reinterpret_cast<const v4f_any*>(a.bias + col);
-    if (a.c) store4(a.c, false, m * a.n + col, z);
-    return z;
+// The parts of tiles [first, tiles), added in their order: 4 columns of the
+// output a thread (and, of a SwiGLU pair, their 4 gates).
+template <int MODE, int BP, int BQ>
+__global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs a, TilePlan plan) {
+  constexpr int PER = BP * BQ / 4 / 256;         // workgroups per tile
+  const int lane = threadIdx.x & 63;
+  const int split = plan.tiles - plan.first, i = blockIdx.x / PER;
+  const int at = (blockIdx.x - i * PER) * 256 + threadIdx.x;
+  const int row = at / (BQ / 4), col = (at - row * (BQ / 4)) * 4;
+  LinearTile t;
+  const int row_tiles = static_cast<int>(((MODE == MODE_DW ? a.n : a.m) + BP - 1) / BP);
+  if (!place<MODE, BP, BQ>(a, plan.first + i, row_tiles, lane, t)) return;
+  const int64_t r = t.row0 + row;
+  const int c = t.col0 + col, cols = out_columns<MODE>(a);
+  if (r >= t.row_end || c >= cols) return;
+  const float* const base = a.partial + static_cast<int64_t>(i) * (BP * BQ) + row * BQ + col;
+  const int64_t stride = static_cast<int64_t>(split) * (BP * BQ);
+  auto sum = [&](int off) __attribute__((always_inline)) {
+    v4f v = *reinterpret_cast<const v4f*>(base + off);
+    for (int q = 1; q < plan.parts; ++q) v += *reinterpret_cast<const v4f*>(base + q * stride + off);
+    return v;
   };
-  v4f z = z_of(n);
-  if (pair) {
-    const v4f gate = z_of(n + 32);
+  if constexpr (MODE != MODE_FORWARD) {
+    store4(MODE == MODE_DX ? static_cast<void*>(a.dx) : a.dw, MODE == MODE_DW && a.out_f32,
+           (MODE == MODE_DW ? static_cast<int64_t>(t.g) * a.n + r : r) * cols + c, sum(0));
+  } else {
+    const bool pair = a.act == LIN_SWIGLU;
+    if (pair && (c & 32)) return;                // a pair's gates are handled with its linear half
+    auto z_of = [&](int off) __attribute__((always_inline)) {
+      v4f z = sum(off);
+      if (a.bias) z += *reinterpret_cast<const v4f_any*>(a.bias + c + off);
+      if (a.c) store4(a.c, false, r * a.n + c + off, z);
+      return z;
+    };
+    v4f z = z_of(0);
+    if (pair) {
+      const v4f gate = z_of(32);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) z[e] = z[e] * (gate[e] * sigmoid_f(gate[e]));
-  } else if (a.act == LIN_GELU) {
+      for (int e = 0; e < 4; ++e) z[e] = z[e] * (gate[e] * sigmoid_f(gate[e]));
+    } else if (a.act == LIN_GELU) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) z[e] = gelu_f(z[e]);
-  } else if (a.act == LIN_SRELU) {
+      for (int e = 0; e < 4; ++e) z[e] = gelu_f(z[e]);
+    } else if (a.act == LIN_SRELU) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float v = fmaxf(z[e], 0.0f);
-      z[e] = v * v;
+      for (int e = 0; e < 4; ++e) {
+        const float v = fmaxf(z[e], 0.0f);
+        z[e] = v * v;
+      }
     }
+    const int n_out = pair ? a.n / 2 : a.n;
+    const int64_t o = r * n_out + (pair ? (c >> 6) * 32 + (c & 31) : c);
+    if (a.residual) {
+      const v2u u = *reinterpret_cast<const v2u*>(a.residual + o);
+      z += v4f{bf_lo(u.x), bf_hi(u.x), bf_lo(u.y), bf_hi(u.y)};
+    }
+    store4(a.y, a.out_f32, o, z);
   }
-  if (a.residual) {
-    const v2u u = *reinterpret_cast<const v2u*>(a.residual + m * n_out + ycol);
-    z += v4f{bf_lo(u.x), bf_hi(u.x), bf_lo(u.y), bf_hi(u.y)};
-  }
-  store4(a.y, a.out_f32, m * n_out + ycol, z);
 }
 
 // ---------------------------------------------------------------------------
@@ -304,65 +313,108 @@ int64_t round_up(int64_t a, int64_t b) { return div_up(a, b) * b; }
 // Row tiles of all groups at most.
 int64_t row_tiles(const LinearArgs& a, int64_t bm) { return div_up(a.m, bm) + (a.groups > 1 ? a.groups - 1 : 0); }
 
+// Tile shapes: how many workgroups the chip holds at once, and what a round of
+// them takes for a step of 64 r and for everything outside the steps, in
+// microseconds; `alone`: a step where one workgroup has its compute unit to
+// itself.
 enum Shape : int { SHAPE_256 = 0, SHAPE_128 = 1, SHAPE_64 = 2 };
+struct ShapeCost {
+  int bp, bq, slots;
+  double step, alone, rest;
+};
+constexpr ShapeCost kShapes[] = {{256, 256, 256, 1.55, 1.55, 8.0}, {128, 128, 512, 1.0, 0.70, 5.0}, {128, 64, 768, 0.80, 0.60, 4.0}};
+
 struct Plan {
   Shape shape;
-  int parts;          // of r
-  int64_t tiles;      // workgroups per part
+  TilePlan tiles;
+  int64_t workgroups;
+  int64_t partial_bytes;
 };
 
-Plan choose(int64_t tiles256, int64_t tiles128, int64_t tiles64, int64_t cols, int64_t r, bool splittable) {
-  Plan p;
-  if (cols <= 64) p = {SHAPE_64, 1, tiles64};
-  else if (tiles256 >= 160) p = {SHAPE_256, 1, tiles256};
-  else p = {SHAPE_128, 1, tiles128};
-  if (splittable && p.shape != SHAPE_256) {
-    const int64_t most = div_up(r, 4 * kR);              // at least 4 steps a part
-    const int64_t fill = 512 / p.tiles;
-    p.parts = static_cast<int>(fill < 1 ? 1 : fill < most ? fill : most);
-    if (p.parts > 64) p.parts = 64;
+// Which tile, and which tiles share their r among several workgroups: the
+// cheapest by rounds of workgroups, where a last round that leaves most of the
+// chip empty (or the only one) may be split, against the bytes of its parts,
+// written and read at about 4 TB/s, and a join's launch.
+// `tiles(s)`: tiles of shape s at most; `r`: length of the sum; `known`: the
+// tiles are these, and may be split.
+template <typename F>
+Plan choose(F&& tiles, int64_t cols, int64_t r, bool known) {
+  Plan best{};
+  double least = 0.0;
+  const int64_t steps = div_up(r > 0 ? r : 1, kR);
+  for (int s = 0; s < 3; ++s) {
+    const ShapeCost& c = kShapes[s];
+    const int64_t total = tiles(c);
+    // the narrow tile is for narrow outputs
+    if ((s == SHAPE_64) != (cols <= 64)) continue;
+    auto rounds = [&](int64_t n, int64_t st) {
+      const int64_t left = n % c.slots;
+      return static_cast<double>(n / c.slots) * (st * c.step + c.rest) +
+             (left ? st * (left <= 256 ? c.alone : c.step) + c.rest : 0.0);
+    };
+    auto take = [&](double cost, int64_t first, int parts) {
+      if (least != 0.0 && cost >= least) return;
+      least = cost;
+      best.shape = static_cast<Shape>(s);
+      best.tiles = {known ? static_cast<int>(total) : -1, static_cast<int>(first), parts};
+      best.workgroups = first + (total - first) * parts;
+      best.partial_bytes = parts > 1 ? (total - first) * parts * c.bp * c.bq * 4 : 0;
+    };
+    take(rounds(total, steps), total, 1);
+    if (!known) continue;
+    for (int64_t first : {int64_t{0}, total / c.slots * c.slots}) {
+      if (first == total || (first == 0 && total > 2 * c.slots)) continue;
+      for (int parts = 2; parts <= 16 && parts * 2 <= steps; ++parts) {
+        const double bytes = static_cast<double>((total - first) * parts) * c.bp * c.bq * 4;
+        take((first ? rounds(first, steps) : 0.0) + rounds((total - first) * parts, div_up(steps, parts)) + 4.0 + 2.0 * bytes / 4e6,
+             first, parts);
+      }
+    }
   }
-  return p;
+  return best;
 }
-// Split only without offsets: the join goes over all rows.  (The workspace is
-// sized without knowing them, so never too small.)
+
+// Split only without offsets, where the host knows the tiles.  (The workspace
+// is sized without knowing the offsets, so never too small.)
 Plan plan_rows(const LinearArgs& a, int64_t cols, int64_t r) {
-  return choose(row_tiles(a, 256) * div_up(cols, 256), row_tiles(a, 128) * div_up(cols, 128),
-                row_tiles(a, 128) * div_up(cols, 64), cols, r, a.groups == 1 && !a.offsets);
+  return choose([&](const ShapeCost& c) { return row_tiles(a, c.bp) * div_up(cols, c.bq); }, cols, r,
+                a.groups == 1 && !a.offsets);
 }
 Plan plan_dw(const LinearArgs& a) {
-  Plan p = choose(a.groups * div_up(a.n, 256) * div_up(a.k, 256), a.groups * div_up(a.n, 128) * div_up(a.k, 128),
-                  a.groups * div_up(a.n, 128) * div_up(a.k, 64), a.k, a.m, a.groups == 1);
-  return p;
+  // a group's share of the rows; groups whose rows the host does not know are not split
+  return choose([&](const ShapeCost& c) { return a.groups * div_up(a.n, c.bp) * div_up(a.k, c.bq); }, a.k,
+                div_up(a.m, a.groups), a.groups == 1);
 }
 bool few_rows(const LinearArgs& a) { return a.m <= 16 * static_cast<int64_t>(a.groups); }
 
-template <int MODE, bool SPLIT>
-void launch_shape(const LinearArgs& a, const Plan& p, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(p.tiles), static_cast<unsigned>(p.parts));
-  switch (p.shape) {
-    case SHAPE_256: hipLaunchKernelGGL((linear_pingpong_kernel<MODE, SPLIT>), grid, dim3(512), 0, s, a, p.parts); break;
-    case SHAPE_128: hipLaunchKernelGGL((linear_tile_kernel<MODE, 128, 128, 2, 2, SPLIT>), grid, dim3(256), 0, s, a, p.parts); break;
-    case SHAPE_64: hipLaunchKernelGGL((linear_tile_kernel<MODE, 128, 64, 4, 1, SPLIT>), grid, dim3(256), 0, s, a, p.parts); break;
-  }
+template <int MODE, int BP, int BQ>
+void launch_join(const LinearArgs& a, const Plan& p, hipStream_t s) {
+  if (p.tiles.parts > 1)
+    hipLaunchKernelGGL((linear_join_kernel<MODE, BP, BQ>),
+                       dim3(static_cast<unsigned>((p.tiles.tiles - p.tiles.first) * (BP * BQ / 1024))), dim3(256), 0, s, a, p.tiles);
 }
 template <int MODE>
-hipError_t launch_tiles(const LinearArgs& a, const Plan& p, int64_t count, hipStream_t s) {
-  if (p.parts == 1) {
-    launch_shape<MODE, false>(a, p, s);
-    return hipGetLastError();
+hipError_t launch_tiles(const LinearArgs& a, const Plan& p, hipStream_t s) {
+  // dw's tiles are the host's in any case (tiles < 0 means counted on the device)
+  TilePlan t = p.tiles;
+  if (MODE == MODE_DW && t.tiles < 0) t = {static_cast<int>(p.workgroups), static_cast<int>(p.workgroups), 1};
+  const dim3 grid(static_cast<unsigned>(p.workgroups));
+  switch (p.shape) {
+    case SHAPE_256:
+      hipLaunchKernelGGL((linear_pingpong_kernel<MODE>), grid, dim3(512), 0, s, a, t);
+      launch_join<MODE, 256, 256>(a, p, s);
+      break;
+    case SHAPE_128:
+      hipLaunchKernelGGL((linear_tile_kernel<MODE, 128, 128, 2, 2>), grid, dim3(256), 0, s, a, t);
+      launch_join<MODE, 128, 128>(a, p, s);
+      break;
+    case SHAPE_64:
+      hipLaunchKernelGGL((linear_tile_kernel<MODE, 128, 64, 4, 1>), grid, dim3(256), 0, s, a, t);
+      launch_join<MODE, 128, 64>(a, p, s);
+      break;
   }
-  launch_shape<MODE, true>(a, p, s);
-  if (MODE == MODE_FORWARD)
-    hipLaunchKernelGGL(linear_join_forward_kernel, dim3(static_cast<unsigned>(div_up(count / (a.act == LIN_SWIGLU ? 2 : 1), 1024))),
-                       dim3(256), 0, s, a, p.parts);
-  else
-    hipLaunchKernelGGL(linear_join_kernel, dim3(static_cast<unsigned>(div_up(count, 1024))), dim3(256), 0, s, a.partial, count,
-                       p.parts, MODE == MODE_DX ? static_cast<void*>(a.dx) : a.dw, MODE == MODE_DW && a.out_f32);
   return hipGetLastError();
 }
-
-int64_t partial_bytes(const Plan& p, int64_t count) { return p.parts > 1 ? p.parts * count * 4 : 0; }
 
 // Workspace of the backward: dz, the column sums of the row tiles, and the
 // parts of dx and dw (one after the other in the same place).
@@ -378,9 +430,9 @@ BackwardWorkspace backward_workspace(const LinearArgs& a, bool dx, bool dw, bool
   if (db) at += round_up(row_tiles(a, kDzRows) * a.n * 4, 256);
   w.partial = at;
   int64_t most = 0;
-  if (dx && a.m) most = partial_bytes(plan_rows(a, a.k, a.n), a.m * a.k);
+  if (dx && a.m) most = plan_rows(a, a.k, a.n).partial_bytes;
   if (dw) {
-    const int64_t b = partial_bytes(plan_dw(a), static_cast<int64_t>(a.groups) * a.n * a.k);
+    const int64_t b = plan_dw(a).partial_bytes;
     most = b > most ? b : most;
   }
   w.total = at + most;
@@ -391,7 +443,7 @@ BackwardWorkspace backward_workspace(const LinearArgs& a, bool dx, bool dw, bool
 
 int64_t linear_workspace(const LinearArgs& a) {
   if (a.m == 0 || few_rows(a)) return 0;
-  return partial_bytes(plan_rows(a, a.n, a.k), a.m * a.n);
+  return plan_rows(a, a.n, a.k).partial_bytes;
 }
 int64_t linear_backward_workspace(const LinearArgs& a, bool dx, bool dw, bool db) {
   return backward_workspace(a, dx, dw, db).total;
@@ -406,7 +458,7 @@ hipError_t launch_linear(const LinearArgs& args, hipStream_t s) {
     return hipGetLastError();
   }
   a.partial = static_cast<float*>(a.workspace);
-  return launch_tiles<MODE_FORWARD>(a, plan_rows(a, a.n, a.k), a.m * a.n, s);
+  return launch_tiles<MODE_FORWARD>(a, plan_rows(a, a.n, a.k), s);
 }
 
 hipError_t launch_linear_backward(const LinearArgs& args, hipStream_t s) {
@@ -430,8 +482,8 @@ hipError_t launch_linear_backward(const LinearArgs& args, hipStream_t s) {
                        s, a, sums);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  if (a.dx && a.m && (e = launch_tiles<MODE_DX>(a, plan_rows(a, a.k, a.n), a.m * a.k, s)) != hipSuccess) return e;
-  if (a.dw && (e = launch_tiles<MODE_DW>(a, plan_dw(a), static_cast<int64_t>(a.groups) * a.n * a.k, s)) != hipSuccess) return e;
+  if (a.dx && a.m && (e = launch_tiles<MODE_DX>(a, plan_rows(a, a.k, a.n), s)) != hipSuccess) return e;
+  if (a.dw && (e = launch_tiles<MODE_DW>(a, plan_dw(a), s)) != hipSuccess) return e;
   return e;
 }
 

@@ -259,52 +259,95 @@ __device__ __forceinline__ float gelu_f(float z) {
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
 
+// How a launch covers the tiles (tile counts on the host, see choose()).
+// Tiles [0, first) have a workgroup each; each later one has `parts`, which
+// share r and leave their sums in the workspace, (parts, tiles - first, BP,
+// BQ) fp32, for a join.  With groups whose rows the host does not know
+// (tiles < 0) there is a workgroup for every tile there may be.
+struct TilePlan {
+  int tiles, first, parts;
+};
+
 // What a workgroup computes: rows [row0, row_end) (up to its tile's), columns
-// from col0 on, r in [r0, r1), of group g.
+// from col0 on, r in [r0, r1), of group g; `slot`: where its part goes, or -1.
 struct LinearTile {
-  int g, col0;
+  int g, col0, slot;
   int64_t row0, row_end, r0, r1;
 };
 
 template <int MODE>
 __device__ __forceinline__ int out_columns(const LinearArgs& a) { return MODE == MODE_FORWARD ? a.n : a.k; }
 
-// blockIdx.x is the tile; SPLIT: blockIdx.y is a part of r.
-template <int MODE, int BP, int BQ, bool SPLIT>
-__device__ __forceinline__ bool locate(const LinearArgs& a, int parts, int lane, LinearTile& t) {
+// Group, rows and columns of tile i.
+template <int MODE, int BP, int BQ>
+__device__ __forceinline__ bool place(const LinearArgs& a, int i, int row_tiles, int lane, LinearTile& t) {
   const int col_tiles = (out_columns<MODE>(a) + BQ - 1) / BQ;
   int rt, ct;
-  t.r0 = 0;
   if constexpr (MODE == MODE_DW) {
-    const int row_tiles = (a.n + BP - 1) / BP;
-    const int i = tile_of_workgroup(blockIdx.x, gridDim.x);
     t.g = i / (row_tiles * col_tiles);
     tile_position(i - t.g * row_tiles * col_tiles, row_tiles, col_tiles, rt, ct);
     t.row0 = static_cast<int64_t>(rt) * BP;
     t.row_end = a.n;
-    group_rows(a, t.g, t.r0, t.r1);
   } else {
-    const int row_tiles = count_row_tiles<BP>(a, lane);
-    const int total = row_tiles * col_tiles;
-    if (static_cast<int>(blockIdx.x) >= total) return false;
-    tile_position(tile_of_workgroup(blockIdx.x, total), row_tiles, col_tiles, rt, ct);
+    tile_position(i, row_tiles, col_tiles, rt, ct);
     if (!find_row_tile<BP>(a, rt, lane, t.g, t.row0, t.row_end)) return false;
-    t.r1 = MODE == MODE_FORWARD ? a.k : a.n;
   }
   t.col0 = ct * BQ;
-  if constexpr (SPLIT) {
+  return true;
+}
+
+template <int MODE, int BP, int BQ>
+__device__ __forceinline__ bool locate(const LinearArgs& a, const TilePlan& p, int lane, LinearTile& t) {
+  const int w = blockIdx.x;
+  const int row_tiles = MODE == MODE_DW ? (a.n + BP - 1) / BP : count_row_tiles<BP>(a, lane);
+  int i = w, part = -1;
+  if (p.tiles < 0) {
+    const int total = row_tiles * ((out_columns<MODE>(a) + BQ - 1) / BQ);
+    if (w >= total) return false;
+    i = tile_of_workgroup(w, total);
+  } else if (w < p.first) {
+    i = tile_of_workgroup(w, p.first);
+  } else {
+    const int split = p.tiles - p.first, j = w - p.first;
+    part = j / split;
+    i = p.first + tile_of_workgroup(j - part * split, split);
+  }
+  t.slot = part < 0 ? -1 : part * (p.tiles - p.first) + i - p.first;
+  if (!place<MODE, BP, BQ>(a, i, row_tiles, lane, t)) return false;
+  t.r0 = 0;
+  t.r1 = MODE == MODE_FORWARD ? a.k : a.n;
+  if constexpr (MODE == MODE_DW) group_rows(a, t.g, t.r0, t.r1);
+  if (part >= 0) {
     const int64_t steps = (t.r1 - t.r0 + kR - 1) / kR;
-    const int64_t lo = steps * blockIdx.y / parts, hi = steps * (blockIdx.y + 1) / parts;
+    const int64_t lo = steps * part / p.parts, hi = steps * (part + 1) / p.parts;
     t.r1 = min(t.r1, t.r0 + hi * kR);
-    t.r0 += lo * kR;
+    t.r0 = min(t.r1, t.r0 + lo * kR);
   }
   return true;
 }
 
+// A wave's accumulators to its place in the workspace: 32 TM rows from row on
+// of the tile, 64 columns from col on.
+template <int BP, int BQ, int TM, int TN>
+__device__ __forceinline__ void store_part(const LinearArgs& a, v16f (&acc)[TM][TN], int slot, int row, int col,
+                                           uint8_t* scratch, int lane) {
+  float* const base = a.partial + static_cast<int64_t>(slot) * (BP * BQ) + row * BQ + col;
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      v4u v[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        v[b] = v4u{__float_as_uint(acc[i][j][4 * b]), __float_as_uint(acc[i][j][4 * b + 1]),
+                   __float_as_uint(acc[i][j][4 * b + 2]), __float_as_uint(acc[i][j][4 * b + 3])};
+      store_block<128>(reinterpret_cast<uint8_t*>(base + i * 32 * BQ + 32 * j), BQ * 4, v, scratch, lane, 32, 128);
+    }
+}
+
 // A wave's accumulators to memory: rows [row, row + 32 TM) of group g up to
-// row_end, 64 columns from ncol on, through 4 KB of LDS scratch.  SPLIT: to
-// the workspace, (parts, rows of the output, columns) fp32.
-template <int MODE, bool SPLIT, int TM, int TN>
+// row_end, 64 columns from ncol on, through 4 KB of LDS scratch.
+template <int MODE, int TM, int TN>
 __device__ __forceinline__ void store_output(const LinearArgs& a, v16f (&acc)[TM][TN], int g, int64_t row, int64_t row_end,
                                              int ncol, uint8_t* scratch, int lane) {
   const int l32 = lane & 31, hi = lane >> 5;
@@ -315,21 +358,7 @@ __device__ __forceinline__ void store_output(const LinearArgs& a, v16f (&acc)[TM
     const int64_t rb = row + i * 32;                        // first row of the block
     const int rows = static_cast<int>(min(row_end - rb, int64_t{32}));
     if (rows <= 0) break;
-    if constexpr (SPLIT) {
-      const int64_t out_rows = MODE == MODE_DW ? static_cast<int64_t>(a.groups) * a.n : a.m;
-      const int64_t r = (MODE == MODE_DW ? static_cast<int64_t>(g) * a.n : 0) + rb;
-      float* const base = a.partial + (blockIdx.y * out_rows + r) * cols + ncol;
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        v4u v[4];
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-          v[b] = v4u{__float_as_uint(acc[i][j][4 * b]), __float_as_uint(acc[i][j][4 * b + 1]),
-                     __float_as_uint(acc[i][j][4 * b + 2]), __float_as_uint(acc[i][j][4 * b + 3])};
-        store_block<128>(reinterpret_cast<uint8_t*>(base + 32 * j), static_cast<int64_t>(cols) * 4, v, scratch, lane, rows,
-                         (cols - ncol - 32 * j) * 4);
-      }
-    } else if constexpr (MODE != MODE_FORWARD) {
+    if constexpr (MODE != MODE_FORWARD) {
       const int64_t r = (MODE == MODE_DW ? static_cast<int64_t>(g) * a.n : 0) + rb;
       if (MODE == MODE_DW && a.out_f32) {
         float* const base = static_cast<float*>(a.dw) + r * cols + ncol;
@@ -446,10 +475,9 @@ __device__ __forceinline__ void store_output(const LinearArgs& a, v16f (&acc)[TM
   }
 }
 
-// The tile kernel.  SPLIT: blockIdx.y is a part of r, and the sums go to
-// the workspace, (parts, rows of the output, columns) fp32.
-template <int MODE, int BP, int BQ, int WP, int WQ, bool SPLIT>
-__global__ __launch_bounds__(64 * WP * WQ, 2) void linear_tile_kernel(LinearArgs a, int parts) {
+// The tile kernel for small tiles.
+template <int MODE, int BP, int BQ, int WP, int WQ>
+__global__ __launch_bounds__(64 * WP * WQ, 2) void linear_tile_kernel(LinearArgs a, TilePlan plan) {
   constexpr int NW = WP * WQ, TM = BP / WP / 32, TN = BQ / WQ / 32;
   using TP = TileOperand<MODE != MODE_DW, BP, NW>;
   using TQ = TileOperand<MODE == MODE_FORWARD, BQ, NW>;
@@ -462,7 +490,7 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void linear_tile_kernel(LinearArgs
   const int wp = wave / WQ, wq = wave % WQ;
 
   LinearTile t;
-  if (!locate<MODE, BP, BQ, SPLIT>(a, parts, lane, t)) return;
+  if (!locate<MODE, BP, BQ>(a, plan, lane, t)) return;
   const int64_t wg = static_cast<int64_t>(t.g) * a.n * a.k;
   TP p;
   TQ q;
@@ -542,7 +570,8 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void linear_tile_kernel(LinearArgs
   // ---- the output ----
   uint8_t* const scratch = (wave & 1 ? sP1 : sP0) + (wave >> 1) * 4096;
   static_assert(TP::BYTES >= (NW + 1) / 2 * 4096, "scratch of the waves");
-  store_output<MODE, SPLIT>(a, acc, t.g, t.row0 + wp * (TM * 32), t.row_end, t.col0 + wq * 64, scratch, lane);
+  if (t.slot >= 0) store_part<BP, BQ>(a, acc, t.slot, wp * (TM * 32), wq * 64, scratch, lane);
+  else store_output<MODE>(a, acc, t.g, t.row0 + wp * (TM * 32), t.row_end, t.col0 + wq * 64, scratch, lane);
 }
 
 // The 256 x 256 tile on the ping-pong schedule of the grouped product (8
@@ -557,8 +586,8 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void linear_tile_kernel(LinearArgs
 // clusters to land and is waited for one cluster and barrier before its use.
 // Steps past the last read zeros, so the steps go in pairs with one exit and
 // every wave has the same loads in flight.
-template <int MODE, bool SPLIT>
-__global__ __launch_bounds__(512, 1) void linear_pingpong_kernel(LinearArgs a, int parts) {
+template <int MODE>
+__global__ __launch_bounds__(512, 1) void linear_pingpong_kernel(LinearArgs a, TilePlan plan) {
   constexpr bool PR = MODE != MODE_DW, QR = MODE == MODE_FORWARD;
   using TL = TileOperand<PR, 128, 8, 0>;
   using TH = TileOperand<PR, 128, 8, 1>;
@@ -572,7 +601,7 @@ __global__ __launch_bounds__(512, 1) void linear_pingpong_kernel(LinearArgs a, i
   const int wp = wave >> 2, wq = wave & 3;
 
   LinearTile t;
-  if (!locate<MODE, 256, 256, SPLIT>(a, parts, lane, t)) return;
+  if (!locate<MODE, 256, 256>(a, plan, lane, t)) return;
   const int64_t wg = static_cast<int64_t>(t.g) * a.n * a.k;
   TL pl;
   TH ph;
@@ -714,7 +743,8 @@ __global__ __launch_bounds__(512, 1) void linear_pingpong_kernel(LinearArgs a, i
     sync();
   }
   uint8_t* const scratch = (wave < 4 ? sL0 : sL1) + (wave & 3) * 4096;
-  store_output<MODE, SPLIT>(a, acc, t.g, t.row0 + wp * 128, t.row_end, t.col0 + wq * 64, scratch, lane);
+  if (t.slot >= 0) store_part<256, 256>(a, acc, t.slot, wp * 128, wq * 64, scratch, lane);
+  else store_output<MODE>(a, acc, t.g, t.row0 + wp * 128, t.row_end, t.col0 + wq * 64, scratch, lane);
 }
 
 }  // namespace
