@@ -25,7 +25,8 @@
 namespace moegg {
 namespace {
 
-constexpr int kR = 64;                 // r per step
+constexpr int kR = 64;                 // r per step of the small tiles, and unit of their parts
+constexpr int kRingR = 32;             // r per step of the 256 x 256 tile
 
 // What a lane reads past the end of r: zeros.
 __device__ const uint32_t kZeros[4] = {0, 0, 0, 0};
@@ -39,11 +40,11 @@ __device__ __forceinline__ int line_swizzle(int r) {
   return (CH >= 16 ? (r & 3) << 2 : ((r >> 1) & 1) << 2) ^ (((r >> 3) & 1) << 1);
 }
 
-// One operand's tile of ROWS rows: staging and fragments.  With HALF 0 or 1
-// the 128 image rows are the ones of a 256-row tile whose bit 6 is HALF.
-template <bool ALONG_R, int ROWS, int NW, int HALF = -1>
+// One operand's tile of ROWS rows and R of r: staging and fragments.
+template <bool ALONG_R, int ROWS, int R, int NW>
 struct TileOperand {
-  static constexpr int BYTES = ROWS * kR * 2;
+  static constexpr int BYTES = ROWS * R * 2;
+  static constexpr int RC = R / 8;                 // chunks per row (along r)
   static constexpr int NI = BYTES / 1024 / NW;     // 1 KB loads per wave and step
   static constexpr int CH = ROWS / 8;              // chunks per line (rows contiguous)
   static_assert(NI * NW * 1024 == BYTES, "tile split over the waves");
@@ -53,15 +54,14 @@ struct TileOperand {
 
   // Image row (ALONG_R) or line of load j, and its source chunk.
   __device__ static __forceinline__ int image_row(int wave, int j, int lane) {
-    return ALONG_R ? (wave * NI + j) * 8 + (lane >> 3) : ((wave * NI + j) * 64 + lane) / CH;
+    return ((wave * NI + j) * 64 + lane) / (ALONG_R ? RC : CH);
   }
+  // Slot of chunk c of a row of r: rows of 128 (64) bytes fill the 64 banks in
+  // pairs (fours), and a read takes one chunk of 16 consecutive rows.
+  __device__ static __forceinline__ int row_swizzle(int row) { return R == 64 ? (row >> 1) & 7 : (row >> 2) & 3; }
   __device__ static __forceinline__ int image_chunk(int wave, int j, int lane) {
     const int r = image_row(wave, j, lane);
-    return ALONG_R ? (lane & 7) ^ ((r >> 1) & 7) : (lane % CH) ^ line_swizzle<CH>(r);
-  }
-  // Tile row of image row i.
-  __device__ static __forceinline__ int tile_row(int i) {
-    return HALF < 0 ? i : (i & 63) | (i & 64) << 1 | HALF << 6;
+    return ALONG_R ? (lane % RC) ^ row_swizzle(r) : (lane % CH) ^ line_swizzle<CH>(r);
   }
   // Tile of rows from i0 on (up to n), from r0 on; rows past the last one
   // repeat it (their results are not stored).
@@ -69,26 +69,26 @@ struct TileOperand {
                                        int lane) {
     if constexpr (ALONG_R) {
       base = reinterpret_cast<const uint8_t*>(src + i0 * ld + r0);
-      advance = kR * 2;
+      advance = R * 2;
       const int last = static_cast<int>(min(n - i0, int64_t{256})) - 1;
 #pragma unroll
       for (int j = 0; j < NI; ++j)
-        off[j] = static_cast<uint32_t>(min(tile_row(image_row(wave, j, lane)), last)) * static_cast<uint32_t>(ld * 2) +
+        off[j] = static_cast<uint32_t>(min(image_row(wave, j, lane), last)) * static_cast<uint32_t>(ld * 2) +
                  image_chunk(wave, j, lane) * 16;
     } else {
       base = reinterpret_cast<const uint8_t*>(src + r0 * ld + i0);
-      advance = kR * ld * 2;
+      advance = R * ld * 2;
       const int last = static_cast<int>(min(n - i0, int64_t{256})) - 8;
 #pragma unroll
       for (int j = 0; j < NI; ++j)
         off[j] = static_cast<uint32_t>(image_row(wave, j, lane)) * static_cast<uint32_t>(ld * 2) +
-                 min(tile_row(image_chunk(wave, j, lane) * 8), last) * 2;
+                 min(image_chunk(wave, j, lane) * 8, last) * 2;
     }
   }
   __device__ __forceinline__ void load(uint8_t* lds, int wave, int j) const {
     dma16(at(base, off[j]), lds + (wave * NI + j) * 1024);
   }
-  // The last step of a ragged r: `left` of its 64 r exist.
+  // The last step of a ragged r: `left` of its r exist.
   __device__ __forceinline__ void load_tail(uint8_t* lds, int wave, int lane, int j, int left) const {
     const int r = ALONG_R ? image_chunk(wave, j, lane) * 8 : image_row(wave, j, lane);
     const uint8_t* src = r < left ? at(base, off[j]) : reinterpret_cast<const uint8_t*>(kZeros);
@@ -101,13 +101,13 @@ struct TileOperand {
   // other way round (the swizzle does not move with the window).
   template <int B>
   struct Frags {
-    static constexpr int N = ALONG_R ? 4 : B;
+    static constexpr int N = ALONG_R ? R / 16 : B;
     uint32_t off[N];
     __device__ __forceinline__ void init(int tb, int lane) {
       if constexpr (ALONG_R) {
-        const int row = tb + (lane & 31), sw = (row >> 1) & 7;
+        const int row = tb + (lane & 31), sw = row_swizzle(row);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) off[k] = row * (kR * 2) + (((2 * k + (lane >> 5)) ^ sw) * 16);
+        for (int k = 0; k < N; ++k) off[k] = row * (R * 2) + (((2 * k + (lane >> 5)) ^ sw) * 16);
       } else {
         const int q = lane >> 4, line = (q >> 1) * 8 + ((lane >> 2) & 3);
 #pragma unroll
@@ -125,7 +125,7 @@ struct TileOperand {
     // Block b, window k: lane l holds row tb + 32 b + l % 32, r 16 k + 8 (l / 32) + [0, 8).
     __device__ __forceinline__ v4u read(const uint8_t* lds, int b, int k) const {
       if constexpr (ALONG_R) {
-        return *reinterpret_cast<const v4u*>(lds + off[k] + b * (32 * kR * 2));
+        return *reinterpret_cast<const v4u*>(lds + off[k] + b * (32 * R * 2));
       } else {
         typedef short v4s __attribute__((ext_vector_type(4)));
         typedef __attribute__((address_space(3))) v4s lds4;
@@ -479,8 +479,8 @@ __device__ __forceinline__ void store_output(const LinearArgs& a, v16f (&acc)[TM
 template <int MODE, int BP, int BQ, int WP, int WQ>
 __global__ __launch_bounds__(64 * WP * WQ, 2) void linear_tile_kernel(LinearArgs a, TilePlan plan) {
   constexpr int NW = WP * WQ, TM = BP / WP / 32, TN = BQ / WQ / 32;
-  using TP = TileOperand<MODE != MODE_DW, BP, NW>;
-  using TQ = TileOperand<MODE == MODE_FORWARD, BQ, NW>;
+  using TP = TileOperand<MODE != MODE_DW, BP, kR, NW>;
+  using TQ = TileOperand<MODE == MODE_FORWARD, BQ, kR, NW>;
   static_assert(TN == 2, "a wave's columns are one pair of 32-column blocks");
   // one array per stage and operand: the compiler then sees that a stage's
   // loads do not touch what is being read
@@ -574,28 +574,24 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void linear_tile_kernel(LinearArgs
   else store_output<MODE>(a, acc, t.g, t.row0 + wp * (TM * 32), t.row_end, t.col0 + wq * 64, scratch, lane);
 }
 
-// The 256 x 256 tile on the ping-pong schedule of the grouped product (8
-// waves, 2 along p x 4 along q, each 128 x 64).  A step is four clusters: M0
-// reads the fragments of Q and of the wave's first two P blocks, C0 runs their
-// MFMAs, M1 reads the other two P blocks, C1 runs theirs.  The two waves of a
-// SIMD (w and w + 4) run one cluster apart, so one issues MFMAs while the
-// other reads LDS.  P lies in two images (its rows with bit 6 clear and set),
-// so that a stage comes in two sets: Q and the low half of P, free again after
-// M0, and the high half of P, free after M1.  Stage s + 2's first set is
-// issued in M1(s) and C1(s), its second in C0(s + 1); a set has about four
-// clusters to land and is waited for one cluster and barrier before its use.
-// Steps past the last read zeros, so the steps go in pairs with one exit and
+// The 256 x 256 tile: 8 waves, 2 along p x 4 along q, each 128 x 64, on the
+// ping-pong schedule of the grouped product.  A step of 32 r is two clusters:
+// M reads the step's 12 fragments from LDS, C runs its 16 MFMAs.  The two
+// waves of a SIMD (w and w + 4) run one cluster apart, so one issues MFMAs
+// while the other reads.  Four stages of 32 KB ring through LDS: stage s + 3 is
+// issued during C(s), into the place of stage s - 1, which both groups have
+// read by then, and is waited for at the end of M(s + 2), four clusters later.
+// Steps past the last read zeros, so the steps go in fours with one exit and
 // every wave has the same loads in flight.
 template <int MODE>
 __global__ __launch_bounds__(512, 1) void linear_pingpong_kernel(LinearArgs a, TilePlan plan) {
-  constexpr bool PR = MODE != MODE_DW, QR = MODE == MODE_FORWARD;
-  using TL = TileOperand<PR, 128, 8, 0>;
-  using TH = TileOperand<PR, 128, 8, 1>;
-  using TQ = TileOperand<QR, 256, 8>;
-  constexpr int N_EA = TL::NI, N_EB = TQ::NI, N_EARLY = N_EA + N_EB, N_LATE = TH::NI;
-  static_assert(N_EA == 2 && N_EB == 4 && N_LATE == 2, "loads per wave and step");
-  __shared__ __attribute__((aligned(16))) uint8_t sL0[TL::BYTES], sL1[TL::BYTES], sH0[TH::BYTES], sH1[TH::BYTES];
-  __shared__ __attribute__((aligned(16))) uint8_t sQ0[TQ::BYTES], sQ1[TQ::BYTES];
+  constexpr int R = kRingR;
+  using TP = TileOperand<MODE != MODE_DW, 256, R, 8>;
+  using TQ = TileOperand<MODE == MODE_FORWARD, 256, R, 8>;
+  constexpr int N = TP::NI + TQ::NI;
+  static_assert(TP::NI == 2 && TQ::NI == 2, "loads per wave and stage");
+  __shared__ __attribute__((aligned(16))) uint8_t sP0[TP::BYTES], sP1[TP::BYTES], sP2[TP::BYTES], sP3[TP::BYTES];
+  __shared__ __attribute__((aligned(16))) uint8_t sQ0[TQ::BYTES], sQ1[TQ::BYTES], sQ2[TQ::BYTES], sQ3[TQ::BYTES];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wp = wave >> 2, wq = wave & 3;
@@ -603,19 +599,14 @@ __global__ __launch_bounds__(512, 1) void linear_pingpong_kernel(LinearArgs a, T
   LinearTile t;
   if (!locate<MODE, 256, 256>(a, plan, lane, t)) return;
   const int64_t wg = static_cast<int64_t>(t.g) * a.n * a.k;
-  TL pl;
-  TH ph;
+  TP p;
   TQ q;
-  {
-    const uint16_t* const src = MODE == MODE_FORWARD ? a.x : a.dz;
-    const int64_t ld = MODE == MODE_FORWARD ? a.k : a.n, n = MODE == MODE_DW ? a.n : t.row_end;
-    pl.init(src, ld, t.row0, n, t.r0, wave, lane);
-    ph.init(src, ld, t.row0, n, t.r0, wave, lane);
-    q.init(MODE == MODE_DW ? a.x : a.w + wg, a.k, t.col0, MODE == MODE_FORWARD ? a.n : a.k, t.r0, wave, lane);
-  }
-  typename TL::template Frags<2> ap;            // both halves of P lie alike
+  p.init(MODE == MODE_FORWARD ? a.x : a.dz, MODE == MODE_FORWARD ? a.k : a.n, t.row0, MODE == MODE_DW ? a.n : t.row_end, t.r0,
+         wave, lane);
+  q.init(MODE == MODE_DW ? a.x : a.w + wg, a.k, t.col0, MODE == MODE_FORWARD ? a.n : a.k, t.r0, wave, lane);
+  typename TP::template Frags<4> ap;
   typename TQ::template Frags<2> aq;
-  ap.init(wp * 64, lane);
+  ap.init(wp * 128, lane);
   aq.init(wq * 64, lane);
   ap.keep();
   aq.keep();
@@ -626,123 +617,90 @@ __global__ __launch_bounds__(512, 1) void linear_pingpong_kernel(LinearArgs a, T
     for (int j = 0; j < 2; ++j) acc[i][j] = v16f{};
 
   const int span = static_cast<int>(t.r1 - t.r0);
-  const int full = span / kR;
+  const int full = span / R;
   struct Stage {
-    uint8_t *l, *h, *q;
+    uint8_t *p, *q;
   };
-  const Stage st0{sL0, sH0, sQ0}, st1{sL1, sH1, sQ1};
-  // loads of stage s (in order per operand: the bases run along); ANY: a
-  // stage that is ragged or past the end
-  auto issue_l = [&](auto any, int s, const Stage& d) __attribute__((always_inline)) {
-#pragma unroll
-    for (int j = 0; j < N_EA; ++j)
-      if constexpr (decltype(any)::value) pl.load_tail(d.l, wave, lane, j, span - s * kR);
-      else pl.load(d.l, wave, j);
-    pl.base += pl.advance;
-  };
-  auto issue_q = [&](auto any, int s, const Stage& d, int j) __attribute__((always_inline)) {
-    if constexpr (decltype(any)::value) q.load_tail(d.q, wave, lane, j, span - s * kR);
-    else q.load(d.q, wave, j);
-    if (j == N_EB - 1) q.base += q.advance;
-  };
-  auto issue_h = [&](auto any, int s, const Stage& d, int j) __attribute__((always_inline)) {
-    if constexpr (decltype(any)::value) ph.load_tail(d.h, wave, lane, j, span - s * kR);
-    else ph.load(d.h, wave, j);
-    if (j == N_LATE - 1) ph.base += ph.advance;
+  const Stage st[4] = {{sP0, sQ0}, {sP1, sQ1}, {sP2, sQ2}, {sP3, sQ3}};
+  // load j (0..3) of stage s (the bases run along); ANY: a stage that is
+  // ragged or past the end
+  auto issue = [&](auto any, int s, const Stage& d, int j) __attribute__((always_inline)) {
+    if (j < TP::NI) {
+      if constexpr (decltype(any)::value) p.load_tail(d.p, wave, lane, j, span - s * R);
+      else p.load(d.p, wave, j);
+      if (j == TP::NI - 1) p.base += p.advance;
+    } else {
+      if constexpr (decltype(any)::value) q.load_tail(d.q, wave, lane, j - TP::NI, span - s * R);
+      else q.load(d.q, wave, j - TP::NI);
+      if (j == N - 1) q.base += q.advance;
+    }
   };
   auto sync = []() __attribute__((always_inline)) {
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
   };
-  typedef v4u Window[4];      // one 32-row block, the step's four windows
-  auto settle = [](Window& f) __attribute__((always_inline)) {
+  auto step = [&](auto any, int s, const Stage& now, const Stage& next3) __attribute__((always_inline)) {
+    v4u fq[2][2], fp[4][2];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) asm volatile("" : "+v"(f[k]));
-  };
-  auto pin = [&]() __attribute__((always_inline)) {
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) fq[j][k] = aq.read(now.q, j, k);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) fp[i][k] = ap.read(now.p, i, k);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) asm volatile("" : "+v"(fq[j][k]));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(fp[i][k]));
+    }
+    wait_vmcnt<N>();                             // stage s + 1
+    sync();
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, fq[j][k]),
+                                                              __builtin_bit_cast(v8bf, fp[i][k]), acc[i][j], 0, 0, 0);
+          const int m = k * 8 + i * 2 + j;
+          if (m % 4 == 0) issue(any, s + 3, next3, m / 4);
+        }
+    // the MFMAs stay in their cluster
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) asm volatile("" : "+v"(acc[i][j]));
-  };
-  auto mma = [&](int i0, const Window* fp, const Window* fq, auto&& hook) __attribute__((always_inline)) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          acc[i0 + i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, fq[j][k]),
-                                                                   __builtin_bit_cast(v8bf, fp[i][k]), acc[i0 + i][j], 0, 0, 0);
-          hook(k * 4 + i * 2 + j);
-        }
-  };
-  // step s out of `st`; `other`: the other buffer
-  auto step = [&](auto any, int s, const Stage& st, const Stage& other) __attribute__((always_inline)) {
-    Window fq[2], fp[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) fq[j][k] = aq.read(st.q, j, k);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) fp[i][k] = ap.read(st.l, i, k);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) settle(fq[j]);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) settle(fp[i]);
-    wait_vmcnt<N_EARLY>();                       // this step's second set
-    sync();
-    mma(0, fp, fq, [&](int m) __attribute__((always_inline)) {
-      if (m % 8 == 0) issue_h(any, s + 1, other, m / 8);
-    });
-    pin();
-    sync();
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) fp[i][k] = ap.read(st.h, i, k);
-    issue_l(any, s + 2, st);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) settle(fp[i]);
-    wait_vmcnt<N_LATE + N_EA>();                 // the next step's first set
-    sync();
-    mma(2, fp, fq, [&](int m) __attribute__((always_inline)) {
-      if (m % 4 == 0) issue_q(any, s + 2, st, m / 4);
-    });
-    pin();
     sync();
   };
   if (span > 0) {
     const std::true_type any{};
     const std::false_type plain{};
-    issue_l(any, 0, st0);
 #pragma unroll
-    for (int j = 0; j < N_EB; ++j) issue_q(any, 0, st0, j);
+    for (int s = 0; s < 3; ++s)
 #pragma unroll
-    for (int j = 0; j < N_LATE; ++j) issue_h(any, 0, st0, j);
-    issue_l(any, 1, st1);
-#pragma unroll
-    for (int j = 0; j < N_EB; ++j) issue_q(any, 1, st1, j);
-    wait_vmcnt<N_LATE + N_EARLY>();
+      for (int j = 0; j < N; ++j) issue(any, s, st[s], j);
+    wait_vmcnt<2 * N>();
     sync();
     if (wp) sync();
     int s = 0;
-    for (; s + 3 < full; s += 2) {
-      step(plain, s, st0, st1);
-      step(plain, s + 1, st1, st0);
+    for (; s + 6 < full; s += 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) step(plain, s + i, st[i], st[(i + 3) & 3]);
     }
-    for (; s * kR < span; s += 2) {
-      step(any, s, st0, st1);
-      step(any, s + 1, st1, st0);
+    for (; s * R < span; s += 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) step(any, s + i, st[i], st[(i + 3) & 3]);
     }
     wait_vmcnt<0>();
     if (!wp) sync();
     sync();
   }
-  uint8_t* const scratch = (wave < 4 ? sL0 : sL1) + (wave & 3) * 4096;
+  uint8_t* const scratch = (wave < 4 ? sP0 : sP1) + (wave & 3) * 4096;
   if (t.slot >= 0) store_part<256, 256>(a, acc, t.slot, wp * 128, wq * 64, scratch, lane);
   else store_output<MODE>(a, acc, t.g, t.row0 + wp * 128, t.row_end, t.col0 + wq * 64, scratch, lane);
 }
