@@ -17,69 +17,79 @@ namespace {
 // few rows: the weights are read once and nothing else matters
 // ---------------------------------------------------------------------------
 //
-// One workgroup computes 16 columns n for up to 16 rows of a group at a time.
-// Its 8 waves share r: each streams its part of the 16 weight rows from
-// global memory into registers (16 bytes a lane, 8 loads in flight) and
-// multiplies it with the rows of x by 16 x 16 x 32 MFMAs; the 8 partial sums
-// meet in LDS.
-constexpr int kFewThreads = 512;
+// One workgroup computes 16 NT columns n for up to 16 rows of a group at a
+// time.  Its NW waves share r: each streams its part of the weight rows from
+// global memory into registers (16 bytes a lane, U steps of 32 r in flight)
+// and multiplies it with the rows of x by 16 x 16 x 32 MFMAs; the partial sums
+// meet in LDS.  The rows of x come from L2, as many bytes a workgroup as one
+// of its NT weight tiles where there are 16 of them.
 constexpr int kFewRows = 16;
 
-__global__ __launch_bounds__(kFewThreads, 2) void linear_few_rows_kernel(LinearArgs a) {
-  constexpr int NW = kFewThreads / 64, U = 8;
-  __shared__ float part[NW][16][17];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+template <int NT, int NW, int U>
+__global__ __launch_bounds__(64 * NW) void linear_few_rows_kernel(LinearArgs a) {
+  typedef float v4f4 __attribute__((ext_vector_type(4)));
+  __shared__ float part[NW][NT][16][17];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, q = lane >> 4;
   const int g = blockIdx.y;
   int64_t begin, end;
   group_rows(a, g, begin, end);
   const bool pair = a.act == LIN_SWIGLU;
-  // weight row of index i: SwiGLU takes 8 linear columns and their 8 gates
-  const int n0 = blockIdx.x * 16;
-  auto column = [&](int i) {
-    if (!pair) return n0 + i;
-    const int j = blockIdx.x * 8 + (i & 7);                 // output column
+  // column of index i of tile t: SwiGLU tiles are 8 linear columns and their 8 gates
+  auto column = [&](int t, int i) {
+    const int tile = blockIdx.x * NT + t;
+    if (!pair) return tile * 16 + i;
+    const int j = tile * 8 + (i & 7);                       // output column
     return (j >> 5) * 64 + (j & 31) + (i & 8) * 4;
   };
-  const int n_w = min(column(l16), a.n - 1);
-  const uint16_t* const wrow = a.w + (static_cast<int64_t>(g) * a.n + n_w) * a.k;
-  const int steps = (a.k + 31) / 32;
+  const uint16_t* wrow[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+    wrow[t] = a.w + (static_cast<int64_t>(g) * a.n + min(column(t, l16), a.n - 1)) * a.k + q * 8;
+  const int steps = (a.k + 31) / 32, whole = a.k / 32;
   const int s0 = steps * wave / NW, s1 = steps * (wave + 1) / NW;
   const int n_out = pair ? a.n / 2 : a.n;
-  typedef float v4f4 __attribute__((ext_vector_type(4)));
   for (int64_t m0 = begin; m0 < end; m0 += kFewRows) {
     const int rows = static_cast<int>(min(end - m0, int64_t{kFewRows}));
-    const uint16_t* const xrow = a.x + (m0 + min(l16, rows - 1)) * a.k;
-    v4f4 acc{};
+    const uint16_t* const xrow = a.x + (m0 + min(l16, rows - 1)) * a.k + q * 8;
+    v4f4 acc[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[t] = v4f4{};
     for (int s = s0; s < s1; s += U) {
-      v4u vw[U], vx[U];
+      v4u vw[NT][U], vx[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int r = (s + u) * 32 + q * 8;
-        vw[u] = v4u{};
         vx[u] = v4u{};
-        if (s + u < s1 && r < a.k) {
-          vw[u] = *reinterpret_cast<const v4u*>(wrow + r);
-          vx[u] = *reinterpret_cast<const v4u*>(xrow + r);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) vw[t][u] = v4u{};
+        if (s + u < s1 && (s + u < whole || (s + u) * 32 + q * 8 < a.k)) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            vw[t][u] = *reinterpret_cast<const v4u*>(wrow[t] + (s + u) * 32);
+          vx[u] = *reinterpret_cast<const v4u*>(xrow + (s + u) * 32);
         }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, vw[u]), __builtin_bit_cast(v8bf, vx[u]), acc,
-                                                      0, 0, 0);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, vw[t][u]), __builtin_bit_cast(v8bf, vx[u]),
+                                                           acc[t], 0, 0, 0);
     }
     // lane: row l16, weight rows 4 q + [0, 4)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) part[wave][l16][4 * q + e] = acc[e];
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) part[wave][t][l16][4 * q + e] = acc[t][e];
     __syncthreads();
-    if (threadIdx.x < 256) {
-      const int i = threadIdx.x & 15, row = threadIdx.x >> 4;
-      const int n = column(i);
+    for (int at = threadIdx.x; at < NT * 256; at += 64 * NW) {
+      const int i = at & 15, row = (at >> 4) & 15, t = at >> 8;
+      const int n = column(t, i);
       if (row < rows && n < a.n) {
         const int64_t m = m0 + row;
         float z = 0.0f;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) z += part[w][row][i];
+        for (int w = 0; w < NW; ++w) z += part[w][t][row][i];
         if (a.bias) z += a.bias[static_cast<int64_t>(g) * a.n + n];
         if (a.c) a.c[m * a.n + n] = static_cast<uint16_t>(bf16x2(z, 0.0f));
         float y = z;
@@ -91,11 +101,11 @@ __global__ __launch_bounds__(kFewThreads, 2) void linear_few_rows_kernel(LinearA
           store = i < 8;
           if (store) {
 #pragma unroll
-            for (int w = 0; w < NW; ++w) gate += part[w][row][i + 8];
+            for (int w = 0; w < NW; ++w) gate += part[w][t][row][i + 8];
             if (a.bias) gate += a.bias[static_cast<int64_t>(g) * a.n + ng];
           }
           y = z * (gate * sigmoid_f(gate));
-          ycol = blockIdx.x * 8 + i;
+          ycol = (blockIdx.x * NT + t) * 8 + i;
         } else if (a.act == LIN_GELU) {
           y = gelu_f(z);
         } else if (a.act == LIN_SRELU) {
@@ -200,83 +210,110 @@ __device__ __forceinline__ v4u pack8(const float* f) {
   return v4u{bf16x2(f[0], f[1]), bf16x2(f[2], f[3]), bf16x2(f[4], f[5]), bf16x2(f[6], f[7])};
 }
 
-// 32 threads run along 256 columns of dy, 8 rows at a time.
+// One row's 8 columns of dy (and of c, or of both halves of a pair) -> dz.
+template <int ACT>
+__device__ __forceinline__ void dz_of(const float* d, v4u c0, v4u c1, float* v, float* w) {
+  if constexpr (ACT == LIN_NONE) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = d[i];
+  } else if constexpr (ACT == LIN_SWIGLU) {
+    float x[8], q[8];
+    unpack8(c0, x);
+    unpack8(c1, q);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float s = sigmoid_f(q[i]);
+      v[i] = d[i] * (q[i] * s);
+      w[i] = d[i] * (x[i] * s) * (1.0f + q[i] * (1.0f - s));
+    }
+  } else {
+    float z[8];
+    unpack8(c0, z);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (ACT == LIN_SRELU) {
+        v[i] = d[i] * (2.0f * fmaxf(z[i], 0.0f));
+      } else {
+        // past 30 s is 0 or 1: keeps 0 times z^3 from becoming NaN
+        const float c = fminf(fmaxf(z[i], -30.0f), 30.0f);
+        const float s = sigmoid_f(2.0f * kGeluC * c * (1.0f + kGeluA * c * c));
+        v[i] = d[i] * (s + c * s * (1.0f - s) * (2.0f * kGeluC) * (1.0f + 3.0f * kGeluA * c * c));
+      }
+    }
+  }
+}
+
+// 32 threads run along 256 columns of dy, 8 rows at a time; four of a
+// thread's rows are in flight at once.
+template <int ACT>
 __global__ __launch_bounds__(256) void linear_dz_kernel(LinearArgs a, uint16_t* dz, float* sums) {
-  __shared__ float red[8][32][17];
+  constexpr bool PAIR = ACT == LIN_SWIGLU;
+  constexpr int S = PAIR ? 16 : 8, U = 4;
+  __shared__ float red[8][32][S + 1];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, lane = threadIdx.x & 63;
   int g;
   int64_t row0, end;
   if (!find_row_tile<kDzRows>(a, blockIdx.x, lane, g, row0, end)) return;
-  const bool pair = a.act == LIN_SWIGLU;
-  const int n_out = pair ? a.n / 2 : a.n;
+  const int n_out = PAIR ? a.n / 2 : a.n;
   const int col = (blockIdx.y * 32 + tx) * 8;                  // of dy
-  const int n = pair ? (col >> 5) * 64 + (col & 31) : col;     // of dz (and n + 32 of a pair)
-  float s[16];
+  const int n = PAIR ? (col >> 5) * 64 + (col & 31) : col;     // of dz (and n + 32 of a pair)
+  float s[S];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) s[i] = 0.0f;
+  for (int i = 0; i < S; ++i) s[i] = 0.0f;
+  const int rows = static_cast<int>(min(end - row0, int64_t{kDzRows}));
   if (col < n_out) {
-    for (int64_t m = row0 + ty; m < min(row0 + kDzRows, end); m += 8) {
-      float d[8], v[8];
-      unpack8(*reinterpret_cast<const v4u*>(a.dy + m * n_out + col), d);
-      if (pair) {
-        float x[8], q[8], w[8];
-        unpack8(*reinterpret_cast<const v4u*>(a.c + m * a.n + n), x);
-        unpack8(*reinterpret_cast<const v4u*>(a.c + m * a.n + n + 32), q);
+    for (int r = ty; r < rows; r += 8 * U) {
+      v4u d[U], c0[U], c1[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t m = row0 + min(r + 8 * u, rows - 1);     // (rows past the end: read, not used)
+        d[u] = *reinterpret_cast<const v4u*>(a.dy + m * n_out + col);
+        c0[u] = v4u{};
+        c1[u] = v4u{};
+        if constexpr (ACT != LIN_NONE) c0[u] = *reinterpret_cast<const v4u*>(a.c + m * a.n + n);
+        if constexpr (PAIR) c1[u] = *reinterpret_cast<const v4u*>(a.c + m * a.n + n + 32);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (r + 8 * u >= rows) break;
+        const int64_t m = row0 + r + 8 * u;
+        float f[8], v[8], w[8];
+        unpack8(d[u], f);
+        dz_of<ACT>(f, c0[u], c1[u], v, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float sg = sigmoid_f(q[i]);
-          v[i] = d[i] * (q[i] * sg);
-          w[i] = d[i] * (x[i] * sg) * (1.0f + q[i] * (1.0f - sg));
           s[i] += v[i];
-          s[8 + i] += w[i];
+          if constexpr (PAIR) s[8 + i] += w[i];
         }
-        if (dz) *reinterpret_cast<v4u*>(dz + m * a.n + n + 32) = pack8(w);
-      } else {
-        if (a.act != LIN_NONE) {
-          float z[8];
-          unpack8(*reinterpret_cast<const v4u*>(a.c + m * a.n + n), z);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (a.act == LIN_SRELU) {
-              v[i] = d[i] * (2.0f * fmaxf(z[i], 0.0f));
-            } else {
-              // past 30 s is 0 or 1: keeps 0 times z^3 from becoming NaN
-              const float c = fminf(fmaxf(z[i], -30.0f), 30.0f);
-              const float sg = sigmoid_f(2.0f * kGeluC * c * (1.0f + kGeluA * c * c));
-              v[i] = d[i] * (sg + c * sg * (1.0f - sg) * (2.0f * kGeluC) * (1.0f + 3.0f * kGeluA * c * c));
-            }
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = d[i];
+        if (dz) {
+          *reinterpret_cast<v4u*>(dz + m * a.n + n) = pack8(v);
+          if constexpr (PAIR) *reinterpret_cast<v4u*>(dz + m * a.n + n + 32) = pack8(w);
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] += v[i];
       }
-      if (dz) *reinterpret_cast<v4u*>(dz + m * a.n + n) = pack8(v);
     }
   }
   if (!sums) return;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) red[ty][tx][i] = s[i];
+  for (int i = 0; i < S; ++i) red[ty][tx][i] = s[i];
   __syncthreads();
-  // 32 x 16 sums, two a thread
+  // 32 x S sums, S / 8 a thread
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < S / 8; ++h) {
     const int i = (threadIdx.x & 7) + 8 * h, t = threadIdx.x >> 3;
     const int c = (blockIdx.y * 32 + t) * 8;
-    if (c >= n_out || (h && !pair)) continue;
+    if (c >= n_out) continue;
     float v = 0.0f;
 #pragma unroll
     for (int y = 0; y < 8; ++y) v += red[y][t][i];
-    const int at = pair ? (c >> 5) * 64 + (c & 31) + (i & 7) + 32 * h : c + (i & 7);
+    const int at = PAIR ? (c >> 5) * 64 + (c & 31) + (i & 7) + 32 * h : c + i;
     sums[static_cast<int64_t>(blockIdx.x) * a.n + at] = v;
   }
 }
 
-__global__ __launch_bounds__(256) void linear_db_kernel(LinearArgs a, const float* sums) {
-  __shared__ float red[4][64];
-  const int lane = threadIdx.x & 63, q = threadIdx.x >> 6, g = blockIdx.y;
+// db of 32 columns of a group: 16 threads a column share the row tiles.
+__global__ __launch_bounds__(512) void linear_db_kernel(LinearArgs a, const float* sums) {
+  __shared__ float red[16][33];
+  const int lane = threadIdx.x & 63, x = threadIdx.x & 31, q = threadIdx.x >> 5, g = blockIdx.y;
   // tiles of the groups before g, and of g
   int before = 0, mine = 0;
   if (a.offsets) {
@@ -294,13 +331,20 @@ __global__ __launch_bounds__(256) void linear_db_kernel(LinearArgs a, const floa
   } else {
     mine = static_cast<int>((a.m + kDzRows - 1) / kDzRows);
   }
-  const int n = blockIdx.x * 64 + lane;
+  const int n = blockIdx.x * 32 + x;
   float s = 0.0f;
-  if (n < a.n)
-    for (int t = q; t < mine; t += 4) s += sums[static_cast<int64_t>(before + t) * a.n + n];
-  red[q][lane] = s;
+  if (n < a.n) {
+#pragma unroll 4
+    for (int t = q; t < mine; t += 16) s += sums[static_cast<int64_t>(before + t) * a.n + n];
+  }
+  red[q][x] = s;
   __syncthreads();
-  if (q == 0 && n < a.n) a.db[static_cast<int64_t>(g) * a.n + n] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+  if (q == 0 && n < a.n) {
+    float v = 0.0f;
+#pragma unroll
+    for (int y = 0; y < 16; ++y) v += red[y][x];
+    a.db[static_cast<int64_t>(g) * a.n + n] = v;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -335,10 +379,11 @@ struct Plan {
 // cheapest by rounds of workgroups, where a last round that leaves most of the
 // chip empty (or the only one) may be split, against the bytes of its parts,
 // written and read at about 4 TB/s, and a join's launch.
-// `tiles(s)`: tiles of shape s at most; `r`: length of the sum; `known`: the
-// tiles are these, and may be split.
-template <typename F>
-Plan choose(F&& tiles, int64_t cols, int64_t r, bool known) {
+// `tiles(s)`: tiles of shape s at most, of which `spare(s)` may not be there
+// (half of them are taken to be); `r`: length of the sum; `known`: the tiles
+// are these, and may be split.
+template <typename F, typename G>
+Plan choose(F&& tiles, G&& spare, int64_t cols, int64_t r, bool known) {
   Plan best{};
   double least = 0.0;
   const int64_t steps = div_up(r > 0 ? r : 1, kR);
@@ -360,7 +405,7 @@ Plan choose(F&& tiles, int64_t cols, int64_t r, bool known) {
       best.workgroups = first + (total - first) * parts;
       best.partial_bytes = parts > 1 ? (total - first) * parts * c.bp * c.bq * 4 : 0;
     };
-    take(rounds(total, steps), total, 1);
+    take(rounds(total - spare(c) / 2, steps), total, 1);
     if (!known) continue;
     for (int64_t first : {int64_t{0}, total / c.slots * c.slots}) {
       if (first == total || (first == 0 && total > 2 * c.slots)) continue;
@@ -377,13 +422,13 @@ Plan choose(F&& tiles, int64_t cols, int64_t r, bool known) {
 // Split only without offsets, where the host knows the tiles.  (The workspace
 // is sized without knowing the offsets, so never too small.)
 Plan plan_rows(const LinearArgs& a, int64_t cols, int64_t r) {
-  return choose([&](const ShapeCost& c) { return row_tiles(a, c.bp) * div_up(cols, c.bq); }, cols, r,
-                a.groups == 1 && !a.offsets);
+  return choose([&](const ShapeCost& c) { return row_tiles(a, c.bp) * div_up(cols, c.bq); },
+                [&](const ShapeCost& c) { return (a.groups - 1) * div_up(cols, c.bq); }, cols, r, a.groups == 1 && !a.offsets);
 }
 Plan plan_dw(const LinearArgs& a) {
   // a group's share of the rows; groups whose rows the host does not know are not split
-  return choose([&](const ShapeCost& c) { return a.groups * div_up(a.n, c.bp) * div_up(a.k, c.bq); }, a.k,
-                div_up(a.m, a.groups), a.groups == 1);
+  return choose([&](const ShapeCost& c) { return a.groups * div_up(a.n, c.bp) * div_up(a.k, c.bq); },
+                [](const ShapeCost&) { return int64_t{0}; }, a.k, div_up(a.m, a.groups), a.groups == 1);
 }
 bool few_rows(const LinearArgs& a) { return a.m <= 16 * static_cast<int64_t>(a.groups); }
 
@@ -453,8 +498,19 @@ hipError_t launch_linear(const LinearArgs& args, hipStream_t s) {
   LinearArgs a = args;
   if (a.m == 0) return hipSuccess;
   if (few_rows(a)) {
-    hipLaunchKernelGGL(linear_few_rows_kernel, dim3(static_cast<unsigned>(div_up(a.n, 16)), static_cast<unsigned>(a.groups)),
-                       dim3(kFewThreads), 0, s, a);
+    // Many workgroups (groups): small ones of 4 waves and 32 columns, four to a
+    // compute unit; few: 8 waves share a narrow tile, which reads fewer rows of
+    // weights but deeper.  Measured, 64 groups of 2048 x 1408, 96 rows: 87 us
+    // with 8 waves, 76 (4.8 TB/s of weights) with 4; one group of 8192 x 8192,
+    // one row: 26 us (5.1 TB/s) with 8 waves, 34 with 4; 2816 x 2048 from the
+    // last-level cache: 5.2 and 7.7 us.
+    const int64_t tiles = div_up(a.n, 16);
+    if (tiles * a.groups >= 2048)
+      hipLaunchKernelGGL((linear_few_rows_kernel<2, 4, 4>), dim3(static_cast<unsigned>(div_up(tiles, 2)), static_cast<unsigned>(a.groups)),
+                         dim3(256), 0, s, a);
+    else
+      hipLaunchKernelGGL((linear_few_rows_kernel<1, 8, 8>), dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(a.groups)), dim3(512),
+                         0, s, a);
     return hipGetLastError();
   }
   a.partial = static_cast<float*>(a.workspace);
@@ -473,12 +529,17 @@ hipError_t launch_linear_backward(const LinearArgs& args, hipStream_t s) {
   hipError_t e = hipSuccess;
   if ((make_dz || a.db) && a.m) {
     const int n_out = a.act == LIN_SWIGLU ? a.n / 2 : a.n;
-    hipLaunchKernelGGL(linear_dz_kernel, dim3(static_cast<unsigned>(row_tiles(a, kDzRows)), static_cast<unsigned>(div_up(n_out, 256))),
-                       dim3(256), 0, s, a, dz, sums);
+    const dim3 grid(static_cast<unsigned>(row_tiles(a, kDzRows)), static_cast<unsigned>(div_up(n_out, 256)));
+    switch (a.act) {
+      case LIN_SWIGLU: hipLaunchKernelGGL((linear_dz_kernel<LIN_SWIGLU>), grid, dim3(256), 0, s, a, dz, sums); break;
+      case LIN_SRELU: hipLaunchKernelGGL((linear_dz_kernel<LIN_SRELU>), grid, dim3(256), 0, s, a, dz, sums); break;
+      case LIN_GELU: hipLaunchKernelGGL((linear_dz_kernel<LIN_GELU>), grid, dim3(256), 0, s, a, dz, sums); break;
+      default: hipLaunchKernelGGL((linear_dz_kernel<LIN_NONE>), grid, dim3(256), 0, s, a, dz, sums); break;
+    }
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (a.db) {
-    hipLaunchKernelGGL(linear_db_kernel, dim3(static_cast<unsigned>(div_up(a.n, 64)), static_cast<unsigned>(a.groups)), dim3(256), 0,
+    hipLaunchKernelGGL(linear_db_kernel, dim3(static_cast<unsigned>(div_up(a.n, 32)), static_cast<unsigned>(a.groups)), dim3(512), 0,
                        s, a, sums);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }

@@ -241,10 +241,12 @@ def sort_tokens(ids, num_experts: int, *, weights=None, m_aligned: int = 128, st
     lib, rows = mg._load(), p.rows
     need = lib.moegg_sort_workspace(p)
     with _on(dev, stream) as s:
-        offsets = ids.new_empty(num_experts)
-        row_of = ids.new_empty(shape)
-        slot_of = ids.new_empty(rows)
-        prob = None if w is None else ids.new_empty(rows, dtype=torch.float32)
+        # one allocation for the plan's tensors
+        sizes = (num_experts, shape[0] * shape[1], rows, rows) if w is not None else \
+            (num_experts, shape[0] * shape[1], rows)
+        offsets, row_of, slot_of, *prob = ids.new_empty(sum(sizes)).split(sizes)
+        row_of = row_of.view(shape)
+        prob = prob[0].view(torch.float32) if prob else None
         ws = ids.new_empty(need, dtype=torch.uint8) if need else None
         _done(lib.moegg_sort(p, ids.data_ptr(), w, offsets.data_ptr(), row_of.data_ptr(), slot_of.data_ptr(),
                              None if prob is None else prob.data_ptr(), None if ws is None else ws.data_ptr(), need, s))
