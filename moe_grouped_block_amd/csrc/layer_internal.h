@@ -121,7 +121,8 @@ struct LinearArgs {
   void* workspace;
   int64_t workspace_bytes;
   const uint16_t* dz;       // (M, N) bf16: dy, or in the workspace    [set by the launchers]
-  float* partial;           // fp32 sums of the parts of r, in the workspace
+  float* dx_partial;        // fp32 sums of the parts of r, in the workspace: of y or dx,
+  float* dw_partial;        // and of dw
   int64_t m;
   int32_t n;
   int32_t k;

@@ -278,6 +278,10 @@ struct LinearTile {
 template <int MODE>
 __device__ __forceinline__ int out_columns(const LinearArgs& a) { return MODE == MODE_FORWARD ? a.n : a.k; }
 
+// Where the parts of a product go.
+template <int MODE>
+__device__ __forceinline__ float* partials(const LinearArgs& a) { return MODE == MODE_DW ? a.dw_partial : a.dx_partial; }
+
 // Group, rows and columns of tile i.
 template <int MODE, int BP, int BQ>
 __device__ __forceinline__ bool place(const LinearArgs& a, int i, int row_tiles, int lane, LinearTile& t) {
@@ -297,8 +301,7 @@ __device__ __forceinline__ bool place(const LinearArgs& a, int i, int row_tiles,
 }
 
 template <int MODE, int BP, int BQ>
-__device__ __forceinline__ bool locate(const LinearArgs& a, const TilePlan& p, int lane, LinearTile& t) {
-  const int w = blockIdx.x;
+__device__ __forceinline__ bool locate(const LinearArgs& a, const TilePlan& p, int w, int lane, LinearTile& t) {
   const int row_tiles = MODE == MODE_DW ? (a.n + BP - 1) / BP : count_row_tiles<BP>(a, lane);
   int i = w, part = -1;
   if (p.tiles < 0) {
@@ -329,9 +332,9 @@ __device__ __forceinline__ bool locate(const LinearArgs& a, const TilePlan& p, i
 // A wave's accumulators to its place in the workspace: 32 TM rows from row on
 // of the tile, 64 columns from col on.
 template <int BP, int BQ, int TM, int TN>
-__device__ __forceinline__ void store_part(const LinearArgs& a, v16f (&acc)[TM][TN], int slot, int row, int col,
+__device__ __forceinline__ void store_part(float* partial, v16f (&acc)[TM][TN], int slot, int row, int col,
                                            uint8_t* scratch, int lane) {
-  float* const base = a.partial + static_cast<int64_t>(slot) * (BP * BQ) + row * BQ + col;
+  float* const base = partial + static_cast<int64_t>(slot) * (BP * BQ) + row * BQ + col;
 #pragma unroll
   for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -490,7 +493,7 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void linear_tile_kernel(LinearArgs
   const int wp = wave / WQ, wq = wave % WQ;
 
   LinearTile t;
-  if (!locate<MODE, BP, BQ>(a, plan, lane, t)) return;
+  if (!locate<MODE, BP, BQ>(a, plan, blockIdx.x, lane, t)) return;
   const int64_t wg = static_cast<int64_t>(t.g) * a.n * a.k;
   TP p;
   TQ q;
@@ -570,7 +573,7 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void linear_tile_kernel(LinearArgs
   // ---- the output ----
   uint8_t* const scratch = (wave & 1 ? sP1 : sP0) + (wave >> 1) * 4096;
   static_assert(TP::BYTES >= (NW + 1) / 2 * 4096, "scratch of the waves");
-  if (t.slot >= 0) store_part<BP, BQ>(a, acc, t.slot, wp * (TM * 32), wq * 64, scratch, lane);
+  if (t.slot >= 0) store_part<BP, BQ>(partials<MODE>(a), acc, t.slot, wp * (TM * 32), wq * 64, scratch, lane);
   else store_output<MODE>(a, acc, t.g, t.row0 + wp * (TM * 32), t.row_end, t.col0 + wq * 64, scratch, lane);
 }
 
@@ -583,21 +586,21 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void linear_tile_kernel(LinearArgs
 // read by then, and is waited for at the end of M(s + 2), four clusters later.
 // Steps past the last read zeros, so the steps go in fours with one exit and
 // every wave has the same loads in flight.
+constexpr int kRingBytes = 256 * kRingR * 2;      // one operand, one stage
 template <int MODE>
-__global__ __launch_bounds__(512, 1) void linear_pingpong_kernel(LinearArgs a, TilePlan plan) {
+__device__ __forceinline__ void pingpong_tile(const LinearArgs& a, const TilePlan& plan, int w, uint8_t* const (&sp)[4],
+                                              uint8_t* const (&sq)[4]) {
   constexpr int R = kRingR;
   using TP = TileOperand<MODE != MODE_DW, 256, R, 8>;
   using TQ = TileOperand<MODE == MODE_FORWARD, 256, R, 8>;
   constexpr int N = TP::NI + TQ::NI;
-  static_assert(TP::NI == 2 && TQ::NI == 2, "loads per wave and stage");
-  __shared__ __attribute__((aligned(16))) uint8_t sP0[TP::BYTES], sP1[TP::BYTES], sP2[TP::BYTES], sP3[TP::BYTES];
-  __shared__ __attribute__((aligned(16))) uint8_t sQ0[TQ::BYTES], sQ1[TQ::BYTES], sQ2[TQ::BYTES], sQ3[TQ::BYTES];
+  static_assert(TP::NI == 2 && TQ::NI == 2 && TP::BYTES == kRingBytes && TQ::BYTES == kRingBytes, "loads per wave and stage");
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wp = wave >> 2, wq = wave & 3;
 
   LinearTile t;
-  if (!locate<MODE, 256, 256>(a, plan, lane, t)) return;
+  if (!locate<MODE, 256, 256>(a, plan, w, lane, t)) return;
   const int64_t wg = static_cast<int64_t>(t.g) * a.n * a.k;
   TP p;
   TQ q;
@@ -621,7 +624,7 @@ __global__ __launch_bounds__(512, 1) void linear_pingpong_kernel(LinearArgs a, T
   struct Stage {
     uint8_t *p, *q;
   };
-  const Stage st[4] = {{sP0, sQ0}, {sP1, sQ1}, {sP2, sQ2}, {sP3, sQ3}};
+  const Stage st[4] = {{sp[0], sq[0]}, {sp[1], sq[1]}, {sp[2], sq[2]}, {sp[3], sq[3]}};
   // load j (0..3) of stage s (the bases run along); ANY: a stage that is
   // ragged or past the end
   auto issue = [&](auto any, int s, const Stage& d, int j) __attribute__((always_inline)) {
@@ -700,9 +703,40 @@ __global__ __launch_bounds__(512, 1) void linear_pingpong_kernel(LinearArgs a, T
     if (!wp) sync();
     sync();
   }
-  uint8_t* const scratch = (wave < 4 ? sP0 : sP1) + (wave & 3) * 4096;
-  if (t.slot >= 0) store_part<256, 256>(a, acc, t.slot, wp * 128, wq * 64, scratch, lane);
+  uint8_t* const scratch = (wave < 4 ? sp[0] : sp[1]) + (wave & 3) * 4096;
+  if (t.slot >= 0) store_part<256, 256>(partials<MODE>(a), acc, t.slot, wp * 128, wq * 64, scratch, lane);
   else store_output<MODE>(a, acc, t.g, t.row0 + wp * 128, t.row_end, t.col0 + wq * 64, scratch, lane);
+}
+
+// One LDS array per stage and operand (see linear_tile_kernel).
+#define MOEGG_RING_STAGES                                                                                     \
+  __shared__ __attribute__((aligned(16))) uint8_t sP0[kRingBytes], sP1[kRingBytes], sP2[kRingBytes], sP3[kRingBytes]; \
+  __shared__ __attribute__((aligned(16))) uint8_t sQ0[kRingBytes], sQ1[kRingBytes], sQ2[kRingBytes], sQ3[kRingBytes]; \
+  uint8_t* const sp[4] = {sP0, sP1, sP2, sP3};                                                                \
+  uint8_t* const sq[4] = {sQ0, sQ1, sQ2, sQ3}
+
+template <int MODE>
+__global__ __launch_bounds__(512, 1) void linear_pingpong_kernel(LinearArgs a, TilePlan plan) {
+  MOEGG_RING_STAGES;
+  pingpong_tile<MODE>(a, plan, blockIdx.x, sp, sq);
+}
+
+// The tiles of dw and then of dx in one launch.  dw's workgroups are counted in
+// eights (a workgroup's number modulo 8 stays its XCD).
+struct BothPlan {
+  TilePlan dx, dw;
+  int dw_eights;
+};
+__global__ __launch_bounds__(512, 1) void linear_both_kernel(LinearArgs a, BothPlan p) {
+  MOEGG_RING_STAGES;
+  const int first_dx = 8 * p.dw_eights;
+  const bool dw = static_cast<int>(blockIdx.x) < first_dx;
+  const int w = blockIdx.x - (dw ? 0 : first_dx);
+  if (dw) {
+    if (w < p.dw.first + (p.dw.tiles - p.dw.first) * p.dw.parts) pingpong_tile<MODE_DW>(a, p.dw, w, sp, sq);
+  } else if (p.dx.tiles < 0 || w < p.dx.first + (p.dx.tiles - p.dx.first) * p.dx.parts) {
+    pingpong_tile<MODE_DX>(a, p.dx, w, sp, sq);
+  }
 }
 
 }  // namespace

@@ -87,12 +87,13 @@ __device__ __forceinline__ uint32_t to_bf16(float f) {
   return static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<__bf16>(f)));
 }
 
-// Lane l of the token's LPT lanes holds experts (i LPT + l) V + v; V is the
-// width of its accesses (16 bytes where EPL and the expert count allow).
+// Lane l of the token's LPT lanes holds experts l EPL + [0, EPL), so that the
+// lowest of several experts sits in the lowest lane; V is the width of its
+// accesses (16 bytes where EPL and the expert count allow).
 template <bool BF16, int LPT, int EPL, int V>
 struct Row {
   static constexpr int NI = EPL / V;
-  __device__ static __forceinline__ int expert(int lane, int i, int v) { return (i * LPT + lane) * V + v; }
+  __device__ static __forceinline__ int expert(int lane, int i, int v) { return lane * EPL + i * V + v; }
   __device__ static __forceinline__ void load(const void* base, int64_t row, int experts, int lane, float* x) {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
@@ -201,27 +202,25 @@ template <typename R, int LPT, int EPL, int V, typename Key>
 __device__ __forceinline__ void choose(Key* key, const float* x, int rounds, int lane, int* ids, float* logits, Key* keys) {
   constexpr Key none = -static_cast<Key>(__builtin_inff());
   for (int j = 0; j < rounds; ++j) {
-    Key best = key[0];
+    Key mine = key[0];
 #pragma unroll
-    for (int q = 1; q < EPL; ++q) best = larger(best, key[q]);
+    for (int q = 1; q < EPL; ++q) mine = larger(mine, key[q]);
+    Key best = mine;
     steps<LPT>([&](auto c) { best = larger(best, partner<decltype(c)::value>(best)); });
-    int at = 0x7FFFFFFF;
-#pragma unroll
-    for (int q = EPL - 1; q >= 0; --q) at = key[q] == best ? R::expert(lane, q / V, q % V) : at;
-    int first = at;
-    steps<LPT>([&](auto c) {
-      first = min(first, static_cast<int>(partner<decltype(c)::value>(static_cast<uint32_t>(first))));
-    });
-    if (at == first) {                       // one lane: the expert's own
+    // the first of the token's lanes that has it
+    const uint64_t have = __ballot(mine == best) >> (threadIdx.x & 63 & ~(LPT - 1));
+    if (lane == __builtin_ctzll(have)) {
+      int at = 0;
       float logit = kNegInf;
 #pragma unroll
-      for (int q = 0; q < EPL; ++q) {
-        const bool it = R::expert(lane, q / V, q % V) == first;
-        logit = it ? x[q] : logit;
-        key[q] = it ? none : key[q];
+      for (int q = EPL - 1; q >= 0; --q) {
+        at = key[q] == best ? q : at;
+        logit = key[q] == best ? x[q] : logit;
       }
+#pragma unroll
+      for (int q = 0; q < EPL; ++q) key[q] = q == at ? none : key[q];
       const bool there = best > none;
-      ids[j] = there ? first : -1;
+      ids[j] = there ? lane * EPL + at : -1;
       logits[j] = there ? logit : kNegInf;
       if (keys) keys[j] = best;
     }
