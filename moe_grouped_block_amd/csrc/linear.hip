@@ -359,14 +359,13 @@ int64_t row_tiles(const LinearArgs& a, int64_t bm) { return div_up(a.m, bm) + (a
 
 // Tile shapes: how many workgroups the chip holds at once, and what a round of
 // them takes for a step of 64 r and for everything outside the steps, in
-// microseconds; `alone`: a step where one workgroup has its compute unit to
-// itself.
+// microseconds; `alone`: a step where at most half of them are there.
 enum Shape : int { SHAPE_256 = 0, SHAPE_128 = 1, SHAPE_64 = 2 };
 struct ShapeCost {
   int bp, bq, slots;
   double step, alone, rest;
 };
-constexpr ShapeCost kShapes[] = {{256, 256, 256, 1.55, 1.55, 8.0}, {128, 128, 512, 1.0, 0.70, 5.0}, {128, 64, 768, 0.80, 0.60, 4.0}};
+constexpr ShapeCost kShapes[] = {{256, 256, 256, 1.55, 1.55, 8.0}, {128, 128, 512, 1.0, 0.70, 5.0}, {64, 64, 256, 0.46, 0.22, 3.0}};
 
 struct Plan {
   Shape shape;
@@ -395,7 +394,7 @@ Plan choose(F&& tiles, G&& spare, int64_t cols, int64_t r, bool known) {
     auto rounds = [&](int64_t n, int64_t st) {
       const int64_t left = n % c.slots;
       return static_cast<double>(n / c.slots) * (st * c.step + c.rest) +
-             (left ? st * (left <= 256 ? c.alone : c.step) + c.rest : 0.0);
+             (left ? st * (left <= c.slots / 2 ? c.alone : c.step) + c.rest : 0.0);
     };
     auto take = [&](double cost, int64_t first, int parts) {
       if (least != 0.0 && cost >= least) return;
@@ -457,8 +456,8 @@ hipError_t launch_tiles(const LinearArgs& a, const Plan& p, hipStream_t s) {
       launch_join<MODE, 128, 128>(a, p, s);
       break;
     case SHAPE_64:
-      hipLaunchKernelGGL((linear_tile_kernel<MODE, 128, 64, 4, 1>), grid, dim3(256), 0, s, a, t);
-      launch_join<MODE, 128, 64>(a, p, s);
+      hipLaunchKernelGGL((linear_narrow_kernel<MODE>), grid, dim3(512), 0, s, a, t);
+      launch_join<MODE, 64, 64>(a, p, s);
       break;
   }
   return hipGetLastError();

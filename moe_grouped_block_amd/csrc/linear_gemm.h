@@ -577,6 +577,110 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void linear_tile_kernel(LinearArgs
   else store_output<MODE>(a, acc, t.g, t.row0 + wp * (TM * 32), t.row_end, t.col0 + wq * 64, scratch, lane);
 }
 
+// The 64 x 64 tile of narrow outputs (a router's product): what counts is that
+// the long operand streams, so that every compute unit has a workgroup and each
+// of them many bytes in flight.  Four pairs of waves share the tile's r, each
+// with two stages of its own, and their sums meet in LDS.
+template <int MODE>
+__global__ __launch_bounds__(512, 2) void linear_narrow_kernel(LinearArgs a, TilePlan plan) {
+  constexpr int G = 4, NW = 2;
+  using TP = TileOperand<MODE != MODE_DW, 64, kR, NW>;
+  using TQ = TileOperand<MODE == MODE_FORWARD, 64, kR, NW>;
+  __shared__ __attribute__((aligned(16))) uint8_t sP0[G * TP::BYTES], sP1[G * TP::BYTES], sQ0[G * TQ::BYTES], sQ1[G * TQ::BYTES];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int grp = wave / NW, wp = wave % NW;
+
+  LinearTile t;
+  if (!locate<MODE, 64, 64>(a, plan, blockIdx.x, lane, t)) return;
+  const int64_t wg = static_cast<int64_t>(t.g) * a.n * a.k;
+  const int64_t steps = (t.r1 - t.r0 + kR - 1) / kR;
+  const int64_t r0 = min(t.r1, t.r0 + steps * grp / G * kR), r1 = min(t.r1, t.r0 + steps * (grp + 1) / G * kR);
+  const int span = static_cast<int>(r1 - r0), full = span / kR, most = static_cast<int>((steps + G - 1) / G);
+  TP p;
+  TQ q;
+  p.init(MODE == MODE_FORWARD ? a.x : a.dz, MODE == MODE_FORWARD ? a.k : a.n, t.row0, MODE == MODE_DW ? a.n : t.row_end, r0, wp,
+         lane);
+  q.init(MODE == MODE_DW ? a.x : a.w + wg, a.k, t.col0, MODE == MODE_FORWARD ? a.n : a.k, r0, wp, lane);
+  typename TP::template Frags<1> fp;
+  typename TQ::template Frags<2> fq;
+  fp.init(wp * 32, lane);
+  fq.init(0, lane);
+  v16f acc[1][2];
+  acc[0][0] = acc[0][1] = v16f{};
+  auto issue = [&](int s, uint8_t* lp, uint8_t* lq) __attribute__((always_inline)) {
+    lp += grp * TP::BYTES;
+    lq += grp * TQ::BYTES;
+    if (s < full) {
+#pragma unroll
+      for (int j = 0; j < TP::NI; ++j) p.load(lp, wp, j);
+#pragma unroll
+      for (int j = 0; j < TQ::NI; ++j) q.load(lq, wp, j);
+    } else {
+#pragma unroll
+      for (int j = 0; j < TP::NI; ++j) p.load_tail(lp, wp, lane, j, span - s * kR);
+#pragma unroll
+      for (int j = 0; j < TQ::NI; ++j) q.load_tail(lq, wp, lane, j, span - s * kR);
+    }
+    p.base += p.advance;
+    q.base += q.advance;
+  };
+  auto compute = [&](const uint8_t* lp, const uint8_t* lq) __attribute__((always_inline)) {
+    lp += grp * TP::BYTES;
+    lq += grp * TQ::BYTES;
+#pragma unroll
+    for (int k = 0; k < kR / 16; ++k) {
+      const v8bf vp = __builtin_bit_cast(v8bf, fp.read(lp, 0, k));
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        acc[0][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, fq.read(lq, j, k)), vp, acc[0][j], 0, 0, 0);
+    }
+  };
+  auto arrive = [&]() __attribute__((always_inline)) {
+    wait_vmcnt<0>();
+    __syncthreads();
+  };
+  // steps in pairs, as in linear_tile_kernel; all pairs of waves take `most` of them
+  if (most > 0) {
+    issue(0, sP0, sQ0);
+    arrive();
+    for (int s = 0; s < most; s += 2) {
+      issue(s + 1, sP1, sQ1);
+      compute(sP0, sQ0);
+      arrive();
+      if (s + 2 < most) issue(s + 2, sP0, sQ0);
+      compute(sP1, sQ1);
+      arrive();
+    }
+  }
+  // sums of pairs 1, 2, 3 to pair 0, added in that order
+  static_assert(G * TP::BYTES >= 2 * NW * 8192, "two pairs' sums in each P image");
+  auto place_of = [&](int from) { return (from < 3 ? sP0 + (from - 1) * (NW * 8192) : sP1) + wp * 8192 + lane * 16; };
+  if (grp > 0) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        *reinterpret_cast<v4f*>(place_of(grp) + (j * 4 + b) * 1024) =
+            v4f{acc[0][j][4 * b], acc[0][j][4 * b + 1], acc[0][j][4 * b + 2], acc[0][j][4 * b + 3]};
+  }
+  __syncthreads();
+  if (grp > 0) return;
+#pragma unroll
+  for (int from = 1; from < G; ++from)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const v4f v = *reinterpret_cast<const v4f*>(place_of(from) + (j * 4 + b) * 1024);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[0][j][4 * b + e] += v[e];
+      }
+  uint8_t* const scratch = sQ0 + wp * 4096;
+  if (t.slot >= 0) store_part<64, 64>(partials<MODE>(a), acc, t.slot, wp * 32, 0, scratch, lane);
+  else store_output<MODE>(a, acc, t.g, t.row0 + wp * 32, t.row_end, t.col0, scratch, lane);
+}
+
 // The 256 x 256 tile: 8 waves, 2 along p x 4 along q, each 128 x 64, on the
 // ping-pong schedule of the grouped product.  A step of 32 r is two clusters:
 // M reads the step's 12 fragments from LDS, C runs its 16 MFMAs.  The two
