@@ -359,13 +359,17 @@ int64_t row_tiles(const LinearArgs& a, int64_t bm) { return div_up(a.m, bm) + (a
 
 // Tile shapes: how many workgroups the chip holds at once, and what a round of
 // them takes for a step of 64 r and for everything outside the steps, in
-// microseconds; `alone`: a step where at most half of them are there.
+// microseconds; `alone`: a step where at most half of them are there.  Per
+// product: forward, dx, dw.
 enum Shape : int { SHAPE_256 = 0, SHAPE_128 = 1, SHAPE_64 = 2 };
 struct ShapeCost {
   int bp, bq, slots;
   double step, alone, rest;
 };
-constexpr ShapeCost kShapes[] = {{256, 256, 256, 1.55, 1.55, 8.0}, {128, 128, 512, 1.0, 0.70, 5.0}, {64, 64, 256, 0.46, 0.22, 3.0}};
+constexpr ShapeCost kShapes[3][3] = {
+    {{256, 256, 256, 1.55, 1.10, 8.0}, {128, 128, 512, 1.10, 0.60, 5.0}, {64, 64, 256, 0.46, 0.22, 3.0}},
+    {{256, 256, 256, 1.40, 1.05, 8.0}, {128, 128, 512, 0.90, 0.56, 4.0}, {64, 64, 256, 0.46, 0.22, 3.0}},
+    {{256, 256, 256, 1.35, 1.00, 8.0}, {128, 128, 512, 0.90, 0.56, 4.0}, {64, 64, 256, 0.46, 0.22, 3.0}}};
 
 struct Plan {
   Shape shape;
@@ -382,12 +386,12 @@ struct Plan {
 // (half of them are taken to be); `r`: length of the sum; `known`: the tiles
 // are these, and may be split.
 template <typename F, typename G>
-Plan choose(F&& tiles, G&& spare, int64_t cols, int64_t r, bool known) {
+Plan choose(LinearMode mode, F&& tiles, G&& spare, int64_t cols, int64_t r, bool known) {
   Plan best{};
   double least = 0.0;
   const int64_t steps = div_up(r > 0 ? r : 1, kR);
   for (int s = 0; s < 3; ++s) {
-    const ShapeCost& c = kShapes[s];
+    const ShapeCost& c = kShapes[mode][s];
     const int64_t total = tiles(c);
     // the narrow tile is for narrow outputs
     if ((s == SHAPE_64) != (cols <= 64)) continue;
@@ -420,13 +424,14 @@ Plan choose(F&& tiles, G&& spare, int64_t cols, int64_t r, bool known) {
 
 // Split only without offsets, where the host knows the tiles.  (The workspace
 // is sized without knowing the offsets, so never too small.)
-Plan plan_rows(const LinearArgs& a, int64_t cols, int64_t r) {
-  return choose([&](const ShapeCost& c) { return row_tiles(a, c.bp) * div_up(cols, c.bq); },
+Plan plan_rows(const LinearArgs& a, LinearMode mode) {
+  const int64_t cols = mode == MODE_FORWARD ? a.n : a.k, r = mode == MODE_FORWARD ? a.k : a.n;
+  return choose(mode, [&](const ShapeCost& c) { return row_tiles(a, c.bp) * div_up(cols, c.bq); },
                 [&](const ShapeCost& c) { return (a.groups - 1) * div_up(cols, c.bq); }, cols, r, a.groups == 1 && !a.offsets);
 }
 Plan plan_dw(const LinearArgs& a) {
   // a group's share of the rows; groups whose rows the host does not know are not split
-  return choose([&](const ShapeCost& c) { return a.groups * div_up(a.n, c.bp) * div_up(a.k, c.bq); },
+  return choose(MODE_DW, [&](const ShapeCost& c) { return a.groups * div_up(a.n, c.bp) * div_up(a.k, c.bq); },
                 [](const ShapeCost&) { return int64_t{0}; }, a.k, div_up(a.m, a.groups), a.groups == 1);
 }
 bool few_rows(const LinearArgs& a) { return a.m <= 16 * static_cast<int64_t>(a.groups); }
@@ -452,7 +457,12 @@ hipError_t launch_tiles(const LinearArgs& a, const Plan& p, hipStream_t s) {
       launch_join<MODE, 256, 256>(a, p, s);
       break;
     case SHAPE_128:
-      hipLaunchKernelGGL((linear_tile_kernel<MODE, 128, 128, 2, 2>), grid, dim3(256), 0, s, a, t);
+      if constexpr (MODE == MODE_FORWARD) {
+        if (p.workgroups > 256) hipLaunchKernelGGL((linear_tile_kernel<MODE, 128, 128, 2, 2>), grid, dim3(256), 0, s, a, t);
+        else hipLaunchKernelGGL((linear_ring_kernel<MODE, 128, 128, 2, 2>), grid, dim3(256), 0, s, a, t);
+      } else {
+        hipLaunchKernelGGL((linear_ring_kernel<MODE, 128, 128, 2, 2>), grid, dim3(256), 0, s, a, t);
+      }
       launch_join<MODE, 128, 128>(a, p, s);
       break;
     case SHAPE_64:
@@ -497,7 +507,7 @@ BackwardWorkspace backward_workspace(const LinearArgs& a, bool dx, bool dw, bool
   };
   w.dz = take(a.act != LIN_NONE && (dx || dw) ? a.m * a.n * 2 : 0);
   w.sums = take(db ? row_tiles(a, kDzRows) * a.n * 4 : 0);
-  w.dx = take(dx && a.m ? plan_rows(a, a.k, a.n).partial_bytes : 0);
+  w.dx = take(dx && a.m ? plan_rows(a, MODE_DX).partial_bytes : 0);
   w.dw = take(dw ? plan_dw(a).partial_bytes : 0);
   w.total = at;
   return w;
@@ -507,7 +517,7 @@ BackwardWorkspace backward_workspace(const LinearArgs& a, bool dx, bool dw, bool
 
 int64_t linear_workspace(const LinearArgs& a) {
   if (a.m == 0 || few_rows(a)) return 0;
-  return plan_rows(a, a.n, a.k).partial_bytes;
+  return plan_rows(a, MODE_FORWARD).partial_bytes;
 }
 int64_t linear_backward_workspace(const LinearArgs& a, bool dx, bool dw, bool db) {
   return backward_workspace(a, dx, dw, db).total;
@@ -533,7 +543,7 @@ hipError_t launch_linear(const LinearArgs& args, hipStream_t s) {
     return hipGetLastError();
   }
   a.dx_partial = static_cast<float*>(a.workspace);
-  return launch_tiles<MODE_FORWARD>(a, plan_rows(a, a.n, a.k), s);
+  return launch_tiles<MODE_FORWARD>(a, plan_rows(a, MODE_FORWARD), s);
 }
 
 hipError_t launch_linear_backward(const LinearArgs& args, hipStream_t s) {
@@ -563,7 +573,7 @@ hipError_t launch_linear_backward(const LinearArgs& args, hipStream_t s) {
                        s, a, sums);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  const Plan pdx = plan_rows(a, a.k, a.n), pdw = plan_dw(a);
+  const Plan pdx = plan_rows(a, MODE_DX), pdw = plan_dw(a);
   if (a.dx && a.dw && both(a, pdx, pdw)) return launch_both(a, pdx, pdw, s);
   if (a.dx && a.m && (e = launch_tiles<MODE_DX>(a, pdx, s)) != hipSuccess) return e;
   if (a.dw && (e = launch_tiles<MODE_DW>(a, pdw, s)) != hipSuccess) return e;

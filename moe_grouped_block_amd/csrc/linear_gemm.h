@@ -478,7 +478,7 @@ __device__ __forceinline__ void store_output(const LinearArgs& a, v16f (&acc)[TM
   }
 }
 
-// The tile kernel for small tiles.
+// The 128 x 128 tile, two stages of 64 r (the forward, see linear_ring_kernel).
 template <int MODE, int BP, int BQ, int WP, int WQ>
 __global__ __launch_bounds__(64 * WP * WQ, 2) void linear_tile_kernel(LinearArgs a, TilePlan plan) {
   constexpr int NW = WP * WQ, TM = BP / WP / 32, TN = BQ / WQ / 32;
@@ -571,6 +571,104 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void linear_tile_kernel(LinearArgs
   }
 
   // ---- the output ----
+  uint8_t* const scratch = (wave & 1 ? sP1 : sP0) + (wave >> 1) * 4096;
+  static_assert(TP::BYTES >= (NW + 1) / 2 * 4096, "scratch of the waves");
+  if (t.slot >= 0) store_part<BP, BQ>(partials<MODE>(a), acc, t.slot, wp * (TM * 32), wq * 64, scratch, lane);
+  else store_output<MODE>(a, acc, t.g, t.row0 + wp * (TM * 32), t.row_end, t.col0 + wq * 64, scratch, lane);
+}
+
+// The same tile in steps of 32 r through a ring of four stages: three stages
+// are in flight, and a step has one barrier (behind it every wave has read the
+// stage before, whose place stage s + 3 takes).  Measured against two stages
+// of 64 r, 256 tiles of 2048^3: 28.7 -> 22 to 23.5 us; dw 2816 x 2048 over 4099
+// rows (352 tiles) 70 -> 60; but the forward with 512 tiles, two workgroups to
+// a compute unit, 55 -> 63: there both operands come in 64-byte pieces, and
+// two workgroups hide the latency well enough.
+template <int MODE, int BP, int BQ, int WP, int WQ>
+__global__ __launch_bounds__(64 * WP * WQ, 2) void linear_ring_kernel(LinearArgs a, TilePlan plan) {
+  constexpr int NW = WP * WQ, TM = BP / WP / 32, TN = BQ / WQ / 32, R = kRingR;
+  using TP = TileOperand<MODE != MODE_DW, BP, R, NW>;
+  using TQ = TileOperand<MODE == MODE_FORWARD, BQ, R, NW>;
+  constexpr int N = TP::NI + TQ::NI;
+  static_assert(TN == 2, "a wave's columns are one pair of 32-column blocks");
+  __shared__ __attribute__((aligned(16))) uint8_t sP0[TP::BYTES], sP1[TP::BYTES], sP2[TP::BYTES], sP3[TP::BYTES];
+  __shared__ __attribute__((aligned(16))) uint8_t sQ0[TQ::BYTES], sQ1[TQ::BYTES], sQ2[TQ::BYTES], sQ3[TQ::BYTES];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wp = wave / WQ, wq = wave % WQ;
+
+  LinearTile t;
+  if (!locate<MODE, BP, BQ>(a, plan, blockIdx.x, lane, t)) return;
+  const int64_t wg = static_cast<int64_t>(t.g) * a.n * a.k;
+  TP p;
+  TQ q;
+  p.init(MODE == MODE_FORWARD ? a.x : a.dz, MODE == MODE_FORWARD ? a.k : a.n, t.row0, MODE == MODE_DW ? a.n : t.row_end, t.r0,
+         wave, lane);
+  q.init(MODE == MODE_DW ? a.x : a.w + wg, a.k, t.col0, MODE == MODE_FORWARD ? a.n : a.k, t.r0, wave, lane);
+  typename TP::template Frags<TM> fp;
+  typename TQ::template Frags<TN> fq;
+  fp.init(wp * (TM * 32), lane);
+  fq.init(wq * (TN * 32), lane);
+  fp.keep();
+  fq.keep();
+  v16f acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = v16f{};
+  const int span = static_cast<int>(t.r1 - t.r0), full = span / R;
+  // ANY: a stage that is ragged or past the end (zeros)
+  auto issue = [&](auto any, int s, uint8_t* lp, uint8_t* lq) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < TP::NI; ++j)
+      if constexpr (decltype(any)::value) p.load_tail(lp, wave, lane, j, span - s * R);
+      else p.load(lp, wave, j);
+#pragma unroll
+    for (int j = 0; j < TQ::NI; ++j)
+      if constexpr (decltype(any)::value) q.load_tail(lq, wave, lane, j, span - s * R);
+      else q.load(lq, wave, j);
+    p.base += p.advance;
+    q.base += q.advance;
+  };
+  auto step = [&](auto any, int s, const uint8_t* lp, const uint8_t* lq, uint8_t* next_p, uint8_t* next_q)
+      __attribute__((always_inline)) {
+    wait_vmcnt<2 * N>();                           // stage s (s + 1 and s + 2 are on their way)
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    issue(any, s + 3, next_p, next_q);
+#pragma unroll
+    for (int kk = 0; kk < R / 16; ++kk) {
+      v8bf vq[TN];
+#pragma unroll
+      for (int j = 0; j < TN; ++j) vq[j] = __builtin_bit_cast(v8bf, fq.read(lq, j, kk));
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        const v8bf vp = __builtin_bit_cast(v8bf, fp.read(lp, i, kk));
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vq[j], vp, acc[i][j], 0, 0, 0);
+      }
+    }
+    __builtin_amdgcn_s_waitcnt(0xC07F);            // this stage read before the next barrier
+  };
+  if (span > 0) {
+    const std::true_type any{};
+    const std::false_type plain{};
+    auto four = [&](auto any, int s) __attribute__((always_inline)) {
+      step(any, s, sP0, sQ0, sP3, sQ3);
+      step(any, s + 1, sP1, sQ1, sP0, sQ0);
+      step(any, s + 2, sP2, sQ2, sP1, sQ1);
+      step(any, s + 3, sP3, sQ3, sP2, sQ2);
+    };
+    issue(any, 0, sP0, sQ0);
+    issue(any, 1, sP1, sQ1);
+    issue(any, 2, sP2, sQ2);
+    int s = 0;
+    for (; s + 6 < full; s += 4) four(plain, s);
+    for (; s * R < span; s += 4) four(any, s);
+    wait_vmcnt<0>();
+    __syncthreads();
+  }
   uint8_t* const scratch = (wave & 1 ? sP1 : sP0) + (wave >> 1) * 4096;
   static_assert(TP::BYTES >= (NW + 1) / 2 * 4096, "scratch of the waves");
   if (t.slot >= 0) store_part<BP, BQ>(partials<MODE>(a), acc, t.slot, wp * (TM * 32), wq * 64, scratch, lane);
