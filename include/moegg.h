@@ -242,8 +242,11 @@ moegg_status moegg_sf_to_kplanes(const uint8_t* src, uint8_t* dst, int64_t rows,
  * asynchronous on `stream`, capturable (kernels only), every argument checked
  * on the host before any HIP call.  Values in index tensors are device data:
  * an index out of range is never followed (each function says what it counts
- * as).  A workspace belongs to one call at a time: calls that may run at the
- * same time (other streams, graphs replayed side by side) need their own.
+ * as).  An output shares no memory with an input, a workspace or another
+ * output, but where a function says so.  A workspace belongs to one call at a
+ * time: calls that may run at the same time (other streams, graphs replayed
+ * side by side) need their own.  A problem that would need more than 2^32
+ * threads in a launch is refused.
  * Results do not depend on the order in which workgroups run.
  * ========================================================================== */
 
@@ -360,7 +363,9 @@ moegg_status moegg_unsort(const float* rows_values, const int32_t* row_of, float
 /* Matrix product with bias, activation and residual, dense or grouped.
  *   z = x w_g^T + bias_g;  c = bf16(z);  y = act(z) + residual
  * for the rows [offsets[g-1], offsets[g]) of group g (any nondecreasing ends,
- * no alignment), or for all m rows where offsets is NULL (num_groups 1).
+ * no alignment; of ends that decrease or leave the rows none is followed outside
+ * them, but what the rows then hold is not defined; y may be residual itself,
+ * both BF16), or for all m rows where offsets is NULL (num_groups 1).
  * act: NONE, SRELU (relu(z)^2), GELU, or SWIGLU on [X | G] pairs of 32 columns
  * as in moegg_run (N_out = n / 2, else N_out = n).  Sums are fp32. */
 typedef struct moegg_linear_problem {

@@ -111,7 +111,9 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
   for (int e0 = 0; e0 < E; e0 += kSortThreads) {
     const int e = e0 + tid;
     const int all = e < E ? total[e] : 0;
-    const int padded = (all + a.m_aligned - 1) / a.m_aligned * a.m_aligned;
+    // (without a sign: the sum before the division may reach 2^31)
+    const uint32_t ma = a.m_aligned;
+    const int padded = static_cast<int>((all + ma - 1u) / ma * ma);
     int scan = padded;
     for (int d = 1; d < 64; d <<= 1) {
       const int y = __shfl_up(scan, d);
@@ -330,7 +332,6 @@ __device__ __forceinline__ void store_row(const ExchangeArgs& a, int64_t row, in
 // These waves come first in a launch and take few rows each: with 64 rows a
 // wave, behind the tokens' waves, the last of them ended 10 us after all
 // others.
-constexpr int kPadRows = 16;
 template <int KIND>
 __device__ __forceinline__ void zero_padding(const ExchangeArgs& a, int64_t q, int lane) {
   const int64_t last = a.offsets[a.experts - 1];
@@ -540,11 +541,8 @@ hipError_t by_kind(int kind, F&& f) {
   }
 }
 
-// Workgroups of 4 waves for `waves` waves; 0 if there are too many.
-unsigned blocks_of(int64_t waves) {
-  const int64_t b = (waves + 3) / 4;
-  return b > 0x7FFFFFFF ? 0u : static_cast<unsigned>(b);
-}
+// Workgroups of 4 waves for `waves` waves (the host has checked exchange_waves()).
+unsigned blocks_of(int64_t waves) { return static_cast<unsigned>((waves + 3) / 4); }
 
 }  // namespace
 
@@ -563,7 +561,6 @@ hipError_t launch_dispatch(const ExchangeArgs& a, hipStream_t s) {
   const int64_t token_waves = a.tokens * ((a.width + cols - 1) / cols);
   const int64_t pad_waves = (a.rows + kPadRows - 1) / kPadRows;
   const unsigned blocks = blocks_of(token_waves + pad_waves);
-  if (!blocks) return hipErrorInvalidValue;
   return by_kind(a.kind, [&](auto c) {
     hipLaunchKernelGGL((dispatch_kernel<decltype(c)::value>), dim3(blocks), dim3(256), 0, s, a, pad_waves);
     return hipGetLastError();
@@ -572,7 +569,6 @@ hipError_t launch_dispatch(const ExchangeArgs& a, hipStream_t s) {
 
 hipError_t launch_combine(const ExchangeArgs& a, hipStream_t s) {
   const unsigned blocks = blocks_of(a.tokens * ((a.width + 511) / 512));
-  if (!blocks) return hipErrorInvalidValue;
   hipLaunchKernelGGL(combine_kernel, dim3(blocks), dim3(256), 0, s, a);
   return hipGetLastError();
 }
@@ -580,7 +576,6 @@ hipError_t launch_combine(const ExchangeArgs& a, hipStream_t s) {
 hipError_t launch_combine_backward(const ExchangeArgs& a, hipStream_t s) {
   const int64_t pad_waves = (a.rows + kPadRows - 1) / kPadRows;
   const unsigned blocks = blocks_of(a.tokens + pad_waves);
-  if (!blocks) return hipErrorInvalidValue;
   return by_kind(a.kind, [&](auto c) {
     hipLaunchKernelGGL((combine_backward_kernel<decltype(c)::value>), dim3(blocks), dim3(256), 0, s, a, pad_waves);
     return hipGetLastError();
@@ -590,7 +585,6 @@ hipError_t launch_combine_backward(const ExchangeArgs& a, hipStream_t s) {
 hipError_t launch_unsort(const float* rows, const int32_t* row_of, float* values, int64_t slots, int64_t n_rows,
                          hipStream_t s) {
   const int64_t b = (slots + 255) / 256;
-  if (b > 0x7FFFFFFF) return hipErrorInvalidValue;
   hipLaunchKernelGGL(unsort_kernel, dim3(static_cast<unsigned>(b)), dim3(256), 0, s, rows, row_of, values, slots, n_rows);
   return hipGetLastError();
 }

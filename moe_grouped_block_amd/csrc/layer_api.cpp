@@ -36,6 +36,25 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
   return x < y + static_cast<uintptr_t>(nb) && y < x + static_cast<uintptr_t>(na);
 }
 
+// No output shares a byte with an input or with another output.
+struct Span {
+  const char* name;
+  const void* p;
+  int64_t bytes;
+};
+template <int NI, int NO>
+moegg_status check_apart(const Span (&in)[NI], const Span (&out)[NO]) {
+  for (int i = 0; i < NO; ++i) {
+    for (const Span& q : in)
+      if (overlap(q.p, q.bytes, out[i].p, out[i].bytes))
+        return set_error(MOEGG_ERROR_INVALID_VALUE, "%s and %s overlap", q.name, out[i].name);
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[j].p, out[j].bytes, out[i].p, out[i].bytes))
+        return set_error(MOEGG_ERROR_INVALID_VALUE, "%s and %s overlap", out[j].name, out[i].name);
+  }
+  return MOEGG_OK;
+}
+
 moegg_status launched(hipError_t e, const char* what) {
   if (e != hipSuccess) return set_error(MOEGG_ERROR_LAUNCH, "%s: %s", what, hipGetErrorString(e));
   clear_error();
@@ -56,6 +75,8 @@ moegg_status check_route(const moegg_route_problem* pp) {
     return set_error(MOEGG_ERROR_NOT_SUPPORTED, "top_k=%d above %d", p.top_k, moegg::kMaxTopK);
   if (p.num_tokens > INT32_MAX / p.top_k)
     return set_error(MOEGG_ERROR_NOT_SUPPORTED, "num_tokens=%lld x top_k=%d above 2^31-1", (long long)p.num_tokens, p.top_k);
+  if (p.num_tokens * (p.num_experts > 256 ? 64 : 16) > moegg::kLaunchThreads)
+    return set_error(MOEGG_ERROR_NOT_SUPPORTED, "num_tokens=%lld: more threads than a launch holds", (long long)p.num_tokens);
   if (p.dtype != MOEGG_DT_BF16 && p.dtype != MOEGG_DT_F32)
     return set_error(MOEGG_ERROR_INVALID_VALUE, "dtype=%d must be BF16 or F32", p.dtype);
   if (p.score != MOEGG_SCORE_SOFTMAX && p.score != MOEGG_SCORE_SIGMOID)
@@ -135,6 +156,9 @@ moegg_status check_exchange(const moegg_exchange_problem* pp) {
   if (p.width < 1 || p.width % step != 0)
     return set_error(MOEGG_ERROR_NOT_SUPPORTED, "width=%d: a positive multiple of %d needed for this row type", p.width, step);
   if (p.width > (1 << 20)) return set_error(MOEGG_ERROR_NOT_SUPPORTED, "width=%d above 2^20", p.width);
+  if (moegg::exchange_waves(p.num_tokens, p.rows, p.width) * 64 > moegg::kLaunchThreads)
+    return set_error(MOEGG_ERROR_NOT_SUPPORTED, "num_tokens=%lld rows=%lld width=%d: more threads than a launch holds",
+                     (long long)p.num_tokens, (long long)p.rows, p.width);
   if (p.sf_layout != MOEGG_SF_ROW_MAJOR && p.sf_layout != MOEGG_SF_KPLANES)
     return set_error(MOEGG_ERROR_INVALID_VALUE, "sf_layout=%d must be ROW_MAJOR or KPLANES", p.sf_layout);
   return MOEGG_OK;
@@ -186,11 +210,17 @@ moegg_status check_linear(const moegg_linear_problem* pp) {
     return set_error(MOEGG_ERROR_NOT_SUPPORTED, "n=%d k=%d: multiples of 8 needed", p.n, p.k);
   if (p.n > (1 << 20) || p.k > (1 << 20))
     return set_error(MOEGG_ERROR_NOT_SUPPORTED, "n=%d k=%d above 2^20", p.n, p.k);
-  // tiles of 128 x 64 at least, of y, dx and dw
-  const int64_t wide = (p.n > p.k ? p.n : p.k) / 64 + 1;
-  if ((p.m / 128 + p.num_groups + 1) * wide > INT32_MAX || p.num_groups * (p.n / 128 + 1) * int64_t{p.k / 64 + 1} > INT32_MAX)
-    return set_error(MOEGG_ERROR_NOT_SUPPORTED, "m=%lld n=%d k=%d num_groups=%d: above 2^31-1 tiles", (long long)p.m, p.n, p.k,
-                     p.num_groups);
+  // Threads of the tiles of y, dx and dw: 512 for 64 x 64 (at most 64 columns),
+  // else 256 for 128 x 128 at most
+  const auto threads = [](int64_t row_tiles64, int64_t row_tiles128, int64_t cols) {
+    return cols <= 64 ? row_tiles64 * 512 : row_tiles128 * (cols / 128 + 1) * 256;
+  };
+  const int64_t rows64 = p.m / 64 + p.num_groups + 1, rows128 = p.m / 128 + p.num_groups + 1;
+  const int64_t dw64 = p.num_groups * int64_t{p.n / 64 + 1}, dw128 = p.num_groups * int64_t{p.n / 128 + 1};
+  if (threads(rows64, rows128, p.n) > moegg::kLaunchThreads || threads(rows64, rows128, p.k) > moegg::kLaunchThreads ||
+      threads(dw64, dw128, p.k) > moegg::kLaunchThreads || rows128 * 256 > moegg::kLaunchThreads)
+    return set_error(MOEGG_ERROR_NOT_SUPPORTED, "m=%lld n=%d k=%d num_groups=%d: more threads than a launch holds",
+                     (long long)p.m, p.n, p.k, p.num_groups);
   return MOEGG_OK;
 }
 
@@ -222,6 +252,8 @@ moegg::LinearArgs linear_args(const moegg_linear_problem& p, const moegg_linear_
   }
   return a;
 }
+
+int64_t w_bytes(const moegg_linear_problem& p) { return int64_t{p.num_groups} * p.n * p.k * 2; }
 
 moegg_status check_linear_pointers(const moegg_linear_problem& p, const moegg_linear_args& a, int64_t workspace) {
   const Pointer ps[] = {{"x", a.x, 16, false},   {"w", a.w, 16, false},     {"residual", a.residual, 16, false},
@@ -383,15 +415,16 @@ moegg_status moegg_combine_backward(const moegg_exchange_problem* problem, const
   moegg_status st = check_exchange(problem);
   if (st != MOEGG_OK) return st;
   const moegg_exchange_problem& p = *problem;
-  const bool any = p.num_tokens > 0 && p.rows > 0;
-  const Pointer ps[] = {{"dy", dy, 16, any}, {"out", out, 16, any}, {"sf", sf, 16, false}, {"rows_in", rows_in, 16, false},
-                        {"row_of", row_of, 4, any}, {"slot_of", slot_of, 4, any},
-                        {"padded_offsets", padded_offsets, 4, any}, {"weights", weights, 4, false},
+  // (without rows every slot is a dropped one: dweights is still written)
+  const bool rows = p.num_tokens > 0 && p.rows > 0, any = rows || (p.num_tokens > 0 && dweights);
+  const Pointer ps[] = {{"dy", dy, 16, any}, {"out", out, 16, rows}, {"sf", sf, 16, false}, {"rows_in", rows_in, 16, false},
+                        {"row_of", row_of, 4, any}, {"slot_of", slot_of, 4, rows},
+                        {"padded_offsets", padded_offsets, 4, rows}, {"weights", weights, 4, false},
                         {"dweights", dweights, 4, false}};
   st = check_pointers(ps);
   if (st != MOEGG_OK) return st;
-  if (any && (st = check_scales(p, sf)) != MOEGG_OK) return st;
-  if (any && (rows_in != nullptr) != (dweights != nullptr))
+  if (rows && (st = check_scales(p, sf)) != MOEGG_OK) return st;
+  if (rows && (rows_in != nullptr) != (dweights != nullptr))
     return set_error(MOEGG_ERROR_INVALID_VALUE, "rows_in and dweights come together");
   const int64_t t_bytes = p.num_tokens * p.width * 2;
   if (overlap(dy, t_bytes, out, row_bytes(p)) || overlap(rows_in, p.rows * p.width * 2, out, row_bytes(p)))
@@ -447,9 +480,13 @@ moegg_status moegg_linear(const moegg_linear_problem* problem, const moegg_linea
   if (st != MOEGG_OK) return st;
   const int64_t n_out = p.act == MOEGG_ACT_SWIGLU ? p.n / 2 : p.n;
   const int64_t y_bytes = p.m * n_out * (a.out_f32 ? 4 : 2);
-  if (overlap(a.x, p.m * p.k * 2, a.y, y_bytes) || overlap(a.c, p.m * p.n * 2, a.y, y_bytes) ||
-      overlap(a.x, p.m * p.k * 2, a.c, p.m * p.n * 2))
-    return set_error(MOEGG_ERROR_INVALID_VALUE, "x, c and y overlap");
+  const int64_t c_bytes = p.m * p.n * 2;
+  const Span in[] = {{"x", a.x, p.m * p.k * 2}, {"w", a.w, w_bytes(p)}, {"bias", a.bias, int64_t{p.num_groups} * p.n * 4},
+                     {"offsets", a.offsets, int64_t{p.num_groups} * 4}};
+  const Span out[] = {{"y", a.y, y_bytes}, {"c", a.c, c_bytes}};
+  if ((st = check_apart(in, out)) != MOEGG_OK) return st;
+  if (overlap(a.residual, p.m * n_out * 2, a.c, c_bytes))
+    return set_error(MOEGG_ERROR_INVALID_VALUE, "residual and c overlap");
   if (overlap(a.residual, p.m * n_out * 2, a.y, y_bytes) && (a.out_f32 || static_cast<const void*>(a.residual) != a.y))
     return set_error(MOEGG_ERROR_INVALID_VALUE, "residual and y overlap without being the same BF16 tensor");
   if (!any) return launched(hipSuccess, "linear");
@@ -473,11 +510,11 @@ moegg_status moegg_linear_backward(const moegg_linear_problem* problem, const mo
   st = check_linear_pointers(p, *args, moegg::linear_backward_workspace(a, a.dx, a.dw, a.db));
   if (st != MOEGG_OK) return st;
   const int64_t n_out = p.act == MOEGG_ACT_SWIGLU ? p.n / 2 : p.n;
-  const int64_t in[][2] = {{reinterpret_cast<int64_t>(a.x), p.m * p.k * 2}, {reinterpret_cast<int64_t>(a.dy), p.m * n_out * 2},
-                           {reinterpret_cast<int64_t>(a.c), p.m * p.n * 2}};
-  for (const auto& q : in)
-    if (overlap(reinterpret_cast<const void*>(q[0]), q[1], a.dx, p.m * p.k * 2))
-      return set_error(MOEGG_ERROR_INVALID_VALUE, "dx overlaps an input");
+  const Span in[] = {{"x", a.x, p.m * p.k * 2}, {"w", a.w, w_bytes(p)}, {"dy", a.dy, p.m * n_out * 2}, {"c", a.c, p.m * p.n * 2},
+                     {"offsets", a.offsets, int64_t{p.num_groups} * 4}};
+  const Span out[] = {{"dx", a.dx, p.m * p.k * 2}, {"dw", a.dw, w_bytes(p) * (a.out_f32 ? 2 : 1)},
+                      {"db", a.db, int64_t{p.num_groups} * p.n * 4}};
+  if ((st = check_apart(in, out)) != MOEGG_OK) return st;
   return launched(moegg::launch_linear_backward(a, static_cast<hipStream_t>(stream)), "linear backward kernel");
 }
 

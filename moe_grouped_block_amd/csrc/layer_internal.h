@@ -72,6 +72,14 @@ inline int32_t sort_blocks(int64_t slots) {
 }
 hipError_t launch_sort(const SortArgs& a, hipStream_t s);
 
+// A launch counts its threads in 32 bits; what would need more is refused.
+constexpr int64_t kLaunchThreads = (int64_t{1} << 32) - 1024;
+constexpr int kPadRows = 16;        // padding rows of one wave, see zero_padding()
+// Waves of the largest of the exchange's launches.
+inline int64_t exchange_waves(int64_t tokens, int64_t rows, int32_t width) {
+  return tokens * ((width + 511) / 512) + (rows + kPadRows - 1) / kPadRows;
+}
+
 // Format of the sorted rows.
 enum RowKind : int { ROW_BF16 = 0, ROW_E4M3 = 1, ROW_E5M2 = 2, ROW_E2M1 = 3 };
 

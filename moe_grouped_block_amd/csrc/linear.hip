@@ -315,12 +315,12 @@ __global__ __launch_bounds__(512) void linear_db_kernel(LinearArgs a, const floa
   __shared__ float red[16][33];
   const int lane = threadIdx.x & 63, x = threadIdx.x & 31, q = threadIdx.x >> 5, g = blockIdx.y;
   // tiles of the groups before g, and of g
-  int before = 0, mine = 0;
+  int64_t before = 0, mine = 0;
   if (a.offsets) {
     for (int i = lane; i <= g; i += 64) {
       int64_t b, e;
       group_rows(a, i, b, e);
-      const int t = static_cast<int>((e - b + kDzRows - 1) / kDzRows);
+      const int64_t t = (e - b + kDzRows - 1) / kDzRows;
       if (i < g) before += t;
       else mine = t;
     }
@@ -328,14 +328,15 @@ __global__ __launch_bounds__(512) void linear_db_kernel(LinearArgs a, const floa
       before += __shfl_xor(before, d);
       mine += __shfl_xor(mine, d);
     }
+    mine = min(mine, most_row_tiles<kDzRows>(a) - before);       // (offsets that decrease: none that were not summed)
   } else {
-    mine = static_cast<int>((a.m + kDzRows - 1) / kDzRows);
+    mine = most_row_tiles<kDzRows>(a);
   }
   const int n = blockIdx.x * 32 + x;
   float s = 0.0f;
   if (n < a.n) {
 #pragma unroll 4
-    for (int t = q; t < mine; t += 16) s += sums[static_cast<int64_t>(before + t) * a.n + n];
+    for (int64_t t = q; t < mine; t += 16) s += sums[(before + t) * a.n + n];
   }
   red[q][x] = s;
   __syncthreads();
@@ -355,7 +356,9 @@ int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t a, int64_t b) { return div_up(a, b) * b; }
 
 // Row tiles of all groups at most.
-int64_t row_tiles(const LinearArgs& a, int64_t bm) { return div_up(a.m, bm) + (a.groups > 1 ? a.groups - 1 : 0); }
+int64_t row_tiles(const LinearArgs& a, int bm) {
+  return bm == 64 ? most_row_tiles<64>(a) : bm == 128 ? most_row_tiles<128>(a) : most_row_tiles<256>(a);
+}
 
 // Tile shapes: how many workgroups the chip holds at once, and what a round of
 // them takes for a step of 64 r and for everything outside the steps, in

@@ -152,19 +152,26 @@ __device__ __forceinline__ void group_rows(const LinearArgs& a, int g, int64_t& 
   }
 }
 
+// Row tiles of all groups at most (and exactly, without offsets).
+template <int BM>
+__host__ __device__ __forceinline__ int64_t most_row_tiles(const LinearArgs& a) {
+  return (a.m + BM - 1) / BM + (a.groups > 1 ? a.groups - 1 : 0);
+}
+
 // Tiles of BM rows of every group (a tile holds rows of one group); the
-// groups run along the lanes, 64 at a time.
+// groups run along the lanes, 64 at a time.  Offsets that decrease name rows
+// several times: the tiles that the launch has no place for are left out.
 template <int BM>
 __device__ __forceinline__ int count_row_tiles(const LinearArgs& a, int lane) {
-  if (!a.offsets) return static_cast<int>((a.m + BM - 1) / BM);
-  int sum = 0;
+  if (!a.offsets) return static_cast<int>(most_row_tiles<BM>(a));
+  int64_t sum = 0;
   for (int g = lane; g < a.groups; g += 64) {
     int64_t b, e;
     group_rows(a, g, b, e);
-    sum += static_cast<int>((e - b + BM - 1) / BM);
+    sum += (e - b + BM - 1) / BM;
   }
   for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
-  return __builtin_amdgcn_readfirstlane(sum);
+  return __builtin_amdgcn_readfirstlane(static_cast<int>(min(sum, most_row_tiles<BM>(a))));
 }
 // Row tile mt: its group, first row and the end of the group's rows.
 template <int BM>

@@ -268,6 +268,21 @@ def test_foreign_plans_are_not_followed():
     assert torch.equal(d.cpu(), want) and (dw.cpu()[ok < 0] == 0).all()
 
 
+def test_combine_backward_without_rows():
+    """No rows: every slot is a dropped one, whose weight has the gradient 0."""
+    t, k, h = 5, 2, 64
+    gen = torch.Generator().manual_seed(2)
+    dy = torch.randn(t, h, generator=gen).to(torch.bfloat16).cuda()
+    plan = mg.SortPlan(3, 1, torch.zeros(3, dtype=torch.int32).cuda(), torch.full((t, k), -1, dtype=torch.int32).cuda(),
+                       torch.empty(0, dtype=torch.int32).cuda())
+    rows = torch.empty(0, h, dtype=torch.bfloat16).cuda()
+    before = torch.full((t, k), 7.0, device="cuda")      # what the next allocation of this size may hold
+    del before
+    d, dw = mg.combine_backward(dy, plan, rows=rows)
+    assert d.shape == (0, h) and (dw == 0).all()
+    assert (mg.combine(rows, plan) == 0).all()
+
+
 def test_more_than_two_to_the_31_elements():
     """Rows whose element numbers pass 32 bits: checked on the last rows."""
     t, k, e, h = 66000, 8, 16, 4096

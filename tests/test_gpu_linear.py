@@ -213,6 +213,64 @@ def test_foreign_offsets_stay_inside():
         assert y.shape == (m, n) and torch.isfinite(dw).all() and torch.isfinite(db).all()
 
 
+def test_offsets_that_name_rows_many_times():
+    """Ends that rise and fall name more row tiles than a launch has: all results
+    stay inside, for every kernel (wide, narrow, few rows)."""
+    groups = 256
+    off = torch.tensor([1000, 0] * (groups // 2), dtype=torch.int32).cuda()
+    for m, n, k in ((5000, 320, 200), (5000, 64, 64), (1000, 64, 64)):
+        print(f"[gpu-case] linear falling offsets m={m} n={n} k={k}", flush=True)
+        x, w, b, _, _, gen = make(m, n, k, "none", groups, 7)
+        dy = torch.randn(m, n, generator=gen).to(torch.bfloat16)
+        y = torch.full((m, n), 7.0, dtype=torch.bfloat16, device="cuda")
+        mg.linear(x.cuda(), w.cuda(), bias=b.cuda(), offsets=off, out=y)
+        assert (y[1000:] == 7).all() and torch.isfinite(y).all()
+        dx, dw, db = mg.linear_backward(dy.cuda(), x.cuda(), w.cuda(), offsets=off)
+        torch.cuda.synchronize()
+        assert torch.isfinite(dw).all() and torch.isfinite(db).all() and (dw[1::2] == 0).all() and (db[1::2] == 0).all()
+        # the first group's own rows come first in every count
+        d, xd = dy[:1000].double(), x[:1000].double()
+        r, mag = d.t() @ xd, d.abs().t() @ xd.abs()
+        assert ((dw[0].cpu().double() - r).abs() <= 1008 * ref.F32 * mag + ref.BF16 * r.abs()).all()
+        assert ((db[0].cpu().double() - d.sum(0)).abs() <= 1008 * ref.F32 * d.abs().sum(0)).all()
+
+
+@pytest.mark.parametrize("n,k", [(64, 2048), (2048, 64), (512, 2048)])
+def test_more_than_two_to_the_31_elements(n, k):
+    """Operands or results whose element numbers pass 32 bits: checked on the
+    last rows, and dw over all of them."""
+    m = 1100000
+    print(f"[gpu-case] linear m={m} n={n} k={k}", flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(m, k, generator=gen, device="cuda", dtype=torch.bfloat16)
+    w = (torch.randn(n, k, generator=gen, device="cuda") / math.sqrt(k)).to(torch.bfloat16)
+    y, c = mg.linear(x, w, act="srelu", save_c=True)
+    assert max(x.numel(), y.numel()) > 2 ** 31
+    wd = w.double()
+    for part in (slice(0, 300), slice(m - 300, m)):
+        xd = x[part].double()
+        z, mag = xd @ wd.t(), xd.abs() @ wd.abs().t()
+        assert ((c[part].double() - z).abs() <= (k + 8) * ref.F32 * mag * 1.01 + ref.BF16 * z.abs()).all()
+    del y, c
+    dy = torch.randn(m, n, generator=gen, device="cuda", dtype=torch.bfloat16)
+    dx, dw, db = mg.linear_backward(dy, x, w, dw_dtype="f32")
+    for part in (slice(0, 300), slice(m - 300, m)):
+        d = dy[part].double()
+        r, mag = d @ wd, d.abs() @ wd.abs()
+        assert ((dx[part].double() - r).abs() <= (n + 8) * ref.F32 * mag + ref.BF16 * r.abs()).all()
+    rows, cols = slice(0, 16), slice(k - 16, k)
+    r = torch.zeros(16, 16, dtype=torch.float64, device="cuda")
+    mag, s, sa = r.clone(), torch.zeros(n, dtype=torch.float64, device="cuda"), torch.zeros(n, dtype=torch.float64, device="cuda")
+    for at in range(0, m, 100000):
+        d, xd = dy[at:at + 100000].double(), x[at:at + 100000, cols].double()
+        r += d[:, rows].t() @ xd
+        mag += d[:, rows].abs().t() @ xd.abs()
+        s += d.sum(0)
+        sa += d.abs().sum(0)
+    assert ((dw[rows, cols].double() - r).abs() <= (m + 8) * ref.F32 * mag + ref.F32 * r.abs()).all()
+    assert ((db.double() - s).abs() <= (m + 8) * ref.F32 * sa).all()
+
+
 def test_activation_extremes():
     """Pre-activations from -1e30 to 1e30 give the activation's limits, no NaN."""
     for act in ("gelu", "swiglu", "srelu"):

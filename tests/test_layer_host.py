@@ -192,6 +192,35 @@ def test_linear_pointer_refusals(back, prob, args, want):
     assert _linear(back, prob, **args) == want, mg.moegg_last_error()
 
 
+@pytest.mark.parametrize("back,prob,args", [
+    (False, {}, dict(y=at(1))), (False, {}, dict(c=at(1, 16))), (False, {}, dict(bias=at(6, 4))),
+    (False, {}, dict(residual=at(7), c=at(7))), (False, {}, dict(offsets=at(6))),
+    (True, {}, dict(dx=at(1))), (True, {}, dict(dx=at(4))), (True, {}, dict(dw=at(0))), (True, {}, dict(dw=at(2, 16))),
+    (True, {}, dict(db=at(1))), (True, {}, dict(db=at(3, 4))), (True, dict(dtype=5), dict(dw=at(1))),
+])
+def test_linear_outputs_lie_apart(back, prob, args):
+    """An output that shares memory with an operand or another output is refused."""
+    size = mg._load().moegg_linear_backward_workspace(ctypes.byref(mg.moegg_linear_problem(100, 128, 64, 1, 0, 3)), 7)
+    if back:
+        args = dict(args, workspace=at(7), workspace_bytes=size)
+    assert _linear(back, prob, **args) == INVALID and "overlap" in mg.moegg_last_error()
+
+
+def test_launches_of_more_threads_than_32_bits_count_are_refused():
+    big = (1 << 31) - 1024
+    for prob in (dict(m=big, n=8, k=8), dict(m=big, n=8, k=512), dict(m=big, n=128, k=8),
+                 dict(m=8, n=1 << 20, k=8, num_groups=1024)):
+        for back in (False, True):
+            assert _linear(back, prob, offsets=at(7, 512)) == NOT_SUPPORTED and "threads" in mg.moegg_last_error()
+    assert mg._load().moegg_linear_workspace(ctypes.byref(mg.moegg_linear_problem(1 << 24, 64, 2048, 1, 0, 3))) >= 0
+    assert _route(dict(num_tokens=1 << 28, top_k=2)) == NOT_SUPPORTED and "threads" in mg.moegg_last_error()
+    assert _route(dict(num_tokens=1 << 26, num_experts=512, top_k=2)) == NOT_SUPPORTED
+    lib = mg._load()
+    for e in (_exchange(num_tokens=1 << 26, rows=1 << 26, top_k=1), _exchange(num_tokens=1 << 23, rows=1 << 10, width=8192)):
+        assert lib.moegg_dispatch(e, at(0), at(1), at(2), at(3), at(4), None, None) == NOT_SUPPORTED
+        assert lib.moegg_combine(e, at(0), at(1), None, None, at(4), None) == NOT_SUPPORTED
+
+
 def test_linear_workspace_of_invalid_problems():
     lib = mg._load()
     assert lib.moegg_linear_workspace(ctypes.byref(mg.moegg_linear_problem(m=-1))) == -1
