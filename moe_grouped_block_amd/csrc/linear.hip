@@ -360,19 +360,20 @@ int64_t row_tiles(const LinearArgs& a, int bm) {
   return bm == 64 ? most_row_tiles<64>(a) : bm == 128 ? most_row_tiles<128>(a) : most_row_tiles<256>(a);
 }
 
-// Tile shapes: how many workgroups the chip holds at once, and what a round of
-// them takes for a step of 64 r and for everything outside the steps, in
-// microseconds; `alone`: a step where at most half of them are there.  Per
-// product: forward, dx, dw.
+// Tile shapes: how many workgroups the chip holds at once, and what they take,
+// in microseconds: a step of 64 r where few of them are there, where half of
+// them are and where more are, and everything outside the steps.  Per product:
+// forward, dx, dw.  Fitted to sweeps of shapes and parts over 30 problems of 40
+// to 16384 rows; what was chosen was the best or within 10 % of it.
 enum Shape : int { SHAPE_256 = 0, SHAPE_128 = 1, SHAPE_64 = 2 };
 struct ShapeCost {
   int bp, bq, slots;
-  double step, alone, rest;
+  double few, half, step, rest;
 };
 constexpr ShapeCost kShapes[3][3] = {
-    {{256, 256, 256, 1.55, 1.10, 8.0}, {128, 128, 512, 1.10, 0.60, 5.0}, {64, 64, 256, 0.46, 0.22, 3.0}},
-    {{256, 256, 256, 1.40, 1.05, 8.0}, {128, 128, 512, 0.90, 0.56, 4.0}, {64, 64, 256, 0.46, 0.22, 3.0}},
-    {{256, 256, 256, 1.35, 1.00, 8.0}, {128, 128, 512, 0.90, 0.56, 4.0}, {64, 64, 256, 0.46, 0.22, 3.0}}};
+    {{256, 256, 256, 1.00, 1.20, 1.55, 8.0}, {128, 128, 512, 0.42, 0.58, 1.10, 5.0}, {64, 64, 256, 0.17, 0.22, 0.25, 4.0}},
+    {{256, 256, 256, 1.00, 1.10, 1.40, 8.0}, {128, 128, 512, 0.38, 0.53, 0.90, 4.8}, {64, 64, 256, 0.17, 0.22, 0.25, 4.0}},
+    {{256, 256, 256, 0.95, 1.05, 1.35, 8.0}, {128, 128, 512, 0.38, 0.53, 0.90, 4.8}, {64, 64, 256, 0.20, 0.25, 0.25, 4.0}}};
 
 struct Plan {
   Shape shape;
@@ -389,19 +390,17 @@ struct Plan {
 // (half of them are taken to be); `r`: length of the sum; `known`: the tiles
 // are these, and may be split.
 template <typename F, typename G>
-Plan choose(LinearMode mode, F&& tiles, G&& spare, int64_t cols, int64_t r, bool known) {
+Plan choose(LinearMode mode, F&& tiles, G&& spare, int64_t r, bool known) {
   Plan best{};
   double least = 0.0;
   const int64_t steps = div_up(r > 0 ? r : 1, kR);
   for (int s = 0; s < 3; ++s) {
     const ShapeCost& c = kShapes[mode][s];
     const int64_t total = tiles(c);
-    // the narrow tile is for narrow outputs
-    if ((s == SHAPE_64) != (cols <= 64)) continue;
     auto rounds = [&](int64_t n, int64_t st) {
       const int64_t left = n % c.slots;
       return static_cast<double>(n / c.slots) * (st * c.step + c.rest) +
-             (left ? st * (left <= c.slots / 2 ? c.alone : c.step) + c.rest : 0.0);
+             (left ? st * (left <= c.slots / 2 ? c.few + (c.half - c.few) * 2 * left / c.slots : c.step) + c.rest : 0.0);
     };
     auto take = [&](double cost, int64_t first, int parts) {
       if (least != 0.0 && cost >= least) return;
@@ -430,12 +429,12 @@ Plan choose(LinearMode mode, F&& tiles, G&& spare, int64_t cols, int64_t r, bool
 Plan plan_rows(const LinearArgs& a, LinearMode mode) {
   const int64_t cols = mode == MODE_FORWARD ? a.n : a.k, r = mode == MODE_FORWARD ? a.k : a.n;
   return choose(mode, [&](const ShapeCost& c) { return row_tiles(a, c.bp) * div_up(cols, c.bq); },
-                [&](const ShapeCost& c) { return (a.groups - 1) * div_up(cols, c.bq); }, cols, r, a.groups == 1 && !a.offsets);
+                [&](const ShapeCost& c) { return (a.groups - 1) * div_up(cols, c.bq); }, r, a.groups == 1 && !a.offsets);
 }
 Plan plan_dw(const LinearArgs& a) {
   // a group's share of the rows; groups whose rows the host does not know are not split
   return choose(MODE_DW, [&](const ShapeCost& c) { return a.groups * div_up(a.n, c.bp) * div_up(a.k, c.bq); },
-                [](const ShapeCost&) { return int64_t{0}; }, a.k, div_up(a.m, a.groups), a.groups == 1);
+                [](const ShapeCost&) { return int64_t{0}; }, div_up(a.m, a.groups), a.groups == 1);
 }
 bool few_rows(const LinearArgs& a) { return a.m <= 16 * static_cast<int64_t>(a.groups); }
 
