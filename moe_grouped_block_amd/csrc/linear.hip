@@ -310,10 +310,12 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinearArgs a, uint16_t* 
   }
 }
 
-// db of 32 columns of a group: 16 threads a column share the row tiles.
+// db of 512 / Q columns of a group: Q threads a column share the row tiles.
+template <int Q>
 __global__ __launch_bounds__(512) void linear_db_kernel(LinearArgs a, const float* sums) {
-  __shared__ float red[16][33];
-  const int lane = threadIdx.x & 63, x = threadIdx.x & 31, q = threadIdx.x >> 5, g = blockIdx.y;
+  constexpr int X = 512 / Q;
+  __shared__ float red[Q][X + 1];
+  const int lane = threadIdx.x & 63, x = threadIdx.x % X, q = threadIdx.x / X, g = blockIdx.y;
   // tiles of the groups before g, and of g
   int64_t before = 0, mine = 0;
   if (a.offsets) {
@@ -332,18 +334,18 @@ __global__ __launch_bounds__(512) void linear_db_kernel(LinearArgs a, const floa
   } else {
     mine = most_row_tiles<kDzRows>(a);
   }
-  const int n = blockIdx.x * 32 + x;
+  const int n = blockIdx.x * X + x;
   float s = 0.0f;
   if (n < a.n) {
 #pragma unroll 4
-    for (int64_t t = q; t < mine; t += 16) s += sums[(before + t) * a.n + n];
+    for (int64_t t = q; t < mine; t += Q) s += sums[(before + t) * a.n + n];
   }
   red[q][x] = s;
   __syncthreads();
   if (q == 0 && n < a.n) {
     float v = 0.0f;
 #pragma unroll
-    for (int y = 0; y < 16; ++y) v += red[y][x];
+    for (int y = 0; y < Q; ++y) v += red[y][x];
     a.db[static_cast<int64_t>(g) * a.n + n] = v;
   }
 }
@@ -571,8 +573,14 @@ hipError_t launch_linear_backward(const LinearArgs& args, hipStream_t s) {
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (a.db) {
-    hipLaunchKernelGGL(linear_db_kernel, dim3(static_cast<unsigned>(div_up(a.n, 32)), static_cast<unsigned>(a.groups)), dim3(512), 0,
-                       s, a, sums);
+    // few row tiles a group: few threads a column, or most of them only wait (64
+    // groups of 2048 columns, 4 tiles each: 15 us with 16 threads, 5 with 2)
+    if (row_tiles(a, kDzRows) <= 16 * static_cast<int64_t>(a.groups))
+      hipLaunchKernelGGL((linear_db_kernel<2>), dim3(static_cast<unsigned>(div_up(a.n, 256)), static_cast<unsigned>(a.groups)),
+                         dim3(512), 0, s, a, sums);
+    else
+      hipLaunchKernelGGL((linear_db_kernel<16>), dim3(static_cast<unsigned>(div_up(a.n, 32)), static_cast<unsigned>(a.groups)),
+                         dim3(512), 0, s, a, sums);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   const Plan pdx = plan_rows(a, MODE_DX), pdw = plan_dw(a);
