@@ -382,6 +382,7 @@ struct Plan {
   TilePlan tiles;
   int64_t workgroups;
   int64_t partial_bytes;
+  double cost;                // microseconds, by kShapes
 };
 
 // Which tile, and which tiles share their r among several workgroups: the
@@ -406,7 +407,7 @@ Plan choose(LinearMode mode, F&& tiles, G&& spare, int64_t r, bool known) {
     };
     auto take = [&](double cost, int64_t first, int parts) {
       if (least != 0.0 && cost >= least) return;
-      least = cost;
+      least = best.cost = cost;
       best.shape = static_cast<Shape>(s);
       best.tiles = {known ? static_cast<int>(total) : -1, static_cast<int>(first), parts};
       best.workgroups = first + (total - first) * parts;
@@ -438,7 +439,28 @@ Plan plan_dw(const LinearArgs& a) {
   return choose(MODE_DW, [&](const ShapeCost& c) { return a.groups * div_up(a.n, c.bp) * div_up(a.k, c.bq); },
                 [](const ShapeCost&) { return int64_t{0}; }, div_up(a.m, a.groups), a.groups == 1);
 }
-bool few_rows(const LinearArgs& a) { return a.m <= 16 * static_cast<int64_t>(a.groups); }
+bool few_rows(const LinearArgs& a) { return a.m <= kFewRows * static_cast<int64_t>(a.groups); }
+
+// The forward's tiles, of all rows but the last `few`: a handful of rows past
+// whole tiles would cost a row of tiles (often a round of its own, or a split
+// and a join), the kernel for few rows a launch and a pass over the weights.
+// Measured: 4099 x 2048 x 2816 64.3 -> 63.0 us, 2050 x 2048 x 2048 37.7 -> 30.0,
+// 8200 x 4096 x 4096 244 -> 230, 16390 x 64 x 2048 28.4 -> 24.0.
+struct ForwardPlan {
+  Plan tiles;
+  int64_t few;
+};
+ForwardPlan plan_forward(const LinearArgs& a) {
+  ForwardPlan f{plan_rows(a, MODE_FORWARD), 0};
+  const int64_t few = a.m % 128;
+  if (a.groups == 1 && !a.offsets && few && few <= kFewRows && few < a.m) {
+    LinearArgs b = a;
+    b.m -= few;
+    const Plan p = plan_rows(b, MODE_FORWARD);
+    if (p.cost + 5.0 + 2.0 * a.n * a.k / 5e6 < f.tiles.cost) f = {p, few};
+  }
+  return f;
+}
 
 template <int MODE, int BP, int BQ>
 void launch_join(const LinearArgs& a, const Plan& p, hipStream_t s) {
@@ -521,33 +543,45 @@ BackwardWorkspace backward_workspace(const LinearArgs& a, bool dx, bool dw, bool
 
 int64_t linear_workspace(const LinearArgs& a) {
   if (a.m == 0 || few_rows(a)) return 0;
-  return plan_rows(a, MODE_FORWARD).partial_bytes;
+  return plan_forward(a).tiles.partial_bytes;
 }
 int64_t linear_backward_workspace(const LinearArgs& a, bool dx, bool dw, bool db) {
   return backward_workspace(a, dx, dw, db).total;
 }
 
+// Many workgroups (groups): small ones of 4 waves and 32 columns, four to a
+// compute unit; few: 8 waves share a narrow tile, which reads fewer rows of
+// weights but deeper.  Measured, 64 groups of 2048 x 1408, 96 rows: 87 us
+// with 8 waves, 76 (4.8 TB/s of weights) with 4; one group of 8192 x 8192,
+// one row: 26 us (5.1 TB/s) with 8 waves, 34 with 4; 2816 x 2048 from the
+// last-level cache: 5.2 and 7.7 us.
+hipError_t launch_few_rows(const LinearArgs& a, hipStream_t s) {
+  const int64_t tiles = div_up(a.n, 16);
+  if (tiles * a.groups >= 2048)
+    hipLaunchKernelGGL((linear_few_rows_kernel<2, 4, 4>), dim3(static_cast<unsigned>(div_up(tiles, 2)), static_cast<unsigned>(a.groups)),
+                       dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((linear_few_rows_kernel<1, 8, 8>), dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(a.groups)), dim3(512), 0,
+                       s, a);
+  return hipGetLastError();
+}
+
 hipError_t launch_linear(const LinearArgs& args, hipStream_t s) {
   LinearArgs a = args;
   if (a.m == 0) return hipSuccess;
-  if (few_rows(a)) {
-    // Many workgroups (groups): small ones of 4 waves and 32 columns, four to a
-    // compute unit; few: 8 waves share a narrow tile, which reads fewer rows of
-    // weights but deeper.  Measured, 64 groups of 2048 x 1408, 96 rows: 87 us
-    // with 8 waves, 76 (4.8 TB/s of weights) with 4; one group of 8192 x 8192,
-    // one row: 26 us (5.1 TB/s) with 8 waves, 34 with 4; 2816 x 2048 from the
-    // last-level cache: 5.2 and 7.7 us.
-    const int64_t tiles = div_up(a.n, 16);
-    if (tiles * a.groups >= 2048)
-      hipLaunchKernelGGL((linear_few_rows_kernel<2, 4, 4>), dim3(static_cast<unsigned>(div_up(tiles, 2)), static_cast<unsigned>(a.groups)),
-                         dim3(256), 0, s, a);
-    else
-      hipLaunchKernelGGL((linear_few_rows_kernel<1, 8, 8>), dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(a.groups)), dim3(512),
-                         0, s, a);
-    return hipGetLastError();
-  }
+  if (few_rows(a)) return launch_few_rows(a, s);
   a.dx_partial = static_cast<float*>(a.workspace);
-  return launch_tiles<MODE_FORWARD>(a, plan_rows(a, MODE_FORWARD), s);
+  const ForwardPlan p = plan_forward(a);
+  a.m -= p.few;
+  const hipError_t e = launch_tiles<MODE_FORWARD>(a, p.tiles, s);
+  if (e != hipSuccess || !p.few) return e;
+  const int64_t n_out = a.act == LIN_SWIGLU ? a.n / 2 : a.n, m = a.m;
+  a.m = p.few;
+  a.x += m * a.k;
+  a.y = static_cast<uint8_t*>(a.y) + m * n_out * (a.out_f32 ? 4 : 2);
+  if (a.c) a.c += m * a.n;
+  if (a.residual) a.residual += m * n_out;
+  return launch_few_rows(a, s);
 }
 
 hipError_t launch_linear_backward(const LinearArgs& args, hipStream_t s) {

@@ -81,6 +81,13 @@ def test_forward_grouped(m, n, k, groups, act):
     check_forward(m, n, k, act, groups, seed=m + groups, residual=groups % 2 == 1)
 
 
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("m,dtype", [(4097, "bf16"), (4099, "f32"), (4112, "bf16"), (4113, "bf16")])
+def test_forward_few_rows_past_whole_tiles(m, act, dtype):
+    """A handful of rows behind whole tiles (up to 16 go by the kernel for few rows)."""
+    check_forward(m, 2048, 200, act, 0, seed=m, residual=True, dtype=dtype)
+
+
 def test_forward_long_sums():
     for m in (2, 40, 300):
         check_forward(m, 64, 16384, "none", 0)
