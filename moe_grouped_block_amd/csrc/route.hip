@@ -116,6 +116,12 @@ struct Row {
 #pragma unroll
     for (int j = 0; j < EPL; ++j) x[j] = x[j] > kMaxF ? kMaxF : x[j];   // NaN stays
   }
+  // one of them, of expert e
+  __device__ static __forceinline__ float one(const void* base, int64_t row, int experts, int e) {
+    const int64_t i = row * experts + e;
+    const float x = BF16 ? from_bf16(static_cast<const uint16_t*>(base)[i]) : static_cast<const float*>(base)[i];
+    return x > kMaxF ? kMaxF : x;
+  }
   __device__ static __forceinline__ void store(void* base, int64_t row, int experts, int lane, const float* x) {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
@@ -193,13 +199,16 @@ __device__ __forceinline__ void chosen_weights(const RouteArgs& a, float top, fl
 // ---- forward ---------------------------------------------------------------
 
 // The `rounds` largest keys of a token (-inf: cannot be chosen), largest
-// first, ties to the lowest expert: its ids[], logits[] and, where wanted,
-// keys[].  A round: the largest key of the token's lanes, the first expert
-// that has it, which is taken out.
+// first, ties to the lowest expert: its ids[] and, where wanted, keys[].  A
+// round: the largest key of the token's lanes, the first expert that has it,
+// which is taken out.  (The first of a lane's equal keys is singled out in the
+// masks of the comparisons, by scalar instructions: three vector instructions
+// a key.  With the logit carried along and the position compared again it was
+// six, and 16381 tokens of 256 experts took 17.6 us instead of 16.8.)
 __device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
 __device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
-template <typename R, int LPT, int EPL, int V, typename Key>
-__device__ __forceinline__ void choose(Key* key, const float* x, int rounds, int lane, int* ids, float* logits, Key* keys) {
+template <int LPT, int EPL, typename Key>
+__device__ __forceinline__ void choose(Key* key, int rounds, int lane, int* ids, Key* keys) {
   constexpr Key none = -static_cast<Key>(__builtin_inff());
   for (int j = 0; j < rounds; ++j) {
     Key mine = key[0];
@@ -211,17 +220,15 @@ __device__ __forceinline__ void choose(Key* key, const float* x, int rounds, int
     const uint64_t have = __ballot(mine == best) >> (threadIdx.x & 63 & ~(LPT - 1));
     if (lane == __builtin_ctzll(have)) {
       int at = 0;
-      float logit = kNegInf;
+      bool found = false;
 #pragma unroll
-      for (int q = EPL - 1; q >= 0; --q) {
-        at = key[q] == best ? q : at;
-        logit = key[q] == best ? x[q] : logit;
+      for (int q = 0; q < EPL; ++q) {
+        const bool hit = key[q] == best && !found;
+        found |= hit;
+        key[q] = hit ? none : key[q];
+        at = hit ? q : at;
       }
-#pragma unroll
-      for (int q = 0; q < EPL; ++q) key[q] = q == at ? none : key[q];
-      const bool there = best > none;
-      ids[j] = there ? lane * EPL + at : -1;
-      logits[j] = there ? logit : kNegInf;
+      ids[j] = best > none ? lane * EPL + at : -1;
       if (keys) keys[j] = best;
     }
   }
@@ -276,7 +283,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
   if constexpr (!BIAS) {
 #pragma unroll
     for (int j = 0; j < EPL; ++j) key[j] = x[j] > kNegInf ? x[j] : kNegInf;
-    choose<R, LPT, EPL, V, float>(key, x, k, lane, s_id[slot], s_logit[slot], nullptr);
+    choose<LPT, EPL, float>(key, k, lane, s_id[slot], s_logit[slot]);   // (the keys are the logits)
     wave_sync();
   } else {
     // a NaN in the softmax's sum leaves the choice among the others
@@ -303,12 +310,20 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
       }
     }
     const int cand = min(k + kSpare, a.experts);
-    choose<R, LPT, EPL, V, float>(key, x, cand, lane, s_id[slot], s_logit[slot], s_key[slot]);
+    choose<LPT, EPL, float>(key, cand, lane, s_id[slot], s_key[slot]);
     float rest = key[0];
 #pragma unroll
     for (int q = 1; q < EPL; ++q) rest = fmaxf(rest, key[q]);
     rest = lanes_max<LPT>(rest);                   // the best that is left
     wave_sync();
+    auto fetch_logits = [&](int n) __attribute__((always_inline)) {
+      for (int j = lane; j < n; j += LPT) {
+        const int e = s_id[slot][j];
+        s_logit[slot][j] = e >= 0 ? R::one(a.logits, row, a.experts, e) : kNegInf;
+      }
+      wave_sync();
+    };
+    fetch_logits(cand);
     // Choice j against the next: 0 clear, 1 the same numbers, 2 in doubt.  A key
     // is off by a rounding of its sum and by p's error: p <= 1, its exponential's
     // argument (p |x| < 0.4), the unit's last places and a sum of up to 16 + 6
@@ -354,7 +369,9 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
             const double q = exact[j] * dt + a.bias[e < a.experts ? e : 0];
             exact[j] = x[j] > kNegInf && q > -__builtin_inf() ? q : -__builtin_inf();
           }
-          choose<R, LPT, EPL, V, double>(exact, x, k, lane, s_id[slot], s_logit[slot], nullptr);
+          choose<LPT, EPL, double>(exact, k, lane, s_id[slot], nullptr);
+          wave_sync();
+          fetch_logits(k);
         } else {
           constexpr int N = (kSlots + LPT - 1) / LPT;
           double mine[N];
