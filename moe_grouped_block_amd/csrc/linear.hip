@@ -389,11 +389,10 @@ struct Plan {
 // cheapest by rounds of workgroups, where a last round that leaves most of the
 // chip empty (or the only one) may be split, against the bytes of its parts,
 // written and read at about 4 TB/s, and a join's launch.
-// `tiles(s)`: tiles of shape s at most, of which `spare(s)` may not be there
-// (half of them are taken to be); `r`: length of the sum; `known`: the tiles
-// are these, and may be split.
+// `tiles(s)`: tiles of shape s at most, of which `likely(s)` are taken to be
+// there; `r`: length of the sum; `known`: the tiles are these, and may be split.
 template <typename F, typename G>
-Plan choose(LinearMode mode, F&& tiles, G&& spare, int64_t r, bool known) {
+Plan choose(LinearMode mode, F&& tiles, G&& likely, int64_t r, bool known) {
   Plan best{};
   double least = 0.0;
   const int64_t steps = div_up(r > 0 ? r : 1, kR);
@@ -413,7 +412,7 @@ Plan choose(LinearMode mode, F&& tiles, G&& spare, int64_t r, bool known) {
       best.workgroups = first + (total - first) * parts;
       best.partial_bytes = parts > 1 ? (total - first) * parts * c.bp * c.bq * 4 : 0;
     };
-    take(rounds(total - spare(c) / 2, steps), total, 1);
+    take(rounds(likely(c), steps), total, 1);
     if (!known) continue;
     for (int64_t first : {int64_t{0}, total / c.slots * c.slots}) {
       if (first == total || (first == 0 && total > 2 * c.slots)) continue;
@@ -431,15 +430,27 @@ Plan choose(LinearMode mode, F&& tiles, G&& spare, int64_t r, bool known) {
 // is sized without knowing the offsets, so never too small.)
 Plan plan_rows(const LinearArgs& a, LinearMode mode) {
   const int64_t cols = mode == MODE_FORWARD ? a.n : a.k, r = mode == MODE_FORWARD ? a.k : a.n;
-  return choose(mode, [&](const ShapeCost& c) { return row_tiles(a, c.bp) * div_up(cols, c.bq); },
-                [&](const ShapeCost& c) { return (a.groups - 1) * div_up(cols, c.bq); }, r, a.groups == 1 && !a.offsets);
+  const auto tiles = [&](const ShapeCost& c) { return row_tiles(a, c.bp) * div_up(cols, c.bq); };
+  // half a tile of every group is not full, but a group with rows has one
+  const auto likely = [&](const ShapeCost& c) {
+    const int64_t most = row_tiles(a, c.bp), filled = a.m < a.groups ? a.m : a.groups, ragged = a.m / c.bp + a.groups / 2;
+    return (a.groups == 1 ? most : ragged < filled ? filled : ragged < most ? ragged : most) * div_up(cols, c.bq);
+  };
+  return choose(mode, tiles, likely, r, a.groups == 1 && !a.offsets);
 }
 Plan plan_dw(const LinearArgs& a) {
   // a group's share of the rows; groups whose rows the host does not know are not split
-  return choose(MODE_DW, [&](const ShapeCost& c) { return a.groups * div_up(a.n, c.bp) * div_up(a.k, c.bq); },
-                [](const ShapeCost&) { return int64_t{0}; }, div_up(a.m, a.groups), a.groups == 1);
+  const auto tiles = [&](const ShapeCost& c) { return a.groups * div_up(a.n, c.bp) * div_up(a.k, c.bq); };
+  return choose(MODE_DW, tiles, tiles, div_up(a.m, a.groups), a.groups == 1);
 }
-bool few_rows(const LinearArgs& a) { return a.m <= kFewRows * static_cast<int64_t>(a.groups); }
+// The kernel for few rows reads a group's weights once for every 16 of its
+// rows, so the rows must be few even where most of them are one group's.
+// Measured, against tiles, 64 groups of 2048 x 1408: 32 rows 27 / 28 us, 64
+// rows 37 / 51, 128 rows 59 / 61, 256 rows 68 / 64; with all rows in one
+// group 128 rows 39 / 18, 512 rows 155 / 18.
+bool few_rows(const LinearArgs& a) {
+  return a.m <= kFewRows || (a.m <= 2 * static_cast<int64_t>(a.groups) && a.m <= 8 * kFewRows);
+}
 
 // The forward's tiles, of all rows but the last `few`: a handful of rows past
 // whole tiles would cost a row of tiles (often a round of its own, or a split

@@ -225,7 +225,7 @@ def test_offsets_that_name_rows_many_times():
     stay inside, for every kernel (wide, narrow, few rows)."""
     groups = 256
     off = torch.tensor([1000, 0] * (groups // 2), dtype=torch.int32).cuda()
-    for m, n, k in ((5000, 320, 200), (5000, 64, 64), (1000, 64, 64)):
+    for m, n, k in ((5000, 320, 200), (5000, 64, 64), (1000, 64, 64), (100, 64, 64)):
         print(f"[gpu-case] linear falling offsets m={m} n={n} k={k}", flush=True)
         x, w, b, _, _, gen = make(m, n, k, "none", groups, 7)
         dy = torch.randn(m, n, generator=gen).to(torch.bfloat16)
