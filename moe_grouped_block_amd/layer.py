@@ -234,10 +234,11 @@ def sort_tokens(ids, num_experts: int, *, weights=None, m_aligned: int = 128, st
     s, guard = _on(dev, stream)
     try:
         # one allocation for the plan's tensors
-        sizes = (num_experts, shape[0] * shape[1], rows, rows) if w is not None else \
-            (num_experts, shape[0] * shape[1], rows)
-        offsets, row_of, slot_of, *prob = ids.new_empty(sum(sizes)).split(sizes)
-        row_of = row_of.view(shape)
+        slots = shape[0] * shape[1]
+        sizes = (slots, num_experts, rows, rows) if w is not None else (slots, num_experts, rows)
+        store = ids.new_empty(sum(sizes))
+        row_of = store.as_strided(shape, (shape[1], 1))
+        _, offsets, slot_of, *prob = torch.split_with_sizes(store, sizes)
         prob = prob[0].view(torch.float32) if prob else None
         ws = ids.new_empty(need, dtype=torch.uint8) if need else None
         _done(lib.moegg_sort(p, ids.data_ptr(), w, offsets.data_ptr(), row_of.data_ptr(), slot_of.data_ptr(),
