@@ -495,7 +495,7 @@ hipError_t launch_tiles(const LinearArgs& a, const Plan& p, hipStream_t s) {
       break;
     case SHAPE_128:
       if constexpr (MODE == MODE_FORWARD) {
-        if (p.workgroups > 256) hipLaunchKernelGGL((linear_tile_kernel<MODE, 128, 128, 2, 2>), grid, dim3(256), 0, s, a, t);
+        if (p.workgroups > 256) hipLaunchKernelGGL((linear_tile_kernel<128, 128, 2, 2>), grid, dim3(256), 0, s, a, t);
         else hipLaunchKernelGGL((linear_ring_kernel<MODE, 128, 128, 2, 2>), grid, dim3(256), 0, s, a, t);
       } else {
         hipLaunchKernelGGL((linear_ring_kernel<MODE, 128, 128, 2, 2>), grid, dim3(256), 0, s, a, t);

@@ -6,14 +6,15 @@
 //   dx        P = dz rows (m),  Q = w columns (k), r = n   Q contiguous along q
 //   dw        P = dz columns (n), Q = x columns (k), r = m   both contiguous along p / q
 //
-// One workgroup computes a BP x BQ tile in steps of 64 r.  Each step's two
-// operand tiles come into LDS by direct global -> LDS loads of 16 bytes a lane,
-// two stages deep.  An operand contiguous along r lies in LDS as rows of 64 r
-// (128 bytes) and is read with 16-byte reads; one contiguous along its rows
-// lies as 64 lines of its rows and is read with the transposing 8-byte reads
-// (ds_read_b64_tr_b16: 16 lanes read 4 lines of 16 elements, and each gets
-// one column's 4), so no operand is ever transposed in memory.  Both images are swizzled in 16-byte
-// chunks so that a read's lanes meet all banks once.
+// One workgroup computes a BP x BQ tile in steps of 64 r through two stages of
+// LDS, or of 32 r through four.  Each step's two operand tiles come into LDS by
+// direct global -> LDS loads of 16 bytes a lane.  An operand contiguous along r
+// lies in LDS as rows of the step's r (128 or 64 bytes) and is read with 16-byte
+// reads; one contiguous along its rows lies as lines of its rows, one for every
+// r, and is read with the transposing 8-byte reads (ds_read_b64_tr_b16: 16 lanes
+// read 4 lines of 16 elements, and each gets one column's 4), so no operand is
+// ever transposed in memory.  Both images are swizzled in 16-byte chunks so that
+// a read's lanes meet all banks once.
 //
 // The Q tile is the matrix instruction's first operand: a lane then holds
 // one row p of the output and runs of 4 contiguous columns.
@@ -25,8 +26,8 @@
 namespace moegg {
 namespace {
 
-constexpr int kR = 64;                 // r per step of the small tiles, and unit of their parts
-constexpr int kRingR = 32;             // r per step of the 256 x 256 tile
+constexpr int kR = 64;                 // r per step of the kernels with two stages, and unit of the parts of r
+constexpr int kRingR = 32;             // r per step of those with a ring of four
 
 // What a lane reads past the end of r: zeros.
 __device__ const uint32_t kZeros[4] = {0, 0, 0, 0};
@@ -485,12 +486,12 @@ __device__ __forceinline__ void store_output(const LinearArgs& a, v16f (&acc)[TM
   }
 }
 
-// The 128 x 128 tile, two stages of 64 r (the forward, see linear_ring_kernel).
-template <int MODE, int BP, int BQ, int WP, int WQ>
+// The forward's 128 x 128 tile, two stages of 64 r (see linear_ring_kernel).
+template <int BP, int BQ, int WP, int WQ>
 __global__ __launch_bounds__(64 * WP * WQ, 2) void linear_tile_kernel(LinearArgs a, TilePlan plan) {
   constexpr int NW = WP * WQ, TM = BP / WP / 32, TN = BQ / WQ / 32;
-  using TP = TileOperand<MODE != MODE_DW, BP, kR, NW>;
-  using TQ = TileOperand<MODE == MODE_FORWARD, BQ, kR, NW>;
+  using TP = TileOperand<true, BP, kR, NW>;
+  using TQ = TileOperand<true, BQ, kR, NW>;
   static_assert(TN == 2, "a wave's columns are one pair of 32-column blocks");
   // one array per stage and operand: the compiler then sees that a stage's
   // loads do not touch what is being read
@@ -500,20 +501,12 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void linear_tile_kernel(LinearArgs
   const int wp = wave / WQ, wq = wave % WQ;
 
   LinearTile t;
-  if (!locate<MODE, BP, BQ>(a, plan, blockIdx.x, lane, t)) return;
+  if (!locate<MODE_FORWARD, BP, BQ>(a, plan, blockIdx.x, lane, t)) return;
   const int64_t wg = static_cast<int64_t>(t.g) * a.n * a.k;
   TP p;
   TQ q;
-  if constexpr (MODE == MODE_FORWARD) {
-    p.init(a.x, a.k, t.row0, t.row_end, t.r0, wave, lane);
-    q.init(a.w + wg, a.k, t.col0, a.n, t.r0, wave, lane);
-  } else if constexpr (MODE == MODE_DX) {
-    p.init(a.dz, a.n, t.row0, t.row_end, t.r0, wave, lane);
-    q.init(a.w + wg, a.k, t.col0, a.k, t.r0, wave, lane);
-  } else {
-    p.init(a.dz, a.n, t.row0, a.n, t.r0, wave, lane);
-    q.init(a.x, a.k, t.col0, a.k, t.r0, wave, lane);
-  }
+  p.init(a.x, a.k, t.row0, t.row_end, t.r0, wave, lane);
+  q.init(a.w + wg, a.k, t.col0, a.n, t.r0, wave, lane);
   typename TP::template Frags<TM> fp;
   typename TQ::template Frags<TN> fq;
   fp.init(wp * (TM * 32), lane);
@@ -580,8 +573,8 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void linear_tile_kernel(LinearArgs
   // ---- the output ----
   uint8_t* const scratch = (wave & 1 ? sP1 : sP0) + (wave >> 1) * 4096;
   static_assert(TP::BYTES >= (NW + 1) / 2 * 4096, "scratch of the waves");
-  if (t.slot >= 0) store_part<BP, BQ>(partials<MODE>(a), acc, t.slot, wp * (TM * 32), wq * 64, scratch, lane);
-  else store_output<MODE>(a, acc, t.g, t.row0 + wp * (TM * 32), t.row_end, t.col0 + wq * 64, scratch, lane);
+  if (t.slot >= 0) store_part<BP, BQ>(partials<MODE_FORWARD>(a), acc, t.slot, wp * (TM * 32), wq * 64, scratch, lane);
+  else store_output<MODE_FORWARD>(a, acc, t.g, t.row0 + wp * (TM * 32), t.row_end, t.col0 + wq * 64, scratch, lane);
 }
 
 // The same tile in steps of 32 r through a ring of four stages: three stages

@@ -278,6 +278,48 @@ def test_more_than_two_to_the_31_elements(n, k):
     assert ((db.double() - s).abs() <= (m + 8) * ref.F32 * sa).all()
 
 
+# every kernel of the forward: few rows, the three tiles, parts of r and their join, few rows past whole tiles
+PATHS = [(5, 320, 200), (256, 512, 512), (300, 256, 4096), (1100, 1024, 512), (4099, 2048, 200), (8192, 2048, 520)]
+
+
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+@pytest.mark.parametrize("m,n,k", PATHS)
+def test_residual_in_place(m, n, k, act):
+    """y may be the residual itself: the same bits as in memory of its own."""
+    x, w, b, _, res, _ = make(m, n, k, act, 0, m, residual=True)
+    print(f"[gpu-case] linear in place m={m} n={n} k={k} {act}", flush=True)
+    want = mg.linear(x.cuda(), w.cuda(), bias=b.cuda(), act=act, residual=res.cuda())
+    y = res.cuda()
+    assert mg.linear(x.cuda(), w.cuda(), bias=b.cuda(), act=act, residual=y, out=y) is y
+    assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("m,n,k", PATHS)
+def test_captured_calls(m, n, k):
+    """Forward and backward in a graph, replayed between eager calls and on new inputs: the eager bits."""
+    x, w, b, _, res, gen = make(m, n, k, "swiglu", 0, m, residual=True)
+    dy = torch.randn(m, n // 2, generator=gen).to(torch.bfloat16)
+    xs = [x.cuda(), x.flip(0).contiguous().cuda(), (x * 0.5).cuda()]
+    w, b, res, dy = w.cuda(), b.cuda(), res.cuda(), dy.cuda()
+    print(f"[gpu-case] linear captured m={m} n={n} k={k}", flush=True)
+
+    def run(x):
+        y, c = mg.linear(x, w, bias=b, act="swiglu", residual=res, save_c=True)
+        return (y, c, *mg.linear_backward(dy, x, w, c=c, act="swiglu"))
+    held = xs[0].clone()
+    run(held)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run(held)
+    for x in xs:
+        held.copy_(x)
+        graph.replay()
+        want = run(x)
+        torch.cuda.synchronize()
+        assert all(torch.equal(u, v) for u, v in zip(got, want))
+
+
 def test_activation_extremes():
     """Pre-activations from -1e30 to 1e30 give the activation's limits, no NaN."""
     for act in ("gelu", "swiglu", "srelu"):
