@@ -367,7 +367,8 @@ moegg_status moegg_unsort(const float* rows_values, const int32_t* row_of, float
  * them, but what the rows then hold is not defined; y may be residual itself,
  * both BF16), or for all m rows where offsets is NULL (num_groups 1).
  * act: NONE, SRELU (relu(z)^2), GELU, or SWIGLU on [X | G] pairs of 32 columns
- * as in moegg_run (N_out = n / 2, else N_out = n).  Sums are fp32. */
+ * as in moegg_run (N_out = n / 2, else N_out = n).  Sums are fp32.  A NaN in z
+ * is a NaN in y, whatever the activation. */
 typedef struct moegg_linear_problem {
   int64_t m;            /* rows, 0..2^31-1024                                  */
   int32_t n;            /* multiple of 8 (64 for SWIGLU), <= 2^20              */

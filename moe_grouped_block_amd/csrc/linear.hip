@@ -109,7 +109,7 @@ __global__ __launch_bounds__(64 * NW) void linear_few_rows_kernel(LinearArgs a) 
         } else if (a.act == LIN_GELU) {
           y = gelu_f(z);
         } else if (a.act == LIN_SRELU) {
-          const float v = fmaxf(z, 0.0f);
+          const float v = relu_f(z);
           y = v * v;
         }
         if (store) {
@@ -177,7 +177,7 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs a, TilePlan
     } else if (a.act == LIN_SRELU) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float v = fmaxf(z[e], 0.0f);
+        const float v = relu_f(z[e]);
         z[e] = v * v;
       }
     }

@@ -264,6 +264,8 @@ constexpr float kGeluA = 0.044715f;
 __device__ __forceinline__ float gelu_f(float z) {
   return z * sigmoid_f(2.0f * kGeluC * z * (1.0f + kGeluA * z * z));
 }
+// relu(z), where a NaN stays one (fmaxf(z, 0) is 0 for it)
+__device__ __forceinline__ float relu_f(float z) { return z < 0.0f ? 0.0f : z; }
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
 
@@ -432,7 +434,7 @@ __device__ __forceinline__ void store_output(const LinearArgs& a, v16f (&acc)[TM
         for (int j = 0; j < TN; ++j)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float v = fmaxf(z[j][e], 0.0f);
+            const float v = relu_f(z[j][e]);
             z[j][e] = v * v;
           }
       }
