@@ -232,7 +232,7 @@ __device__ __forceinline__ void dz_of(const float* d, v4u c0, v4u c1, float* v, 
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if constexpr (ACT == LIN_SRELU) {
-        v[i] = d[i] * (2.0f * fmaxf(z[i], 0.0f));
+        v[i] = d[i] * (2.0f * relu_f(z[i]));
       } else {
         // past 30 s is 0 or 1: keeps 0 times z^3 from becoming NaN
         const float c = fminf(fmaxf(z[i], -30.0f), 30.0f);
