@@ -234,8 +234,8 @@ __device__ __forceinline__ void dz_of(const float* d, v4u c0, v4u c1, float* v, 
       if constexpr (ACT == LIN_SRELU) {
         v[i] = d[i] * (2.0f * relu_f(z[i]));
       } else {
-        // past 30 s is 0 or 1: keeps 0 times z^3 from becoming NaN
-        const float c = fminf(fmaxf(z[i], -30.0f), 30.0f);
+        // past 30 s is 0 or 1: keeps 0 times z^3 from becoming NaN (comparisons, so that a NaN stays one)
+        const float c = z[i] > 30.0f ? 30.0f : z[i] < -30.0f ? -30.0f : z[i];
         const float s = sigmoid_f(2.0f * kGeluC * c * (1.0f + kGeluA * c * c));
         v[i] = d[i] * (s + c * s * (1.0f - s) * (2.0f * kGeluC) * (1.0f + 3.0f * kGeluA * c * c));
       }

@@ -125,3 +125,9 @@ def check_backward(m, n, k, act, groups, dw_dtype):
                                           (2000, 512, 328, 3)])
 def test_backward_keeps_nan(m, n, k, groups, act):
     check_backward(m, n, k, act, groups, "f32" if m % 3 else "bf16")
+
+
+@pytest.mark.parametrize("m,n,k,groups", [(5, 320, 200, 0), (300, 256, 1032, 0), (2100, 512, 512, 0), (20, 128, 256, 16),
+                                          (2000, 512, 328, 3)])
+def test_gelu_backward_keeps_nan(m, n, k, groups):
+    check_backward(m, n, k, "gelu", groups, "f32" if m % 3 else "bf16")
