@@ -140,9 +140,9 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
     __syncthreads();
   }
   // padding rows of the experts, dealt out over the blocks, and rows behind
-  // the last expert
+  // the last expert (rows are counted in 64 bits: a thread's first may pass 2^31)
   for (int e = b; e < E; e += nb)
-    for (int64_t r = total[e] + tid; r < min(static_cast<int64_t>(finish[e]), a.rows); r += kSortThreads) {
+    for (int64_t r = static_cast<int64_t>(total[e]) + tid; r < min(static_cast<int64_t>(finish[e]), a.rows); r += kSortThreads) {
       a.slot_of[r] = -1;
       if (a.prob) a.prob[r] = 0.0f;
     }
