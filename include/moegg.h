@@ -407,7 +407,8 @@ moegg_status moegg_linear(const moegg_linear_problem* problem, const moegg_linea
  * dx = dz w_g (rows behind the last group left as they were); dw_g = dz^T x
  * and db_g = column sums of the unrounded dz over the group's rows (zero for
  * an empty group; rows behind the last group are not read).  Whatever is NULL
- * of dx, dw and db is not computed.  The residual's gradient is dy itself.  A
+ * of dx, dw and db is not computed (all three may be NULL where m is 0, else
+ * one is required).  The residual's gradient is dy itself.  A
  * NaN in c is a NaN in dz. */
 moegg_status moegg_linear_backward(const moegg_linear_problem* problem, const moegg_linear_args* args, void* stream);
 

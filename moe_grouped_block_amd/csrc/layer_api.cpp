@@ -502,7 +502,9 @@ moegg_status moegg_linear_backward(const moegg_linear_problem* problem, const mo
   const bool any = p.m > 0;
   if (a.bias || a.residual || a.y)
     return set_error(MOEGG_ERROR_INVALID_VALUE, "bias, residual and y are for moegg_linear");
-  if (!a.dx && !a.dw && !a.db) return set_error(MOEGG_ERROR_INVALID_VALUE, "one of dx, dw and db is required");
+  // (without rows dx has no elements, and its pointer may be NULL)
+  const bool none = !a.dx && !a.dw && !a.db;
+  if (any && none) return set_error(MOEGG_ERROR_INVALID_VALUE, "one of dx, dw and db is required");
   if (any && !a.dy) return set_error(MOEGG_ERROR_INVALID_VALUE, "dy is required");
   if (any && a.act != moegg::LIN_NONE && !a.c) return set_error(MOEGG_ERROR_INVALID_VALUE, "this activation's gradient needs c");
   if (any && a.dx && !a.w) return set_error(MOEGG_ERROR_INVALID_VALUE, "dx needs w");
@@ -515,6 +517,7 @@ moegg_status moegg_linear_backward(const moegg_linear_problem* problem, const mo
   const Span out[] = {{"dx", a.dx, p.m * p.k * 2}, {"dw", a.dw, w_bytes(p) * (a.out_f32 ? 2 : 1)},
                       {"db", a.db, int64_t{p.num_groups} * p.n * 4}};
   if ((st = check_apart(in, out)) != MOEGG_OK) return st;
+  if (none) return launched(hipSuccess, "linear backward");
   return launched(moegg::launch_linear_backward(a, static_cast<hipStream_t>(stream)), "linear backward kernel");
 }
 
