@@ -92,6 +92,13 @@ def _count(v, name: str) -> int:
     return v
 
 
+def _fits(*sizes) -> None:
+    """Refuse tensors' sizes that the C structs do not hold (a 32-bit field
+    would cut them without a word)."""
+    if max(sizes) >= 1 << 31:
+        raise ValueError(f"sizes {sizes}: above 2^31-1")
+
+
 class _Guard:
     """Makes a device and a stream other than the current ones current until
     close(), so that what a call allocates belongs to its stream."""
@@ -141,6 +148,7 @@ def _done(status: int) -> None:
 def _route_problem(logits, top_k, score, renormalise, scale):
     """The problem struct (fields in the order of the C struct)."""
     rows, experts = logits.shape
+    _fits(experts, top_k)
     return mg.moegg_route_problem(rows, experts, top_k, 3 if logits.dtype is torch.bfloat16 else 5,
                                   _code(mg.SCORES, score, "score"), 1 if renormalise else 0, scale)
 
@@ -228,6 +236,7 @@ def sort_tokens(ids, num_experts: int, *, weights=None, m_aligned: int = 128, st
     dev = _lead(ids, "ids", (torch.int32,), 2)
     shape = ids.shape
     w = None if weights is None else _want(weights, "weights", torch.float32, shape, dev)
+    _fits(shape[1])
     p = _sort_problem(shape[0], shape[1], num_experts, m_aligned)
     lib, rows = mg._load(), p.rows
     need = lib.moegg_sort_workspace(p)
@@ -301,6 +310,7 @@ def dispatch(x, plan: SortPlan, *, dtype="bf16", sf_layout: str = "row_major", o
     tokens, top_k, rows, row_of, slot_of, offsets = _plan_pointers(plan, dev)
     width = x.shape[1]
     xp = _want(x, "x", torch.bfloat16, (tokens, width), dev)
+    _fits(top_k, width)
     p = mg.moegg_exchange_problem(tokens, rows, top_k, plan.num_experts, width, kind, layout)
     s, guard = _on(dev, stream)
     try:
@@ -322,6 +332,7 @@ def combine(rows, plan: SortPlan, *, weights=None, residual=None, out=None, stre
     shape = (tokens, width)
     w = None if weights is None else _want(weights, "weights", torch.float32, (tokens, top_k), dev)
     r = None if residual is None else _want(residual, "residual", bf16, shape, dev)
+    _fits(top_k, width)
     p = mg.moegg_exchange_problem(tokens, n_rows, top_k, plan.num_experts, width, 3, 0)
     s, guard = _on(dev, stream)
     try:
@@ -345,6 +356,7 @@ def combine_backward(dy, plan: SortPlan, *, rows=None, weights=None, dtype="bf16
     dp = _want(dy, "dy", torch.bfloat16, (tokens, width), dev)
     rp = None if rows is None else _want(rows, "rows", torch.bfloat16, (n_rows, width), dev)
     w = None if weights is None else _want(weights, "weights", torch.float32, (tokens, top_k), dev)
+    _fits(top_k, width)
     p = mg.moegg_exchange_problem(tokens, n_rows, top_k, plan.num_experts, width, kind, layout)
     s, guard = _on(dev, stream)
     try:
@@ -400,6 +412,7 @@ def _linear_problem(x, w, act, dtype, offsets):
         groups, n = offsets.shape[0], w.shape[1]
         lead, op = (groups,), _want(offsets, "offsets", torch.int32, (groups,), dev)
     wp = _want(w, "w", bf16, (*lead, n, k), dev)
+    _fits(n, k, groups)
     return dev, mg.moegg_linear_problem(m, n, k, groups, act_code, dtype_code), lead, x.data_ptr(), wp, op
 
 
