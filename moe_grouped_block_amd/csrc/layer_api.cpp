@@ -29,9 +29,9 @@ moegg_status check_pointers(const Pointer (&ps)[N]) {
   return MOEGG_OK;
 }
 
-// Whether [a, a + na) and [b, b + nb) share a byte.
+// Whether [a, a + na) and [b, b + nb) share a byte (no byte, none shared).
 bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
-  if (!a || !b) return false;
+  if (!a || !b || na <= 0 || nb <= 0) return false;
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + static_cast<uintptr_t>(nb) && y < x + static_cast<uintptr_t>(na);
 }
@@ -85,6 +85,10 @@ moegg_status check_route(const moegg_route_problem* pp) {
     return set_error(MOEGG_ERROR_INVALID_VALUE, "renormalise=%d must be 0 or 1", p.renormalise);
   if (!std::isfinite(p.scale)) return set_error(MOEGG_ERROR_INVALID_VALUE, "scale must be finite");
   return MOEGG_OK;
+}
+
+int64_t logits_bytes(const moegg_route_problem& p) {
+  return p.num_tokens * p.num_experts * (p.dtype == MOEGG_DT_BF16 ? 2 : 4);
 }
 
 moegg::RouteArgs route_args(const moegg_route_problem& p) {
@@ -181,6 +185,9 @@ int64_t row_bytes(const moegg_exchange_problem& p) {
   const int64_t n = p.rows * p.width;
   return p.dtype == MOEGG_DT_BF16 ? 2 * n : p.dtype == MOEGG_DT_E2M1X2 ? n / 2 : n;
 }
+
+int64_t scale_bytes(const moegg_exchange_problem& p) { return p.rows * (p.width / 32); }
+int64_t slot_bytes(const moegg_exchange_problem& p) { return p.num_tokens * p.top_k * 4; }
 
 moegg_status check_scales(const moegg_exchange_problem& p, const uint8_t* sf) {
   const bool mx = p.dtype != MOEGG_DT_BF16;
@@ -283,6 +290,10 @@ moegg_status moegg_route(const moegg_route_problem* problem, const void* logits,
   st = check_pointers(ps);
   if (st != MOEGG_OK) return st;
   if (!any) return launched(hipSuccess, "route");
+  const int64_t chosen = problem->num_tokens * problem->top_k * 4;
+  const Span in[] = {{"logits", logits, logits_bytes(*problem)}, {"bias", bias, int64_t{problem->num_experts} * 4}};
+  const Span out[] = {{"ids", ids, chosen}, {"weights", weights, chosen}};
+  if ((st = check_apart(in, out)) != MOEGG_OK) return st;
   moegg::RouteArgs a = route_args(*problem);
   a.logits = logits;
   a.bias = bias;
@@ -299,11 +310,11 @@ moegg_status moegg_route_backward(const moegg_route_problem* problem, const void
   const Pointer ps[] = {{"logits", logits, 16, any}, {"dlogits", dlogits, 16, any}, {"ids", ids, 4, any}, {"dweights", dweights, 4, any}};
   st = check_pointers(ps);
   if (st != MOEGG_OK) return st;
-  if (any) {
-    const int64_t bytes = problem->num_tokens * problem->num_experts * (problem->dtype == MOEGG_DT_BF16 ? 2 : 4);
-    if (overlap(logits, bytes, dlogits, bytes)) return set_error(MOEGG_ERROR_INVALID_VALUE, "logits and dlogits overlap");
-  }
   if (!any) return launched(hipSuccess, "route");
+  const int64_t chosen = problem->num_tokens * problem->top_k * 4;
+  const Span in[] = {{"logits", logits, logits_bytes(*problem)}, {"ids", ids, chosen}, {"dweights", dweights, chosen}};
+  const Span out[] = {{"dlogits", dlogits, logits_bytes(*problem)}};
+  if ((st = check_apart(in, out)) != MOEGG_OK) return st;
   moegg::RouteArgs a = route_args(*problem);
   a.logits = logits;
   a.ids = const_cast<int32_t*>(ids);
@@ -342,6 +353,11 @@ moegg_status moegg_sort(const moegg_sort_problem* problem, const int32_t* ids, c
   const int64_t need = sort_workspace_bytes(p);
   if (need > 0 && (!workspace || workspace_bytes < need))
     return set_error(MOEGG_ERROR_INVALID_VALUE, "workspace of %lld bytes needed", (long long)need);
+  const int64_t slot_bytes = p.num_tokens * p.top_k * 4;
+  const Span in[] = {{"ids", ids, slot_bytes}, {"weights", weights, slot_bytes}};
+  const Span out[] = {{"padded_offsets", padded_offsets, int64_t{p.num_experts} * 4}, {"row_of", row_of, slot_bytes},
+                      {"slot_of", slot_of, p.rows * 4}, {"prob", prob, p.rows * 4}, {"workspace", workspace, need}};
+  if ((st = check_apart(in, out)) != MOEGG_OK) return st;
   moegg::SortArgs a{};
   a.ids = ids;
   a.weights = weights;
@@ -371,8 +387,10 @@ moegg_status moegg_dispatch(const moegg_exchange_problem* problem, const void* x
   st = check_pointers(ps);
   if (st != MOEGG_OK) return st;
   if (any && (st = check_scales(p, sf)) != MOEGG_OK) return st;
-  if (overlap(x, p.num_tokens * p.width * 2, out, row_bytes(p)))
-    return set_error(MOEGG_ERROR_INVALID_VALUE, "x and out overlap");
+  const Span in[] = {{"x", x, p.num_tokens * p.width * 2}, {"row_of", row_of, slot_bytes(p)}, {"slot_of", slot_of, p.rows * 4},
+                     {"padded_offsets", padded_offsets, int64_t{p.num_experts} * 4}};
+  const Span outs[] = {{"out", out, row_bytes(p)}, {"sf", sf, scale_bytes(p)}};
+  if (any && (st = check_apart(in, outs)) != MOEGG_OK) return st;
   if (!any) return launched(hipSuccess, "dispatch");
   moegg::ExchangeArgs a = exchange_args(p);
   a.x = static_cast<const uint16_t*>(x);
@@ -396,7 +414,9 @@ moegg_status moegg_combine(const moegg_exchange_problem* problem, const void* ro
   st = check_pointers(ps);
   if (st != MOEGG_OK) return st;
   const int64_t y_bytes = p.num_tokens * p.width * 2;
-  if (overlap(rows_in, row_bytes(p), y, y_bytes)) return set_error(MOEGG_ERROR_INVALID_VALUE, "rows_in and y overlap");
+  const Span in[] = {{"rows_in", rows_in, row_bytes(p)}, {"row_of", row_of, slot_bytes(p)}, {"weights", weights, slot_bytes(p)}};
+  const Span out[] = {{"y", y, y_bytes}};
+  if ((st = check_apart(in, out)) != MOEGG_OK) return st;
   if (residual != y && overlap(residual, y_bytes, y, y_bytes))
     return set_error(MOEGG_ERROR_INVALID_VALUE, "residual and y overlap without being the same tensor");
   if (!any) return launched(hipSuccess, "combine");
@@ -426,9 +446,11 @@ moegg_status moegg_combine_backward(const moegg_exchange_problem* problem, const
   if (rows && (st = check_scales(p, sf)) != MOEGG_OK) return st;
   if (rows && (rows_in != nullptr) != (dweights != nullptr))
     return set_error(MOEGG_ERROR_INVALID_VALUE, "rows_in and dweights come together");
-  const int64_t t_bytes = p.num_tokens * p.width * 2;
-  if (overlap(dy, t_bytes, out, row_bytes(p)) || overlap(rows_in, p.rows * p.width * 2, out, row_bytes(p)))
-    return set_error(MOEGG_ERROR_INVALID_VALUE, "out overlaps an input");
+  const Span in[] = {{"dy", dy, p.num_tokens * p.width * 2}, {"row_of", row_of, slot_bytes(p)}, {"slot_of", slot_of, p.rows * 4},
+                     {"padded_offsets", padded_offsets, int64_t{p.num_experts} * 4},
+                     {"rows_in", rows_in, p.rows * p.width * 2}, {"weights", weights, slot_bytes(p)}};
+  const Span outs[] = {{"out", out, row_bytes(p)}, {"sf", sf, scale_bytes(p)}, {"dweights", dweights, slot_bytes(p)}};
+  if (any && (st = check_apart(in, outs)) != MOEGG_OK) return st;
   if (!any) return launched(hipSuccess, "combine backward");
   moegg::ExchangeArgs a = exchange_args(p);
   a.x = static_cast<const uint16_t*>(dy);
@@ -449,8 +471,11 @@ moegg_status moegg_unsort(const float* rows_values, const int32_t* row_of, float
     return set_error(MOEGG_ERROR_INVALID_VALUE, "num_slots=%lld rows=%lld outside 0..2^31-1", (long long)num_slots, (long long)rows);
   const bool any = num_slots > 0;
   const Pointer ps[] = {{"rows_values", rows_values, 4, any && rows > 0}, {"row_of", row_of, 4, any}, {"values", values, 4, any}};
-  const moegg_status st = check_pointers(ps);
+  moegg_status st = check_pointers(ps);
   if (st != MOEGG_OK) return st;
+  const Span in[] = {{"rows_values", rows_values, rows * 4}, {"row_of", row_of, num_slots * 4}};
+  const Span out[] = {{"values", values, num_slots * 4}};
+  if ((st = check_apart(in, out)) != MOEGG_OK) return st;
   if (!any) return launched(hipSuccess, "unsort");
   return launched(moegg::launch_unsort(rows_values, row_of, values, num_slots, rows, static_cast<hipStream_t>(stream)),
                   "unsort kernel");
@@ -476,17 +501,18 @@ moegg_status moegg_linear(const moegg_linear_problem* problem, const moegg_linea
   if (any && (!a.x || !a.w || !a.y)) return set_error(MOEGG_ERROR_INVALID_VALUE, "x, w and y are required");
   if (a.dy || a.dx || a.dw || a.db)
     return set_error(MOEGG_ERROR_INVALID_VALUE, "dy, dx, dw and db are for moegg_linear_backward");
-  st = check_linear_pointers(p, *args, moegg::linear_workspace(a));
+  const int64_t workspace = moegg::linear_workspace(a);
+  st = check_linear_pointers(p, *args, workspace);
   if (st != MOEGG_OK) return st;
   const int64_t n_out = p.act == MOEGG_ACT_SWIGLU ? p.n / 2 : p.n;
   const int64_t y_bytes = p.m * n_out * (a.out_f32 ? 4 : 2);
   const int64_t c_bytes = p.m * p.n * 2;
   const Span in[] = {{"x", a.x, p.m * p.k * 2}, {"w", a.w, w_bytes(p)}, {"bias", a.bias, int64_t{p.num_groups} * p.n * 4},
                      {"offsets", a.offsets, int64_t{p.num_groups} * 4}};
-  const Span out[] = {{"y", a.y, y_bytes}, {"c", a.c, c_bytes}};
+  const Span out[] = {{"y", a.y, y_bytes}, {"c", a.c, c_bytes}, {"workspace", a.workspace, workspace}};
   if ((st = check_apart(in, out)) != MOEGG_OK) return st;
-  if (overlap(a.residual, p.m * n_out * 2, a.c, c_bytes))
-    return set_error(MOEGG_ERROR_INVALID_VALUE, "residual and c overlap");
+  if (overlap(a.residual, p.m * n_out * 2, a.c, c_bytes) || overlap(a.residual, p.m * n_out * 2, a.workspace, workspace))
+    return set_error(MOEGG_ERROR_INVALID_VALUE, "residual and c or the workspace overlap");
   if (overlap(a.residual, p.m * n_out * 2, a.y, y_bytes) && (a.out_f32 || static_cast<const void*>(a.residual) != a.y))
     return set_error(MOEGG_ERROR_INVALID_VALUE, "residual and y overlap without being the same BF16 tensor");
   if (!any) return launched(hipSuccess, "linear");
@@ -509,13 +535,14 @@ moegg_status moegg_linear_backward(const moegg_linear_problem* problem, const mo
   if (any && a.act != moegg::LIN_NONE && !a.c) return set_error(MOEGG_ERROR_INVALID_VALUE, "this activation's gradient needs c");
   if (any && a.dx && !a.w) return set_error(MOEGG_ERROR_INVALID_VALUE, "dx needs w");
   if (any && a.dw && !a.x) return set_error(MOEGG_ERROR_INVALID_VALUE, "dw needs x");
-  st = check_linear_pointers(p, *args, moegg::linear_backward_workspace(a, a.dx, a.dw, a.db));
+  const int64_t workspace = moegg::linear_backward_workspace(a, a.dx, a.dw, a.db);
+  st = check_linear_pointers(p, *args, workspace);
   if (st != MOEGG_OK) return st;
   const int64_t n_out = p.act == MOEGG_ACT_SWIGLU ? p.n / 2 : p.n;
   const Span in[] = {{"x", a.x, p.m * p.k * 2}, {"w", a.w, w_bytes(p)}, {"dy", a.dy, p.m * n_out * 2}, {"c", a.c, p.m * p.n * 2},
                      {"offsets", a.offsets, int64_t{p.num_groups} * 4}};
   const Span out[] = {{"dx", a.dx, p.m * p.k * 2}, {"dw", a.dw, w_bytes(p) * (a.out_f32 ? 2 : 1)},
-                      {"db", a.db, int64_t{p.num_groups} * p.n * 4}};
+                      {"db", a.db, int64_t{p.num_groups} * p.n * 4}, {"workspace", a.workspace, workspace}};
   if ((st = check_apart(in, out)) != MOEGG_OK) return st;
   if (none) return launched(hipSuccess, "linear backward");
   return launched(moegg::launch_linear_backward(a, static_cast<hipStream_t>(stream)), "linear backward kernel");
