@@ -13,22 +13,27 @@ plus ``make_problem`` / ``make_args`` (fill the C structs from a problem dict
 and torch tensors' device pointers) and ``run`` / ``check`` (build the structs,
 call, raise ``MoeggError`` on a non-OK status).  The layer operators
 around the grouped product (``route``, ``sort_tokens``, ``dispatch``,
-``combine``, ``linear`` and their gradients) are called with torch tensors
-and live in ``layer``.  Every step of the computation
+``combine``, ``linear`` and their gradients) are called with torch tensors,
+live in ``layer`` and are imported at their first use.  Every step of the computation
 runs in the HIP library; this module never computes.  If ``libmoegg.so`` has
 not been built the first call raises ``RuntimeError``: there is no fallback.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib
+import importlib.util
 import os
 
 __all__ = ["MoeggError", "moegg_check", "moegg_run", "moegg_check_offsets", "moegg_n_out",
            "moegg_status_string", "moegg_last_error", "moegg_abi_version", "moegg_set_grid_limit", "make_problem",
            "make_args", "run", "check", "lib_path", "ABI_VERSION", "DTYPES", "ACTS", "STATUS", "SF_LAYOUTS",
-           "moegg_sf_to_kplanes", "sf_to_kplanes", "SCORES", "route", "route_backward", "SortPlan", "sort_tokens",
-           "sort_rows", "dispatch", "dispatch_backward", "combine", "combine_backward", "unsort", "linear",
-           "linear_backward"]
+           "moegg_sf_to_kplanes", "sf_to_kplanes", "SCORES"]
+# the layer operators are imported at their first use: they need torch, which the rest does not
+_LAYER = ("route", "route_backward", "SortPlan", "sort_tokens", "sort_rows", "dispatch", "dispatch_backward",
+          "combine", "combine_backward", "unsort", "linear", "linear_backward")
+if importlib.util.find_spec("torch") is not None:
+    __all__ += _LAYER
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libmoegg.so")
@@ -252,6 +257,13 @@ def run(problem: dict, tensors: dict, stream=None) -> None:
         raise MoeggError(st, moegg_last_error())
 
 
-# the layer operators (they use the names above)
-from .layer import (SortPlan, combine, combine_backward, dispatch, dispatch_backward, linear, linear_backward,  # noqa: E402
-                    route, route_backward, sort_rows, sort_tokens, unsort)
+def __getattr__(name: str):
+    if name != "layer" and name not in _LAYER:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    layer = importlib.import_module(".layer", __name__)
+    globals().update({n: getattr(layer, n) for n in _LAYER})
+    return layer if name == "layer" else globals()[name]
+
+
+def __dir__():
+    return sorted({*globals(), *_LAYER, "layer"})
