@@ -89,7 +89,7 @@
 extern "C" {
 #endif
 
-#define MOEGG_ABI_VERSION 5
+#define MOEGG_ABI_VERSION 5 /* counts changes of the structs and of what a function takes, not new functions */
 
 typedef enum moegg_status {
   MOEGG_OK = 0,

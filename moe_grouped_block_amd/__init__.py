@@ -38,7 +38,7 @@ if importlib.util.find_spec("torch") is not None:
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libmoegg.so")
 
-ABI_VERSION = 5   # MOEGG_ABI_VERSION of the structs below
+ABI_VERSION = 5   # MOEGG_ABI_VERSION: counts changes of the structs below, not new functions
 DTYPES = {None: 0, "none": 0, "e4m3": 1, "e2m1x2": 2, "bf16": 3, "e5m2": 4, "f32": 5}
 ACTS = {"none": 0, "swiglu": 1, "srelu": 2, "dswiglu": 3, "dsrelu": 4, "geglu": 5, "dgeglu": 6, "gelu": 7}
 SCORES = {"softmax": 0, "sigmoid": 1}
@@ -109,25 +109,34 @@ def _load():
             raise RuntimeError(f"{lib_path} is not built; run __graft_entry__.build() "
                                "(there is no fallback path)")
         lib = ctypes.CDLL(lib_path)
-        P, A = ctypes.POINTER(moegg_problem), ctypes.POINTER(moegg_args)
-        lib.moegg_check.argtypes, lib.moegg_check.restype = [P, A], ctypes.c_int
-        lib.moegg_run.argtypes, lib.moegg_run.restype = [P, A, ctypes.c_void_p], ctypes.c_int
-        lib.moegg_check_offsets.argtypes = [P, ctypes.c_void_p, ctypes.c_void_p]
-        lib.moegg_check_offsets.restype = ctypes.c_int
-        lib.moegg_n_out.argtypes, lib.moegg_n_out.restype = [P], ctypes.c_int64
-        lib.moegg_status_string.argtypes, lib.moegg_status_string.restype = [ctypes.c_int], ctypes.c_char_p
-        lib.moegg_last_error.argtypes, lib.moegg_last_error.restype = [], ctypes.c_char_p
-        lib.moegg_abi_version.argtypes, lib.moegg_abi_version.restype = [], ctypes.c_int
-        lib.moegg_set_grid_limit.argtypes, lib.moegg_set_grid_limit.restype = [ctypes.c_int], ctypes.c_int
-        lib.moegg_sf_to_kplanes.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32,
-                                            ctypes.c_void_p]
-        lib.moegg_sf_to_kplanes.restype = ctypes.c_int
-        _declare_layer(lib)
-        if lib.moegg_abi_version() != ABI_VERSION:
-            raise RuntimeError(f"{lib_path} has ABI {lib.moegg_abi_version()}, these bindings "
-                               f"expect {ABI_VERSION}: rebuild it with __graft_entry__.build()")
+        try:
+            lib.moegg_abi_version.argtypes, lib.moegg_abi_version.restype = [], ctypes.c_int
+            if lib.moegg_abi_version() != ABI_VERSION:
+                raise RuntimeError(f"{lib_path} has ABI {lib.moegg_abi_version()}, these bindings "
+                                   f"expect {ABI_VERSION}: rebuild it with __graft_entry__.build()")
+            _declare(lib)
+            _declare_layer(lib)
+        except AttributeError as e:
+            raise RuntimeError(f"{lib_path} lacks a function that these bindings call ({e}): "
+                               "rebuild it with __graft_entry__.build()") from None
         _lib = lib
     return _lib
+
+
+def _declare(lib) -> None:
+    """Signatures of the grouped product's functions."""
+    P, A = ctypes.POINTER(moegg_problem), ctypes.POINTER(moegg_args)
+    lib.moegg_check.argtypes, lib.moegg_check.restype = [P, A], ctypes.c_int
+    lib.moegg_run.argtypes, lib.moegg_run.restype = [P, A, ctypes.c_void_p], ctypes.c_int
+    lib.moegg_check_offsets.argtypes = [P, ctypes.c_void_p, ctypes.c_void_p]
+    lib.moegg_check_offsets.restype = ctypes.c_int
+    lib.moegg_n_out.argtypes, lib.moegg_n_out.restype = [P], ctypes.c_int64
+    lib.moegg_status_string.argtypes, lib.moegg_status_string.restype = [ctypes.c_int], ctypes.c_char_p
+    lib.moegg_last_error.argtypes, lib.moegg_last_error.restype = [], ctypes.c_char_p
+    lib.moegg_set_grid_limit.argtypes, lib.moegg_set_grid_limit.restype = [ctypes.c_int], ctypes.c_int
+    lib.moegg_sf_to_kplanes.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32,
+                                        ctypes.c_void_p]
+    lib.moegg_sf_to_kplanes.restype = ctypes.c_int
 
 
 def _declare_layer(lib) -> None:
