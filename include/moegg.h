@@ -46,8 +46,10 @@
  *   MOEGG_SF_KPLANES).  Each pointer must be 16-byte aligned
  *   (the kernel ignores its low 4 bits); entries of experts with no rows are
  *   never read.
- *   padded_offsets (L) int32, cumulative group ends; padded_offsets[L-1] ==
- *                          valid_m; every entry a multiple of m_aligned and
+ *   padded_offsets (L) int32, cumulative group ends; padded_offsets[L-1] <=
+ *                          valid_m (the pages: equal to it; where it is less,
+ *                          the rows behind it are neither read nor written);
+ *                          every entry a multiple of m_aligned and
  *                          nondecreasing (empty groups repeat the previous end)
  *   alpha, beta (L) fp32; prob (valid_m) fp32; norm_const (1) fp32
  *   C       (valid_m, N) BF16                      [optional forward output]
@@ -145,8 +147,9 @@ typedef enum moegg_act {
 typedef struct moegg_problem {
   int32_t num_groups;   /* L, 1..1024 ("Shapes and Divisibility": expert count <= 1024) */
   int32_t m_aligned;    /* group row alignment; multiple of 128 here                     */
-  int64_t valid_m;      /* rows of A == padded_offsets[L-1] (or more: rows behind the last
-                           group are left as they were); multiple of m_aligned, < 2^31 here */
+  int64_t valid_m;      /* rows of A and of every row tensor: padded_offsets[L-1], or more (rows
+                           behind the last group are left as they were); multiple of
+                           m_aligned, < 2^31 here                                         */
   int32_t n;            /* GEMM N (rows of each expert's B); multiple of 32, <= 2^20 here
                            (64 for SwiGLU / GeGLU)                                        */
   int32_t k;            /* reduction length K; multiple of 128 bytes per row here (128
@@ -196,9 +199,9 @@ typedef struct moegg_args {
  * and Constraints: §Layouts and Strides (16-byte alignment), §Data Types and
  * §Additional Type Constraints (A and B of one dtype, the SFD trio together),
  * §Scale Factor Output Requirements (amax with a BF16 D), §Shapes and
- * Divisibility (L <= 1024, groups aligned to m_aligned, valid_m =
- * padded_offsets[L-1]); "Grouped GEMM + dGLU (SM100)", §Support Surface and
- * Constraints for the backward tensors), plus this library's own limits,
+ * Divisibility (L <= 1024, groups aligned to m_aligned; that valid_m covers
+ * padded_offsets[L-1] is device data and not checked here); "Grouped GEMM +
+ * dGLU (SM100)", §Support Surface and Constraints for the backward tensors), plus this library's own limits,
  * reported as MOEGG_ERROR_NOT_SUPPORTED (K a multiple of 128 bytes per row,
  * N a multiple of 32, m_aligned a multiple of 128). */
 moegg_status moegg_check(const moegg_problem* problem, const moegg_args* args);
@@ -215,7 +218,10 @@ moegg_status moegg_run(const moegg_problem* problem, const moegg_args* args, voi
  * cumulative sum of aligned group sizes with valid_m its last entry; §Shapes
  * and Divisibility: every group aligned to m_aligned): entries nondecreasing,
  * multiples of m_aligned, last == valid_m.  MOEGG_OK or
- * MOEGG_ERROR_INVALID_VALUE (MOEGG_ERROR_LAUNCH if the copy fails). */
+ * MOEGG_ERROR_INVALID_VALUE (MOEGG_ERROR_LAUNCH if the copy fails).  Where
+ * valid_m is a capacity (moegg_sort_rows) and not the rows in use, which only
+ * the device knows, this is stricter than moegg_run: a plan of moegg_sort is
+ * checked with its last offset as valid_m. */
 moegg_status moegg_check_offsets(const moegg_problem* problem, const int32_t* padded_offsets,
                                  void* stream);
 
