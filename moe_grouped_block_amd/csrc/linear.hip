@@ -232,7 +232,8 @@ __device__ __forceinline__ void dz_of(const float* d, v4u c0, v4u c1, float* v, 
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if constexpr (ACT == LIN_SRELU) {
-        v[i] = d[i] * (2.0f * relu_f(z[i]));
+        const float t = d[i] * relu_f(z[i]);           // (2 z may overflow where 2 d z does not)
+        v[i] = t + t;
       } else {
         // past 30 s is 0 or 1: keeps 0 times z^3 from becoming NaN (comparisons, so that a NaN stays one)
         const float c = z[i] > 30.0f ? 30.0f : z[i] < -30.0f ? -30.0f : z[i];
