@@ -92,11 +92,11 @@ def _count(v, name: str) -> int:
     return v
 
 
-def _fits(*sizes) -> None:
-    """Refuse tensors' sizes that the C structs do not hold (a 32-bit field
-    would cut them without a word)."""
-    if max(sizes) >= 1 << 31:
-        raise ValueError(f"sizes {sizes}: above 2^31-1")
+def _fits(sizes: int) -> None:
+    """Refuse tensors' sizes (or-ed together) that the C structs do not hold: a
+    32-bit field would cut them without a word."""
+    if sizes >> 31:
+        raise ValueError("a tensor's size above 2^31-1")
 
 
 class _Guard:
@@ -148,7 +148,7 @@ def _done(status: int) -> None:
 def _route_problem(logits, top_k, score, renormalise, scale):
     """The problem struct (fields in the order of the C struct)."""
     rows, experts = logits.shape
-    _fits(experts, top_k)
+    _fits(experts | top_k)
     return mg.moegg_route_problem(rows, experts, top_k, 3 if logits.dtype is torch.bfloat16 else 5,
                                   _code(mg.SCORES, score, "score"), 1 if renormalise else 0, scale)
 
@@ -310,7 +310,7 @@ def dispatch(x, plan: SortPlan, *, dtype="bf16", sf_layout: str = "row_major", o
     tokens, top_k, rows, row_of, slot_of, offsets = _plan_pointers(plan, dev)
     width = x.shape[1]
     xp = _want(x, "x", torch.bfloat16, (tokens, width), dev)
-    _fits(top_k, width)
+    _fits(top_k | width)
     p = mg.moegg_exchange_problem(tokens, rows, top_k, plan.num_experts, width, kind, layout)
     s, guard = _on(dev, stream)
     try:
@@ -332,7 +332,7 @@ def combine(rows, plan: SortPlan, *, weights=None, residual=None, out=None, stre
     shape = (tokens, width)
     w = None if weights is None else _want(weights, "weights", torch.float32, (tokens, top_k), dev)
     r = None if residual is None else _want(residual, "residual", bf16, shape, dev)
-    _fits(top_k, width)
+    _fits(top_k | width)
     p = mg.moegg_exchange_problem(tokens, n_rows, top_k, plan.num_experts, width, 3, 0)
     s, guard = _on(dev, stream)
     try:
@@ -356,7 +356,7 @@ def combine_backward(dy, plan: SortPlan, *, rows=None, weights=None, dtype="bf16
     dp = _want(dy, "dy", torch.bfloat16, (tokens, width), dev)
     rp = None if rows is None else _want(rows, "rows", torch.bfloat16, (n_rows, width), dev)
     w = None if weights is None else _want(weights, "weights", torch.float32, (tokens, top_k), dev)
-    _fits(top_k, width)
+    _fits(top_k | width)
     p = mg.moegg_exchange_problem(tokens, n_rows, top_k, plan.num_experts, width, kind, layout)
     s, guard = _on(dev, stream)
     try:
@@ -412,7 +412,7 @@ def _linear_problem(x, w, act, dtype, offsets):
         groups, n = offsets.shape[0], w.shape[1]
         lead, op = (groups,), _want(offsets, "offsets", torch.int32, (groups,), dev)
     wp = _want(w, "w", bf16, (*lead, n, k), dev)
-    _fits(n, k, groups)
+    _fits(n | k | groups)
     return dev, mg.moegg_linear_problem(m, n, k, groups, act_code, dtype_code), lead, x.data_ptr(), wp, op
 
 
