@@ -13,6 +13,11 @@ tensors' device); outputs and workspaces are allocated on that stream, and a
 workspace is never shared between calls, so calls on several streams and
 captured graphs do not meet in one.  Tensors made on another stream have to
 be ready and kept alive as for any other kernel launch.
+
+The functions stand outside autograd: results have no history, whether an
+operand requires a gradient or not, and writing to an ``out`` is not noted
+there.  Each operator's gradient is the function named after it (for a
+``torch.autograd.Function``, what its ``backward`` calls).
 """
 from __future__ import annotations
 
@@ -421,7 +426,9 @@ def linear(x, w, *, bias=None, act: str = "none", residual=None, offsets=None, s
     """y = act(x w^T + bias) + residual: x (M, K) bf16, w (N, K) bf16, or with
     ``offsets`` (L, int32 ends of the groups' rows) w (L, N, K) and bias
     (L, N).  ``dtype`` of y: bf16 or f32.  With ``save_c`` returns (y, c), c
-    the bf16 pre-activation that linear_backward() takes."""
+    the bf16 pre-activation that linear_backward() takes.  Rows behind the
+    last group are not written: `out` keeps them, new tensors (c too) hold
+    anything there."""
     dtype = _dtype_name(dtype)
     dev, p, lead, xp, wp, op = _linear_problem(x, w, act, dtype, offsets)
     m, n = p.m, p.n
@@ -449,7 +456,8 @@ def linear(x, w, *, bias=None, act: str = "none", residual=None, offsets=None, s
 def linear_backward(dy, x, w, *, c=None, act: str = "none", offsets=None, need=("dx", "dw", "db"), dw_dtype="bf16",
                     stream=None):
     """(dx, dw, db) of linear(), None for those not in ``need``; c is what
-    linear(save_c=True) returned (not needed for act "none")."""
+    linear(save_c=True) returned (not needed for act "none"), dy bf16 whatever
+    linear()'s ``dtype`` was.  Rows of dx behind the last group hold anything."""
     dw_dtype = _dtype_name(dw_dtype)
     need = set(need)
     if not need or not need <= {"dx", "dw", "db"}:
