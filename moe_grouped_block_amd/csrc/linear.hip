@@ -197,6 +197,10 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs a, TilePlan
 //
 // One pass over dy and c: dz in bf16, and the column sums of the unrounded
 // dz over tiles of kDzRows rows of one group, summed per group afterwards.
+// dz is the operand of both products: kept in two bf16 parts it would double
+// their work.  With its one rounding dx and dw are 0.0023 off the 64-bit values
+// (root mean square, 16384 x 2816 x 2048 with SwiGLU), where the rounding of the
+// results alone is 0.0017.
 constexpr int kDzRows = 128;
 
 __device__ __forceinline__ void unpack8(v4u u, float* f) {
