@@ -107,7 +107,7 @@ typedef enum moegg_dtype {
   MOEGG_DT_E2M1X2 = 2, /* packed OCP E2M1 pairs: A/B operands (MXFP4) */
   MOEGG_DT_BF16 = 3,   /* A/B operands (dense BF16 backend) or C / D outputs */
   MOEGG_DT_E5M2 = 4,   /* OCP E5M2: A/B operands (MXFP8, "Grouped GEMM + Quant", §Data Types) */
-  MOEGG_DT_F32 = 5     /* fp32: layer operators only (router logits, linear's y and dw) */
+  MOEGG_DT_F32 = 5     /* fp32: layer operators only (router logits, linear's y and dw, the norm's stream) */
 } moegg_dtype;
 
 typedef enum moegg_sf_layout {
@@ -240,8 +240,9 @@ moegg_status moegg_sf_to_kplanes(const uint8_t* src, uint8_t* dst, int64_t rows,
 
 /* ==========================================================================
  * Layer operators: what stands around the grouped product in an MoE layer.
- * The router's choice, tokens sorted by expert and back, and the matrix
- * product with bias, activation and residual, each with its gradient.
+ * The norm before it, the router's choice, tokens sorted by expert and back,
+ * and the matrix product with bias, activation and residual, each with its
+ * gradient; and activations kept in 8 bits for those gradients.
  *
  * They follow the conventions above: caller-owned dense row-major device
  * tensors (16-byte aligned; vectors 4-byte aligned), no device allocation,
@@ -290,6 +291,24 @@ moegg_status moegg_route(const moegg_route_problem* problem, const void* logits,
  * counts twice).  The choice itself, and so the bias, has no gradient. */
 moegg_status moegg_route_backward(const moegg_route_problem* problem, const void* logits, const int32_t* ids,
                                   const float* dweights, void* dlogits, void* stream);
+
+/* Router that chooses groups of experts first: moegg_route among the experts of
+ * the top_groups groups with the largest scores (ties to the lowest group).
+ * Experts [i, i + 1) E / num_groups are group i.  A group's score is the sum
+ * of its `best` largest p_e + bias_e (p_e without a bias), or with best = 1 and
+ * no bias its largest logit, among the experts that can be chosen (where fewer
+ * than `best` can, of those; a group of none comes last).  Scores are decided
+ * in 64 bits.  p, weights and what cannot be chosen are as in moegg_route (p
+ * over all experts, of all groups); the gradient is moegg_route_backward with
+ * these ids. */
+typedef struct moegg_route_groups {
+  int32_t num_groups;   /* 1..64, a divisor of E                               */
+  int32_t top_groups;   /* 1..num_groups                                       */
+  int32_t best;         /* 1 or 2                                              */
+} moegg_route_groups;
+
+moegg_status moegg_route_grouped(const moegg_route_problem* problem, const moegg_route_groups* groups, const void* logits,
+                                 const float* bias, int32_t* ids, float* weights, void* stream);
 
 typedef struct moegg_sort_problem {
   int64_t num_tokens;   /* T >= 0                                              */
@@ -417,6 +436,88 @@ moegg_status moegg_linear(const moegg_linear_problem* problem, const moegg_linea
  * one is required).  The residual's gradient is dy itself.  A
  * NaN in c is a NaN in dz. */
 moegg_status moegg_linear_backward(const moegg_linear_problem* problem, const moegg_linear_args* args, void* stream);
+
+/* moegg_linear with c kept in 8 bits, and moegg_linear_backward from an input
+ * or a pre-activation kept in 8 bits.  8-bit tensors are MX rows: E4M3 or E5M2
+ * codes with an E8M0 byte for every 32 columns, as moegg_dispatch,
+ * moegg_rms_norm and moegg_quantise write them (and as moegg_run takes its A).
+ * c is formed from the unrounded z, a block with a NaN or an infinity as in
+ * moegg_dispatch; it is read back as the values that its codes stand for.  x
+ * is read as those values in BF16 (exact but below 2^-126), the operand of dw. */
+typedef struct moegg_linear_saved {
+  int32_t x_dtype;        /* of args.x: BF16, or in the backward E4M3 | E5M2: codes (m, k), k a multiple of 32 */
+  int32_t x_sf_layout;    /* moegg_sf_layout of x_sf (K-block planes: k a multiple of 128) */
+  int32_t c_dtype;        /* of args.c: BF16, or E4M3 | E5M2: codes (m, n), n a multiple of 32 */
+  int32_t reserved;       /* 0                                                 */
+  const uint8_t* x_sf;    /* (m, k/32) or (k/128, m, 4); NULL for a BF16 x      */
+  uint8_t* c_sf;          /* (m, n/32): written by the forward, read by the backward; NULL for a BF16 c */
+} moegg_linear_saved;
+
+/* Workspace bytes; -1 for an invalid problem. */
+int64_t moegg_linear_saving_workspace(const moegg_linear_problem* problem, const moegg_linear_saved* saved);
+int64_t moegg_linear_saved_backward_workspace(const moegg_linear_problem* problem, const moegg_linear_saved* saved,
+                                              int32_t want);
+/* As moegg_linear; args.c is required where c_dtype is one of 8 bits. */
+moegg_status moegg_linear_saving(const moegg_linear_problem* problem, const moegg_linear_args* args,
+                                 const moegg_linear_saved* saved, void* stream);
+/* As moegg_linear_backward. */
+moegg_status moegg_linear_saved_backward(const moegg_linear_problem* problem, const moegg_linear_args* args,
+                                         const moegg_linear_saved* saved, void* stream);
+
+/* Rows to 8 bits and back: x (rows, width) BF16 or F32 (`x_dtype`) to codes of
+ * `dtype` (E4M3 | E5M2) and E8M0 scales sf, (rows, width/32) or with
+ * MOEGG_SF_KPLANES (width/128, rows, 4), scaled and rounded as in
+ * moegg_dispatch; and codes and scales to x, rounded once to nearest even (a
+ * scale byte of 255 stands for NaN).  width: a multiple of 32 (planes: 128),
+ * <= 2^20; rows: 0..2^31-1.  The operand that is not written is read only. */
+moegg_status moegg_quantise(const void* x, int32_t x_dtype, int64_t rows, int32_t width, int32_t dtype, int32_t sf_layout,
+                            uint8_t* codes, uint8_t* sf, void* stream);
+moegg_status moegg_dequantise(const uint8_t* codes, const uint8_t* sf, int64_t rows, int32_t width, int32_t dtype,
+                              int32_t sf_layout, void* x, int32_t x_dtype, void* stream);
+
+/* Root-mean-square norm with the residual's addition:
+ *   h = x + residual, rounded once to the stream's type (without a residual h is x)
+ *   y = h / sqrt(mean(h^2) + eps) * weight
+ * over each row of `width` columns, the norm of the h that is stored.  y comes
+ * as BF16, as MX rows (codes with scales, scaled and rounded from the unrounded
+ * y as in moegg_dispatch: moegg_run's A and SFA) or as both.  Sums are held in
+ * 64 bits: no finite h overflows or vanishes in them.  A NaN or an infinity in a
+ * row is one of that row alone. */
+typedef struct moegg_norm_problem {
+  int64_t rows;         /* 0..2^31-1                                           */
+  int32_t width;        /* multiple of 8 (128 for MX rows, 256 for E2M1X2), <= 32768 */
+  int32_t x_dtype;      /* x: BF16 | F32 (the stream's without a residual)     [forward] */
+  int32_t stream_dtype; /* residual, h, dh and dx: BF16 | F32 (F32 where x is) */
+  int32_t mx_dtype;     /* codes: NONE | E4M3 | E5M2 | E2M1X2                  [forward] */
+  int32_t sf_layout;    /* moegg_sf_layout of sf                               [forward] */
+  float eps;            /* > 0, finite                                         */
+} moegg_norm_problem;
+
+typedef struct moegg_norm_args {
+  const void* x;          /* (rows, width)                                     [forward] */
+  const void* residual;   /* (rows, width) or NULL                             [forward] */
+  const float* weight;    /* (width) fp32                                      */
+  void* h;                /* (rows, width): forward: written, with a residual (may be the residual itself),
+                             NULL without one; backward: read (x where there was no residual) */
+  void* y;                /* (rows, width) BF16; NULL: MX rows alone           [forward] */
+  uint8_t* codes;         /* (rows, width) (E2M1X2: width / 2), with mx_dtype  [forward] */
+  uint8_t* sf;            /* (rows, width/32) or (width/128, rows, 4)          [forward] */
+  const void* dy;         /* (rows, width) BF16                                [backward] */
+  const void* dh;         /* (rows, width) or NULL: what reaches h from elsewhere (the residual stream) [backward] */
+  void* dx;               /* (rows, width) or NULL; may be dh itself           [backward] */
+  float* dweight;         /* (width) fp32 or NULL                              [backward] */
+  void* workspace;        /* 16-byte aligned (with dweight)                    [backward] */
+  int64_t workspace_bytes;
+} moegg_norm_args;
+
+moegg_status moegg_rms_norm(const moegg_norm_problem* problem, const moegg_norm_args* args, void* stream);
+
+/* Gradients: dx of x and of the residual alike (both are h's), dh included;
+ * dweight = sum over the rows (zero without rows).  Whatever is NULL of dx and
+ * dweight is not computed (both may be NULL where rows is 0, else one is
+ * required).  The workspace is needed with dweight alone. */
+int64_t moegg_rms_norm_backward_workspace(const moegg_norm_problem* problem);
+moegg_status moegg_rms_norm_backward(const moegg_norm_problem* problem, const moegg_norm_args* args, void* stream);
 
 /* Output width N_out for a problem (N/2 SwiGLU / GeGLU, 2N dSwiGLU / dGeGLU, else N);
  * -1 if invalid act. */

@@ -12,8 +12,8 @@ The C ABI (include/moegg.h) is mirrored name for name:
 plus ``make_problem`` / ``make_args`` (fill the C structs from a problem dict
 and torch tensors' device pointers) and ``run`` / ``check`` (build the structs,
 call, raise ``MoeggError`` on a non-OK status).  The layer operators
-around the grouped product (``route``, ``sort_tokens``, ``dispatch``,
-``combine``, ``linear`` and their gradients) are called with torch tensors,
+around the grouped product (``rms_norm``, ``route``, ``sort_tokens``, ``dispatch``,
+``combine``, ``linear``, their gradients, ``quantise`` and ``dequantise``) are called with torch tensors,
 live in ``layer`` and are imported at their first use.  Every step of the computation
 runs in the HIP library; this module never computes.  If ``libmoegg.so`` has
 not been built the first call raises ``RuntimeError``: there is no fallback.
@@ -31,7 +31,8 @@ __all__ = ["MoeggError", "moegg_check", "moegg_run", "moegg_check_offsets", "moe
            "moegg_sf_to_kplanes", "sf_to_kplanes", "SCORES"]
 # the layer operators are imported at their first use: they need torch, which the rest does not
 _LAYER = ("route", "route_backward", "SortPlan", "sort_tokens", "sort_rows", "dispatch", "dispatch_backward",
-          "combine", "combine_backward", "unsort", "linear", "linear_backward")
+          "combine", "combine_backward", "unsort", "linear", "linear_backward", "rms_norm", "rms_norm_backward",
+          "quantise", "dequantise")
 if importlib.util.find_spec("torch") is not None:
     __all__ += _LAYER
 
@@ -71,6 +72,10 @@ class moegg_route_problem(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+class moegg_route_groups(ctypes.Structure):
+    _fields_ = [("num_groups", ctypes.c_int32), ("top_groups", ctypes.c_int32), ("best", ctypes.c_int32)]
+
+
 class moegg_sort_problem(ctypes.Structure):
     _fields_ = [("num_tokens", ctypes.c_int64), ("top_k", ctypes.c_int32), ("num_experts", ctypes.c_int32),
                 ("m_aligned", ctypes.c_int32), ("rows", ctypes.c_int64)]
@@ -90,6 +95,22 @@ class moegg_linear_problem(ctypes.Structure):
 class moegg_linear_args(ctypes.Structure):
     _fields_ = [(f, ctypes.c_void_p) for f in ("x", "w", "bias", "residual", "offsets", "y", "c", "dy", "dx", "dw",
                                                "db", "workspace")] + [("workspace_bytes", ctypes.c_int64)]
+
+
+class moegg_linear_saved(ctypes.Structure):
+    _fields_ = [("x_dtype", ctypes.c_int32), ("x_sf_layout", ctypes.c_int32), ("c_dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("x_sf", ctypes.c_void_p), ("c_sf", ctypes.c_void_p)]
+
+
+class moegg_norm_problem(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("width", ctypes.c_int32), ("x_dtype", ctypes.c_int32),
+                ("stream_dtype", ctypes.c_int32), ("mx_dtype", ctypes.c_int32), ("sf_layout", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+
+class moegg_norm_args(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in ("x", "residual", "weight", "h", "y", "codes", "sf", "dy", "dh", "dx",
+                                               "dweight", "workspace")] + [("workspace_bytes", ctypes.c_int64)]
 
 
 class MoeggError(RuntimeError):
@@ -143,9 +164,11 @@ def _declare_layer(lib) -> None:
     """Signatures of the layer operators (called by ``layer``)."""
     v, i64, i32, ref = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.POINTER
     route, sort, exch = ref(moegg_route_problem), ref(moegg_sort_problem), ref(moegg_exchange_problem)
-    lin, lin_args = ref(moegg_linear_problem), ref(moegg_linear_args)
+    lin, lin_args, saved = ref(moegg_linear_problem), ref(moegg_linear_args), ref(moegg_linear_saved)
+    norm, norm_args = ref(moegg_norm_problem), ref(moegg_norm_args)
     for name, args, res in (("moegg_route", [route] + [v] * 5, ctypes.c_int),
                             ("moegg_route_backward", [route] + [v] * 5, ctypes.c_int),
+                            ("moegg_route_grouped", [route, ref(moegg_route_groups)] + [v] * 5, ctypes.c_int),
                             ("moegg_sort_rows", [sort], i64),
                             ("moegg_sort_workspace", [sort], i64),
                             ("moegg_sort", [sort] + [v] * 7 + [i64, v], ctypes.c_int),
@@ -156,7 +179,16 @@ def _declare_layer(lib) -> None:
                             ("moegg_linear_workspace", [lin], i64),
                             ("moegg_linear_backward_workspace", [lin, i32], i64),
                             ("moegg_linear", [lin, lin_args, v], ctypes.c_int),
-                            ("moegg_linear_backward", [lin, lin_args, v], ctypes.c_int)):
+                            ("moegg_linear_backward", [lin, lin_args, v], ctypes.c_int),
+                            ("moegg_linear_saving_workspace", [lin, saved], i64),
+                            ("moegg_linear_saved_backward_workspace", [lin, saved, i32], i64),
+                            ("moegg_linear_saving", [lin, lin_args, saved, v], ctypes.c_int),
+                            ("moegg_linear_saved_backward", [lin, lin_args, saved, v], ctypes.c_int),
+                            ("moegg_quantise", [v, i32, i64, i32, i32, i32, v, v, v], ctypes.c_int),
+                            ("moegg_dequantise", [v, v, i64, i32, i32, i32, v, i32, v], ctypes.c_int),
+                            ("moegg_rms_norm", [norm, norm_args, v], ctypes.c_int),
+                            ("moegg_rms_norm_backward_workspace", [norm], i64),
+                            ("moegg_rms_norm_backward", [norm, norm_args, v], ctypes.c_int)):
         f = getattr(lib, name)
         f.argtypes, f.restype = args, res
 

@@ -33,7 +33,7 @@ COMMON = [
     f"-I{os.path.join(ROOT, 'include')}", f"-I{CSRC}",
 ]
 SOURCES = ["moegg_api.cpp", "moegg_kernels.hip", "inst_e4m3.hip", "inst_e2m1.hip", "inst_bf16.hip", "inst_e5m2.hip",
-           "layer_api.cpp", "route.hip", "exchange.hip", "linear.hip"]
+           "layer_api.cpp", "route.hip", "exchange.hip", "linear.hip", "norm.hip", "saved.hip"]
 
 
 def _compile(src: str) -> str:

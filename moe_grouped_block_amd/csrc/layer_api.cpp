@@ -1,5 +1,5 @@
 // C-ABI front of the layer operators (route, sort / dispatch / combine,
-// linear): host-side validation and dispatch.  As in moegg_api.cpp every rule
+// linear, norm, rows kept in 8 bits): host-side validation and dispatch.  As in moegg_api.cpp every rule
 // is checked before any HIP call, so a rejected call enqueues nothing.
 #include "layer_internal.h"
 
@@ -100,7 +100,53 @@ moegg::RouteArgs route_args(const moegg_route_problem& p) {
   a.softmax = p.score == MOEGG_SCORE_SOFTMAX;
   a.renormalise = p.renormalise != 0;
   a.scale = p.scale;
+  a.groups = 1;
   return a;
+}
+
+moegg_status check_groups(const moegg_route_problem& p, const moegg_route_groups* pg) {
+  if (!pg) return set_error(MOEGG_ERROR_INVALID_VALUE, "groups must be non-NULL");
+  const moegg_route_groups& g = *pg;
+  if (g.num_groups < 1 || p.num_experts % g.num_groups != 0)
+    return set_error(MOEGG_ERROR_INVALID_VALUE, "num_groups=%d does not divide num_experts=%d", g.num_groups, p.num_experts);
+  if (g.num_groups > moegg::kMaxGroups)
+    return set_error(MOEGG_ERROR_NOT_SUPPORTED, "num_groups=%d above %d", g.num_groups, moegg::kMaxGroups);
+  if (g.top_groups < 1 || g.top_groups > g.num_groups)
+    return set_error(MOEGG_ERROR_INVALID_VALUE, "top_groups=%d outside 1..num_groups=%d", g.top_groups, g.num_groups);
+  if (g.best != 1 && g.best != 2) return set_error(MOEGG_ERROR_INVALID_VALUE, "best=%d must be 1 or 2", g.best);
+  if (p.top_k > g.top_groups * (p.num_experts / g.num_groups))
+    return set_error(MOEGG_ERROR_INVALID_VALUE, "top_k=%d above the %d experts of %d groups", p.top_k,
+                     g.top_groups * (p.num_experts / g.num_groups), g.top_groups);
+  return MOEGG_OK;
+}
+
+moegg_status run_route(const moegg_route_problem* problem, const moegg_route_groups* groups, bool grouped, const void* logits,
+                       const float* bias, int32_t* ids, float* weights, void* stream) {
+  moegg_status st = check_route(problem);
+  if (st != MOEGG_OK) return st;
+  if (grouped && (st = check_groups(*problem, groups)) != MOEGG_OK) return st;
+  const bool any = problem->num_tokens > 0;
+  const Pointer ps[] = {{"logits", logits, 16, any}, {"ids", ids, 4, any}, {"weights", weights, 4, any}, {"bias", bias, 4, false}};
+  st = check_pointers(ps);
+  if (st != MOEGG_OK) return st;
+  if (!any) return launched(hipSuccess, "route");
+  const int64_t chosen = problem->num_tokens * problem->top_k * 4;
+  const Span in[] = {{"logits", logits, logits_bytes(*problem)}, {"bias", bias, int64_t{problem->num_experts} * 4}};
+  const Span out[] = {{"ids", ids, chosen}, {"weights", weights, chosen}};
+  if ((st = check_apart(in, out)) != MOEGG_OK) return st;
+  moegg::RouteArgs a = route_args(*problem);
+  a.logits = logits;
+  a.bias = bias;
+  a.ids = ids;
+  a.weights = weights;
+  if (grouped && groups->top_groups < groups->num_groups) {    // (of all groups: no choice)
+    a.groups = groups->num_groups;
+    a.top_groups = groups->top_groups;
+    a.group_sums = groups->best == 2;
+    // (e magic) >> 22 = e / size for every e < 1024: e size < 2^22
+    a.group_magic = (1u << 22) / static_cast<uint32_t>(problem->num_experts / groups->num_groups) + 1;
+  }
+  return launched(moegg::launch_route(a, static_cast<hipStream_t>(stream)), "route kernel");
 }
 
 // ---- sort and exchange ---------------------------------------------------------
@@ -231,7 +277,8 @@ moegg_status check_linear(const moegg_linear_problem* pp) {
   return MOEGG_OK;
 }
 
-moegg::LinearArgs linear_args(const moegg_linear_problem& p, const moegg_linear_args* pa) {
+moegg::LinearArgs linear_args(const moegg_linear_problem& p, const moegg_linear_args* pa,
+                              const moegg_linear_saved* saved = nullptr) {
   moegg::LinearArgs a{};
   a.m = p.m;
   a.n = p.n;
@@ -257,23 +304,211 @@ moegg::LinearArgs linear_args(const moegg_linear_problem& p, const moegg_linear_
     a.workspace = pa->workspace;
     a.workspace_bytes = pa->workspace_bytes;
   }
+  if (saved) {
+    a.c_kind = row_kind(saved->c_dtype);
+    a.c_sf = saved->c_sf;
+    a.x8 = {static_cast<const uint8_t*>(pa ? pa->x : nullptr), saved->x_sf, row_kind(saved->x_dtype),
+            saved->x_sf_layout == MOEGG_SF_KPLANES};
+  }
   return a;
 }
 
 int64_t w_bytes(const moegg_linear_problem& p) { return int64_t{p.num_groups} * p.n * p.k * 2; }
 
-moegg_status check_linear_pointers(const moegg_linear_problem& p, const moegg_linear_args& a, int64_t workspace) {
+// 8 bits, or BF16 (-1: neither).
+int kept_kind(int dtype) {
+  const int kind = row_kind(dtype);
+  return kind == moegg::ROW_E2M1 ? -1 : kind;
+}
+int64_t kept_bytes(int kind, int64_t n) { return kind == moegg::ROW_BF16 ? 2 * n : n; }
+
+moegg_status check_saved(const moegg_linear_problem& p, const moegg_linear_saved& s) {
+  if (kept_kind(s.x_dtype) < 0 || kept_kind(s.c_dtype) < 0)
+    return set_error(MOEGG_ERROR_INVALID_VALUE, "x_dtype=%d c_dtype=%d must be BF16, E4M3 or E5M2", s.x_dtype, s.c_dtype);
+  if (s.x_sf_layout != MOEGG_SF_ROW_MAJOR && s.x_sf_layout != MOEGG_SF_KPLANES)
+    return set_error(MOEGG_ERROR_INVALID_VALUE, "x_sf_layout=%d must be ROW_MAJOR or KPLANES", s.x_sf_layout);
+  if (s.reserved != 0) return set_error(MOEGG_ERROR_INVALID_VALUE, "reserved=%d must be 0", s.reserved);
+  const bool x8 = s.x_dtype != MOEGG_DT_BF16, c8 = s.c_dtype != MOEGG_DT_BF16;
+  const int step = s.x_sf_layout == MOEGG_SF_KPLANES ? 128 : 32;
+  if (x8 && p.k % step != 0)
+    return set_error(MOEGG_ERROR_NOT_SUPPORTED, "k=%d: a multiple of %d needed for x in 8 bits", p.k, step);
+  if (c8 && p.n % 32 != 0) return set_error(MOEGG_ERROR_NOT_SUPPORTED, "n=%d: a multiple of 32 needed for c in 8 bits", p.n);
+  if (!x8 && s.x_sf) return set_error(MOEGG_ERROR_INVALID_VALUE, "a BF16 x takes no x_sf");
+  if (!c8 && s.c_sf) return set_error(MOEGG_ERROR_INVALID_VALUE, "a BF16 c takes no c_sf");
+  if (x8 && (p.m * p.k + 4095) / 4096 * 256 > moegg::kLaunchThreads)
+    return set_error(MOEGG_ERROR_NOT_SUPPORTED, "m=%lld k=%d: more threads than a launch holds", (long long)p.m, p.k);
+  return MOEGG_OK;
+}
+
+moegg_status check_linear_pointers(const moegg_linear_problem& p, const moegg_linear_args& a, const moegg_linear_saved* saved,
+                                   int64_t workspace) {
   const Pointer ps[] = {{"x", a.x, 16, false},   {"w", a.w, 16, false},     {"residual", a.residual, 16, false},
                         {"y", a.y, 16, false},   {"c", a.c, 16, false},     {"dy", a.dy, 16, false},
                         {"dx", a.dx, 16, false}, {"dw", a.dw, 16, false},   {"workspace", a.workspace, 16, false},
                         {"bias", a.bias, 4, false}, {"offsets", a.offsets, 4, false}, {"db", a.db, 4, false}};
-  const moegg_status st = check_pointers(ps);
+  moegg_status st = check_pointers(ps);
   if (st != MOEGG_OK) return st;
+  if (saved) {
+    const Pointer sf[] = {{"x_sf", saved->x_sf, 16, false}, {"c_sf", saved->c_sf, 16, false}};
+    if ((st = check_pointers(sf)) != MOEGG_OK) return st;
+  }
   if (!a.offsets && p.num_groups != 1)
     return set_error(MOEGG_ERROR_INVALID_VALUE, "num_groups=%d needs offsets", p.num_groups);
   if (workspace > 0 && (!a.workspace || a.workspace_bytes < workspace))
     return set_error(MOEGG_ERROR_INVALID_VALUE, "workspace of %lld bytes needed, %lld given", (long long)workspace,
                      (long long)(a.workspace ? a.workspace_bytes : 0));
+  return MOEGG_OK;
+}
+
+// Forward; `saved`: which of the tensors are in 8 bits, or null.
+moegg_status run_linear(const moegg_linear_problem* problem, const moegg_linear_args* args, const moegg_linear_saved* saved,
+                        void* stream) {
+  moegg_status st = check_linear(problem);
+  if (st != MOEGG_OK) return st;
+  if (saved && (st = check_saved(*problem, *saved)) != MOEGG_OK) return st;
+  if (!args) return set_error(MOEGG_ERROR_INVALID_VALUE, "args must be non-NULL");
+  const moegg_linear_problem& p = *problem;
+  const moegg::LinearArgs a = linear_args(p, args, saved);
+  const bool any = p.m > 0;
+  if (any && (!a.x || !a.w || !a.y)) return set_error(MOEGG_ERROR_INVALID_VALUE, "x, w and y are required");
+  if (a.dy || a.dx || a.dw || a.db)
+    return set_error(MOEGG_ERROR_INVALID_VALUE, "dy, dx, dw and db are for moegg_linear_backward");
+  if (a.x8.kind != moegg::ROW_BF16) return set_error(MOEGG_ERROR_NOT_SUPPORTED, "x_dtype: the forward reads a BF16 x");
+  if (any && a.c_kind != moegg::ROW_BF16 && (!a.c || !a.c_sf))
+    return set_error(MOEGG_ERROR_INVALID_VALUE, "c and c_sf are required with c_dtype");
+  const int64_t workspace = moegg::linear_workspace(a);
+  st = check_linear_pointers(p, *args, saved, workspace);
+  if (st != MOEGG_OK) return st;
+  const int64_t n_out = p.act == MOEGG_ACT_SWIGLU ? p.n / 2 : p.n;
+  const int64_t y_bytes = p.m * n_out * (a.out_f32 ? 4 : 2);
+  const int64_t c_bytes = kept_bytes(a.c_kind, p.m * p.n), sf_bytes = p.m * (p.n / 32);
+  const Span in[] = {{"x", a.x, p.m * p.k * 2}, {"w", a.w, w_bytes(p)}, {"bias", a.bias, int64_t{p.num_groups} * p.n * 4},
+                     {"offsets", a.offsets, int64_t{p.num_groups} * 4}};
+  const Span out[] = {{"y", a.y, y_bytes}, {"c", a.c, c_bytes}, {"c_sf", a.c_sf, sf_bytes},
+                      {"workspace", a.workspace, workspace}};
+  if ((st = check_apart(in, out)) != MOEGG_OK) return st;
+  if (overlap(a.residual, p.m * n_out * 2, a.c, c_bytes) || overlap(a.residual, p.m * n_out * 2, a.c_sf, sf_bytes) ||
+      overlap(a.residual, p.m * n_out * 2, a.workspace, workspace))
+    return set_error(MOEGG_ERROR_INVALID_VALUE, "residual and c, c_sf or the workspace overlap");
+  if (overlap(a.residual, p.m * n_out * 2, a.y, y_bytes) && (a.out_f32 || static_cast<const void*>(a.residual) != a.y))
+    return set_error(MOEGG_ERROR_INVALID_VALUE, "residual and y overlap without being the same BF16 tensor");
+  if (!any) return launched(hipSuccess, "linear");
+  return launched(moegg::launch_linear(a, static_cast<hipStream_t>(stream)), "linear kernel");
+}
+
+moegg_status run_linear_backward(const moegg_linear_problem* problem, const moegg_linear_args* args,
+                                 const moegg_linear_saved* saved, void* stream) {
+  moegg_status st = check_linear(problem);
+  if (st != MOEGG_OK) return st;
+  if (saved && (st = check_saved(*problem, *saved)) != MOEGG_OK) return st;
+  if (!args) return set_error(MOEGG_ERROR_INVALID_VALUE, "args must be non-NULL");
+  const moegg_linear_problem& p = *problem;
+  const moegg::LinearArgs a = linear_args(p, args, saved);
+  const bool any = p.m > 0;
+  if (a.bias || a.residual || a.y)
+    return set_error(MOEGG_ERROR_INVALID_VALUE, "bias, residual and y are for moegg_linear");
+  // (without rows dx has no elements, and its pointer may be NULL)
+  const bool none = !a.dx && !a.dw && !a.db;
+  if (any && none) return set_error(MOEGG_ERROR_INVALID_VALUE, "one of dx, dw and db is required");
+  if (any && !a.dy) return set_error(MOEGG_ERROR_INVALID_VALUE, "dy is required");
+  if (any && a.act != moegg::LIN_NONE && !a.c) return set_error(MOEGG_ERROR_INVALID_VALUE, "this activation's gradient needs c");
+  if (any && a.dx && !a.w) return set_error(MOEGG_ERROR_INVALID_VALUE, "dx needs w");
+  if (any && a.dw && !a.x) return set_error(MOEGG_ERROR_INVALID_VALUE, "dw needs x");
+  if (any && a.c && a.c_kind != moegg::ROW_BF16 && !a.c_sf) return set_error(MOEGG_ERROR_INVALID_VALUE, "c in 8 bits needs c_sf");
+  if (any && a.dw && a.x8.kind != moegg::ROW_BF16 && !a.x8.scales)
+    return set_error(MOEGG_ERROR_INVALID_VALUE, "x in 8 bits needs x_sf");
+  const int64_t workspace = moegg::linear_backward_workspace(a, a.dx, a.dw, a.db);
+  st = check_linear_pointers(p, *args, saved, workspace);
+  if (st != MOEGG_OK) return st;
+  const int64_t n_out = p.act == MOEGG_ACT_SWIGLU ? p.n / 2 : p.n;
+  const Span in[] = {{"x", args->x, kept_bytes(a.x8.kind, p.m * p.k)}, {"w", a.w, w_bytes(p)}, {"dy", a.dy, p.m * n_out * 2},
+                     {"c", a.c, kept_bytes(a.c_kind, p.m * p.n)}, {"offsets", a.offsets, int64_t{p.num_groups} * 4},
+                     {"x_sf", a.x8.scales, p.m * (p.k / 32)}, {"c_sf", a.c_sf, p.m * (p.n / 32)}};
+  const Span out[] = {{"dx", a.dx, p.m * p.k * 2}, {"dw", a.dw, w_bytes(p) * (a.out_f32 ? 2 : 1)},
+                      {"db", a.db, int64_t{p.num_groups} * p.n * 4}, {"workspace", a.workspace, workspace}};
+  if ((st = check_apart(in, out)) != MOEGG_OK) return st;
+  if (none) return launched(hipSuccess, "linear backward");
+  return launched(moegg::launch_linear_backward(a, static_cast<hipStream_t>(stream)), "linear backward kernel");
+}
+
+// ---- norm, rows kept in 8 bits -----------------------------------------------------
+
+moegg_status check_norm(const moegg_norm_problem* pp, bool backward) {
+  if (!pp) return set_error(MOEGG_ERROR_INVALID_VALUE, "problem must be non-NULL");
+  const moegg_norm_problem& p = *pp;
+  if (p.rows < 0) return set_error(MOEGG_ERROR_INVALID_VALUE, "rows=%lld negative", (long long)p.rows);
+  if (p.rows > INT32_MAX) return set_error(MOEGG_ERROR_NOT_SUPPORTED, "rows=%lld above 2^31-1", (long long)p.rows);
+  if (p.stream_dtype != MOEGG_DT_BF16 && p.stream_dtype != MOEGG_DT_F32)
+    return set_error(MOEGG_ERROR_INVALID_VALUE, "stream_dtype=%d must be BF16 or F32", p.stream_dtype);
+  if (!(p.eps > 0.0f) || !std::isfinite(p.eps)) return set_error(MOEGG_ERROR_INVALID_VALUE, "eps must be positive and finite");
+  int step = 8;
+  if (!backward) {
+    if (p.x_dtype != MOEGG_DT_BF16 && p.x_dtype != MOEGG_DT_F32)
+      return set_error(MOEGG_ERROR_INVALID_VALUE, "x_dtype=%d must be BF16 or F32", p.x_dtype);
+    if (p.x_dtype == MOEGG_DT_F32 && p.stream_dtype != MOEGG_DT_F32)
+      return set_error(MOEGG_ERROR_NOT_SUPPORTED, "an F32 x goes with an F32 stream");
+    if (p.mx_dtype != MOEGG_DT_NONE && (row_kind(p.mx_dtype) < 0 || p.mx_dtype == MOEGG_DT_BF16))
+      return set_error(MOEGG_ERROR_INVALID_VALUE, "mx_dtype=%d must be NONE, E4M3, E5M2 or E2M1X2", p.mx_dtype);
+    if (p.sf_layout != MOEGG_SF_ROW_MAJOR && p.sf_layout != MOEGG_SF_KPLANES)
+      return set_error(MOEGG_ERROR_INVALID_VALUE, "sf_layout=%d must be ROW_MAJOR or KPLANES", p.sf_layout);
+    step = p.mx_dtype == MOEGG_DT_NONE ? 8 : p.mx_dtype == MOEGG_DT_E2M1X2 ? 256 : 128;
+  }
+  if (p.width < 1 || p.width % step != 0)
+    return set_error(MOEGG_ERROR_NOT_SUPPORTED, "width=%d: a positive multiple of %d needed", p.width, step);
+  if (p.width > moegg::kMaxNormWidth)
+    return set_error(MOEGG_ERROR_NOT_SUPPORTED, "width=%d above %d", p.width, moegg::kMaxNormWidth);
+  // (at most 16 waves a row, twice as many as its pieces of 1024 columns need; the backward's grid is bounded)
+  const int64_t waves = (p.width + 1023) / 1024 * 2;
+  if (!backward && (p.rows + 4) * waves * 64 > moegg::kLaunchThreads)
+    return set_error(MOEGG_ERROR_NOT_SUPPORTED, "rows=%lld width=%d: more threads than a launch holds", (long long)p.rows, p.width);
+  return MOEGG_OK;
+}
+
+moegg::NormArgs norm_args(const moegg_norm_problem& p, const moegg_norm_args& q, bool backward) {
+  moegg::NormArgs a{};
+  a.weight = q.weight;
+  if (backward) {
+    a.dy = static_cast<const uint16_t*>(q.dy);
+    a.stored = q.h;
+    a.dh = q.dh;
+    a.dx = q.dx;
+    a.dw = q.dweight;
+    a.partial = q.dweight ? static_cast<float*>(q.workspace) : nullptr;
+  } else {
+    a.x = q.x;
+    a.residual = q.residual;
+    a.h = q.h;
+    a.y = static_cast<uint16_t*>(q.y);
+    a.codes = q.codes;
+    a.scales = q.sf;
+    a.kind = p.mx_dtype == MOEGG_DT_NONE ? moegg::ROW_BF16 : row_kind(p.mx_dtype);
+    a.x_f32 = p.x_dtype == MOEGG_DT_F32;
+    a.kplanes = p.sf_layout == MOEGG_SF_KPLANES;
+  }
+  a.rows = p.rows;
+  a.width = p.width;
+  a.stream_f32 = p.stream_dtype == MOEGG_DT_F32;
+  a.eps = p.eps;
+  a.inverse_width = 1.0 / p.width;
+  return a;
+}
+
+// Sizes and types of rows and their 8 bits.
+moegg_status check_kept_rows(int32_t x_dtype, int64_t rows, int32_t width, int32_t dtype, int32_t sf_layout) {
+  if (x_dtype != MOEGG_DT_BF16 && x_dtype != MOEGG_DT_F32)
+    return set_error(MOEGG_ERROR_INVALID_VALUE, "x_dtype=%d must be BF16 or F32", x_dtype);
+  if (dtype != MOEGG_DT_E4M3 && dtype != MOEGG_DT_E5M2)
+    return set_error(MOEGG_ERROR_INVALID_VALUE, "dtype=%d must be E4M3 or E5M2", dtype);
+  if (sf_layout != MOEGG_SF_ROW_MAJOR && sf_layout != MOEGG_SF_KPLANES)
+    return set_error(MOEGG_ERROR_INVALID_VALUE, "sf_layout=%d must be ROW_MAJOR or KPLANES", sf_layout);
+  if (rows < 0) return set_error(MOEGG_ERROR_INVALID_VALUE, "rows=%lld negative", (long long)rows);
+  if (rows > INT32_MAX) return set_error(MOEGG_ERROR_NOT_SUPPORTED, "rows=%lld above 2^31-1", (long long)rows);
+  const int step = sf_layout == MOEGG_SF_KPLANES ? 128 : 32;
+  if (width < 1 || width % step != 0)
+    return set_error(MOEGG_ERROR_NOT_SUPPORTED, "width=%d: a positive multiple of %d needed", width, step);
+  if (width > (1 << 20)) return set_error(MOEGG_ERROR_NOT_SUPPORTED, "width=%d above 2^20", width);
+  if ((rows * width + 4095) / 4096 * 256 > moegg::kLaunchThreads)
+    return set_error(MOEGG_ERROR_NOT_SUPPORTED, "rows=%lld width=%d: more threads than a launch holds", (long long)rows, width);
   return MOEGG_OK;
 }
 
@@ -283,23 +518,12 @@ extern "C" {
 
 moegg_status moegg_route(const moegg_route_problem* problem, const void* logits, const float* bias, int32_t* ids,
                          float* weights, void* stream) {
-  moegg_status st = check_route(problem);
-  if (st != MOEGG_OK) return st;
-  const bool any = problem->num_tokens > 0;
-  const Pointer ps[] = {{"logits", logits, 16, any}, {"ids", ids, 4, any}, {"weights", weights, 4, any}, {"bias", bias, 4, false}};
-  st = check_pointers(ps);
-  if (st != MOEGG_OK) return st;
-  if (!any) return launched(hipSuccess, "route");
-  const int64_t chosen = problem->num_tokens * problem->top_k * 4;
-  const Span in[] = {{"logits", logits, logits_bytes(*problem)}, {"bias", bias, int64_t{problem->num_experts} * 4}};
-  const Span out[] = {{"ids", ids, chosen}, {"weights", weights, chosen}};
-  if ((st = check_apart(in, out)) != MOEGG_OK) return st;
-  moegg::RouteArgs a = route_args(*problem);
-  a.logits = logits;
-  a.bias = bias;
-  a.ids = ids;
-  a.weights = weights;
-  return launched(moegg::launch_route(a, static_cast<hipStream_t>(stream)), "route kernel");
+  return run_route(problem, nullptr, false, logits, bias, ids, weights, stream);
+}
+
+moegg_status moegg_route_grouped(const moegg_route_problem* problem, const moegg_route_groups* groups, const void* logits,
+                                 const float* bias, int32_t* ids, float* weights, void* stream) {
+  return run_route(problem, groups, true, logits, bias, ids, weights, stream);
 }
 
 moegg_status moegg_route_backward(const moegg_route_problem* problem, const void* logits, const int32_t* ids,
@@ -491,61 +715,128 @@ int64_t moegg_linear_backward_workspace(const moegg_linear_problem* problem, int
   return moegg::linear_backward_workspace(linear_args(*problem, nullptr), want & 1, want & 2, want & 4);
 }
 
+int64_t moegg_linear_saving_workspace(const moegg_linear_problem* problem, const moegg_linear_saved* saved) {
+  if (check_linear(problem) != MOEGG_OK || (saved && check_saved(*problem, *saved) != MOEGG_OK)) return -1;
+  return moegg::linear_workspace(linear_args(*problem, nullptr, saved));
+}
+
+int64_t moegg_linear_saved_backward_workspace(const moegg_linear_problem* problem, const moegg_linear_saved* saved,
+                                              int32_t want) {
+  if (check_linear(problem) != MOEGG_OK || (saved && check_saved(*problem, *saved) != MOEGG_OK)) return -1;
+  return moegg::linear_backward_workspace(linear_args(*problem, nullptr, saved), want & 1, want & 2, want & 4);
+}
+
 moegg_status moegg_linear(const moegg_linear_problem* problem, const moegg_linear_args* args, void* stream) {
-  moegg_status st = check_linear(problem);
-  if (st != MOEGG_OK) return st;
-  if (!args) return set_error(MOEGG_ERROR_INVALID_VALUE, "args must be non-NULL");
-  const moegg_linear_problem& p = *problem;
-  const moegg::LinearArgs a = linear_args(p, args);
-  const bool any = p.m > 0;
-  if (any && (!a.x || !a.w || !a.y)) return set_error(MOEGG_ERROR_INVALID_VALUE, "x, w and y are required");
-  if (a.dy || a.dx || a.dw || a.db)
-    return set_error(MOEGG_ERROR_INVALID_VALUE, "dy, dx, dw and db are for moegg_linear_backward");
-  const int64_t workspace = moegg::linear_workspace(a);
-  st = check_linear_pointers(p, *args, workspace);
-  if (st != MOEGG_OK) return st;
-  const int64_t n_out = p.act == MOEGG_ACT_SWIGLU ? p.n / 2 : p.n;
-  const int64_t y_bytes = p.m * n_out * (a.out_f32 ? 4 : 2);
-  const int64_t c_bytes = p.m * p.n * 2;
-  const Span in[] = {{"x", a.x, p.m * p.k * 2}, {"w", a.w, w_bytes(p)}, {"bias", a.bias, int64_t{p.num_groups} * p.n * 4},
-                     {"offsets", a.offsets, int64_t{p.num_groups} * 4}};
-  const Span out[] = {{"y", a.y, y_bytes}, {"c", a.c, c_bytes}, {"workspace", a.workspace, workspace}};
-  if ((st = check_apart(in, out)) != MOEGG_OK) return st;
-  if (overlap(a.residual, p.m * n_out * 2, a.c, c_bytes) || overlap(a.residual, p.m * n_out * 2, a.workspace, workspace))
-    return set_error(MOEGG_ERROR_INVALID_VALUE, "residual and c or the workspace overlap");
-  if (overlap(a.residual, p.m * n_out * 2, a.y, y_bytes) && (a.out_f32 || static_cast<const void*>(a.residual) != a.y))
-    return set_error(MOEGG_ERROR_INVALID_VALUE, "residual and y overlap without being the same BF16 tensor");
-  if (!any) return launched(hipSuccess, "linear");
-  return launched(moegg::launch_linear(a, static_cast<hipStream_t>(stream)), "linear kernel");
+  return run_linear(problem, args, nullptr, stream);
 }
 
 moegg_status moegg_linear_backward(const moegg_linear_problem* problem, const moegg_linear_args* args, void* stream) {
-  moegg_status st = check_linear(problem);
+  return run_linear_backward(problem, args, nullptr, stream);
+}
+
+moegg_status moegg_linear_saving(const moegg_linear_problem* problem, const moegg_linear_args* args,
+                                 const moegg_linear_saved* saved, void* stream) {
+  return run_linear(problem, args, saved, stream);
+}
+
+moegg_status moegg_linear_saved_backward(const moegg_linear_problem* problem, const moegg_linear_args* args,
+                                         const moegg_linear_saved* saved, void* stream) {
+  return run_linear_backward(problem, args, saved, stream);
+}
+
+moegg_status moegg_quantise(const void* x, int32_t x_dtype, int64_t rows, int32_t width, int32_t dtype, int32_t sf_layout,
+                            uint8_t* codes, uint8_t* sf, void* stream) {
+  moegg_status st = check_kept_rows(x_dtype, rows, width, dtype, sf_layout);
+  if (st != MOEGG_OK) return st;
+  const bool any = rows > 0;
+  const Pointer ps[] = {{"x", x, 16, any}, {"codes", codes, 16, any}, {"sf", sf, 16, any}};
+  if ((st = check_pointers(ps)) != MOEGG_OK) return st;
+  const Span in[] = {{"x", x, rows * width * (x_dtype == MOEGG_DT_F32 ? 4 : 2)}};
+  const Span out[] = {{"codes", codes, rows * width}, {"sf", sf, rows * (width / 32)}};
+  if ((st = check_apart(in, out)) != MOEGG_OK) return st;
+  if (!any) return launched(hipSuccess, "quantise");
+  return launched(moegg::launch_quantise(x, x_dtype == MOEGG_DT_F32, codes, sf, row_kind(dtype), sf_layout == MOEGG_SF_KPLANES,
+                                         rows, width, static_cast<hipStream_t>(stream)),
+                  "quantise kernel");
+}
+
+moegg_status moegg_dequantise(const uint8_t* codes, const uint8_t* sf, int64_t rows, int32_t width, int32_t dtype,
+                              int32_t sf_layout, void* x, int32_t x_dtype, void* stream) {
+  moegg_status st = check_kept_rows(x_dtype, rows, width, dtype, sf_layout);
+  if (st != MOEGG_OK) return st;
+  const bool any = rows > 0;
+  const Pointer ps[] = {{"x", x, 16, any}, {"codes", codes, 16, any}, {"sf", sf, 16, any}};
+  if ((st = check_pointers(ps)) != MOEGG_OK) return st;
+  const Span in[] = {{"codes", codes, rows * width}, {"sf", sf, rows * (width / 32)}};
+  const Span out[] = {{"x", x, rows * width * (x_dtype == MOEGG_DT_F32 ? 4 : 2)}};
+  if ((st = check_apart(in, out)) != MOEGG_OK) return st;
+  if (!any) return launched(hipSuccess, "dequantise");
+  const moegg::SavedRows q{codes, sf, row_kind(dtype), sf_layout == MOEGG_SF_KPLANES};
+  return launched(moegg::launch_dequantise(q, x, x_dtype == MOEGG_DT_F32, rows, width, static_cast<hipStream_t>(stream)),
+                  "dequantise kernel");
+}
+
+moegg_status moegg_rms_norm(const moegg_norm_problem* problem, const moegg_norm_args* args, void* stream) {
+  moegg_status st = check_norm(problem, false);
   if (st != MOEGG_OK) return st;
   if (!args) return set_error(MOEGG_ERROR_INVALID_VALUE, "args must be non-NULL");
-  const moegg_linear_problem& p = *problem;
-  const moegg::LinearArgs a = linear_args(p, args);
-  const bool any = p.m > 0;
-  if (a.bias || a.residual || a.y)
-    return set_error(MOEGG_ERROR_INVALID_VALUE, "bias, residual and y are for moegg_linear");
-  // (without rows dx has no elements, and its pointer may be NULL)
-  const bool none = !a.dx && !a.dw && !a.db;
-  if (any && none) return set_error(MOEGG_ERROR_INVALID_VALUE, "one of dx, dw and db is required");
-  if (any && !a.dy) return set_error(MOEGG_ERROR_INVALID_VALUE, "dy is required");
-  if (any && a.act != moegg::LIN_NONE && !a.c) return set_error(MOEGG_ERROR_INVALID_VALUE, "this activation's gradient needs c");
-  if (any && a.dx && !a.w) return set_error(MOEGG_ERROR_INVALID_VALUE, "dx needs w");
-  if (any && a.dw && !a.x) return set_error(MOEGG_ERROR_INVALID_VALUE, "dw needs x");
-  const int64_t workspace = moegg::linear_backward_workspace(a, a.dx, a.dw, a.db);
-  st = check_linear_pointers(p, *args, workspace);
-  if (st != MOEGG_OK) return st;
-  const int64_t n_out = p.act == MOEGG_ACT_SWIGLU ? p.n / 2 : p.n;
-  const Span in[] = {{"x", a.x, p.m * p.k * 2}, {"w", a.w, w_bytes(p)}, {"dy", a.dy, p.m * n_out * 2}, {"c", a.c, p.m * p.n * 2},
-                     {"offsets", a.offsets, int64_t{p.num_groups} * 4}};
-  const Span out[] = {{"dx", a.dx, p.m * p.k * 2}, {"dw", a.dw, w_bytes(p) * (a.out_f32 ? 2 : 1)},
-                      {"db", a.db, int64_t{p.num_groups} * p.n * 4}, {"workspace", a.workspace, workspace}};
+  const moegg_norm_problem& p = *problem;
+  const moegg_norm_args& q = *args;
+  const bool any = p.rows > 0, mx = p.mx_dtype != MOEGG_DT_NONE;
+  const Pointer ps[] = {{"x", q.x, 16, any}, {"weight", q.weight, 4, any}, {"residual", q.residual, 16, false},
+                        {"h", q.h, 16, any && q.residual}, {"y", q.y, 16, any && !mx}, {"codes", q.codes, 16, any && mx},
+                        {"sf", q.sf, 16, any && mx}};
+  if ((st = check_pointers(ps)) != MOEGG_OK) return st;
+  if (q.dy || q.dh || q.dx || q.dweight)
+    return set_error(MOEGG_ERROR_INVALID_VALUE, "dy, dh, dx and dweight are for moegg_rms_norm_backward");
+  if (any && !q.residual && q.h) return set_error(MOEGG_ERROR_INVALID_VALUE, "h without a residual is x");
+  if (any && !q.residual && p.x_dtype != p.stream_dtype)
+    return set_error(MOEGG_ERROR_INVALID_VALUE, "without a residual x has the stream's type");
+  if (!mx && (q.codes || q.sf)) return set_error(MOEGG_ERROR_INVALID_VALUE, "codes and sf need mx_dtype");
+  const int64_t n = p.rows * p.width, stream_bytes = n * (p.stream_dtype == MOEGG_DT_F32 ? 4 : 2);
+  const Span in[] = {{"x", q.x, n * (p.x_dtype == MOEGG_DT_F32 ? 4 : 2)}, {"weight", q.weight, int64_t{p.width} * 4}};
+  const Span out[] = {{"h", q.h, stream_bytes}, {"y", q.y, n * 2}, {"codes", q.codes, p.mx_dtype == MOEGG_DT_E2M1X2 ? n / 2 : n},
+                      {"sf", q.sf, p.rows * (p.width / 32)}};
   if ((st = check_apart(in, out)) != MOEGG_OK) return st;
-  if (none) return launched(hipSuccess, "linear backward");
-  return launched(moegg::launch_linear_backward(a, static_cast<hipStream_t>(stream)), "linear backward kernel");
+  for (const Span& o : out)
+    if (overlap(q.residual, stream_bytes, o.p, o.bytes) && (o.p != q.h || q.residual != q.h))
+      return set_error(MOEGG_ERROR_INVALID_VALUE, "residual and %s overlap", o.name);
+  if (!any) return launched(hipSuccess, "rms_norm");
+  return launched(moegg::launch_rms_norm(norm_args(p, q, false), static_cast<hipStream_t>(stream)), "rms_norm kernel");
+}
+
+int64_t moegg_rms_norm_backward_workspace(const moegg_norm_problem* problem) {
+  if (check_norm(problem, true) != MOEGG_OK) return -1;
+  return moegg::rms_norm_backward_workspace(problem->rows, problem->width);
+}
+
+moegg_status moegg_rms_norm_backward(const moegg_norm_problem* problem, const moegg_norm_args* args, void* stream) {
+  moegg_status st = check_norm(problem, true);
+  if (st != MOEGG_OK) return st;
+  if (!args) return set_error(MOEGG_ERROR_INVALID_VALUE, "args must be non-NULL");
+  const moegg_norm_problem& p = *problem;
+  const moegg_norm_args& q = *args;
+  const bool any = p.rows > 0, none = !q.dx && !q.dweight;
+  if (any && none) return set_error(MOEGG_ERROR_INVALID_VALUE, "one of dx and dweight is required");
+  const Pointer ps[] = {{"dy", q.dy, 16, any}, {"h", q.h, 16, any}, {"weight", q.weight, 4, any}, {"dh", q.dh, 16, false},
+                        {"dx", q.dx, 16, false}, {"dweight", q.dweight, 4, false}, {"workspace", q.workspace, 16, false}};
+  if ((st = check_pointers(ps)) != MOEGG_OK) return st;
+  if (q.x || q.residual || q.y || q.codes || q.sf)
+    return set_error(MOEGG_ERROR_INVALID_VALUE, "x, residual, y, codes and sf are for moegg_rms_norm");
+  const int64_t need = q.dweight ? moegg::rms_norm_backward_workspace(p.rows, p.width) : 0;
+  if (need > 0 && (!q.workspace || q.workspace_bytes < need))
+    return set_error(MOEGG_ERROR_INVALID_VALUE, "workspace of %lld bytes needed, %lld given", (long long)need,
+                     (long long)(q.workspace ? q.workspace_bytes : 0));
+  const int64_t n = p.rows * p.width, stream_bytes = n * (p.stream_dtype == MOEGG_DT_F32 ? 4 : 2);
+  const Span in[] = {{"dy", q.dy, n * 2}, {"h", q.h, stream_bytes}, {"weight", q.weight, int64_t{p.width} * 4}};
+  const Span out[] = {{"dx", q.dx, stream_bytes}, {"dweight", q.dweight, int64_t{p.width} * 4}, {"workspace", q.workspace, need}};
+  if ((st = check_apart(in, out)) != MOEGG_OK) return st;
+  for (const Span& o : out)
+    if (overlap(q.dh, stream_bytes, o.p, o.bytes) && (o.p != q.dx || q.dh != q.dx))
+      return set_error(MOEGG_ERROR_INVALID_VALUE, "dh and %s overlap", o.name);
+  if (none) return launched(hipSuccess, "rms_norm backward");
+  return launched(moegg::launch_rms_norm_backward(norm_args(p, q, true), static_cast<hipStream_t>(stream)),
+                  "rms_norm backward kernel");
 }
 
 }  // extern "C"

@@ -1,6 +1,6 @@
 // Internal interface between the C-ABI front of the layer operators
 // (layer_api.cpp) and their HIP kernels (route.hip, exchange.hip,
-// linear.hip).  Not installed, not part of the ABI.
+// linear.hip, norm.hip, saved.hip).  Not installed, not part of the ABI.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -18,6 +18,7 @@ void clear_error();
 
 constexpr int kMaxExperts = 1024;   // as the grouped product's num_groups
 constexpr int kMaxTopK = 32;
+constexpr int kMaxGroups = 64;
 
 struct RouteArgs {
   const void* logits;      // (T, E) fp32 or bf16
@@ -33,6 +34,10 @@ struct RouteArgs {
   bool softmax;
   bool renormalise;
   float scale;
+  int32_t groups;          // 1: none
+  int32_t top_groups;
+  bool group_sums;         // a group's score: its two largest keys added, else its largest
+  uint32_t group_magic;    // expert e is in group (e magic) >> 22
 };
 hipError_t launch_route(const RouteArgs& a, hipStream_t s);
 hipError_t launch_route_backward(const RouteArgs& a, hipStream_t s);
@@ -110,6 +115,50 @@ hipError_t launch_combine_backward(const ExchangeArgs& a, hipStream_t s);
 hipError_t launch_unsort(const float* rows, const int32_t* row_of, float* values, int64_t slots, int64_t n_rows,
                          hipStream_t s);
 
+// ---- norm ------------------------------------------------------------------
+
+constexpr int kMaxNormWidth = 32768;  // 16 waves of 4 pieces of 8 columns a lane
+
+struct NormArgs {
+  const void* x;            // (T, H) bf16 or fp32
+  const void* residual;     // (T, H) in the stream's type, or null
+  const float* weight;      // (H)
+  void* h;                  // (T, H) in the stream's type: with a residual
+  uint16_t* y;              // (T, H) bf16 or null
+  uint8_t* codes;           // (T, H) in `kind`, MX kinds
+  uint8_t* scales;
+  const uint16_t* dy;       // (T, H) bf16                     [backward]
+  const void* stored;       // (T, H) in the stream's type: h  [backward]
+  const void* dh;           // the same, or null               [backward]
+  void* dx;                 // the same, or null               [backward]
+  float* dw;                // (H) or null                     [backward]
+  float* partial;           // workspace (with dw): rows of dw's parts
+  int64_t rows;
+  int32_t width;
+  int32_t kind;             // RowKind of the codes (ROW_BF16: y alone)
+  bool x_f32;
+  bool stream_f32;
+  bool kplanes;
+  double eps;
+  double inverse_width;
+};
+hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s);
+int64_t rms_norm_backward_workspace(int64_t rows, int32_t width);
+hipError_t launch_rms_norm_backward(const NormArgs& a, hipStream_t s);
+
+// ---- rows kept in 8 bits -----------------------------------------------------
+
+struct SavedRows {
+  const uint8_t* codes;     // (rows, width) E4M3 or E5M2
+  const uint8_t* scales;    // (rows, width / 32), or (width / 128, rows, 4) planes
+  int32_t kind;             // ROW_E4M3 | ROW_E5M2
+  bool kplanes;
+};
+// codes and scales of x (bf16 or fp32); out (bf16 or fp32) of codes and scales
+hipError_t launch_quantise(const void* x, bool x_f32, uint8_t* codes, uint8_t* scales, int kind, bool kplanes, int64_t rows,
+                           int32_t width, hipStream_t s);
+hipError_t launch_dequantise(const SavedRows& q, void* out, bool out_f32, int64_t rows, int32_t width, hipStream_t s);
+
 // ---- linear ----------------------------------------------------------------
 
 enum LinearAct : int { LIN_NONE = 0, LIN_SWIGLU = 1, LIN_SRELU = 2, LIN_GELU = 3 };
@@ -137,6 +186,9 @@ struct LinearArgs {
   int32_t groups;
   int32_t act;              // LinearAct
   bool out_f32;             // y (forward) or dw (backward) in fp32
+  int32_t c_kind;           // RowKind of c: ROW_BF16, or 8 bits (c holds codes)
+  uint8_t* c_sf;            // scales of an 8-bit c, (M, N / 32)
+  SavedRows x8;             // x in 8 bits (kind ROW_BF16: none)    [backward]
 };
 // Bytes of workspace (pointers in `a` only say what is asked for).
 int64_t linear_workspace(const LinearArgs& a);

@@ -132,6 +132,23 @@ __device__ __forceinline__ void store4(void* base, bool f32, int64_t i, v4f v) {
   else *reinterpret_cast<v2u*>(static_cast<uint16_t*>(base) + i) = v2u{bf16x2(v.x, v.y), bf16x2(v.z, v.w)};
 }
 
+// Four columns of z (c's columns at, ...), kept in 8 bits: 8 neighbouring
+// threads have a block of 32.
+template <int KIND>
+__device__ __forceinline__ void save4(const LinearArgs& a, int64_t row, int col, v4f z) {
+  const float f[4] = {z.x, z.y, z.z, z.w};
+  uint32_t amax = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) amax = max(amax, __float_as_uint(f[e]) & 0x7FFFFFFFu);
+  amax = max(amax, dpp_u<0xB1>(amax));
+  amax = max(amax, dpp_u<0x4E>(amax));
+  amax = max(amax, dpp_u<0x141>(amax));
+  const uint32_t byte = mx_block_byte<KIND>(amax);
+  *reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(a.c) + row * a.n + col) =
+      byte == 255u ? 0u : mx_codes<KIND>(f, mx_factor(byte));
+  if ((col & 31) == 0) a.c_sf[row * (a.n >> 5) + (col >> 5)] = static_cast<uint8_t>(byte);
+}
+
 // The parts of tiles [first, tiles), added in their order: 4 columns of the
 // output a thread (and, of a SwiGLU pair, their 4 gates).
 template <int MODE, int BP, int BQ>
@@ -163,7 +180,9 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs a, TilePlan
     auto z_of = [&](int off) __attribute__((always_inline)) {
       v4f z = sum(off);
       if (a.bias) z += *reinterpret_cast<const v4f_any*>(a.bias + c + off);
-      if (a.c) store4(a.c, false, r * a.n + c + off, z);
+      if (a.c && a.c_kind == ROW_E4M3) save4<ROW_E4M3>(a, r, c + off, z);
+      else if (a.c && a.c_kind == ROW_E5M2) save4<ROW_E5M2>(a, r, c + off, z);
+      else if (a.c) store4(a.c, false, r * a.n + c + off, z);
       return z;
     };
     v4f z = z_of(0);
@@ -214,16 +233,45 @@ __device__ __forceinline__ v4u pack8(const float* f) {
   return v4u{bf16x2(f[0], f[1]), bf16x2(f[2], f[3]), bf16x2(f[4], f[5]), bf16x2(f[6], f[7])};
 }
 
+// Eight columns of a row of c: BF16, or codes and their block's scale byte.
+template <int CK>
+struct EightOfC {
+  v2u codes;
+  uint32_t byte;
+  __device__ __forceinline__ void clear() {
+    codes = v2u{};
+    byte = 0;
+  }
+  __device__ __forceinline__ void load(const LinearArgs& a, int64_t row, int n) {
+    codes = *reinterpret_cast<const v2u*>(reinterpret_cast<const uint8_t*>(a.c) + row * a.n + n);
+    byte = a.c_sf[row * (a.n >> 5) + (n >> 5)];
+  }
+  __device__ __forceinline__ void get(float* z) const {
+    const float f = mx_scale_value(byte);
+    mx_four<CK>(codes.x, f, z);
+    mx_four<CK>(codes.y, f, z + 4);
+  }
+};
+template <>
+struct EightOfC<ROW_BF16> {
+  v4u u;
+  __device__ __forceinline__ void clear() { u = v4u{}; }
+  __device__ __forceinline__ void load(const LinearArgs& a, int64_t row, int n) {
+    u = *reinterpret_cast<const v4u*>(a.c + row * a.n + n);
+  }
+  __device__ __forceinline__ void get(float* z) const { unpack8(u, z); }
+};
+
 // One row's 8 columns of dy (and of c, or of both halves of a pair) -> dz.
-template <int ACT>
-__device__ __forceinline__ void dz_of(const float* d, v4u c0, v4u c1, float* v, float* w) {
+template <int ACT, int CK>
+__device__ __forceinline__ void dz_of(const float* d, const EightOfC<CK>& c0, const EightOfC<CK>& c1, float* v, float* w) {
   if constexpr (ACT == LIN_NONE) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = d[i];
   } else if constexpr (ACT == LIN_SWIGLU) {
     float x[8], q[8];
-    unpack8(c0, x);
-    unpack8(c1, q);
+    c0.get(x);
+    c1.get(q);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float s = sigmoid_f(q[i]);
@@ -232,7 +280,7 @@ __device__ __forceinline__ void dz_of(const float* d, v4u c0, v4u c1, float* v, 
     }
   } else {
     float z[8];
-    unpack8(c0, z);
+    c0.get(z);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if constexpr (ACT == LIN_SRELU) {
@@ -250,7 +298,7 @@ __device__ __forceinline__ void dz_of(const float* d, v4u c0, v4u c1, float* v, 
 
 // 32 threads run along 256 columns of dy, 8 rows at a time; four of a
 // thread's rows are in flight at once.
-template <int ACT>
+template <int ACT, int CK>
 __global__ __launch_bounds__(256) void linear_dz_kernel(LinearArgs a, uint16_t* dz, float* sums) {
   constexpr bool PAIR = ACT == LIN_SWIGLU;
   constexpr int S = PAIR ? 16 : 8, U = 4;
@@ -268,15 +316,16 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinearArgs a, uint16_t* 
   const int rows = static_cast<int>(min(end - row0, int64_t{kDzRows}));
   if (col < n_out) {
     for (int r = ty; r < rows; r += 8 * U) {
-      v4u d[U], c0[U], c1[U];
+      v4u d[U];
+      EightOfC<CK> c0[U], c1[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t m = row0 + min(r + 8 * u, rows - 1);     // (rows past the end: read, not used)
         d[u] = *reinterpret_cast<const v4u*>(a.dy + m * n_out + col);
-        c0[u] = v4u{};
-        c1[u] = v4u{};
-        if constexpr (ACT != LIN_NONE) c0[u] = *reinterpret_cast<const v4u*>(a.c + m * a.n + n);
-        if constexpr (PAIR) c1[u] = *reinterpret_cast<const v4u*>(a.c + m * a.n + n + 32);
+        c0[u].clear();
+        c1[u].clear();
+        if constexpr (ACT != LIN_NONE) c0[u].load(a, m, n);
+        if constexpr (PAIR) c1[u].load(a, m, n + 32);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -284,7 +333,7 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinearArgs a, uint16_t* 
         const int64_t m = row0 + r + 8 * u;
         float f[8], v[8], w[8];
         unpack8(d[u], f);
-        dz_of<ACT>(f, c0[u], c1[u], v, w);
+        dz_of<ACT, CK>(f, c0[u], c1[u], v, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           s[i] += v[i];
@@ -453,7 +502,10 @@ Plan plan_dw(const LinearArgs& a) {
 // Measured, against tiles, 64 groups of 2048 x 1408: 32 rows 27 / 28 us, 64
 // rows 37 / 51, 128 rows 59 / 61, 256 rows 68 / 64; with all rows in one
 // group 128 rows 39 / 18, 512 rows 155 / 18.
+// Its columns are spread over workgroups, so it does not keep c in 8 bits,
+// whose blocks are 32 columns: tiles do.
 bool few_rows(const LinearArgs& a) {
+  if (a.c_kind != ROW_BF16) return false;
   return a.m <= kFewRows || (a.m <= 2 * static_cast<int64_t>(a.groups) && a.m <= 8 * kFewRows);
 }
 
@@ -469,7 +521,7 @@ struct ForwardPlan {
 ForwardPlan plan_forward(const LinearArgs& a) {
   ForwardPlan f{plan_rows(a, MODE_FORWARD), 0};
   const int64_t few = a.m % 128;
-  if (a.groups == 1 && !a.offsets && few && few <= kFewRows && few < a.m) {
+  if (a.c_kind == ROW_BF16 && a.groups == 1 && !a.offsets && few && few <= kFewRows && few < a.m) {
     LinearArgs b = a;
     b.m -= few;
     const Plan p = plan_rows(b, MODE_FORWARD);
@@ -534,10 +586,10 @@ hipError_t launch_both(const LinearArgs& a, const Plan& dx, const Plan& dw, hipS
   return hipGetLastError();
 }
 
-// Workspace of the backward: dz, the column sums of the row tiles, and the
-// parts of dx and of dw.
+// Workspace of the backward: dz, the column sums of the row tiles, the parts
+// of dx and of dw, and x in BF16 where it is kept in 8 bits.
 struct BackwardWorkspace {
-  int64_t dz, sums, dx, dw, total;
+  int64_t dz, sums, dx, dw, x, total;
 };
 BackwardWorkspace backward_workspace(const LinearArgs& a, bool dx, bool dw, bool db) {
   BackwardWorkspace w{};
@@ -551,6 +603,7 @@ BackwardWorkspace backward_workspace(const LinearArgs& a, bool dx, bool dw, bool
   w.sums = take(db ? row_tiles(a, kDzRows) * a.n * 4 : 0);
   w.dx = take(dx && a.m ? plan_rows(a, MODE_DX).partial_bytes : 0);
   w.dw = take(dw ? plan_dw(a).partial_bytes : 0);
+  w.x = take(dw && a.x8.kind != ROW_BF16 ? a.m * a.k * 2 : 0);
   w.total = at;
   return w;
 }
@@ -600,6 +653,18 @@ hipError_t launch_linear(const LinearArgs& args, hipStream_t s) {
   return launch_few_rows(a, s);
 }
 
+namespace {
+template <int CK>
+void launch_dz(const LinearArgs& a, dim3 grid, uint16_t* dz, float* sums, hipStream_t s) {
+  switch (a.act) {
+    case LIN_SWIGLU: hipLaunchKernelGGL((linear_dz_kernel<LIN_SWIGLU, CK>), grid, dim3(256), 0, s, a, dz, sums); break;
+    case LIN_SRELU: hipLaunchKernelGGL((linear_dz_kernel<LIN_SRELU, CK>), grid, dim3(256), 0, s, a, dz, sums); break;
+    case LIN_GELU: hipLaunchKernelGGL((linear_dz_kernel<LIN_GELU, CK>), grid, dim3(256), 0, s, a, dz, sums); break;
+    default: hipLaunchKernelGGL((linear_dz_kernel<LIN_NONE, ROW_BF16>), grid, dim3(256), 0, s, a, dz, sums); break;
+  }
+}
+}  // namespace
+
 hipError_t launch_linear_backward(const LinearArgs& args, hipStream_t s) {
   LinearArgs a = args;
   const BackwardWorkspace w = backward_workspace(a, a.dx, a.dw, a.db);
@@ -614,13 +679,17 @@ hipError_t launch_linear_backward(const LinearArgs& args, hipStream_t s) {
   if ((make_dz || a.db) && a.m) {
     const int n_out = a.act == LIN_SWIGLU ? a.n / 2 : a.n;
     const dim3 grid(static_cast<unsigned>(row_tiles(a, kDzRows)), static_cast<unsigned>(div_up(n_out, 256)));
-    switch (a.act) {
-      case LIN_SWIGLU: hipLaunchKernelGGL((linear_dz_kernel<LIN_SWIGLU>), grid, dim3(256), 0, s, a, dz, sums); break;
-      case LIN_SRELU: hipLaunchKernelGGL((linear_dz_kernel<LIN_SRELU>), grid, dim3(256), 0, s, a, dz, sums); break;
-      case LIN_GELU: hipLaunchKernelGGL((linear_dz_kernel<LIN_GELU>), grid, dim3(256), 0, s, a, dz, sums); break;
-      default: hipLaunchKernelGGL((linear_dz_kernel<LIN_NONE>), grid, dim3(256), 0, s, a, dz, sums); break;
+    switch (a.c_kind) {
+      case ROW_E4M3: launch_dz<ROW_E4M3>(a, grid, dz, sums, s); break;
+      case ROW_E5M2: launch_dz<ROW_E5M2>(a, grid, dz, sums, s); break;
+      default: launch_dz<ROW_BF16>(a, grid, dz, sums, s); break;
     }
     if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (a.dw && a.x8.kind != ROW_BF16) {
+    uint16_t* const x = reinterpret_cast<uint16_t*>(ws + w.x);
+    if (a.m && (e = launch_dequantise(a.x8, x, false, a.m, a.k, s)) != hipSuccess) return e;
+    a.x = x;
   }
   if (a.db) {
     // few row tiles a group: few threads a column, or most of them only wait (64

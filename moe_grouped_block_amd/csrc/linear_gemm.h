@@ -22,6 +22,7 @@
 
 #include "grouped_gemm.h"
 #include "layer_internal.h"
+#include "mx_rows.h"
 
 namespace moegg {
 namespace {
@@ -358,6 +359,34 @@ __device__ __forceinline__ void store_part(float* partial, v16f (&acc)[TM][TN], 
     }
 }
 
+// z of a 32-row block and 32 TN columns from ncol on, kept in 8 bits: c's codes
+// and scale bytes.  A lane and its partner in the other half hold a row's block
+// of 32, so its largest magnitude is one exchange away.
+template <int KIND, int TN>
+__device__ __forceinline__ void store_saved(const LinearArgs& a, const float (&z)[TN][16], int64_t rb, int rows, int ncol,
+                                            uint8_t* scratch, int lane) {
+  const int l32 = lane & 31, hi = lane >> 5;
+  v4u q[TN];
+  uint32_t mine = 0;
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {
+    uint32_t amax = 0;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) amax = max(amax, __float_as_uint(z[j][e]) & 0x7FFFFFFFu);
+    amax = max(amax, other_half(amax, hi));
+    const uint32_t byte = mx_block_byte<KIND>(amax), keep = byte == 255u ? 0u : 0xFFFFFFFFu;
+    const float f = mx_factor(byte);
+    uint32_t w[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) w[b] = mx_codes<KIND>(&z[j][4 * b], f) & keep;
+    q[j] = e4m3_piece(w);
+    if (j == hi) mine = byte;
+  }
+  store_block<32 * TN>(reinterpret_cast<uint8_t*>(a.c) + rb * a.n + ncol, a.n, q, scratch, lane, rows, a.n - ncol);
+  if (l32 < rows && ncol + 32 * hi < a.n)
+    a.c_sf[(rb + l32) * (a.n >> 5) + (ncol >> 5) + hi] = static_cast<uint8_t>(mine);
+}
+
 // A wave's accumulators to memory: rows [row, row + 32 TM) of group g up to
 // row_end, 64 columns from ncol on, through 4 KB of LDS scratch.
 template <int MODE, int TM, int TN>
@@ -411,7 +440,11 @@ __device__ __forceinline__ void store_output(const LinearArgs& a, v16f (&acc)[TM
 #pragma unroll
           for (int e = 0; e < 4; ++e) z[j][4 * b + e] = acc[i][j][4 * b + e] + v[e];
         }
-      if (a.c) {
+      if (a.c && a.c_kind == ROW_E4M3) {
+        store_saved<ROW_E4M3>(a, z, rb, rows, ncol, scratch, lane);
+      } else if (a.c && a.c_kind == ROW_E5M2) {
+        store_saved<ROW_E5M2>(a, z, rb, rows, ncol, scratch, lane);
+      } else if (a.c) {
         v4u v[4];
 #pragma unroll
         for (int j = 0; j < TN; ++j) bf16_pieces(z[j], v + 2 * j);

@@ -1,0 +1,164 @@
+// MX rows: 8- or 4-bit codes in blocks of 32 with an E8M0 scale byte each, from
+// BF16 or fp32 and (8 bits) back.
+#pragma once
+
+#include "lanes.h"
+#include "layer_internal.h"
+
+namespace moegg {
+namespace {
+
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+
+// E8M0 byte of the smallest power of two s with amax <= s q_max, q_max =
+// (1 + M / 8) 2^EMAX, read off the bits of amax (fp32, >= 0), so that no
+// rounding decides it; 0 for a block of zeros, 255 (NaN) for one that holds a
+// NaN or an infinity.
+template <int EMAX, uint32_t M>
+__device__ __forceinline__ uint32_t mx_byte(uint32_t amax) {
+  const int e = static_cast<int>(amax >> 23);
+  if (e == 255) return 255u;
+  const int byte = e - EMAX + ((amax & 0x7FFFFFu) > (M << 20) ? 1 : 0);
+  return static_cast<uint32_t>(byte < 0 ? 0 : byte);
+}
+
+// Scale byte of a block whose largest magnitude has the fp32 bits amax.
+template <int KIND>
+__device__ __forceinline__ uint32_t mx_block_byte(uint32_t amax) {
+  if constexpr (KIND == ROW_E4M3) return mx_byte<8, 6>(amax);
+  else if constexpr (KIND == ROW_E5M2) return mx_byte<15, 6>(amax);
+  else return mx_byte<2, 4>(amax);
+}
+
+// MX rows: lane l holds columns 16 l + [0, 16) of a 1024-column chunk; a block
+// of 32 is 2 lanes, a scale word (128 columns) 8.
+
+// A block's amax (fp32 bits) in its lanes -> its scale byte; the scale word of
+// the lane's 128 columns (all 8 lanes alike).
+template <int KIND>
+__device__ __forceinline__ uint32_t mx_scale(uint32_t amax, uint32_t& word) {
+  amax = max(amax, dpp_u<0xB1>(amax));
+  const uint32_t byte = mx_block_byte<KIND>(amax);
+  word = byte << (8 * ((threadIdx.x >> 1) & 3));
+  word |= dpp_u<0x4E>(word);        // lanes 2 apart: two bytes
+  word |= dpp_u<0x141>(word);       // mirrored halves of 8: all four
+  return byte;
+}
+
+// The scaled conversions divide by the power of two given as fp32 (2^-127 is
+// its subnormal) and round to nearest even.
+typedef short v2s __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ float mx_factor(uint32_t byte) { return __uint_as_float(byte ? byte << 23 : 0x00400000u); }
+
+// 16 bf16 (two 16-byte pieces) -> codes: 16 bytes, or 8 of E2M1; zeros in a
+// block that holds a NaN or an infinity.
+template <int KIND>
+__device__ __forceinline__ uint32_t mx_from_bf16(v4u a, v4u b, v4u& codes) {
+  typedef uint16_t v2h __attribute__((ext_vector_type(2)));
+  typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+  const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  v2h m = __builtin_bit_cast(v2h, u[0] & 0x7FFF7FFFu);       // magnitudes; NaN bits are the largest
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(v2h, u[i] & 0x7FFF7FFFu));
+  uint32_t word;
+  const uint32_t byte = mx_scale<KIND>(static_cast<uint32_t>(max(m.x, m.y)) << 16, word);
+  const float f = mx_factor(byte);
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const v2b x = __builtin_bit_cast(v2b, u[2 * i]), y = __builtin_bit_cast(v2b, u[2 * i + 1]);
+    if constexpr (KIND == ROW_E4M3) {
+      v2s c = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(v2s{0, 0}, x, f, false);
+      w[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(c, y, f, true));
+    } else if constexpr (KIND == ROW_E5M2) {
+      v2s c = __builtin_amdgcn_cvt_scalef32_pk_bf8_bf16(v2s{0, 0}, x, f, false);
+      w[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf8_bf16(c, y, f, true));
+    } else if (i & 1) {
+      w[i / 2] = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w[i / 2], x, f, 2);
+      w[i / 2] = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w[i / 2], y, f, 3);
+    } else {
+      w[i / 2] = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w[i / 2], x, f, 0);
+      w[i / 2] = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w[i / 2], y, f, 1);
+    }
+  }
+  const uint32_t keep = byte == 255u ? 0u : 0xFFFFFFFFu;
+  codes = v4u{w[0] & keep, w[1] & keep, w[2] & keep, w[3] & keep};
+  return word;
+}
+
+// The same from 16 fp32.
+template <int KIND>
+__device__ __forceinline__ uint32_t mx_from_f32(const float* v, v4u& codes) {
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  uint32_t word;
+  const uint32_t byte = mx_scale<KIND>(amax, word);
+  const float f = mx_factor(byte);
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float* const q = v + 4 * i;
+    if constexpr (KIND == ROW_E4M3) {
+      v2s c = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(v2s{0, 0}, q[0], q[1], f, false);
+      w[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(c, q[2], q[3], f, true));
+    } else if constexpr (KIND == ROW_E5M2) {
+      v2s c = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(v2s{0, 0}, q[0], q[1], f, false);
+      w[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(c, q[2], q[3], f, true));
+    } else if (i & 1) {
+      w[i / 2] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[i / 2], q[0], q[1], f, 2);
+      w[i / 2] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[i / 2], q[2], q[3], f, 3);
+    } else {
+      w[i / 2] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[i / 2], q[0], q[1], f, 0);
+      w[i / 2] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[i / 2], q[2], q[3], f, 1);
+    }
+  }
+  const uint32_t keep = byte == 255u ? 0u : 0xFFFFFFFFu;
+  codes = v4u{w[0] & keep, w[1] & keep, w[2] & keep, w[3] & keep};
+  return word;
+}
+
+// Four fp32 of a block with the scale factor f -> four codes of 8 bits.
+template <int KIND>
+__device__ __forceinline__ uint32_t mx_codes(const float* v, float f) {
+  if constexpr (KIND == ROW_E4M3) {
+    const v2s c = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(v2s{0, 0}, v[0], v[1], f, false);
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(c, v[2], v[3], f, true));
+  } else {
+    const v2s c = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(v2s{0, 0}, v[0], v[1], f, false);
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(c, v[2], v[3], f, true));
+  }
+}
+
+// ---- back ------------------------------------------------------------------
+
+// What a scale byte stands for: NaN for 255.
+__device__ __forceinline__ float mx_scale_value(uint32_t byte) {
+  return byte == 255u ? __builtin_nanf("") : mx_factor(byte);
+}
+
+// Place of the scale byte of 32-column block b of row r.
+__device__ __forceinline__ int64_t scale_at(const SavedRows& s, int64_t rows, int32_t width, int64_t r, int b) {
+  return s.kplanes ? ((b >> 2) * rows + r) * 4 + (b & 3) : r * (width >> 5) + b;
+}
+
+// Four codes -> what they stand for under the scale f.
+template <int KIND>
+__device__ __forceinline__ void mx_four(uint32_t codes, float f, float* v) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  f2 a, b;
+  if constexpr (KIND == ROW_E4M3) {
+    a = __builtin_amdgcn_cvt_pk_f32_fp8(codes, false);
+    b = __builtin_amdgcn_cvt_pk_f32_fp8(codes, true);
+  } else {
+    a = __builtin_amdgcn_cvt_pk_f32_bf8(codes, false);
+    b = __builtin_amdgcn_cvt_pk_f32_bf8(codes, true);
+  }
+  v[0] = a.x * f;
+  v[1] = a.y * f;
+  v[2] = b.x * f;
+  v[3] = b.y * f;
+}
+
+}  // namespace
+}  // namespace moegg

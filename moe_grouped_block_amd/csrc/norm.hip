@@ -1,0 +1,413 @@
+// Root-mean-square norm with the residual's addition, and its gradient.
+//
+//   h  = x + residual, rounded once to the stream's type; the norm goes on with
+//        the rounded h, so that the gradient taken from the stored h is the one
+//        of what was computed
+//   r  = 1 / sqrt(mean(h^2) + eps),  y = (h r) w
+//
+//   g  = dy w,  xh = h r
+//   dx = r (g - xh mean(g xh)) + dh       (of x and of the residual alike)
+//   dw = sum over rows of dy xh
+//
+// Both are bound by HBM: every value is read once and stays in registers until
+// its row's sums are known.  A row belongs to one wave (up to 2048 columns) or
+// to several of a workgroup, whose sums meet in LDS.
+//
+// Squares and products are summed in 64 bits: no h in range overflows or
+// vanishes in them, and the rate of 64-bit operations is far from being needed.
+// r is kept as a power of two a and a factor b in (0.5, 2): (h a) b does not
+// leave the range of fp32 where the result does not.
+#include "mx_rows.h"
+
+namespace moegg {
+namespace {
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v4f_any __attribute__((ext_vector_type(4), aligned(4)));
+
+__device__ __forceinline__ uint32_t bf16x2(float a, float b) {
+  typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, bf2));
+}
+__device__ __forceinline__ v4u pack8(const float* f) {
+  return v4u{bf16x2(f[0], f[1]), bf16x2(f[2], f[3]), bf16x2(f[4], f[5]), bf16x2(f[6], f[7])};
+}
+__device__ __forceinline__ void unpack8(v4u u, float* f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(u[i] << 16);
+    f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+  }
+}
+
+// Eight values of a BF16 or fp32 tensor, from element i (a multiple of 8) on.
+template <bool F32>
+struct Eight {
+  v4u u[F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* base, int64_t i) {
+    const v4u* const p = reinterpret_cast<const v4u*>(static_cast<const uint8_t*>(base) + i * (F32 ? 4 : 2));
+#pragma unroll
+    for (int q = 0; q < (F32 ? 2 : 1); ++q) u[q] = p[q];
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int q = 0; q < (F32 ? 2 : 1); ++q) u[q] = v4u{};
+  }
+  __device__ __forceinline__ void get(float* f) const {
+    if constexpr (F32) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) f[q] = __uint_as_float(u[q >> 2][q & 3]);
+    } else {
+      unpack8(u[0], f);
+    }
+  }
+  __device__ __forceinline__ void set(const float* f) {
+    if constexpr (F32) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) u[q >> 2][q & 3] = __float_as_uint(f[q]);
+    } else {
+      u[0] = pack8(f);
+    }
+  }
+  __device__ __forceinline__ void store(void* base, int64_t i) const {
+    v4u* const p = reinterpret_cast<v4u*>(static_cast<uint8_t*>(base) + i * (F32 ? 4 : 2));
+#pragma unroll
+    for (int q = 0; q < (F32 ? 2 : 1); ++q) p[q] = u[q];
+  }
+};
+
+// 1 / sqrt(v) = a b for v > 0 (NaN: b is NaN; +inf: b is 0): a a power of two, b in (0.5, 2).
+__device__ __forceinline__ void inverse_root(double v, float& a, float& b) {
+  const int e = (static_cast<int>(__builtin_bit_cast(uint64_t, v) >> 52) - 1023) & ~1;      // even, so that its half is whole
+  a = ldexpf(1.0f, -e / 2);
+  b = __builtin_amdgcn_rsqf(static_cast<float>(ldexp(v, -e)));                              // of [1, 4)
+}
+
+// The sum over a row's lanes, the same in all of them: `waves` waves from the
+// team's first on.  Every thread of the workgroup calls it (`turn`: another
+// one from call to call, two sums' places take turns).
+__device__ __forceinline__ void row_sums(double& s, double& t, int waves, int wave, double (*place)[2], bool two) {
+  s = lanes_sum<64>(s);
+  if (two) t = lanes_sum<64>(t);
+  if (waves == 1) return;
+  if ((threadIdx.x & 63) == 0) {
+    place[wave][0] = s;
+    place[wave][1] = t;
+  }
+  __syncthreads();
+  const int first = wave & ~(waves - 1);
+  s = t = 0.0;
+  for (int i = 0; i < waves; ++i) {
+    s += place[first + i][0];
+    t += place[first + i][1];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// forward
+// ---------------------------------------------------------------------------
+
+// P pieces of C columns a lane: piece p of wave w of the row's `waves` starts
+// at column ((p waves + w) 64 + lane) C.
+template <bool XF32, bool SF32, int KIND, int P>
+__global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a, int waves) {
+  constexpr int C = KIND == ROW_BF16 ? 8 : 16, E = C / 8;
+  __shared__ double place[16][2];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int teams = (blockDim.x >> 6) / waves, team = wave / waves, w = wave & (waves - 1);
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * teams + team;
+  const bool live = row < a.rows;
+  const int64_t first = (live ? row : 0) * a.width;
+  int col[P];
+  bool in[P];
+  Eight<XF32> x[P][E];
+  Eight<SF32> r[P][E];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    col[p] = ((p * waves + w) * 64 + lane) * C;
+    in[p] = live && col[p] < a.width;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      x[p][e].clear();
+      r[p][e].clear();
+      if (in[p]) x[p][e].load(a.x, first + col[p] + 8 * e);
+      if (in[p] && a.residual) r[p][e].load(a.residual, first + col[p] + 8 * e);
+    }
+  }
+  float h[P][C];
+  double sum = 0.0, none = 0.0;
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      float* const f = h[p] + 8 * e;
+      x[p][e].get(f);
+      if (a.residual) {
+        float g[8];
+        r[p][e].get(g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] += f[i];
+        r[p][e].set(g);
+        r[p][e].get(f);                          // as it is kept
+        if (in[p]) r[p][e].store(a.h, first + col[p] + 8 * e);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum = fma(static_cast<double>(f[i]), static_cast<double>(f[i]), sum);
+    }
+  row_sums(sum, none, waves, wave, place, false);
+  float ra, rb;
+  inverse_root(sum * a.inverse_width + a.eps, ra, rb);
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+#pragma unroll
+    for (int i = 0; i < C; i += 4) {
+      v4f v{};
+      if (in[p]) v = *reinterpret_cast<const v4f_any*>(a.weight + col[p] + i);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) h[p][i + q] = h[p][i + q] * ra * rb * v[q];
+    }
+    const int64_t at = first + col[p];
+    if (KIND == ROW_BF16 || a.y) {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (in[p]) *reinterpret_cast<v4u*>(a.y + at + 8 * e) = pack8(h[p] + 8 * e);
+    }
+    if constexpr (KIND != ROW_BF16) {
+      v4u q;
+      const uint32_t word = mx_from_f32<KIND>(h[p], q);
+      if (!in[p]) continue;
+      if constexpr (KIND == ROW_E2M1) *reinterpret_cast<v2u*>(a.codes + at / 2) = v2u{q.x, q.y};
+      else *reinterpret_cast<v4u*>(a.codes + at) = q;
+      if ((lane & 7) == 0) {
+        const int64_t k = col[p] >> 7;
+        reinterpret_cast<uint32_t*>(a.scales)[a.kplanes ? k * a.rows + row : at >> 7] = word;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// backward
+// ---------------------------------------------------------------------------
+
+// A workgroup's teams take rows in turn and add up their part of dw in
+// registers; the teams' parts meet in LDS, the workgroups' in norm_dw_kernel,
+// in a fixed order.
+template <bool SF32, int P>
+__global__ __launch_bounds__(1024) void rms_norm_backward_kernel(NormArgs a, int waves) {
+  __shared__ double place[2][16][2];
+  __shared__ v4f part[4][P * 2][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int teams = (blockDim.x >> 6) / waves, team = wave / waves, w = wave & (waves - 1);
+  int col[P];
+  float weight[P][8], acc[P][8];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    col[p] = ((p * waves + w) * 64 + lane) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+      v4f v{};
+      if (col[p] < a.width) v = *reinterpret_cast<const v4f_any*>(a.weight + col[p] + i);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        weight[p][i + q] = v[q];
+        acc[p][i + q] = 0.0f;
+      }
+    }
+  }
+  int turn = 0;
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * teams; base < a.rows;
+       base += static_cast<int64_t>(gridDim.x) * teams, turn ^= 1) {
+    const int64_t row = base + team;
+    const bool live = row < a.rows;
+    const int64_t first = (live ? row : 0) * a.width;
+    Eight<false> dy[P];
+    Eight<SF32> h[P], dh[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      dy[p].clear();
+      h[p].clear();
+      dh[p].clear();
+      if (live && col[p] < a.width) {
+        dy[p].load(a.dy, first + col[p]);
+        h[p].load(a.stored, first + col[p]);
+        if (a.dh) dh[p].load(a.dh, first + col[p]);
+      }
+    }
+    double sq = 0.0, dot = 0.0;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      float d[8], v[8];
+      dy[p].get(d);
+      h[p].get(v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sq = fma(static_cast<double>(v[i]), static_cast<double>(v[i]), sq);
+        dot = fma(static_cast<double>(d[i] * weight[p][i]), static_cast<double>(v[i]), dot);
+      }
+    }
+    row_sums(sq, dot, waves, wave, place[turn], true);
+    float ra, rb;
+    inverse_root(sq * a.inverse_width + a.eps, ra, rb);
+    const float mean = static_cast<float>(dot * a.inverse_width * ra * rb);
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      float d[8], v[8], g[8];
+      dy[p].get(d);
+      h[p].get(v);
+      dh[p].get(g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float xh = v[i] * ra * rb;
+        acc[p][i] = fmaf(d[i], xh, acc[p][i]);
+        v[i] = fmaf((d[i] * weight[p][i] - xh * mean) * ra, rb, g[i]);
+      }
+      if (a.dx && live && col[p] < a.width) {
+        h[p].set(v);
+        h[p].store(a.dx, first + col[p]);
+      }
+    }
+  }
+  if (!a.partial) return;
+  if (teams > 1) {
+    // (waves of a workgroup with several teams: 4)
+    if (team > 0) {
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          part[wave][2 * p + q][lane] = v4f{acc[p][4 * q], acc[p][4 * q + 1], acc[p][4 * q + 2], acc[p][4 * q + 3]};
+    }
+    __syncthreads();
+    if (team > 0) return;
+    for (int t = 1; t < teams; ++t)
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const v4f v = part[t * waves + w][2 * p + q][lane];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[p][4 * q + i] += v[i];
+        }
+  }
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+    if (col[p] < a.width) {
+      v4f* const out = reinterpret_cast<v4f*>(a.partial + static_cast<int64_t>(blockIdx.x) * a.width + col[p]);
+      out[0] = v4f{acc[p][0], acc[p][1], acc[p][2], acc[p][3]};
+      out[1] = v4f{acc[p][4], acc[p][5], acc[p][6], acc[p][7]};
+    }
+}
+
+// dw of 16 columns: 16 threads a column share the workgroups' parts.
+__global__ __launch_bounds__(256) void norm_dw_kernel(const float* partial, float* dw, int width, int parts) {
+  __shared__ float red[16][17];
+  const int x = threadIdx.x & 15, q = threadIdx.x >> 4, col = blockIdx.x * 16 + x;
+  float s = 0.0f;
+  if (col < width) {
+#pragma unroll 8
+    for (int i = q; i < parts; i += 16) s += partial[static_cast<int64_t>(i) * width + col];
+  }
+  red[q][x] = s;
+  __syncthreads();
+  if (q == 0 && col < width) {
+    float v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v += red[i][x];
+    dw[col] = v;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// choices
+// ---------------------------------------------------------------------------
+
+// Pieces a lane and waves a row, both powers of two, for `pieces` pieces of a wave.
+struct Shape {
+  int p, waves;
+};
+Shape shape_of(int pieces, int most) {
+  Shape s{1, 1};
+  while (s.p < most && s.p < pieces) s.p *= 2;
+  while (s.p * s.waves < pieces) s.waves *= 2;
+  return s;
+}
+int threads_of(const Shape& s) { return s.waves > 4 ? 64 * s.waves : 256; }
+
+template <typename F>
+hipError_t by_pieces(int p, F&& f) {
+  switch (p) {
+    case 1: return f(std::integral_constant<int, 1>{});
+    case 2: return f(std::integral_constant<int, 2>{});
+    default: return f(std::integral_constant<int, 4>{});
+  }
+}
+
+template <bool XF32, bool SF32, int KIND, int P>
+hipError_t launch_norm_kernel(const NormArgs& a, const Shape& sh, hipStream_t s) {
+  const int threads = threads_of(sh), teams = threads / 64 / sh.waves;
+  const unsigned blocks = static_cast<unsigned>((a.rows + teams - 1) / teams);
+  hipLaunchKernelGGL((rms_norm_kernel<XF32, SF32, KIND, P>), dim3(blocks), dim3(threads), 0, s, a, sh.waves);
+  return hipGetLastError();
+}
+template <bool XF32, bool SF32, int KIND>
+hipError_t launch_norm_kind(const NormArgs& a, hipStream_t s) {
+  if constexpr (KIND == ROW_BF16) {
+    const Shape sh = shape_of((a.width + 511) / 512, 4);
+    return by_pieces(sh.p, [&](auto p) { return launch_norm_kernel<XF32, SF32, KIND, decltype(p)::value>(a, sh, s); });
+  } else {
+    const Shape sh = shape_of((a.width + 1023) / 1024, 2);
+    return sh.p == 1 ? launch_norm_kernel<XF32, SF32, KIND, 1>(a, sh, s) : launch_norm_kernel<XF32, SF32, KIND, 2>(a, sh, s);
+  }
+}
+template <bool XF32, bool SF32>
+hipError_t launch_norm_types(const NormArgs& a, hipStream_t s) {
+  switch (a.kind) {
+    case ROW_E4M3: return launch_norm_kind<XF32, SF32, ROW_E4M3>(a, s);
+    case ROW_E5M2: return launch_norm_kind<XF32, SF32, ROW_E5M2>(a, s);
+    case ROW_E2M1: return launch_norm_kind<XF32, SF32, ROW_E2M1>(a, s);
+    default: return launch_norm_kind<XF32, SF32, ROW_BF16>(a, s);
+  }
+}
+
+Shape backward_shape(int width) { return shape_of((width + 511) / 512, 4); }
+
+// Workgroups of the backward: two of four waves to a compute unit.
+int64_t backward_blocks(int64_t rows, int width) {
+  const Shape sh = backward_shape(width);
+  const int teams = threads_of(sh) / 64 / sh.waves;
+  const int64_t all = (rows + teams - 1) / teams;
+  return all < 512 ? all : 512;
+}
+
+}  // namespace
+
+hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s) {
+  if (a.rows == 0) return hipSuccess;
+  if (a.x_f32) return launch_norm_types<true, true>(a, s);
+  return a.stream_f32 ? launch_norm_types<false, true>(a, s) : launch_norm_types<false, false>(a, s);
+}
+
+int64_t rms_norm_backward_workspace(int64_t rows, int32_t width) { return backward_blocks(rows, width) * width * 4; }
+
+hipError_t launch_rms_norm_backward(const NormArgs& a, hipStream_t s) {
+  const int64_t blocks = backward_blocks(a.rows, a.width);
+  if (blocks > 0) {
+    const Shape sh = backward_shape(a.width);
+    const dim3 grid(static_cast<unsigned>(blocks)), block(threads_of(sh));
+    const hipError_t e = by_pieces(sh.p, [&](auto p) {
+      constexpr int P = decltype(p)::value;
+      if (a.stream_f32) hipLaunchKernelGGL((rms_norm_backward_kernel<true, P>), grid, block, 0, s, a, sh.waves);
+      else hipLaunchKernelGGL((rms_norm_backward_kernel<false, P>), grid, block, 0, s, a, sh.waves);
+      return hipGetLastError();
+    });
+    if (e != hipSuccess) return e;
+  }
+  if (!a.dw) return hipSuccess;
+  hipLaunchKernelGGL(norm_dw_kernel, dim3((a.width + 15) / 16), dim3(256), 0, s, a.partial, a.dw, a.width,
+                     static_cast<int>(blocks));
+  return hipGetLastError();
+}
+
+}  // namespace moegg

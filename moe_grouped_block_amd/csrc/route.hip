@@ -5,6 +5,10 @@
 //   key_e     l_e without a bias (both scores grow with the logit), p_e + bias_e with one
 //   ids       the top_k experts of the largest keys, ties to the lowest index
 //   weights   scale p_j, or scale p_j / (sum of the chosen p) with `renormalise`
+//   groups    (where asked for) only experts of the top_groups groups with the
+//             largest scores can be chosen, ties to the lowest group; a group's
+//             score is the largest key of its experts, or the sum of its two
+//             largest p_e + bias_e
 //
 // An expert with a logit of -inf or NaN is never chosen; a token with fewer
 // than top_k experts to choose from ends in ids of -1 with weight 0.  +inf
@@ -14,10 +18,7 @@
 // each, in registers: one pass over the logits.  Four tokens of 16 lanes
 // share a wave, so the exchanges of one of the k rounds (best key over the
 // token's lanes) are four DPP steps for four tokens.
-#include <hip/hip_runtime.h>
-
-#include <type_traits>
-
+#include "lanes.h"
 #include "layer_internal.h"
 
 namespace moegg {
@@ -25,60 +26,6 @@ namespace {
 
 constexpr float kNegInf = -__builtin_inff();
 constexpr float kMaxF = 3.4028234663852886e38f;
-
-typedef uint32_t v2u __attribute__((ext_vector_type(2)));
-
-// ---- exchanges over a token's lanes: every lane ends with the result --------
-
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp_u(uint32_t x) {
-  return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), CTRL, 0xF, 0xF, false));
-}
-
-// STEP 0..3 pair lanes inside a 16-lane row (1, 2 apart, mirrored halves,
-// mirrored row), 4 and 5 exchange rows and half waves.
-template <int STEP>
-__device__ __forceinline__ uint32_t partner(uint32_t x) {
-  if constexpr (STEP == 0) return dpp_u<0xB1>(x);
-  else if constexpr (STEP == 1) return dpp_u<0x4E>(x);
-  else if constexpr (STEP == 2) return dpp_u<0x141>(x);
-  else if constexpr (STEP == 3) return dpp_u<0x140>(x);
-  else if constexpr (STEP == 4) {
-    const v2u s = __builtin_amdgcn_permlane16_swap(x, x, false, false);
-    return (threadIdx.x & 16) ? s.x : s.y;
-  } else {
-    const v2u s = __builtin_amdgcn_permlane32_swap(x, x, false, false);
-    return (threadIdx.x & 32) ? s.x : s.y;
-  }
-}
-template <int STEP>
-__device__ __forceinline__ float partner(float x) {
-  return __uint_as_float(partner<STEP>(__float_as_uint(x)));
-}
-template <int STEP>
-__device__ __forceinline__ double partner(double x) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, x);
-  const uint64_t lo = partner<STEP>(static_cast<uint32_t>(u)), hi = partner<STEP>(static_cast<uint32_t>(u >> 32));
-  return __builtin_bit_cast(double, lo | hi << 32);
-}
-
-template <int LPT, int STEP = 0, typename F>
-__device__ __forceinline__ void steps(F&& f) {
-  if constexpr ((1 << STEP) < LPT) {
-    f(std::integral_constant<int, STEP>{});
-    steps<LPT, STEP + 1>(f);
-  }
-}
-template <int LPT, typename T>
-__device__ __forceinline__ T lanes_sum(T v) {
-  steps<LPT>([&](auto c) { v += partner<decltype(c)::value>(v); });
-  return v;
-}
-template <int LPT>
-__device__ __forceinline__ float lanes_max(float v) {
-  steps<LPT>([&](auto c) { v = fmaxf(v, partner<decltype(c)::value>(v)); });
-  return v;
-}
 
 // ---- a token's logits ------------------------------------------------------
 
@@ -249,10 +196,134 @@ __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp
 constexpr int kSpare = 2;
 constexpr int kSlots = kMaxTopK + kSpare;
 
-template <bool BF16, int LPT, int EPL, int V, bool BIAS>
+// What a key p + bias is off by, formed in fp32: a rounding of its sum and p's
+// error: p <= 1, its exponential's argument (p |x| < 0.4), the unit's last
+// places and a sum of up to 16 + 6 terms, below 50 2^-24.
+constexpr float kKeyP = 50.0f * 5.9604645e-8f, kKeySum = 2.4e-7f;
+
+// LDS of the choice of groups: a token's scores, its groups' scores (twice:
+// by group and by rank) and what they may be off by.
+template <int LPT, int EPL>
+struct GroupScratch {
+  float score[256 / LPT][LPT * (EPL + 1)];
+  float group[256 / LPT][kMaxGroups];
+  float ranked[256 / LPT][kMaxGroups][2];
+  double exact[256 / LPT][kMaxGroups];
+};
+
+// Bits of the lane's EPL experts that are in no chosen group.  `score`: what
+// the groups' scores are made of (-inf: not there); `sums`: the two largest
+// added, else the largest.  Lane g scans group g's experts through LDS (rows of
+// a lane's EPL scores and a word more, so that neither side of the exchange
+// meets a bank twice), then counts the groups before its own.  Scores are
+// formed in fp32; where the last group in and the first one out are nearer than
+// the error of both, the wave's tokens form them in 64 bits.
+template <typename R, int LPT, int EPL>
+__device__ __forceinline__ uint32_t closed_groups(const RouteArgs& a, GroupScratch<LPT, EPL>& lds, const float* x, const float* score,
+                                                  bool sums, bool logits, float top, int64_t row, int lane, int slot) {
+  constexpr int N = kMaxGroups / LPT;            // groups of a lane
+  constexpr double kNone = -__builtin_inf();
+  const int groups = a.groups, size = a.experts / groups;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) lds.score[slot][lane * (EPL + 1) + j] = score[j];
+  wave_sync();
+  auto rank_of = [&](const auto* all, auto mine, int g) __attribute__((always_inline)) {
+    int rank = 0;
+    for (int o = 0; o < groups; ++o) rank += all[o] > mine || (all[o] == mine && o < g);
+    return rank;
+  };
+  bool open[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int g = lane + i * LPT;
+    if (g >= groups) continue;
+    float b0 = kNegInf, b1 = kNegInf;
+    for (int e = g * size; e < (g + 1) * size; ++e) {
+      const float v = lds.score[slot][e + e / EPL];
+      b1 = fmaxf(b1, fminf(b0, v));
+      b0 = fmaxf(b0, v);
+    }
+    const bool two = sums && b1 > kNegInf;
+    lds.group[slot][g] = two ? b0 + b1 : b0;
+    lds.ranked[slot][g][1] = logits ? 0.0f : two ? 2.0f * kKeyP + kKeySum * (fabsf(b0) + fabsf(b1)) : kKeyP + kKeySum * fabsf(b0);
+  }
+  wave_sync();
+  float off[N];
+  int rank[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int g = lane + i * LPT;
+    rank[i] = kMaxGroups;
+    if (g < groups) {
+      rank[i] = rank_of(lds.group[slot], lds.group[slot][g], g);
+      off[i] = lds.ranked[slot][g][1];
+    }
+  }
+  wave_sync();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int g = lane + i * LPT;
+    open[i] = rank[i] < a.top_groups;
+    if (g < groups) {
+      lds.ranked[slot][rank[i]][0] = lds.group[slot][g];
+      lds.ranked[slot][rank[i]][1] = off[i];
+    }
+  }
+  wave_sync();
+  bool doubt = false;
+  if (!logits && a.top_groups < groups) {
+    const float in = lds.ranked[slot][a.top_groups - 1][0], out = lds.ranked[slot][a.top_groups][0];
+    doubt = out > kNegInf && !(in - out > lds.ranked[slot][a.top_groups - 1][1] + lds.ranked[slot][a.top_groups][1]);
+  }
+  if (__any(doubt)) {
+    double total = 1.0;
+    if (a.softmax) {
+      total = 0.0;
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) total += x[j] == x[j] ? exp(static_cast<double>(x[j]) - top) : 0.0;
+      total = lanes_sum<LPT>(total);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int g = lane + i * LPT;
+      if (g >= groups) continue;
+      double b0 = kNone, b1 = kNone;
+      for (int e = g * size; e < (g + 1) * size; ++e) {
+        const double l = R::one(a.logits, row, a.experts, e);
+        const double q = (a.softmax ? exp(l - top) / total : 1.0 / (1.0 + exp(-l))) + (a.bias ? a.bias[e] : 0.0f);
+        const double v = l > kNone && q > kNone ? q : kNone;           // NaN: false
+        b1 = fmax(b1, fmin(b0, v));
+        b0 = fmax(b0, v);
+      }
+      lds.exact[slot][g] = sums && b1 > kNone ? b0 + b1 : b0;
+    }
+    wave_sync();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int g = lane + i * LPT;
+      open[i] = g < groups && rank_of(lds.exact[slot], lds.exact[slot][g], g) < a.top_groups;
+    }
+  }
+  uint64_t mask = 0;                             // the token's open groups
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint64_t all = __ballot(open[i]);
+    mask |= (LPT == 64 ? all : (all >> (threadIdx.x & 63 & ~(LPT - 1))) & ((1ull << (LPT & 63)) - 1)) << (i * LPT);
+  }
+  uint32_t closed = 0;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    const uint32_t g = (static_cast<uint32_t>(lane * EPL + j) * a.group_magic) >> 22;
+    closed |= (g < kMaxGroups && (mask >> g & 1) ? 0u : 1u) << j;
+  }
+  return closed;
+}
+
+template <bool BF16, int LPT, int EPL, int V, bool BIAS, bool GROUPS>
 __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
   using R = Row<BF16, LPT, EPL, V>;
   constexpr int TPB = 256 / LPT, JPL = kJpl<LPT>;
+  uint32_t closed = 0;
   __shared__ float s_logit[TPB][kSlots];
   __shared__ int s_id[TPB][kSlots];
   __shared__ float s_key[BIAS ? TPB : 1][kSlots];
@@ -283,6 +354,26 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
   if constexpr (!BIAS) {
 #pragma unroll
     for (int j = 0; j < EPL; ++j) key[j] = x[j] > kNegInf ? x[j] : kNegInf;
+    if constexpr (GROUPS) {
+      __shared__ GroupScratch<LPT, EPL> scratch;
+      float score[EPL];
+      float valid = total;
+      if (a.softmax && __any(!(total == total))) {     // (a NaN leaves the choice among the others)
+        valid = 0.0f;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) valid += x[j] == x[j] ? fast_exp(x[j] - top) : 0.0f;
+        valid = lanes_sum<LPT>(valid);
+      }
+      const float rt = 1.0f / valid;
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) {
+        const float p = a.softmax ? fast_exp(key[j] - top) * rt : __builtin_amdgcn_rcpf(1.0f + fast_exp(-key[j]));
+        score[j] = a.group_sums && key[j] > kNegInf ? p : key[j];
+      }
+      closed = closed_groups<R>(a, scratch, x, score, a.group_sums, !a.group_sums, top, row, lane, slot);
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) key[j] = closed >> j & 1 ? kNegInf : key[j];
+    }
     choose<LPT, EPL, float>(key, k, lane, s_id[slot], s_logit[slot]);   // (the keys are the logits)
     wave_sync();
   } else {
@@ -309,6 +400,12 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
         key[j] = x[j] > kNegInf && q > kNegInf ? q : kNegInf;    // NaN: false
       }
     }
+    if constexpr (GROUPS) {
+      __shared__ GroupScratch<LPT, EPL> scratch;
+      closed = closed_groups<R>(a, scratch, x, key, a.group_sums, false, top, row, lane, slot);
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) key[j] = closed >> j & 1 ? kNegInf : key[j];
+    }
     const int cand = min(k + kSpare, a.experts);
     choose<LPT, EPL, float>(key, cand, lane, s_id[slot], s_key[slot]);
     float rest = key[0];
@@ -324,11 +421,8 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
       wave_sync();
     };
     fetch_logits(cand);
-    // Choice j against the next: 0 clear, 1 the same numbers, 2 in doubt.  A key
-    // is off by a rounding of its sum and by p's error: p <= 1, its exponential's
-    // argument (p |x| < 0.4), the unit's last places and a sum of up to 16 + 6
-    // terms, below 50 2^-24.
-    constexpr float kP = 2.0f * 50.0f * 5.9604645e-8f, kSum = 2.4e-7f;
+    // Choice j against the next: 0 clear, 1 the same numbers, 2 in doubt.
+    constexpr float kP = 2.0f * kKeyP, kSum = kKeySum;
     bool maybe = false;
     for (int j = lane; j < cand; j += LPT) {
       const float k0 = s_key[slot][j], k1 = j + 1 < cand ? s_key[slot][j + 1] : rest;
@@ -367,7 +461,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
           for (int j = 0; j < EPL; ++j) {
             const int e = R::expert(lane, j / V, j % V);
             const double q = exact[j] * dt + a.bias[e < a.experts ? e : 0];
-            exact[j] = x[j] > kNegInf && q > -__builtin_inf() ? q : -__builtin_inf();
+            exact[j] = x[j] > kNegInf && !(closed >> j & 1) && q > -__builtin_inf() ? q : -__builtin_inf();
           }
           choose<LPT, EPL, double>(exact, k, lane, s_id[slot], nullptr);
           wave_sync();
@@ -524,8 +618,10 @@ hipError_t launch_shape(const RouteArgs& a, bool backward, hipStream_t s) {
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(blocks)), block(256);
   if (backward) hipLaunchKernelGGL((route_backward_kernel<BF16, LPT, EPL, V>), grid, block, 0, s, a);
-  else if (a.bias) hipLaunchKernelGGL((route_kernel<BF16, LPT, EPL, V, true>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((route_kernel<BF16, LPT, EPL, V, false>), grid, block, 0, s, a);
+  else if (a.bias && a.groups > 1) hipLaunchKernelGGL((route_kernel<BF16, LPT, EPL, V, true, true>), grid, block, 0, s, a);
+  else if (a.bias) hipLaunchKernelGGL((route_kernel<BF16, LPT, EPL, V, true, false>), grid, block, 0, s, a);
+  else if (a.groups > 1) hipLaunchKernelGGL((route_kernel<BF16, LPT, EPL, V, false, true>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((route_kernel<BF16, LPT, EPL, V, false, false>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 

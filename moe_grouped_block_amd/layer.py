@@ -1,5 +1,5 @@
-"""Layer operators of libmoegg on torch tensors: route, sort / dispatch /
-combine, linear, each with its gradient.
+"""Layer operators of libmoegg on torch tensors: rms_norm, route, sort /
+dispatch / combine, linear, each with its gradient, and rows kept in 8 bits.
 
 Like the rest of the binding this module marshals arguments and never
 computes: it checks types, shapes, contiguity and devices, allocates the
@@ -31,7 +31,8 @@ import torch
 import moe_grouped_block_amd as mg
 
 __all__ = ["route", "route_backward", "SortPlan", "sort_tokens", "sort_rows", "dispatch", "dispatch_backward",
-           "combine", "combine_backward", "unsort", "linear", "linear_backward"]
+           "combine", "combine_backward", "unsort", "linear", "linear_backward", "rms_norm", "rms_norm_backward",
+           "quantise", "dequantise"]
 
 _NAMES = {"bfloat16": "bf16", "float32": "f32"}
 
@@ -159,16 +160,27 @@ def _route_problem(logits, top_k, score, renormalise, scale):
 
 
 def route(logits, top_k: int, *, score: str = "softmax", bias=None, renormalise: bool = True, scale: float = 1.0,
-          stream=None):
-    """(ids int32 (T, top_k), weights fp32 (T, top_k)) of the router logits (T, E), fp32 or bf16."""
+          num_groups: int = 1, top_groups: int = 1, group_best: int = 1, stream=None):
+    """(ids int32 (T, top_k), weights fp32 (T, top_k)) of the router logits (T, E), fp32 or bf16.  With
+    ``num_groups`` the experts come in that many groups of neighbours and only those of the ``top_groups``
+    groups with the largest scores can be chosen; a group's score is the sum of its ``group_best`` (1 or 2)
+    largest scores with bias.  The gradient is route_backward() either way."""
     dev = _lead(logits, "logits", (torch.float32, torch.bfloat16), 2)
     p = _route_problem(logits, _count(top_k, "top_k"), score, renormalise, scale)
     b = None if bias is None else _want(bias, "bias", torch.float32, (p.num_experts,), dev)
+    g = None
+    if num_groups != 1 or top_groups != 1 or group_best != 1:
+        g = mg.moegg_route_groups(_count(num_groups, "num_groups"), _count(top_groups, "top_groups"),
+                                  _count(group_best, "group_best"))
     s, guard = _on(dev, stream)
     try:
         ids = logits.new_empty((p.num_tokens, p.top_k), dtype=torch.int32)
         weights = logits.new_empty((p.num_tokens, p.top_k), dtype=torch.float32)
-        _done(mg._load().moegg_route(p, logits.data_ptr(), b, ids.data_ptr(), weights.data_ptr(), s))
+        if g is None:
+            st = mg._load().moegg_route(p, logits.data_ptr(), b, ids.data_ptr(), weights.data_ptr(), s)
+        else:
+            st = mg._load().moegg_route_grouped(p, g, logits.data_ptr(), b, ids.data_ptr(), weights.data_ptr(), s)
+        _done(st)
     finally:
         if guard is not None:
             guard.close()
@@ -396,17 +408,175 @@ def unsort(values, plan: SortPlan, *, stream=None):
     return out
 
 
+# ---- norm ------------------------------------------------------------------------
+
+_STREAMS = (torch.bfloat16, torch.float32)
+_TYPE_CODES = {torch.bfloat16: 3, torch.float32: 5}
+
+
+def _mx_kind(dtype, what: str):
+    """Name and code of an MX type."""
+    dtype = _dtype_name(dtype)
+    if dtype not in ("e4m3", "e5m2", "e2m1x2"):
+        raise ValueError(f"{what}={dtype!r}: one of e4m3, e5m2, e2m1x2 expected")
+    return dtype, mg.DTYPES[dtype]
+
+
+def rms_norm(x, weight, *, residual=None, h=None, eps: float = 1e-6, dtype="bf16", copy=None,
+             sf_layout: str = "row_major", stream=None):
+    """y = h / sqrt(mean(h^2) + eps) * weight over the rows of h = x + residual
+    (T, H), weight (H) fp32.  ``dtype`` of y: bf16, or an MX type as (codes,
+    scales) that moegg_run takes; ``copy``: with a bf16 y, also the same in an
+    MX type (what linear_backward() reads as x, or moegg_run as A).
+
+    x is bf16 or fp32, the residual bf16 or fp32 (fp32 where x is); with one,
+    the sum is returned last, in the residual's type: in ``h``, which may be
+    the residual itself, or a new tensor.  Returns y, or a tuple of y, the
+    copy and h as far as they were asked for."""
+    dev = _lead(x, "x", _STREAMS, 2)
+    rows, width = x.shape
+    _fits(width)
+    wp = _want(weight, "weight", torch.float32, (width,), dev)
+    kind = x.dtype
+    rp = hp = None
+    if residual is not None:
+        if _lead(residual, "residual", _STREAMS, 2) != dev:
+            _want(residual, "residual", residual.dtype, (rows, width), dev)
+        kind = residual.dtype
+        rp = _want(residual, "residual", kind, (rows, width), dev)
+    elif h is not None:
+        raise ValueError("h: the sum with a residual, and none was given")
+    name, mx, layout = _row_kind(dtype, sf_layout)
+    bf16 = name == "bf16"
+    if bf16 and copy is not None:
+        name, mx = _mx_kind(copy, "copy")
+    elif copy is not None:
+        raise ValueError("copy: for a bf16 y")
+    elif bf16:
+        name, mx = None, 0
+    p = mg.moegg_norm_problem(rows, width, _TYPE_CODES[x.dtype], _TYPE_CODES[kind], mx, layout, eps)
+    s, guard = _on(dev, stream)
+    try:
+        out = []
+        y = codes = sf = None
+        if bf16:
+            y = x.new_empty((rows, width), dtype=torch.bfloat16)
+            out.append(y)
+        if name is not None:
+            codes, cp, sf, sp = _row_outputs(None, x, rows, width, name, sf_layout, dev)
+            out.append((codes, sf))
+        else:
+            cp = sp = None
+        if residual is not None:
+            h = residual.new_empty((rows, width)) if h is None else h
+            hp = _want(h, "h", kind, (rows, width), dev)
+            out.append(h)
+        a = mg.moegg_norm_args(x.data_ptr(), rp, wp, hp, None if y is None else y.data_ptr(), cp, sp)
+        _done(mg._load().moegg_rms_norm(p, a, s))
+    finally:
+        if guard is not None:
+            guard.close()
+    return out[0] if len(out) == 1 else tuple(out)
+
+
+def rms_norm_backward(dy, h, weight, *, dh=None, eps: float = 1e-6, need=("dx", "dw"), stream=None):
+    """(dx, dw) of rms_norm(), None for those not in ``need``: dy (T, H) bf16
+    (an MX y's gradient is y's), h what rms_norm() returned (x where there was
+    no residual), dh the gradient that reaches h from elsewhere (the residual
+    stream), in h's type.  dx, in h's type and with dh included, is the gradient
+    of x and of the residual alike."""
+    need = set(need)
+    if not need or not need <= {"dx", "dw"}:
+        raise ValueError(f"need={sorted(need)}: some of dx, dw expected")
+    dev = _lead(h, "h", _STREAMS, 2)
+    rows, width = h.shape
+    _fits(width)
+    dp = _want(dy, "dy", torch.bfloat16, (rows, width), dev)
+    wp = _want(weight, "weight", torch.float32, (width,), dev)
+    gp = None if dh is None else _want(dh, "dh", h.dtype, (rows, width), dev)
+    code = _TYPE_CODES[h.dtype]
+    p = mg.moegg_norm_problem(rows, width, code, code, 0, 0, eps)
+    lib = mg._load()
+    size = lib.moegg_rms_norm_backward_workspace(p) if "dw" in need else 0     # -1: an invalid problem, which the call refuses
+    s, guard = _on(dev, stream)
+    try:
+        dx = torch.empty_like(h) if "dx" in need else None
+        dw = weight.new_empty((width,)) if "dw" in need else None
+        ws = h.new_empty(size, dtype=torch.uint8) if size > 0 else None
+        a = mg.moegg_norm_args(None, None, wp, h.data_ptr(), None, None, None, dp, gp, None if dx is None else dx.data_ptr(),
+                               None if dw is None else dw.data_ptr(), None if ws is None else ws.data_ptr(), size)
+        _done(lib.moegg_rms_norm_backward(p, a, s))
+    finally:
+        if guard is not None:
+            guard.close()
+    return dx, dw
+
+
+# ---- rows kept in 8 bits -------------------------------------------------------------
+
+_KEPT = {"e4m3": 1, "e5m2": 4}
+
+
+def _pair(t, name: str, rows: int, width: int, sf_layout: str, dev: int):
+    """Addresses of the codes (rows, width) and scales of rows kept in 8 bits."""
+    if not isinstance(t, (tuple, list)) or len(t) != 2:
+        raise TypeError(f"{name}: a pair (codes, scales) expected")
+    shape = (width // 128, rows, 4) if sf_layout == "kplanes" else (rows, width // 32)
+    return (_want(t[0], f"{name}[0]", torch.uint8, (rows, width), dev),
+            _want(t[1], f"{name}[1]", torch.uint8, shape, dev))
+
+
+def quantise(x, *, dtype="e4m3", sf_layout: str = "row_major", out=None, stream=None):
+    """(codes, scales) of x (T, H), bf16 or fp32, in 8 bits (e4m3 or e5m2): the
+    rows that dispatch() and rms_norm() write and linear_backward() reads.
+    ``out``: a pair to write to."""
+    dev = _lead(x, "x", _STREAMS, 2)
+    rows, width = x.shape
+    _fits(width)
+    dtype = _dtype_name(dtype)
+    kind, layout = _code(_KEPT, dtype, "dtype"), _code(mg.SF_LAYOUTS, sf_layout, "sf_layout")
+    s, guard = _on(dev, stream)
+    try:
+        codes, cp, sf, sp = _row_outputs(out, x, rows, width, dtype, sf_layout, dev)
+        _done(mg._load().moegg_quantise(x.data_ptr(), _TYPE_CODES[x.dtype], rows, width, kind, layout, cp, sp, s))
+    finally:
+        if guard is not None:
+            guard.close()
+    return codes, sf
+
+
+def dequantise(rows, *, dtype="e4m3", sf_layout: str = "row_major", to="bf16", stream=None):
+    """x (T, H) in bf16 or fp32 (``to``) of its (codes, scales)."""
+    if not isinstance(rows, (tuple, list)) or len(rows) != 2:
+        raise TypeError("rows: a pair (codes, scales) expected")
+    dev = _lead(rows[0], "rows[0]", (torch.uint8,), 2)
+    n, width = rows[0].shape
+    _fits(width)
+    kind, layout = _code(_KEPT, _dtype_name(dtype), "dtype"), _code(mg.SF_LAYOUTS, sf_layout, "sf_layout")
+    to = _dtype_name(to)
+    code = _code(_LINEAR_DTYPES, to, "to")
+    cp, sp = _pair(rows, "rows", n, width, sf_layout, dev)
+    s, guard = _on(dev, stream)
+    try:
+        x = rows[0].new_empty((n, width), dtype=torch.float32 if to == "f32" else torch.bfloat16)
+        _done(mg._load().moegg_dequantise(cp, sp, n, width, kind, layout, x.data_ptr(), code, s))
+    finally:
+        if guard is not None:
+            guard.close()
+    return x
+
+
 # ---- linear ----------------------------------------------------------------------
 
 _LINEAR_ACTS = {"none": 0, "swiglu": 1, "srelu": 2, "gelu": 7}
 _LINEAR_DTYPES = {"bf16": 3, "f32": 5}
 
 
-def _linear_problem(x, w, act, dtype, offsets):
+def _linear_problem(x, w, act, dtype, offsets, x_dtype=torch.bfloat16):
     """(device, problem struct, leading shape of w, bias and their gradients, addresses of x, w and offsets)."""
     act_code, dtype_code = _code(_LINEAR_ACTS, act, "act"), _code(_LINEAR_DTYPES, dtype, "dtype")
     bf16 = torch.bfloat16
-    dev = _lead(x, "x", (bf16,), 2)
+    dev = _lead(x, "x", (x_dtype,), 2)
     m, k = x.shape
     if offsets is None:
         _lead(w, "w", (bf16,), 2)
@@ -421,12 +591,13 @@ def _linear_problem(x, w, act, dtype, offsets):
     return dev, mg.moegg_linear_problem(m, n, k, groups, act_code, dtype_code), lead, x.data_ptr(), wp, op
 
 
-def linear(x, w, *, bias=None, act: str = "none", residual=None, offsets=None, save_c: bool = False, dtype="bf16",
+def linear(x, w, *, bias=None, act: str = "none", residual=None, offsets=None, save_c=False, dtype="bf16",
            out=None, stream=None):
     """y = act(x w^T + bias) + residual: x (M, K) bf16, w (N, K) bf16, or with
     ``offsets`` (L, int32 ends of the groups' rows) w (L, N, K) and bias
     (L, N).  ``dtype`` of y: bf16 or f32.  With ``save_c`` returns (y, c), c
-    the bf16 pre-activation that linear_backward() takes.  Rows behind the
+    the pre-activation that linear_backward() takes: in bf16 (True), or kept in
+    8 bits ("e4m3" or "e5m2") as (codes, scales (M, N / 32)).  Rows behind the
     last group are not written: `out` keeps them, new tensors (c too) hold
     anything there."""
     dtype = _dtype_name(dtype)
@@ -437,51 +608,81 @@ def linear(x, w, *, bias=None, act: str = "none", residual=None, offsets=None, s
     bp = None if bias is None else _want(bias, "bias", torch.float32, (*lead, n), dev)
     rp = None if residual is None else _want(residual, "residual", torch.bfloat16, shape, dev)
     lib = mg._load()
-    need = lib.moegg_linear_workspace(p)          # -1: an invalid problem, which the call refuses
+    keep = None
+    if save_c is not False and save_c is not True:
+        keep = mg.moegg_linear_saved(3, 0, _code(_KEPT, _dtype_name(save_c), "save_c"))
+    # (-1: an invalid problem, which the call refuses)
+    need = lib.moegg_linear_workspace(p) if keep is None else lib.moegg_linear_saving_workspace(p, keep)
     s, guard = _on(dev, stream)
     try:
         y = x.new_empty(shape, dtype=kind) if out is None else out
         yp = _want(y, "out", kind, shape, dev)
-        c = x.new_empty((m, n)) if save_c else None
+        c = sf = None
+        if keep is not None:
+            c, sf = x.new_empty((m, n), dtype=torch.uint8), x.new_empty((m, n // 32), dtype=torch.uint8)
+            keep.c_sf = sf.data_ptr()
+        elif save_c:
+            c = x.new_empty((m, n))
         ws = x.new_empty(need, dtype=torch.uint8) if need > 0 else None
         a = mg.moegg_linear_args(xp, wp, bp, rp, op, yp, None if c is None else c.data_ptr(), None, None, None, None,
                                  None if ws is None else ws.data_ptr(), need)
-        _done(lib.moegg_linear(p, a, s))
+        _done(lib.moegg_linear(p, a, s) if keep is None else lib.moegg_linear_saving(p, a, keep, s))
     finally:
         if guard is not None:
             guard.close()
-    return (y, c) if save_c else y
+    return (y, (c, sf)) if keep is not None else (y, c) if save_c else y
 
 
 def linear_backward(dy, x, w, *, c=None, act: str = "none", offsets=None, need=("dx", "dw", "db"), dw_dtype="bf16",
-                    stream=None):
+                    x_dtype="bf16", c_dtype="bf16", sf_layout: str = "row_major", stream=None):
     """(dx, dw, db) of linear(), None for those not in ``need``; c is what
     linear(save_c=True) returned (not needed for act "none"), dy bf16 whatever
-    linear()'s ``dtype`` was.  Rows of dx behind the last group hold anything."""
+    linear()'s ``dtype`` was.  Rows of dx behind the last group hold anything.
+
+    x and c may be kept in 8 bits, each as a pair (codes, scales) with its
+    ``x_dtype`` / ``c_dtype`` ("e4m3" or "e5m2"): c what linear(save_c=...)
+    returned, x what rms_norm(), dispatch() or quantise() wrote, with its scales
+    in ``sf_layout``."""
     dw_dtype = _dtype_name(dw_dtype)
     need = set(need)
     if not need or not need <= {"dx", "dw", "db"}:
         raise ValueError(f"need={sorted(need)}: some of dx, dw, db expected")
-    dev, p, lead, xp, wp, op = _linear_problem(x, w, act, dw_dtype, offsets)
+    x_dtype, c_dtype = _dtype_name(x_dtype), _dtype_name(c_dtype)
+    x8, c8 = x_dtype != "bf16", c is not None and c_dtype != "bf16"
+    keep = None
+    if x8 or c8:
+        codes = {"bf16": 3, **_KEPT}
+        keep = mg.moegg_linear_saved(_code(codes, x_dtype, "x_dtype"), _code(mg.SF_LAYOUTS, sf_layout, "sf_layout"),
+                                     _code(codes, c_dtype if c8 else "bf16", "c_dtype"))
+    if x8 and (not isinstance(x, (tuple, list)) or len(x) != 2):
+        raise TypeError("x: a pair (codes, scales) expected")
+    dev, p, lead, xp, wp, op = _linear_problem(x[0] if x8 else x, w, act, dw_dtype, offsets,
+                                               torch.uint8 if x8 else torch.bfloat16)
     m, n, k = p.m, p.n, p.k
+    if x8:
+        _, keep.x_sf = _pair(x, "x", m, k, sf_layout, dev)
     dp = _want(dy, "dy", torch.bfloat16, (m, n // 2 if act == "swiglu" else n), dev)
     cp = None
-    if c is not None:
+    if c is not None and c8:
+        cp, keep.c_sf = _pair(c, "c", m, n, "row_major", dev)
+    elif c is not None:
         cp = _want(c, "c", torch.bfloat16, (m, n), dev)
     elif act != "none":
         raise ValueError(f"act={act!r} needs c")
     lib = mg._load()
-    size = lib.moegg_linear_backward_workspace(p, ("dx" in need) | ("dw" in need) << 1 | ("db" in need) << 2)
+    want = ("dx" in need) | ("dw" in need) << 1 | ("db" in need) << 2
+    size = lib.moegg_linear_backward_workspace(p, want) if keep is None \
+        else lib.moegg_linear_saved_backward_workspace(p, keep, want)
     s, guard = _on(dev, stream)
     try:
-        ws = x.new_empty(size, dtype=torch.uint8) if size > 0 else None
-        dx = x.new_empty((m, k)) if "dx" in need else None
-        dw = x.new_empty((*lead, n, k), dtype=torch.float32 if dw_dtype == "f32" else torch.bfloat16) \
+        ws = w.new_empty(size, dtype=torch.uint8) if size > 0 else None
+        dx = w.new_empty((m, k)) if "dx" in need else None
+        dw = w.new_empty((*lead, n, k), dtype=torch.float32 if dw_dtype == "f32" else torch.bfloat16) \
             if "dw" in need else None
-        db = x.new_empty((*lead, n), dtype=torch.float32) if "db" in need else None
+        db = w.new_empty((*lead, n), dtype=torch.float32) if "db" in need else None
         dxp, dwp, dbp, wsp = (None if t is None else t.data_ptr() for t in (dx, dw, db, ws))
         a = mg.moegg_linear_args(xp, wp, None, None, op, None, cp, dp, dxp, dwp, dbp, wsp, size)
-        _done(lib.moegg_linear_backward(p, a, s))
+        _done(lib.moegg_linear_backward(p, a, s) if keep is None else lib.moegg_linear_saved_backward(p, a, keep, s))
     finally:
         if guard is not None:
             guard.close()
