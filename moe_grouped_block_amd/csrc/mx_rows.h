@@ -130,6 +130,37 @@ __device__ __forceinline__ uint32_t mx_codes(const float* v, float f) {
   }
 }
 
+// U fp32 a lane (4 or 8), a block of 32 in 32 / U neighbouring lanes: the codes
+// (4 of 8 bits or 8 of 4 a word; 4 of 4 bits in the low half) and the scale word
+// of the 128 columns in 128 / U lanes (all of them alike).
+template <int KIND, int U>
+__device__ __forceinline__ void mx_unit(const float* v, uint32_t* codes, uint32_t& word) {
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < U; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  amax = max(amax, dpp_u<0xB1>(amax));
+  amax = max(amax, dpp_u<0x4E>(amax));
+  if constexpr (U == 4) amax = max(amax, dpp_u<0x141>(amax));
+  const uint32_t byte = mx_block_byte<KIND>(amax), keep = byte == 255u ? 0u : 0xFFFFFFFFu;
+  const float f = mx_factor(byte);
+  if constexpr (KIND == ROW_E2M1) {
+    codes[0] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v[0], v[1], f, 0);
+    codes[0] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes[0], v[2], v[3], f, 1);
+    if constexpr (U == 8) {
+      codes[0] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes[0], v[4], v[5], f, 2);
+      codes[0] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes[0], v[6], v[7], f, 3);
+    }
+    codes[0] &= keep;
+  } else {
+#pragma unroll
+    for (int i = 0; i < U / 4; ++i) codes[i] = mx_codes<KIND>(v + 4 * i, f) & keep;
+  }
+  word = byte << (8 * ((threadIdx.x / (32 / U)) & 3));
+  if constexpr (U == 8) word |= partner<2>(word);        // the other block of 8 lanes
+  word |= partner<3>(word);                              // the other 8 of 16 lanes
+  if constexpr (U == 4) word |= partner<4>(word);        // the other 16 of 32
+}
+
 // ---- back ------------------------------------------------------------------
 
 // What a scale byte stands for: NaN for 255.

@@ -30,50 +30,46 @@ __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
   typedef float f2 __attribute__((ext_vector_type(2)));
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, bf2));
 }
-__device__ __forceinline__ v4u pack8(const float* f) {
-  return v4u{bf16x2(f[0], f[1]), bf16x2(f[2], f[3]), bf16x2(f[4], f[5]), bf16x2(f[6], f[7])};
-}
-__device__ __forceinline__ void unpack8(v4u u, float* f) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(u[i] << 16);
-    f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-  }
-}
-
-// Eight values of a BF16 or fp32 tensor, from element i (a multiple of 8) on.
-template <bool F32>
-struct Eight {
-  v4u u[F32 ? 2 : 1];
+// U values of a BF16 or fp32 tensor from element i (a multiple of U) on: 8 or 16
+// bytes of BF16, 16 or 32 of fp32.
+template <bool F32, int U>
+struct Unit {
+  static constexpr int W = U * (F32 ? 4 : 2) / 4;        // words
+  typedef uint32_t vec __attribute__((ext_vector_type(W > 4 ? 4 : W)));
+  static constexpr int N = W > 4 ? W / 4 : 1;
+  vec u[N];
   __device__ __forceinline__ void load(const void* base, int64_t i) {
-    const v4u* const p = reinterpret_cast<const v4u*>(static_cast<const uint8_t*>(base) + i * (F32 ? 4 : 2));
+    const vec* const p = reinterpret_cast<const vec*>(static_cast<const uint8_t*>(base) + i * (F32 ? 4 : 2));
 #pragma unroll
-    for (int q = 0; q < (F32 ? 2 : 1); ++q) u[q] = p[q];
+    for (int q = 0; q < N; ++q) u[q] = p[q];
   }
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int q = 0; q < (F32 ? 2 : 1); ++q) u[q] = v4u{};
+    for (int q = 0; q < N; ++q) u[q] = vec{};
   }
   __device__ __forceinline__ void get(float* f) const {
-    if constexpr (F32) {
 #pragma unroll
-      for (int q = 0; q < 8; ++q) f[q] = __uint_as_float(u[q >> 2][q & 3]);
-    } else {
-      unpack8(u[0], f);
+    for (int i = 0; i < W; ++i) {
+      const uint32_t x = u[i >> 2][i & 3];
+      if constexpr (F32) {
+        f[i] = __uint_as_float(x);
+      } else {
+        f[2 * i] = __uint_as_float(x << 16);
+        f[2 * i + 1] = __uint_as_float(x & 0xFFFF0000u);
+      }
     }
   }
   __device__ __forceinline__ void set(const float* f) {
-    if constexpr (F32) {
 #pragma unroll
-      for (int q = 0; q < 8; ++q) u[q >> 2][q & 3] = __float_as_uint(f[q]);
-    } else {
-      u[0] = pack8(f);
+    for (int i = 0; i < W; ++i) {
+      if constexpr (F32) u[i >> 2][i & 3] = __float_as_uint(f[i]);
+      else u[i >> 2][i & 3] = bf16x2(f[2 * i], f[2 * i + 1]);
     }
   }
   __device__ __forceinline__ void store(void* base, int64_t i) const {
-    v4u* const p = reinterpret_cast<v4u*>(static_cast<uint8_t*>(base) + i * (F32 ? 4 : 2));
+    vec* const p = reinterpret_cast<vec*>(static_cast<uint8_t*>(base) + i * (F32 ? 4 : 2));
 #pragma unroll
-    for (int q = 0; q < (F32 ? 2 : 1); ++q) p[q] = u[q];
+    for (int q = 0; q < N; ++q) p[q] = u[q];
   }
 };
 
@@ -108,79 +104,81 @@ __device__ __forceinline__ void row_sums(double& s, double& t, int waves, int wa
 // forward
 // ---------------------------------------------------------------------------
 
-// P pieces of C columns a lane: piece p of wave w of the row's `waves` starts
-// at column ((p waves + w) 64 + lane) C.
+// P pieces of U columns a lane: piece p of wave w of the row's `waves` starts at
+// column ((p waves + w) 64 + lane) U.  U is what makes 16 bytes of the stream, so
+// that every access of a wave is one run: with 16 columns a lane (as dispatch has
+// them for MX rows) 16381 x 2048 with an fp32 stream took 102 us, 4999 x 4096
+// with E4M3 rows 33.
 template <bool XF32, bool SF32, int KIND, int P>
 __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a, int waves) {
-  constexpr int C = KIND == ROW_BF16 ? 8 : 16, E = C / 8;
+  constexpr int U = SF32 ? 4 : 8;
   __shared__ double place[16][2];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int teams = (blockDim.x >> 6) / waves, team = wave / waves, w = wave & (waves - 1);
   const int64_t row = static_cast<int64_t>(blockIdx.x) * teams + team;
   const bool live = row < a.rows;
   const int64_t first = (live ? row : 0) * a.width;
-  int col[P];
-  bool in[P];
-  Eight<XF32> x[P][E];
-  Eight<SF32> r[P][E];
+  const int col0 = (w * 64 + lane) * U, step = waves * 64 * U;
+  Unit<XF32, U> x[P];
+  Unit<SF32, U> r[P];
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    col[p] = ((p * waves + w) * 64 + lane) * C;
-    in[p] = live && col[p] < a.width;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      x[p][e].clear();
-      r[p][e].clear();
-      if (in[p]) x[p][e].load(a.x, first + col[p] + 8 * e);
-      if (in[p] && a.residual) r[p][e].load(a.residual, first + col[p] + 8 * e);
+    const int col = col0 + p * step;
+    x[p].clear();
+    r[p].clear();
+    if (live && col < a.width) {
+      x[p].load(a.x, first + col);
+      if (a.residual) r[p].load(a.residual, first + col);
     }
   }
-  float h[P][C];
+  float h[P][U];
   double sum = 0.0, none = 0.0;
 #pragma unroll
-  for (int p = 0; p < P; ++p)
+  for (int p = 0; p < P; ++p) {
+    const int col = col0 + p * step;
+    x[p].get(h[p]);
+    if (a.residual) {
+      float g[U];
+      r[p].get(g);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      float* const f = h[p] + 8 * e;
-      x[p][e].get(f);
-      if (a.residual) {
-        float g[8];
-        r[p][e].get(g);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] += f[i];
-        r[p][e].set(g);
-        r[p][e].get(f);                          // as it is kept
-        if (in[p]) r[p][e].store(a.h, first + col[p] + 8 * e);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fma(static_cast<double>(f[i]), static_cast<double>(f[i]), sum);
+      for (int i = 0; i < U; ++i) g[i] += h[p][i];
+      r[p].set(g);
+      r[p].get(h[p]);                            // as it is kept
+      if (live && col < a.width) r[p].store(a.h, first + col);
     }
+#pragma unroll
+    for (int i = 0; i < U; ++i) sum = fma(static_cast<double>(h[p][i]), static_cast<double>(h[p][i]), sum);
+  }
   row_sums(sum, none, waves, wave, place, false);
   float ra, rb;
   inverse_root(sum * a.inverse_width + a.eps, ra, rb);
 #pragma unroll
   for (int p = 0; p < P; ++p) {
+    const int col = col0 + p * step;
+    const bool in = live && col < a.width;
+    const int64_t at = first + col;
 #pragma unroll
-    for (int i = 0; i < C; i += 4) {
+    for (int i = 0; i < U; i += 4) {
       v4f v{};
-      if (in[p]) v = *reinterpret_cast<const v4f_any*>(a.weight + col[p] + i);
+      if (in) v = *reinterpret_cast<const v4f_any*>(a.weight + col + i);
 #pragma unroll
       for (int q = 0; q < 4; ++q) h[p][i + q] = h[p][i + q] * ra * rb * v[q];
     }
-    const int64_t at = first + col[p];
     if (KIND == ROW_BF16 || a.y) {
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (in[p]) *reinterpret_cast<v4u*>(a.y + at + 8 * e) = pack8(h[p] + 8 * e);
+      Unit<false, U> y;
+      y.set(h[p]);
+      if (in) y.store(a.y, at);
     }
     if constexpr (KIND != ROW_BF16) {
-      v4u q;
-      const uint32_t word = mx_from_f32<KIND>(h[p], q);
-      if (!in[p]) continue;
-      if constexpr (KIND == ROW_E2M1) *reinterpret_cast<v2u*>(a.codes + at / 2) = v2u{q.x, q.y};
-      else *reinterpret_cast<v4u*>(a.codes + at) = q;
-      if ((lane & 7) == 0) {
-        const int64_t k = col[p] >> 7;
+      uint32_t codes[U / 4], word;
+      mx_unit<KIND, U>(h[p], codes, word);
+      if (!in) continue;
+      if constexpr (KIND == ROW_E2M1 && U == 4) *reinterpret_cast<uint16_t*>(a.codes + at / 2) = static_cast<uint16_t>(codes[0]);
+      else if constexpr (KIND == ROW_E2M1) *reinterpret_cast<uint32_t*>(a.codes + at / 2) = codes[0];
+      else if constexpr (U == 4) *reinterpret_cast<uint32_t*>(a.codes + at) = codes[0];
+      else *reinterpret_cast<v2u*>(a.codes + at) = v2u{codes[0], codes[1]};
+      if ((lane & (128 / U - 1)) == 0) {
+        const int64_t k = col >> 7;
         reinterpret_cast<uint32_t*>(a.scales)[a.kplanes ? k * a.rows + row : at >> 7] = word;
       }
     }
@@ -194,8 +192,8 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a, int waves) {
 // A workgroup's teams take rows in turn and add up their part of dw in
 // registers; the teams' parts meet in LDS, the workgroups' in norm_dw_kernel,
 // in a fixed order.
-template <bool SF32, int P>
-__global__ __launch_bounds__(1024) void rms_norm_backward_kernel(NormArgs a, int waves) {
+template <bool SF32, int P, int THREADS>
+__global__ __launch_bounds__(THREADS) void rms_norm_backward_kernel(NormArgs a, int waves) {
   __shared__ double place[2][16][2];
   __shared__ v4f part[4][P * 2][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -222,8 +220,8 @@ __global__ __launch_bounds__(1024) void rms_norm_backward_kernel(NormArgs a, int
     const int64_t row = base + team;
     const bool live = row < a.rows;
     const int64_t first = (live ? row : 0) * a.width;
-    Eight<false> dy[P];
-    Eight<SF32> h[P], dh[P];
+    Unit<false, 8> dy[P];
+    Unit<SF32, 8> h[P], dh[P];
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       dy[p].clear();
@@ -340,26 +338,22 @@ hipError_t by_pieces(int p, F&& f) {
   switch (p) {
     case 1: return f(std::integral_constant<int, 1>{});
     case 2: return f(std::integral_constant<int, 2>{});
-    default: return f(std::integral_constant<int, 4>{});
+    case 4: return f(std::integral_constant<int, 4>{});
+    default: return f(std::integral_constant<int, 8>{});
   }
 }
 
-template <bool XF32, bool SF32, int KIND, int P>
-hipError_t launch_norm_kernel(const NormArgs& a, const Shape& sh, hipStream_t s) {
-  const int threads = threads_of(sh), teams = threads / 64 / sh.waves;
-  const unsigned blocks = static_cast<unsigned>((a.rows + teams - 1) / teams);
-  hipLaunchKernelGGL((rms_norm_kernel<XF32, SF32, KIND, P>), dim3(blocks), dim3(threads), 0, s, a, sh.waves);
-  return hipGetLastError();
-}
 template <bool XF32, bool SF32, int KIND>
 hipError_t launch_norm_kind(const NormArgs& a, hipStream_t s) {
-  if constexpr (KIND == ROW_BF16) {
-    const Shape sh = shape_of((a.width + 511) / 512, 4);
-    return by_pieces(sh.p, [&](auto p) { return launch_norm_kernel<XF32, SF32, KIND, decltype(p)::value>(a, sh, s); });
-  } else {
-    const Shape sh = shape_of((a.width + 1023) / 1024, 2);
-    return sh.p == 1 ? launch_norm_kernel<XF32, SF32, KIND, 1>(a, sh, s) : launch_norm_kernel<XF32, SF32, KIND, 2>(a, sh, s);
-  }
+  constexpr int kPiece = SF32 ? 256 : 512;
+  const Shape sh = shape_of((a.width + kPiece - 1) / kPiece, 2048 / kPiece);
+  return by_pieces(sh.p, [&](auto p) {
+    constexpr int P = decltype(p)::value < 2048 / kPiece ? decltype(p)::value : 2048 / kPiece;
+    const int threads = threads_of(sh), teams = threads / 64 / sh.waves;
+    const unsigned blocks = static_cast<unsigned>((a.rows + teams - 1) / teams);
+    hipLaunchKernelGGL((rms_norm_kernel<XF32, SF32, KIND, P>), dim3(blocks), dim3(threads), 0, s, a, sh.waves);
+    return hipGetLastError();
+  });
 }
 template <bool XF32, bool SF32>
 hipError_t launch_norm_types(const NormArgs& a, hipStream_t s) {
@@ -381,6 +375,12 @@ int64_t backward_blocks(int64_t rows, int width) {
   return all < 512 ? all : 512;
 }
 
+template <int P, int THREADS>
+void launch_backward_kernel(const NormArgs& a, dim3 grid, int waves, hipStream_t s) {
+  if (a.stream_f32) hipLaunchKernelGGL((rms_norm_backward_kernel<true, P, THREADS>), grid, dim3(THREADS), 0, s, a, waves);
+  else hipLaunchKernelGGL((rms_norm_backward_kernel<false, P, THREADS>), grid, dim3(THREADS), 0, s, a, waves);
+}
+
 }  // namespace
 
 hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s) {
@@ -395,11 +395,14 @@ hipError_t launch_rms_norm_backward(const NormArgs& a, hipStream_t s) {
   const int64_t blocks = backward_blocks(a.rows, a.width);
   if (blocks > 0) {
     const Shape sh = backward_shape(a.width);
-    const dim3 grid(static_cast<unsigned>(blocks)), block(threads_of(sh));
+    const dim3 grid(static_cast<unsigned>(blocks));
     const hipError_t e = by_pieces(sh.p, [&](auto p) {
-      constexpr int P = decltype(p)::value;
-      if (a.stream_f32) hipLaunchKernelGGL((rms_norm_backward_kernel<true, P>), grid, block, 0, s, a, sh.waves);
-      else hipLaunchKernelGGL((rms_norm_backward_kernel<false, P>), grid, block, 0, s, a, sh.waves);
+      constexpr int P = decltype(p)::value < 4 ? decltype(p)::value : 4;
+      if (sh.waves <= 4) launch_backward_kernel<P, 256>(a, grid, sh.waves, s);
+      else if constexpr (P == 4) {
+        if (sh.waves == 8) launch_backward_kernel<P, 512>(a, grid, sh.waves, s);
+        else launch_backward_kernel<P, 1024>(a, grid, sh.waves, s);
+      }
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;
