@@ -457,7 +457,7 @@ moegg_status check_norm(const moegg_norm_problem* pp, bool backward) {
     return set_error(MOEGG_ERROR_NOT_SUPPORTED, "width=%d: a positive multiple of %d needed", p.width, step);
   if (p.width > moegg::kMaxNormWidth)
     return set_error(MOEGG_ERROR_NOT_SUPPORTED, "width=%d above %d", p.width, moegg::kMaxNormWidth);
-  // (at most 16 waves a row, twice as many as its pieces of 1024 columns need; the backward's grid is bounded)
+  // (a power of two of waves, below twice the pieces of 1024 columns; the backward's grid is bounded)
   const int64_t waves = (p.width + 1023) / 1024 * 2;
   if (!backward && (p.rows + 4) * waves * 64 > moegg::kLaunchThreads)
     return set_error(MOEGG_ERROR_NOT_SUPPORTED, "rows=%lld width=%d: more threads than a launch holds", (long long)p.rows, p.width);
