@@ -335,7 +335,9 @@ moegg_status check_saved(const moegg_linear_problem& p, const moegg_linear_saved
   if (c8 && p.n % 32 != 0) return set_error(MOEGG_ERROR_NOT_SUPPORTED, "n=%d: a multiple of 32 needed for c in 8 bits", p.n);
   if (!x8 && s.x_sf) return set_error(MOEGG_ERROR_INVALID_VALUE, "a BF16 x takes no x_sf");
   if (!c8 && s.c_sf) return set_error(MOEGG_ERROR_INVALID_VALUE, "a BF16 c takes no c_sf");
-  if (x8 && (p.m * p.k + 4095) / 4096 * 256 > moegg::kLaunchThreads)
+  // (x's way to BF16 shares a launch with dz)
+  const int64_t dz = (p.m / 128 + p.num_groups + 1) * int64_t{p.n / 256 + 2} * 256;
+  if (x8 && (p.m * p.k + 4095) / 4096 * 256 + dz > moegg::kLaunchThreads)
     return set_error(MOEGG_ERROR_NOT_SUPPORTED, "m=%lld k=%d: more threads than a launch holds", (long long)p.m, p.k);
   return MOEGG_OK;
 }

@@ -38,6 +38,7 @@ struct RouteArgs {
   int32_t top_groups;
   bool group_sums;         // a group's score: its two largest keys added, else its largest
   uint32_t group_magic;    // expert e is in group (e magic) >> 22
+  int32_t group_lanes;     // a group is so many whole lanes, or 0       [set by the launchers]
 };
 hipError_t launch_route(const RouteArgs& a, hipStream_t s);
 hipError_t launch_route_backward(const RouteArgs& a, hipStream_t s);

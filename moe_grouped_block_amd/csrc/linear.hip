@@ -215,13 +215,13 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs a, TilePlan
 // ---------------------------------------------------------------------------
 //
 // One pass over dy and c: dz in bf16, and the column sums of the unrounded
-// dz over tiles of kDzRows rows of one group, summed per group afterwards.
+// dz over tiles of dz_rows() rows of one group, summed per group afterwards.
+// An x in 8 bits becomes BF16 in the same launch (it is an operand of dw as dz
+// is): its workgroups run beside the others.
 // dz is the operand of both products: kept in two bf16 parts it would double
 // their work.  With its one rounding dx and dw are 0.0023 off the 64-bit values
 // (root mean square, 16384 x 2816 x 2048 with SwiGLU), where the rounding of the
 // results alone is 0.0017.
-constexpr int kDzRows = 128;
-
 __device__ __forceinline__ void unpack8(v4u u, float* f) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -296,24 +296,43 @@ __device__ __forceinline__ void dz_of(const float* d, const EightOfC<CK>& c0, co
   }
 }
 
+// Rows and columns of dy that a workgroup of linear_dz_kernel takes, and the
+// rest of its launch.
+struct DzPlan {
+  uint16_t* dz;             // or null
+  float* sums;              // or null
+  uint16_t* x;              // where an x in 8 bits goes, or null: by the workgroups from y = cols on
+  int rows, cols;           // rows of a tile, workgroups along the columns
+};
+
 // 32 threads run along 256 columns of dy, 8 rows at a time; four of a
 // thread's rows are in flight at once.
-template <int ACT, int CK>
-__global__ __launch_bounds__(256) void linear_dz_kernel(LinearArgs a, uint16_t* dz, float* sums) {
+template <int ACT, int CK, bool X8>
+__global__ __launch_bounds__(256) void linear_dz_kernel(LinearArgs a, DzPlan plan) {
+  if constexpr (X8) {
+    if (static_cast<int>(blockIdx.y) >= plan.cols) {
+      const int64_t chunk = static_cast<int64_t>(blockIdx.y - plan.cols) * gridDim.x + blockIdx.x;
+      if (a.x8.kind == ROW_E4M3) dequantise_chunk<ROW_E4M3, false>(a.x8, plan.x, a.m, a.k, chunk);
+      else dequantise_chunk<ROW_E5M2, false>(a.x8, plan.x, a.m, a.k, chunk);
+      return;
+    }
+  }
+  uint16_t* const dz = plan.dz;
+  float* const sums = plan.sums;
   constexpr bool PAIR = ACT == LIN_SWIGLU;
   constexpr int S = PAIR ? 16 : 8, U = 4;
   __shared__ float red[8][32][S + 1];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, lane = threadIdx.x & 63;
   int g;
   int64_t row0, end;
-  if (!find_row_tile<kDzRows>(a, blockIdx.x, lane, g, row0, end)) return;
+  if (!find_row_tile(a, plan.rows, blockIdx.x, lane, g, row0, end)) return;
   const int n_out = PAIR ? a.n / 2 : a.n;
   const int col = (blockIdx.y * 32 + tx) * 8;                  // of dy
   const int n = PAIR ? (col >> 5) * 64 + (col & 31) : col;     // of dz (and n + 32 of a pair)
   float s[S];
 #pragma unroll
   for (int i = 0; i < S; ++i) s[i] = 0.0f;
-  const int rows = static_cast<int>(min(end - row0, int64_t{kDzRows}));
+  const int rows = static_cast<int>(min(end - row0, int64_t{plan.rows}));
   if (col < n_out) {
     for (int r = ty; r < rows; r += 8 * U) {
       v4u d[U];
@@ -364,9 +383,10 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinearArgs a, uint16_t* 
   }
 }
 
-// db of 512 / Q columns of a group: Q threads a column share the row tiles.
+// db of 512 / Q columns of a group: Q threads a column share the row tiles (of
+// `rows` rows).
 template <int Q>
-__global__ __launch_bounds__(512) void linear_db_kernel(LinearArgs a, const float* sums) {
+__global__ __launch_bounds__(512) void linear_db_kernel(LinearArgs a, const float* sums, int rows) {
   constexpr int X = 512 / Q;
   __shared__ float red[Q][X + 1];
   const int lane = threadIdx.x & 63, x = threadIdx.x % X, q = threadIdx.x / X, g = blockIdx.y;
@@ -376,7 +396,7 @@ __global__ __launch_bounds__(512) void linear_db_kernel(LinearArgs a, const floa
     for (int i = lane; i <= g; i += 64) {
       int64_t b, e;
       group_rows(a, i, b, e);
-      const int64_t t = (e - b + kDzRows - 1) / kDzRows;
+      const int64_t t = (e - b + rows - 1) / rows;
       if (i < g) before += t;
       else mine = t;
     }
@@ -384,9 +404,9 @@ __global__ __launch_bounds__(512) void linear_db_kernel(LinearArgs a, const floa
       before += __shfl_xor(before, d);
       mine += __shfl_xor(mine, d);
     }
-    mine = min(mine, most_row_tiles<kDzRows>(a) - before);       // (offsets that decrease: none that were not summed)
+    mine = min(mine, most_row_tiles(a, rows) - before);       // (offsets that decrease: none that were not summed)
   } else {
-    mine = most_row_tiles<kDzRows>(a);
+    mine = most_row_tiles(a, rows);
   }
   const int n = blockIdx.x * X + x;
   float s = 0.0f;
@@ -412,9 +432,13 @@ int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t a, int64_t b) { return div_up(a, b) * b; }
 
 // Row tiles of all groups at most.
-int64_t row_tiles(const LinearArgs& a, int bm) {
-  return bm == 64 ? most_row_tiles<64>(a) : bm == 128 ? most_row_tiles<128>(a) : most_row_tiles<256>(a);
-}
+int64_t row_tiles(const LinearArgs& a, int bm) { return most_row_tiles(a, bm); }
+
+// Workgroups of linear_dz_kernel along the columns, and rows of a tile: 128, or
+// 32 where that leaves most of the chip empty (129 x 512, GELU: 13.7 us with
+// 128, DZ_US with 32).
+int dz_cols(const LinearArgs& a) { return static_cast<int>(div_up(a.act == LIN_SWIGLU ? a.n / 2 : a.n, 256)); }
+int dz_rows(const LinearArgs& a) { return row_tiles(a, 128) * dz_cols(a) < 512 ? 32 : 128; }
 
 // Tile shapes: how many workgroups the chip holds at once, and what they take,
 // in microseconds: a step of 64 r where few of them are there, where half of
@@ -600,7 +624,7 @@ BackwardWorkspace backward_workspace(const LinearArgs& a, bool dx, bool dw, bool
     return here;
   };
   w.dz = take(a.act != LIN_NONE && (dx || dw) ? a.m * a.n * 2 : 0);
-  w.sums = take(db ? row_tiles(a, kDzRows) * a.n * 4 : 0);
+  w.sums = take(db ? row_tiles(a, dz_rows(a)) * a.n * 4 : 0);
   w.dx = take(dx && a.m ? plan_rows(a, MODE_DX).partial_bytes : 0);
   w.dw = take(dw ? plan_dw(a).partial_bytes : 0);
   w.x = take(dw && a.x8.kind != ROW_BF16 ? a.m * a.k * 2 : 0);
@@ -654,13 +678,21 @@ hipError_t launch_linear(const LinearArgs& args, hipStream_t s) {
 }
 
 namespace {
-template <int CK>
-void launch_dz(const LinearArgs& a, dim3 grid, uint16_t* dz, float* sums, hipStream_t s) {
+template <int CK, bool X8>
+void launch_dz(const LinearArgs& a, const DzPlan& p, dim3 grid, hipStream_t s) {
   switch (a.act) {
-    case LIN_SWIGLU: hipLaunchKernelGGL((linear_dz_kernel<LIN_SWIGLU, CK>), grid, dim3(256), 0, s, a, dz, sums); break;
-    case LIN_SRELU: hipLaunchKernelGGL((linear_dz_kernel<LIN_SRELU, CK>), grid, dim3(256), 0, s, a, dz, sums); break;
-    case LIN_GELU: hipLaunchKernelGGL((linear_dz_kernel<LIN_GELU, CK>), grid, dim3(256), 0, s, a, dz, sums); break;
-    default: hipLaunchKernelGGL((linear_dz_kernel<LIN_NONE, ROW_BF16>), grid, dim3(256), 0, s, a, dz, sums); break;
+    case LIN_SWIGLU: hipLaunchKernelGGL((linear_dz_kernel<LIN_SWIGLU, CK, X8>), grid, dim3(256), 0, s, a, p); break;
+    case LIN_SRELU: hipLaunchKernelGGL((linear_dz_kernel<LIN_SRELU, CK, X8>), grid, dim3(256), 0, s, a, p); break;
+    case LIN_GELU: hipLaunchKernelGGL((linear_dz_kernel<LIN_GELU, CK, X8>), grid, dim3(256), 0, s, a, p); break;
+    default: hipLaunchKernelGGL((linear_dz_kernel<LIN_NONE, ROW_BF16, X8>), grid, dim3(256), 0, s, a, p); break;
+  }
+}
+template <bool X8>
+void launch_dz_kind(const LinearArgs& a, const DzPlan& p, dim3 grid, hipStream_t s) {
+  switch (a.c_kind) {
+    case ROW_E4M3: launch_dz<ROW_E4M3, X8>(a, p, grid, s); break;
+    case ROW_E5M2: launch_dz<ROW_E5M2, X8>(a, p, grid, s); break;
+    default: launch_dz<ROW_BF16, X8>(a, p, grid, s); break;
   }
 }
 }  // namespace
@@ -670,36 +702,39 @@ hipError_t launch_linear_backward(const LinearArgs& args, hipStream_t s) {
   const BackwardWorkspace w = backward_workspace(a, a.dx, a.dw, a.db);
   uint8_t* const ws = static_cast<uint8_t*>(a.workspace);
   const bool make_dz = a.act != LIN_NONE && (a.dx || a.dw) && a.m;
+  const bool x8 = a.dw && a.x8.kind != ROW_BF16;
   uint16_t* const dz = make_dz ? reinterpret_cast<uint16_t*>(ws + w.dz) : nullptr;
   float* const sums = a.db ? reinterpret_cast<float*>(ws + w.sums) : nullptr;
+  uint16_t* const x = x8 ? reinterpret_cast<uint16_t*>(ws + w.x) : nullptr;
+  const int rows = dz_rows(a);
   a.dz = make_dz ? dz : a.dy;
   a.dx_partial = reinterpret_cast<float*>(ws + w.dx);
   a.dw_partial = reinterpret_cast<float*>(ws + w.dw);
   hipError_t e = hipSuccess;
   if ((make_dz || a.db) && a.m) {
-    const int n_out = a.act == LIN_SWIGLU ? a.n / 2 : a.n;
-    const dim3 grid(static_cast<unsigned>(row_tiles(a, kDzRows)), static_cast<unsigned>(div_up(n_out, 256)));
-    switch (a.c_kind) {
-      case ROW_E4M3: launch_dz<ROW_E4M3>(a, grid, dz, sums, s); break;
-      case ROW_E5M2: launch_dz<ROW_E5M2>(a, grid, dz, sums, s); break;
-      default: launch_dz<ROW_BF16>(a, grid, dz, sums, s); break;
+    const int64_t tiles = row_tiles(a, rows);
+    const DzPlan p{dz, sums, x, rows, dz_cols(a)};
+    dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(p.cols));
+    if (x8) {
+      grid.y += static_cast<unsigned>(div_up(div_up(a.m * a.k, kSavedChunk), tiles));
+      launch_dz_kind<true>(a, p, grid, s);
+    } else {
+      launch_dz_kind<false>(a, p, grid, s);
     }
     if ((e = hipGetLastError()) != hipSuccess) return e;
+  } else if (x8 && a.m && (e = launch_dequantise(a.x8, x, false, a.m, a.k, s)) != hipSuccess) {
+    return e;
   }
-  if (a.dw && a.x8.kind != ROW_BF16) {
-    uint16_t* const x = reinterpret_cast<uint16_t*>(ws + w.x);
-    if (a.m && (e = launch_dequantise(a.x8, x, false, a.m, a.k, s)) != hipSuccess) return e;
-    a.x = x;
-  }
+  if (x8) a.x = x;
   if (a.db) {
     // few row tiles a group: few threads a column, or most of them only wait (64
     // groups of 2048 columns, 4 tiles each: 15 us with 16 threads, 5 with 2)
-    if (row_tiles(a, kDzRows) <= 16 * static_cast<int64_t>(a.groups))
+    if (row_tiles(a, rows) <= 16 * static_cast<int64_t>(a.groups))
       hipLaunchKernelGGL((linear_db_kernel<2>), dim3(static_cast<unsigned>(div_up(a.n, 256)), static_cast<unsigned>(a.groups)),
-                         dim3(512), 0, s, a, sums);
+                         dim3(512), 0, s, a, sums, rows);
     else
       hipLaunchKernelGGL((linear_db_kernel<16>), dim3(static_cast<unsigned>(div_up(a.n, 32)), static_cast<unsigned>(a.groups)),
-                         dim3(512), 0, s, a, sums);
+                         dim3(512), 0, s, a, sums, rows);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   const Plan pdx = plan_rows(a, MODE_DX), pdw = plan_dw(a);

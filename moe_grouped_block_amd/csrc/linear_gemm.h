@@ -154,10 +154,13 @@ __device__ __forceinline__ void group_rows(const LinearArgs& a, int g, int64_t& 
   }
 }
 
-// Row tiles of all groups at most (and exactly, without offsets).
+// Row tiles of all groups at most (and exactly, without offsets), of bm rows.
+__host__ __device__ __forceinline__ int64_t most_row_tiles(const LinearArgs& a, int bm) {
+  return (a.m + bm - 1) / bm + (a.groups > 1 ? a.groups - 1 : 0);
+}
 template <int BM>
 __host__ __device__ __forceinline__ int64_t most_row_tiles(const LinearArgs& a) {
-  return (a.m + BM - 1) / BM + (a.groups > 1 ? a.groups - 1 : 0);
+  return most_row_tiles(a, BM);
 }
 
 // Tiles of BM rows of every group (a tile holds rows of one group); the
@@ -175,12 +178,11 @@ __device__ __forceinline__ int count_row_tiles(const LinearArgs& a, int lane) {
   for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
   return __builtin_amdgcn_readfirstlane(static_cast<int>(min(sum, most_row_tiles<BM>(a))));
 }
-// Row tile mt: its group, first row and the end of the group's rows.
-template <int BM>
-__device__ __forceinline__ bool find_row_tile(const LinearArgs& a, int mt, int lane, int& g, int64_t& row0, int64_t& end) {
+// Row tile mt of bm rows: its group, first row and the end of the group's rows.
+__device__ __forceinline__ bool find_row_tile(const LinearArgs& a, int bm, int mt, int lane, int& g, int64_t& row0, int64_t& end) {
   if (!a.offsets) {
     g = 0;
-    row0 = static_cast<int64_t>(mt) * BM;
+    row0 = static_cast<int64_t>(mt) * bm;
     end = a.m;
     return row0 < end;
   }
@@ -188,7 +190,7 @@ __device__ __forceinline__ bool find_row_tile(const LinearArgs& a, int mt, int l
   for (int g0 = 0; g0 < a.groups; g0 += 64) {
     int64_t b = 0, e = 0;
     if (g0 + lane < a.groups) group_rows(a, g0 + lane, b, e);
-    const int tiles = static_cast<int>((e - b + BM - 1) / BM);
+    const int tiles = static_cast<int>((e - b + bm - 1) / bm);
     int scan = tiles;
     for (int d = 1; d < 64; d <<= 1) {
       const int y = __shfl_up(scan, d);
@@ -200,7 +202,7 @@ __device__ __forceinline__ bool find_row_tile(const LinearArgs& a, int mt, int l
       g = __builtin_amdgcn_readfirstlane(g0 + l);
       const int first = before + __builtin_amdgcn_readlane(scan, l) - __builtin_amdgcn_readlane(tiles, l);
       const int bl = __builtin_amdgcn_readlane(static_cast<int>(b), l);
-      row0 = bl + static_cast<int64_t>(mt - first) * BM;
+      row0 = bl + static_cast<int64_t>(mt - first) * bm;
       end = __builtin_amdgcn_readlane(static_cast<int>(e), l);
       return true;
     }
@@ -305,7 +307,7 @@ __device__ __forceinline__ bool place(const LinearArgs& a, int i, int row_tiles,
     t.row_end = a.n;
   } else {
     tile_position(i, row_tiles, col_tiles, rt, ct);
-    if (!find_row_tile<BP>(a, rt, lane, t.g, t.row0, t.row_end)) return false;
+    if (!find_row_tile(a, BP, rt, lane, t.g, t.row0, t.row_end)) return false;
   }
   t.col0 = ct * BQ;
   return true;

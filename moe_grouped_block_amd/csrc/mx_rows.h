@@ -191,5 +191,43 @@ __device__ __forceinline__ void mx_four(uint32_t codes, float f, float* v) {
   v[3] = b.y * f;
 }
 
+// Elements of a workgroup of 4 waves that brings rows to 8 bits or back.
+constexpr int kSavedChunk = 4096;
+
+// Chunk number `chunk` of the rows, back to BF16 or fp32: 16 values a thread.
+template <int KIND, bool F32>
+__device__ __forceinline__ void dequantise_chunk(const SavedRows& s, void* out, int64_t rows, int width, int64_t chunk) {
+  const int64_t i = chunk * kSavedChunk + threadIdx.x * 16;
+  if (i >= rows * width) return;
+  const v4u q = *reinterpret_cast<const v4u*>(s.codes + i);
+  int64_t at = i >> 5;
+  if (s.kplanes) {
+    const int64_t r = i / width;
+    at = scale_at(s, rows, width, r, static_cast<int>(i - r * width) >> 5);
+  }
+  const float f = mx_scale_value(s.scales[at]);
+  float v[16];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) mx_four<KIND>(q[j], f, v + 4 * j);
+  if constexpr (F32) {
+    typedef float v4f __attribute__((ext_vector_type(4)));
+    v4f* const p = reinterpret_cast<v4f*>(static_cast<float*>(out) + i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[j] = v4f{v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]};
+  } else {
+    typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    v4u* const p = reinterpret_cast<v4u*>(static_cast<uint16_t*>(out) + i);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      v4u o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        o[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{v[8 * j + 2 * e], v[8 * j + 2 * e + 1]}, bf2));
+      p[j] = o;
+    }
+  }
+}
+
 }  // namespace
 }  // namespace moegg

@@ -201,115 +201,160 @@ constexpr int kSlots = kMaxTopK + kSpare;
 // places and a sum of up to 16 + 6 terms, below 50 2^-24.
 constexpr float kKeyP = 50.0f * 5.9604645e-8f, kKeySum = 2.4e-7f;
 
-// LDS of the choice of groups: a token's scores, its groups' scores (twice:
-// by group and by rank) and what they may be off by.
+// LDS of the choice of groups: a token's scores, then (in their place) its
+// groups' scores in 64 bits; its groups' scores and what they may be off by; the
+// last group in and the first one out.  Four workgroups fit a compute unit.
 template <int LPT, int EPL>
 struct GroupScratch {
-  float score[256 / LPT][LPT * (EPL + 1)];
+  union {
+    float score[256 / LPT][LPT * (EPL + 1)];
+    double exact[256 / LPT][kMaxGroups];
+  };
   float group[256 / LPT][kMaxGroups];
-  float ranked[256 / LPT][kMaxGroups][2];
-  double exact[256 / LPT][kMaxGroups];
+  float edge[256 / LPT][2][2];
 };
+
+// The two largest of a set, one more value or another set's two taken in.
+__device__ __forceinline__ void take(float& b0, float& b1, float v) {
+  b1 = fmaxf(b1, fminf(b0, v));
+  b0 = fmaxf(b0, v);
+}
 
 // Bits of the lane's EPL experts that are in no chosen group.  `score`: what
 // the groups' scores are made of (-inf: not there); `sums`: the two largest
-// added, else the largest.  Lane g scans group g's experts through LDS (rows of
-// a lane's EPL scores and a word more, so that neither side of the exchange
-// meets a bank twice), then counts the groups before its own.  Scores are
-// formed in fp32; where the last group in and the first one out are nearer than
-// the error of both, the wave's tokens form them in 64 bits.
+// added, else the largest; `logits`: they are exact.  A group that is whole
+// lanes, a power of two of them (256 experts in 8 groups: 2), is reduced in
+// registers; of others lane g scans group g's experts through LDS (rows of a
+// lane's EPL scores and a word more, so that neither side of the exchange meets
+// a bank twice).  Then lane g counts the groups before its own.
+// Scores are formed in fp32; where the last group in and the first one out are
+// nearer than the error of both, the wave's tokens form them in 64 bits.
+// Measured, 16381 tokens, 4 of 8 groups of 32 by their two best, sigmoid with
+// bias: 24.4 us with all groups through LDS and three workgroups to a compute
+// unit, GROUPED_US in registers; without groups 16.
 template <typename R, int LPT, int EPL>
 __device__ __forceinline__ uint32_t closed_groups(const RouteArgs& a, GroupScratch<LPT, EPL>& lds, const float* x, const float* score,
                                                   bool sums, bool logits, float top, int64_t row, int lane, int slot) {
   constexpr int N = kMaxGroups / LPT;            // groups of a lane
   constexpr double kNone = -__builtin_inf();
   const int groups = a.groups, size = a.experts / groups;
-#pragma unroll
-  for (int j = 0; j < EPL; ++j) lds.score[slot][lane * (EPL + 1) + j] = score[j];
-  wave_sync();
-  auto rank_of = [&](const auto* all, auto mine, int g) __attribute__((always_inline)) {
-    int rank = 0;
-    for (int o = 0; o < groups; ++o) rank += all[o] > mine || (all[o] == mine && o < g);
-    return rank;
-  };
-  bool open[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int g = lane + i * LPT;
-    if (g >= groups) continue;
-    float b0 = kNegInf, b1 = kNegInf;
-    for (int e = g * size; e < (g + 1) * size; ++e) {
-      const float v = lds.score[slot][e + e / EPL];
-      b1 = fmaxf(b1, fminf(b0, v));
-      b0 = fmaxf(b0, v);
-    }
+  float mine[N], off[N];
+  auto set = [&](int i, float b0, float b1) __attribute__((always_inline)) {
     const bool two = sums && b1 > kNegInf;
-    lds.group[slot][g] = two ? b0 + b1 : b0;
-    lds.ranked[slot][g][1] = logits ? 0.0f : two ? 2.0f * kKeyP + kKeySum * (fabsf(b0) + fabsf(b1)) : kKeyP + kKeySum * fabsf(b0);
-  }
-  wave_sync();
-  float off[N];
-  int rank[N];
+    mine[i] = two ? b0 + b1 : b0;
+    off[i] = logits ? 0.0f : two ? 2.0f * kKeyP + kKeySum * (fabsf(b0) + fabsf(b1)) : kKeyP + kKeySum * fabsf(b0);
+  };
+  if (a.group_lanes) {
+    float b0 = kNegInf, b1 = kNegInf;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int g = lane + i * LPT;
-    rank[i] = kMaxGroups;
-    if (g < groups) {
-      rank[i] = rank_of(lds.group[slot], lds.group[slot][g], g);
-      off[i] = lds.ranked[slot][g][1];
-    }
-  }
-  wave_sync();
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int g = lane + i * LPT;
-    open[i] = rank[i] < a.top_groups;
-    if (g < groups) {
-      lds.ranked[slot][rank[i]][0] = lds.group[slot][g];
-      lds.ranked[slot][rank[i]][1] = off[i];
-    }
-  }
-  wave_sync();
-  bool doubt = false;
-  if (!logits && a.top_groups < groups) {
-    const float in = lds.ranked[slot][a.top_groups - 1][0], out = lds.ranked[slot][a.top_groups][0];
-    doubt = out > kNegInf && !(in - out > lds.ranked[slot][a.top_groups - 1][1] + lds.ranked[slot][a.top_groups][1]);
-  }
-  if (__any(doubt)) {
-    double total = 1.0;
-    if (a.softmax) {
-      total = 0.0;
-#pragma unroll
-      for (int j = 0; j < EPL; ++j) total += x[j] == x[j] ? exp(static_cast<double>(x[j]) - top) : 0.0;
-      total = lanes_sum<LPT>(total);
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int g = lane + i * LPT;
-      if (g >= groups) continue;
-      double b0 = kNone, b1 = kNone;
-      for (int e = g * size; e < (g + 1) * size; ++e) {
-        const double l = R::one(a.logits, row, a.experts, e);
-        const double q = (a.softmax ? exp(l - top) / total : 1.0 / (1.0 + exp(-l))) + (a.bias ? a.bias[e] : 0.0f);
-        const double v = l > kNone && q > kNone ? q : kNone;           // NaN: false
-        b1 = fmax(b1, fmin(b0, v));
-        b0 = fmax(b0, v);
-      }
-      lds.exact[slot][g] = sums && b1 > kNone ? b0 + b1 : b0;
+    for (int j = 0; j < EPL; ++j) take(b0, b1, score[j]);
+    steps<LPT>([&](auto c) {
+      constexpr int S = decltype(c)::value;
+      if ((1 << S) >= a.group_lanes) return;     // (the same for all lanes)
+      const float o0 = partner<S>(b0), o1 = partner<S>(b1);
+      b1 = fmaxf(fmaxf(b1, o1), fminf(b0, o0));
+      b0 = fmaxf(b0, o0);
+    });
+    set(0, b0, b1);
+    // by group, for lane g
+    if (lane % a.group_lanes == 0) {
+      lds.group[slot][lane / a.group_lanes] = mine[0];
+      lds.score[slot][lane / a.group_lanes] = off[0];
     }
     wave_sync();
 #pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i * LPT < groups) {
+        mine[i] = lane + i * LPT < groups ? lds.group[slot][lane + i * LPT] : kNegInf;
+        off[i] = lane + i * LPT < groups ? lds.score[slot][lane + i * LPT] : 0.0f;
+      }
+    wave_sync();
+  } else {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) lds.score[slot][lane * (EPL + 1) + j] = score[j];
+    wave_sync();
+#pragma unroll
     for (int i = 0; i < N; ++i) {
+      if (i * LPT >= groups) break;
       const int g = lane + i * LPT;
-      open[i] = g < groups && rank_of(lds.exact[slot], lds.exact[slot][g], g) < a.top_groups;
+      float b0 = kNegInf, b1 = kNegInf;
+      if (g < groups) {
+#pragma unroll 4
+        for (int e = g * size; e < (g + 1) * size; ++e) take(b0, b1, lds.score[slot][e + e / EPL]);
+      }
+      set(i, b0, b1);
     }
+    wave_sync();
   }
+  // (places behind the last group, up to a multiple of 4: -inf, never counted)
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (i * LPT < groups) lds.group[slot][lane + i * LPT] = lane + i * LPT < groups ? mine[i] : kNegInf;
+  wave_sync();
+  auto rank_of = [&](float v, int g) __attribute__((always_inline)) {
+    typedef float v4f __attribute__((ext_vector_type(4)));
+    int rank = 0;
+    for (int o = 0; o < groups; o += 4) {
+      const v4f q = *reinterpret_cast<const v4f*>(&lds.group[slot][o]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) rank += q[e] > v || (q[e] == v && o + e < g);
+    }
+    return rank;
+  };
   uint64_t mask = 0;                             // the token's open groups
+  auto add = [&](int i, bool open) __attribute__((always_inline)) {
+    const uint64_t all = __ballot(open);
+    mask |= (LPT == 64 ? all : (all >> (threadIdx.x & 63 & ~(LPT - 1))) & ((1ull << (LPT & 63)) - 1)) << (i * LPT);
+  };
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const uint64_t all = __ballot(open[i]);
-    mask |= (LPT == 64 ? all : (all >> (threadIdx.x & 63 & ~(LPT - 1))) & ((1ull << (LPT & 63)) - 1)) << (i * LPT);
+    if (i * LPT >= groups) break;
+    const int g = lane + i * LPT, rank = g < groups ? rank_of(mine[i], g) : kMaxGroups;
+    add(i, rank < a.top_groups);
+    if (rank == a.top_groups - 1 || rank == a.top_groups) {
+      lds.edge[slot][rank == a.top_groups][0] = mine[i];
+      lds.edge[slot][rank == a.top_groups][1] = off[i];
+    }
   }
+  if (!logits) {
+    wave_sync();
+    const float in = lds.edge[slot][0][0], out = lds.edge[slot][1][0];
+    if (__any(out > kNegInf && !(in - out > lds.edge[slot][0][1] + lds.edge[slot][1][1]))) {
+      double total = 1.0;
+      if (a.softmax) {
+        total = 0.0;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) total += x[j] == x[j] ? exp(static_cast<double>(x[j]) - top) : 0.0;
+        total = lanes_sum<LPT>(total);
+      }
+      for (int g = lane; g < groups; g += LPT) {
+        double b0 = kNone, b1 = kNone;
+        for (int e = g * size; e < (g + 1) * size; ++e) {
+          const double l = R::one(a.logits, row, a.experts, e);
+          const double q = (a.softmax ? exp(l - top) / total : 1.0 / (1.0 + exp(-l))) + (a.bias ? a.bias[e] : 0.0f);
+          const double v = l > kNone && q > kNone ? q : kNone;         // NaN: false
+          b1 = fmax(b1, fmin(b0, v));
+          b0 = fmax(b0, v);
+        }
+        lds.exact[slot][g] = sums && b1 > kNone ? b0 + b1 : b0;
+      }
+      wave_sync();
+      mask = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (i * LPT >= groups) break;
+        const int g = lane + i * LPT;
+        int rank = kMaxGroups;
+        if (g < groups) {
+          const double v = lds.exact[slot][g];
+          rank = 0;
+          for (int o = 0; o < groups; ++o) rank += lds.exact[slot][o] > v || (lds.exact[slot][o] == v && o < g);
+        }
+        add(i, rank < a.top_groups);
+      }
+    }
+  }
+  if (a.group_lanes) return mask >> (lane / a.group_lanes & 63) & 1 ? 0u : ~0u;
   uint32_t closed = 0;
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
@@ -628,7 +673,10 @@ hipError_t launch_shape(const RouteArgs& a, bool backward, hipStream_t s) {
 // Accesses of up to 16 bytes where every token's logits start on such a
 // boundary (the host checks that the tensors do), else one element each.
 template <bool BF16, int LPT, int EPL>
-hipError_t launch_width(const RouteArgs& a, bool backward, hipStream_t s) {
+hipError_t launch_width(const RouteArgs& args, bool backward, hipStream_t s) {
+  RouteArgs a = args;
+  const int lanes = a.experts / a.groups / EPL;
+  a.group_lanes = a.experts / a.groups % EPL == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
   constexpr int V = EPL < (BF16 ? 8 : 4) ? EPL : (BF16 ? 8 : 4);
   return a.experts % V == 0 ? launch_shape<BF16, LPT, EPL, V>(a, backward, s)
                             : launch_shape<BF16, LPT, EPL, 1>(a, backward, s);

@@ -10,20 +10,11 @@ namespace {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ uint32_t bf16x2(float a, float b) {
-  typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
-  typedef float f2 __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, bf2));
-}
-
-// Elements of a workgroup of 4 waves.
-constexpr int kChunk = 4096;
-
 template <int KIND, bool F32>
 __global__ __launch_bounds__(256) void quantise_kernel(const void* x, uint8_t* codes, uint8_t* scales, bool kplanes, int64_t rows,
                                                        int width) {
   const int64_t n = rows * width;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kChunk + threadIdx.x * 16;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kSavedChunk + threadIdx.x * 16;
   const bool in = i < n;
   v4u q{};
   uint32_t word;
@@ -65,32 +56,10 @@ __global__ __launch_bounds__(256) void quantise_kernel(const void* x, uint8_t* c
 
 template <int KIND, bool F32>
 __global__ __launch_bounds__(256) void dequantise_kernel(SavedRows s, void* out, int64_t rows, int width) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kChunk + threadIdx.x * 16;
-  if (i >= rows * width) return;
-  const v4u q = *reinterpret_cast<const v4u*>(s.codes + i);
-  int64_t at = i >> 5;
-  if (s.kplanes) {
-    const int64_t r = i / width;
-    at = scale_at(s, rows, width, r, static_cast<int>(i - r * width) >> 5);
-  }
-  const float f = mx_scale_value(s.scales[at]);
-  float v[16];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) mx_four<KIND>(q[j], f, v + 4 * j);
-  if constexpr (F32) {
-    v4f* const p = reinterpret_cast<v4f*>(static_cast<float*>(out) + i);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) p[j] = v4f{v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]};
-  } else {
-    v4u* const p = reinterpret_cast<v4u*>(static_cast<uint16_t*>(out) + i);
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      p[j] = v4u{bf16x2(v[8 * j], v[8 * j + 1]), bf16x2(v[8 * j + 2], v[8 * j + 3]), bf16x2(v[8 * j + 4], v[8 * j + 5]),
-                 bf16x2(v[8 * j + 6], v[8 * j + 7])};
-  }
+  dequantise_chunk<KIND, F32>(s, out, rows, width, blockIdx.x);
 }
 
-unsigned blocks_of(int64_t rows, int width) { return static_cast<unsigned>((rows * width + kChunk - 1) / kChunk); }
+unsigned blocks_of(int64_t rows, int width) { return static_cast<unsigned>((rows * width + kSavedChunk - 1) / kSavedChunk); }
 
 }  // namespace
 
