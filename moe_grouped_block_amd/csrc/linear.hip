@@ -383,45 +383,10 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinearArgs a, DzPlan pla
   }
 }
 
-// db of 512 / Q columns of a group: Q threads a column share the row tiles (of
-// `rows` rows).
 template <int Q>
-__global__ __launch_bounds__(512) void linear_db_kernel(LinearArgs a, const float* sums, int rows) {
-  constexpr int X = 512 / Q;
-  __shared__ float red[Q][X + 1];
-  const int lane = threadIdx.x & 63, x = threadIdx.x % X, q = threadIdx.x / X, g = blockIdx.y;
-  // tiles of the groups before g, and of g
-  int64_t before = 0, mine = 0;
-  if (a.offsets) {
-    for (int i = lane; i <= g; i += 64) {
-      int64_t b, e;
-      group_rows(a, i, b, e);
-      const int64_t t = (e - b + rows - 1) / rows;
-      if (i < g) before += t;
-      else mine = t;
-    }
-    for (int d = 32; d; d >>= 1) {
-      before += __shfl_xor(before, d);
-      mine += __shfl_xor(mine, d);
-    }
-    mine = min(mine, most_row_tiles(a, rows) - before);       // (offsets that decrease: none that were not summed)
-  } else {
-    mine = most_row_tiles(a, rows);
-  }
-  const int n = blockIdx.x * X + x;
-  float s = 0.0f;
-  if (n < a.n) {
-#pragma unroll 4
-    for (int64_t t = q; t < mine; t += Q) s += sums[(before + t) * a.n + n];
-  }
-  red[q][x] = s;
-  __syncthreads();
-  if (q == 0 && n < a.n) {
-    float v = 0.0f;
-#pragma unroll
-    for (int y = 0; y < Q; ++y) v += red[y][x];
-    a.db[static_cast<int64_t>(g) * a.n + n] = v;
-  }
+__global__ __launch_bounds__(512) void linear_db_kernel(LinearArgs a, DbPlan p) {
+  __shared__ float red[kDbWords];
+  db_columns<Q>(a, p, blockIdx.x, blockIdx.y, red);
 }
 
 // ---------------------------------------------------------------------------
@@ -436,7 +401,7 @@ int64_t row_tiles(const LinearArgs& a, int bm) { return most_row_tiles(a, bm); }
 
 // Workgroups of linear_dz_kernel along the columns, and rows of a tile: 128, or
 // 32 where that leaves most of the chip empty (129 x 512, GELU: 13.7 us with
-// 128, DZ_US with 32).
+// 128, 5.5 with 32).
 int dz_cols(const LinearArgs& a) { return static_cast<int>(div_up(a.act == LIN_SWIGLU ? a.n / 2 : a.n, 256)); }
 int dz_rows(const LinearArgs& a) { return row_tiles(a, 128) * dz_cols(a) < 512 ? 32 : 128; }
 
@@ -591,22 +556,34 @@ hipError_t launch_tiles(const LinearArgs& a, const Plan& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-// dx and dw with 256 x 256 tiles in one launch: dx's tiles fill what dw's last
-// round leaves empty.  Measured against two launches: 64 groups of 2048 x
-// 1408, 24571 rows, 565 -> 514 us (fp32 dw), 456 -> 422 (BF16 dw); dense
-// 16384 x 2816 x 2048 and 4096^3, 1 to 2 % less.  (The tiles of the two spread
-// over each other took 546 instead of 516 us in the first case.)
+// db, dx and dw in one launch where both products have the same tiles, of 256 x
+// 256 or 64 x 64: dx's tiles fill what dw's last round leaves empty, and db's
+// few workgroups are beside them.  Measured against launches of their own: 64
+// groups of 2048 x 1408, 24571 rows, 565 -> 514 us (fp32 dw), 456 -> 422 (BF16
+// dw); dense 16384 x 2816 x 2048 and 4096^3, 1 to 2 % less.  (The tiles of the
+// two spread over each other took 546 instead of 516 us in the first case.)
+// 129 rows of 512 x 512 from 8 bits: 25 -> 17 us.
 bool both(const LinearArgs& a, const Plan& dx, const Plan& dw) {
-  return a.m && dx.shape == SHAPE_256 && dw.shape == SHAPE_256 && dx.workgroups + dw.workgroups + 16 <= INT32_MAX;
+  return a.m && dx.shape == dw.shape && dx.shape != SHAPE_128 &&
+         (dx.workgroups + dw.workgroups + div_up(a.n, 32) * a.groups + 16) * 512 <= kLaunchThreads;
 }
-hipError_t launch_both(const LinearArgs& a, const Plan& dx, const Plan& dw, hipStream_t s) {
+hipError_t launch_both(const LinearArgs& a, const Plan& dx, const Plan& dw, const DbPlan& db, hipStream_t s) {
   BothPlan p{};
   p.dx = dx.tiles;
   p.dw = dw_tiles(dw);
+  p.db = db;
+  p.db_eights = static_cast<int>(div_up(int64_t{db.cols} * db.groups, 8));
   p.dw_eights = static_cast<int>(div_up(dw.workgroups, 8));
-  hipLaunchKernelGGL(linear_both_kernel, dim3(static_cast<unsigned>(8 * p.dw_eights + dx.workgroups)), dim3(512), 0, s, a, p);
-  launch_join<MODE_DX, 256, 256>(a, dx, s);
-  launch_join<MODE_DW, 256, 256>(a, dw, s);
+  const dim3 grid(static_cast<unsigned>(8 * (p.db_eights + p.dw_eights) + dx.workgroups)), block(512);
+  if (dx.shape == SHAPE_256) {
+    hipLaunchKernelGGL(linear_both_kernel, grid, block, 0, s, a, p);
+    launch_join<MODE_DX, 256, 256>(a, dx, s);
+    launch_join<MODE_DW, 256, 256>(a, dw, s);
+  } else {
+    hipLaunchKernelGGL(linear_narrow_both_kernel, grid, block, 0, s, a, p);
+    launch_join<MODE_DX, 64, 64>(a, dx, s);
+    launch_join<MODE_DW, 64, 64>(a, dw, s);
+  }
   return hipGetLastError();
 }
 
@@ -726,19 +703,21 @@ hipError_t launch_linear_backward(const LinearArgs& args, hipStream_t s) {
     return e;
   }
   if (x8) a.x = x;
+  // db by few row tiles a group: few threads a column, or most of them only wait
+  // (64 groups of 2048 columns, 4 tiles each: 15 us with 16 threads, 5 with 2)
+  DbPlan db{};
   if (a.db) {
-    // few row tiles a group: few threads a column, or most of them only wait (64
-    // groups of 2048 columns, 4 tiles each: 15 us with 16 threads, 5 with 2)
-    if (row_tiles(a, rows) <= 16 * static_cast<int64_t>(a.groups))
-      hipLaunchKernelGGL((linear_db_kernel<2>), dim3(static_cast<unsigned>(div_up(a.n, 256)), static_cast<unsigned>(a.groups)),
-                         dim3(512), 0, s, a, sums, rows);
-    else
-      hipLaunchKernelGGL((linear_db_kernel<16>), dim3(static_cast<unsigned>(div_up(a.n, 32)), static_cast<unsigned>(a.groups)),
-                         dim3(512), 0, s, a, sums, rows);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    const int q = row_tiles(a, rows) <= 16 * static_cast<int64_t>(a.groups) ? 2 : 16;
+    db = {sums, rows, q, static_cast<int>(div_up(a.n, 512 / q)), a.groups};
   }
   const Plan pdx = plan_rows(a, MODE_DX), pdw = plan_dw(a);
-  if (a.dx && a.dw && both(a, pdx, pdw)) return launch_both(a, pdx, pdw, s);
+  if (a.dx && a.dw && both(a, pdx, pdw)) return launch_both(a, pdx, pdw, db, s);
+  if (a.db) {
+    const dim3 grid(static_cast<unsigned>(db.cols), static_cast<unsigned>(db.groups));
+    if (db.q == 2) hipLaunchKernelGGL((linear_db_kernel<2>), grid, dim3(512), 0, s, a, db);
+    else hipLaunchKernelGGL((linear_db_kernel<16>), grid, dim3(512), 0, s, a, db);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
   if (a.dx && a.m && (e = launch_tiles<MODE_DX>(a, pdx, s)) != hipSuccess) return e;
   if (a.dw && (e = launch_tiles<MODE_DW>(a, pdw, s)) != hipSuccess) return e;
   return e;

@@ -712,6 +712,64 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void linear_ring_kernel(LinearArgs
   else store_output<MODE>(a, acc, t.g, t.row0 + wp * (TM * 32), t.row_end, t.col0 + wq * 64, scratch, lane);
 }
 
+// The column sums of dz's row tiles (of `rows` rows), added to db: Q threads a
+// column, workgroups along the columns and the groups (0: none).
+struct DbPlan {
+  const float* sums;
+  int rows, q, cols, groups;
+};
+
+// db of columns [512 / Q block, + 512 / Q) of group g.
+constexpr int kDbWords = 2 * (256 + 1) > 16 * (32 + 1) ? 2 * (256 + 1) : 16 * (32 + 1);
+template <int Q>
+__device__ __forceinline__ void db_columns(const LinearArgs& a, const DbPlan& p, int block, int g, float* lds) {
+  constexpr int X = 512 / Q;
+  float (*const red)[X + 1] = reinterpret_cast<float (*)[X + 1]>(lds);
+  static_assert(Q * (X + 1) <= kDbWords, "scratch of the sums");
+  const float* const sums = p.sums;
+  const int rows = p.rows;
+  const int lane = threadIdx.x & 63, x = threadIdx.x % X, q = threadIdx.x / X;
+  // tiles of the groups before g, and of g
+  int64_t before = 0, mine = 0;
+  if (a.offsets) {
+    for (int i = lane; i <= g; i += 64) {
+      int64_t b, e;
+      group_rows(a, i, b, e);
+      const int64_t t = (e - b + rows - 1) / rows;
+      if (i < g) before += t;
+      else mine = t;
+    }
+    for (int d = 32; d; d >>= 1) {
+      before += __shfl_xor(before, d);
+      mine += __shfl_xor(mine, d);
+    }
+    mine = min(mine, most_row_tiles(a, rows) - before);       // (offsets that decrease: none that were not summed)
+  } else {
+    mine = most_row_tiles(a, rows);
+  }
+  const int n = block * X + x;
+  float s = 0.0f;
+  if (n < a.n) {
+#pragma unroll 4
+    for (int64_t t = q; t < mine; t += Q) s += sums[(before + t) * a.n + n];
+  }
+  red[q][x] = s;
+  __syncthreads();
+  if (q == 0 && n < a.n) {
+    float v = 0.0f;
+#pragma unroll
+    for (int y = 0; y < Q; ++y) v += red[y][x];
+    a.db[static_cast<int64_t>(g) * a.n + n] = v;
+  }
+}
+// The same by the workgroup's number in a launch of other work.
+__device__ __forceinline__ void db_workgroup(const LinearArgs& a, const DbPlan& p, int w, float* lds) {
+  const int g = w / p.cols, block = w - g * p.cols;
+  if (g >= p.groups) return;
+  if (p.q == 2) db_columns<2>(a, p, block, g, lds);
+  else db_columns<16>(a, p, block, g, lds);
+}
+
 // The 64 x 64 tile of small outputs (a router's product, some hundred rows):
 // what counts is that every compute unit has a workgroup and each of them many
 // bytes in flight.  Four pairs of waves share the tile's r, each with two
@@ -720,18 +778,20 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void linear_ring_kernel(LinearArgs
 // 2048 x 2048 15.0 -> 10.2 us, 1000 x 512 x 512 8.3 -> 6.1, 951 rows of 15
 // groups of 392 x 2144 27.0 -> 17.9; with more tiles than compute units 128 x
 // 128 wins (3311 x 288 x 1008, 260 tiles: 11.7 against 14.4).
+constexpr int kNarrowBytes = 4 * 64 * kR * 2;     // one operand, one stage of all pairs
 template <int MODE>
-__global__ __launch_bounds__(512, 2) void linear_narrow_kernel(LinearArgs a, TilePlan plan) {
+__device__ __forceinline__ void narrow_tile(const LinearArgs& a, const TilePlan& plan, int w, uint8_t* sP0, uint8_t* sP1,
+                                            uint8_t* sQ0, uint8_t* sQ1) {
   constexpr int G = 4, NW = 2;
   using TP = TileOperand<MODE != MODE_DW, 64, kR, NW>;
   using TQ = TileOperand<MODE == MODE_FORWARD, 64, kR, NW>;
-  __shared__ __attribute__((aligned(16))) uint8_t sP0[G * TP::BYTES], sP1[G * TP::BYTES], sQ0[G * TQ::BYTES], sQ1[G * TQ::BYTES];
+  static_assert(G * TP::BYTES == kNarrowBytes && G * TQ::BYTES == kNarrowBytes, "stages of the pairs");
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int grp = wave / NW, wp = wave % NW;
 
   LinearTile t;
-  if (!locate<MODE, 64, 64>(a, plan, blockIdx.x, lane, t)) return;
+  if (!locate<MODE, 64, 64>(a, plan, w, lane, t)) return;
   const int64_t wg = static_cast<int64_t>(t.g) * a.n * a.k;
   const int64_t steps = (t.r1 - t.r0 + kR - 1) / kR;
   const int64_t r0 = min(t.r1, t.r0 + steps * grp / G * kR), r1 = min(t.r1, t.r0 + steps * (grp + 1) / G * kR);
@@ -818,6 +878,14 @@ __global__ __launch_bounds__(512, 2) void linear_narrow_kernel(LinearArgs a, Til
   uint8_t* const scratch = sQ0 + wp * 4096;
   if (t.slot >= 0) store_part<64, 64>(partials<MODE>(a), acc, t.slot, wp * 32, 0, scratch, lane);
   else store_output<MODE>(a, acc, t.g, t.row0 + wp * 32, t.row_end, t.col0, scratch, lane);
+}
+#define MOEGG_NARROW_STAGES                                                                                        \
+  __shared__ __attribute__((aligned(16))) uint8_t sP0[kNarrowBytes], sP1[kNarrowBytes], sQ0[kNarrowBytes], sQ1[kNarrowBytes]
+
+template <int MODE>
+__global__ __launch_bounds__(512, 2) void linear_narrow_kernel(LinearArgs a, TilePlan plan) {
+  MOEGG_NARROW_STAGES;
+  narrow_tile<MODE>(a, plan, blockIdx.x, sP0, sP1, sQ0, sQ1);
 }
 
 // The 256 x 256 tile: 8 waves, 2 along p x 4 along q, each 128 x 64, on the
@@ -964,22 +1032,37 @@ __global__ __launch_bounds__(512, 1) void linear_pingpong_kernel(LinearArgs a, T
   pingpong_tile<MODE>(a, plan, blockIdx.x, sp, sq);
 }
 
-// The tiles of dw and then of dx in one launch.  dw's workgroups are counted in
-// eights (a workgroup's number modulo 8 stays its XCD).
+// db, the tiles of dw and then those of dx in one launch.  The workgroups of
+// each are counted in eights (a workgroup's number modulo 8 stays its XCD).
 struct BothPlan {
   TilePlan dx, dw;
-  int dw_eights;
+  DbPlan db;
+  int db_eights, dw_eights;
 };
+// Which part a workgroup has, and its number in it.
+__device__ __forceinline__ int both_part(const BothPlan& p, int& w) {
+  w = blockIdx.x;
+  if (w < 8 * p.db_eights) return 0;
+  w -= 8 * p.db_eights;
+  if (w < 8 * p.dw_eights) return w < p.dw.first + (p.dw.tiles - p.dw.first) * p.dw.parts ? 1 : 3;
+  w -= 8 * p.dw_eights;
+  return p.dx.tiles < 0 || w < p.dx.first + (p.dx.tiles - p.dx.first) * p.dx.parts ? 2 : 3;
+}
 __global__ __launch_bounds__(512, 1) void linear_both_kernel(LinearArgs a, BothPlan p) {
   MOEGG_RING_STAGES;
-  const int first_dx = 8 * p.dw_eights;
-  const bool dw = static_cast<int>(blockIdx.x) < first_dx;
-  const int w = blockIdx.x - (dw ? 0 : first_dx);
-  if (dw) {
-    if (w < p.dw.first + (p.dw.tiles - p.dw.first) * p.dw.parts) pingpong_tile<MODE_DW>(a, p.dw, w, sp, sq);
-  } else if (p.dx.tiles < 0 || w < p.dx.first + (p.dx.tiles - p.dx.first) * p.dx.parts) {
-    pingpong_tile<MODE_DX>(a, p.dx, w, sp, sq);
-  }
+  int w;
+  const int part = both_part(p, w);
+  if (part == 0) db_workgroup(a, p.db, w, reinterpret_cast<float*>(sP0));
+  else if (part == 1) pingpong_tile<MODE_DW>(a, p.dw, w, sp, sq);
+  else if (part == 2) pingpong_tile<MODE_DX>(a, p.dx, w, sp, sq);
+}
+__global__ __launch_bounds__(512, 2) void linear_narrow_both_kernel(LinearArgs a, BothPlan p) {
+  MOEGG_NARROW_STAGES;
+  int w;
+  const int part = both_part(p, w);
+  if (part == 0) db_workgroup(a, p.db, w, reinterpret_cast<float*>(sP0));
+  else if (part == 1) narrow_tile<MODE_DW>(a, p.dw, w, sP0, sP1, sQ0, sQ1);
+  else if (part == 2) narrow_tile<MODE_DX>(a, p.dx, w, sP0, sP1, sQ0, sQ1);
 }
 
 }  // namespace

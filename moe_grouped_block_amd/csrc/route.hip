@@ -230,8 +230,8 @@ __device__ __forceinline__ void take(float& b0, float& b1, float v) {
 // Scores are formed in fp32; where the last group in and the first one out are
 // nearer than the error of both, the wave's tokens form them in 64 bits.
 // Measured, 16381 tokens, 4 of 8 groups of 32 by their two best, sigmoid with
-// bias: 24.4 us with all groups through LDS and three workgroups to a compute
-// unit, GROUPED_US in registers; without groups 16.
+// bias: 24 to 28 us with all groups through LDS and three workgroups to a compute
+// unit, 19 to 22 in registers; without groups 16.
 template <typename R, int LPT, int EPL>
 __device__ __forceinline__ uint32_t closed_groups(const RouteArgs& a, GroupScratch<LPT, EPL>& lds, const float* x, const float* score,
                                                   bool sums, bool logits, float top, int64_t row, int lane, int slot) {
