@@ -778,6 +778,8 @@ __device__ __forceinline__ void db_workgroup(const LinearArgs& a, const DbPlan& 
 // 2048 x 2048 15.0 -> 10.2 us, 1000 x 512 x 512 8.3 -> 6.1, 951 rows of 15
 // groups of 392 x 2144 27.0 -> 17.9; with more tiles than compute units 128 x
 // 128 wins (3311 x 288 x 1008, 260 tiles: 11.7 against 14.4).
+// (Four stages of 32 r in a ring, as in linear_ring_kernel, do not help here: both
+// operands then come in 64-byte pieces, 193 x 2816 x 2048 10.0 -> 11.9 us.)
 constexpr int kNarrowBytes = 4 * 64 * kR * 2;     // one operand, one stage of all pairs
 template <int MODE>
 __device__ __forceinline__ void narrow_tile(const LinearArgs& a, const TilePlan& plan, int w, uint8_t* sP0, uint8_t* sP1,

@@ -201,17 +201,18 @@ constexpr int kSlots = kMaxTopK + kSpare;
 // places and a sum of up to 16 + 6 terms, below 50 2^-24.
 constexpr float kKeyP = 50.0f * 5.9604645e-8f, kKeySum = 2.4e-7f;
 
-// LDS of the choice of groups: a token's scores, then (in their place) its
-// groups' scores in 64 bits; its groups' scores and what they may be off by; the
-// last group in and the first one out.  Four workgroups fit a compute unit.
+// LDS of the choice of groups for a token (its lanes' own: nothing of it is
+// another wave's): its scores, then in their place its groups' scores in 64
+// bits; its groups' scores; the last group in and the first one out.  Four
+// workgroups fit a compute unit.
 template <int LPT, int EPL>
 struct GroupScratch {
   union {
-    float score[256 / LPT][LPT * (EPL + 1)];
-    double exact[256 / LPT][kMaxGroups];
+    float score[LPT * (EPL + 1)];
+    double exact[kMaxGroups];
   };
-  float group[256 / LPT][kMaxGroups];
-  float edge[256 / LPT][2][2];
+  float group[kMaxGroups];
+  float edge[4];
 };
 
 // The two largest of a set, one more value or another set's two taken in.
@@ -228,50 +229,56 @@ __device__ __forceinline__ void take(float& b0, float& b1, float v) {
 // lane's EPL scores and a word more, so that neither side of the exchange meets
 // a bank twice).  Then lane g counts the groups before its own.
 // Scores are formed in fp32; where the last group in and the first one out are
-// nearer than the error of both, the wave's tokens form them in 64 bits.
-// Measured, 16381 tokens, 4 of 8 groups of 32 by their two best, sigmoid with
-// bias: 24 to 28 us with all groups through LDS and three workgroups to a compute
-// unit, 19 to 22 in registers; without groups 16.
+// nearer than the error of both, the groups that may be on either side form
+// theirs again in 64 bits.  (It is rare, but among 16381 tokens there always are
+// such, and their waves are the last to end.)
+// Measured, 16381 tokens, top 8 of 4 of 8 groups of 32 by their two best,
+// sigmoid, without a bias (with one): 14.0 (18.3) us, where groups by their best
+// logit take 12.1 and no groups 9.5 (16.1); with 64 bits for all experts of a
+// wave in doubt 20.6 (22 to 24); with all groups through LDS besides, three
+// workgroups to a compute unit, (24 to 28).
 template <typename R, int LPT, int EPL>
 __device__ __forceinline__ uint32_t closed_groups(const RouteArgs& a, GroupScratch<LPT, EPL>& lds, const float* x, const float* score,
-                                                  bool sums, bool logits, float top, int64_t row, int lane, int slot) {
+                                                  bool sums, bool logits, float top, int64_t row, int lane) {
   constexpr int N = kMaxGroups / LPT;            // groups of a lane
   constexpr double kNone = -__builtin_inf();
   const int groups = a.groups, size = a.experts / groups;
   float mine[N], off[N];
+  float low0[N], low1[N], g0 = kNegInf, g1 = kNegInf;     // the groups' two largest: of lane g's, of the lane's own
   auto set = [&](int i, float b0, float b1) __attribute__((always_inline)) {
+    low0[i] = b0;
+    low1[i] = b1;
     const bool two = sums && b1 > kNegInf;
     mine[i] = two ? b0 + b1 : b0;
     off[i] = logits ? 0.0f : two ? 2.0f * kKeyP + kKeySum * (fabsf(b0) + fabsf(b1)) : kKeyP + kKeySum * fabsf(b0);
   };
   if (a.group_lanes) {
-    float b0 = kNegInf, b1 = kNegInf;
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) take(b0, b1, score[j]);
+    for (int j = 0; j < EPL; ++j) take(g0, g1, score[j]);
     steps<LPT>([&](auto c) {
       constexpr int S = decltype(c)::value;
       if ((1 << S) >= a.group_lanes) return;     // (the same for all lanes)
-      const float o0 = partner<S>(b0), o1 = partner<S>(b1);
-      b1 = fmaxf(fmaxf(b1, o1), fminf(b0, o0));
-      b0 = fmaxf(b0, o0);
+      const float o0 = partner<S>(g0), o1 = partner<S>(g1);
+      g1 = fmaxf(fmaxf(g1, o1), fminf(g0, o0));
+      g0 = fmaxf(g0, o0);
     });
-    set(0, b0, b1);
+    set(0, g0, g1);
     // by group, for lane g
     if (lane % a.group_lanes == 0) {
-      lds.group[slot][lane / a.group_lanes] = mine[0];
-      lds.score[slot][lane / a.group_lanes] = off[0];
+      lds.group[lane / a.group_lanes] = mine[0];
+      lds.score[lane / a.group_lanes] = off[0];
     }
     wave_sync();
 #pragma unroll
     for (int i = 0; i < N; ++i)
       if (i * LPT < groups) {
-        mine[i] = lane + i * LPT < groups ? lds.group[slot][lane + i * LPT] : kNegInf;
-        off[i] = lane + i * LPT < groups ? lds.score[slot][lane + i * LPT] : 0.0f;
+        mine[i] = lane + i * LPT < groups ? lds.group[lane + i * LPT] : kNegInf;
+        off[i] = lane + i * LPT < groups ? lds.score[lane + i * LPT] : 0.0f;
       }
     wave_sync();
   } else {
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) lds.score[slot][lane * (EPL + 1) + j] = score[j];
+    for (int j = 0; j < EPL; ++j) lds.score[lane * (EPL + 1) + j] = score[j];
     wave_sync();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -280,7 +287,7 @@ __device__ __forceinline__ uint32_t closed_groups(const RouteArgs& a, GroupScrat
       float b0 = kNegInf, b1 = kNegInf;
       if (g < groups) {
 #pragma unroll 4
-        for (int e = g * size; e < (g + 1) * size; ++e) take(b0, b1, lds.score[slot][e + e / EPL]);
+        for (int e = g * size; e < (g + 1) * size; ++e) take(b0, b1, lds.score[e + e / EPL]);
       }
       set(i, b0, b1);
     }
@@ -289,13 +296,13 @@ __device__ __forceinline__ uint32_t closed_groups(const RouteArgs& a, GroupScrat
   // (places behind the last group, up to a multiple of 4: -inf, never counted)
 #pragma unroll
   for (int i = 0; i < N; ++i)
-    if (i * LPT < groups) lds.group[slot][lane + i * LPT] = lane + i * LPT < groups ? mine[i] : kNegInf;
+    if (i * LPT < groups) lds.group[lane + i * LPT] = lane + i * LPT < groups ? mine[i] : kNegInf;
   wave_sync();
   auto rank_of = [&](float v, int g) __attribute__((always_inline)) {
     typedef float v4f __attribute__((ext_vector_type(4)));
     int rank = 0;
     for (int o = 0; o < groups; o += 4) {
-      const v4f q = *reinterpret_cast<const v4f*>(&lds.group[slot][o]);
+      const v4f q = *reinterpret_cast<const v4f*>(&lds.group[o]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) rank += q[e] > v || (q[e] == v && o + e < g);
     }
@@ -311,15 +318,18 @@ __device__ __forceinline__ uint32_t closed_groups(const RouteArgs& a, GroupScrat
     if (i * LPT >= groups) break;
     const int g = lane + i * LPT, rank = g < groups ? rank_of(mine[i], g) : kMaxGroups;
     add(i, rank < a.top_groups);
-    if (rank == a.top_groups - 1 || rank == a.top_groups) {
-      lds.edge[slot][rank == a.top_groups][0] = mine[i];
-      lds.edge[slot][rank == a.top_groups][1] = off[i];
-    }
+    if (rank == a.top_groups - 1 || rank == a.top_groups) lds.edge[rank == a.top_groups] = mine[i];
   }
   if (!logits) {
     wave_sync();
-    const float in = lds.edge[slot][0][0], out = lds.edge[slot][1][0];
-    if (__any(out > kNegInf && !(in - out > lds.edge[slot][0][1] + lds.edge[slot][1][1]))) {
+    float most = 0.0f;                           // what any of the token's groups may be off by
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i * LPT < groups) most = fmaxf(most, lane + i * LPT < groups ? off[i] : 0.0f);
+    most = 2.0f * lanes_max<LPT>(most);
+    const float in = lds.edge[0], out = lds.edge[1];
+    const bool doubt = out > kNegInf && !(in - out > most);
+    if (__any(doubt)) {
       double total = 1.0;
       if (a.softmax) {
         total = 0.0;
@@ -327,18 +337,75 @@ __device__ __forceinline__ uint32_t closed_groups(const RouteArgs& a, GroupScrat
         for (int j = 0; j < EPL; ++j) total += x[j] == x[j] ? exp(static_cast<double>(x[j]) - top) : 0.0;
         total = lanes_sum<LPT>(total);
       }
-      for (int g = lane; g < groups; g += LPT) {
+      auto exact = [&](double l, int e) __attribute__((always_inline)) {
+        const double q = (a.softmax ? exp(l - top) / total : 1.0 / (1.0 + exp(-l))) + (a.bias ? a.bias[e] : 0.0f);
+        return l > kNone && q > kNone ? q : kNone;                     // NaN: false
+      };
+      auto take2 = [](double& b0, double& b1, double v) __attribute__((always_inline)) {
+        b1 = fmax(b1, fmin(b0, v));
+        b0 = fmax(b0, v);
+      };
+      // Groups that are in or out whatever the errors are count as infinities;
+      // of the others the experts that may be among the two largest are formed again.
+      auto sure = [&](float v) __attribute__((always_inline)) {
+        return v - out > most ? __builtin_inf() : in - v > most ? kNone : 0.0;
+      };
+      auto near = [&](float v, float b0, float b1) __attribute__((always_inline)) {
+        const float least = sums && b1 > kNegInf ? b1 : b0;
+        return v > kNegInf && !(least - v > 2.0f * (kKeyP + kKeySum * fabsf(least)));
+      };
+      double again[N];
+      if (a.group_lanes) {
+        const float own = lds.group[lane / a.group_lanes & (kMaxGroups - 1)];
+        const bool hot = doubt && lane / a.group_lanes < groups && sure(own) == 0.0;
         double b0 = kNone, b1 = kNone;
-        for (int e = g * size; e < (g + 1) * size; ++e) {
-          const double l = R::one(a.logits, row, a.experts, e);
-          const double q = (a.softmax ? exp(l - top) / total : 1.0 / (1.0 + exp(-l))) + (a.bias ? a.bias[e] : 0.0f);
-          const double v = l > kNone && q > kNone ? q : kNone;         // NaN: false
-          b1 = fmax(b1, fmin(b0, v));
-          b0 = fmax(b0, v);
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+          const bool want = hot && near(score[j], g0, g1);
+          if (!__any(want)) continue;
+          const double v = exact(x[j], min(lane * EPL + j, a.experts - 1));
+          if (want) take2(b0, b1, v);
         }
-        lds.exact[slot][g] = sums && b1 > kNone ? b0 + b1 : b0;
+        steps<LPT>([&](auto c) {
+          constexpr int S = decltype(c)::value;
+          if ((1 << S) >= a.group_lanes) return;
+          const double o0 = partner<S>(b0), o1 = partner<S>(b1);
+          b1 = fmax(fmax(b1, o1), fmin(b0, o0));
+          b0 = fmax(b0, o0);
+        });
+        if (lane % a.group_lanes == 0 && lane / a.group_lanes < groups)
+          lds.exact[lane / a.group_lanes] = hot ? (sums && b1 > kNone ? b0 + b1 : b0) : sure(own);
+        wave_sync();
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (i * LPT < groups) again[i] = lane + i * LPT < groups ? lds.exact[lane + i * LPT] : kNone;
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          if (i * LPT >= groups) break;
+          const int g = lane + i * LPT;
+          again[i] = g < groups ? sure(mine[i]) : kNone;
+          int e = doubt && again[i] == 0.0 ? g * size : a.experts;
+          const int end = e + size;
+          double b0 = kNone, b1 = kNone;
+          while (true) {                          // (the lanes' next experts are found first, then formed together)
+            while (e < min(end, a.experts) && !near(lds.score[e + e / EPL], low0[i], low1[i])) ++e;
+            const bool some = e < min(end, a.experts);
+            if (!__any(some)) break;
+            if (some) {
+              take2(b0, b1, exact(R::one(a.logits, row, a.experts, e), e));
+              ++e;
+            }
+          }
+          if (again[i] == 0.0) again[i] = sums && b1 > kNone ? b0 + b1 : b0;
+        }
       }
       wave_sync();
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i * LPT < groups && lane + i * LPT < groups) lds.exact[lane + i * LPT] = again[i];
+      wave_sync();
+      const uint64_t before = mask;
       mask = 0;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
@@ -346,12 +413,12 @@ __device__ __forceinline__ uint32_t closed_groups(const RouteArgs& a, GroupScrat
         const int g = lane + i * LPT;
         int rank = kMaxGroups;
         if (g < groups) {
-          const double v = lds.exact[slot][g];
           rank = 0;
-          for (int o = 0; o < groups; ++o) rank += lds.exact[slot][o] > v || (lds.exact[slot][o] == v && o < g);
+          for (int o = 0; o < groups; ++o) rank += lds.exact[o] > again[i] || (lds.exact[o] == again[i] && o < g);
         }
         add(i, rank < a.top_groups);
       }
+      if (!doubt) mask = before;
     }
   }
   if (a.group_lanes) return mask >> (lane / a.group_lanes & 63) & 1 ? 0u : ~0u;
@@ -400,7 +467,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
 #pragma unroll
     for (int j = 0; j < EPL; ++j) key[j] = x[j] > kNegInf ? x[j] : kNegInf;
     if constexpr (GROUPS) {
-      __shared__ GroupScratch<LPT, EPL> scratch;
+      __shared__ GroupScratch<LPT, EPL> scratch[TPB];
       float score[EPL];
       float valid = total;
       if (a.softmax && __any(!(total == total))) {     // (a NaN leaves the choice among the others)
@@ -415,7 +482,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
         const float p = a.softmax ? fast_exp(key[j] - top) * rt : __builtin_amdgcn_rcpf(1.0f + fast_exp(-key[j]));
         score[j] = a.group_sums && key[j] > kNegInf ? p : key[j];
       }
-      closed = closed_groups<R>(a, scratch, x, score, a.group_sums, !a.group_sums, top, row, lane, slot);
+      closed = closed_groups<R>(a, scratch[slot], x, score, a.group_sums, !a.group_sums, top, row, lane);
 #pragma unroll
       for (int j = 0; j < EPL; ++j) key[j] = closed >> j & 1 ? kNegInf : key[j];
     }
@@ -446,8 +513,8 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
       }
     }
     if constexpr (GROUPS) {
-      __shared__ GroupScratch<LPT, EPL> scratch;
-      closed = closed_groups<R>(a, scratch, x, key, a.group_sums, false, top, row, lane, slot);
+      __shared__ GroupScratch<LPT, EPL> scratch[TPB];
+      closed = closed_groups<R>(a, scratch[slot], x, key, a.group_sums, false, top, row, lane);
 #pragma unroll
       for (int j = 0; j < EPL; ++j) key[j] = closed >> j & 1 ? kNegInf : key[j];
     }
