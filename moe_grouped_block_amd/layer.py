@@ -412,14 +412,13 @@ def unsort(values, plan: SortPlan, *, stream=None):
 
 _STREAMS = (torch.bfloat16, torch.float32)
 _TYPE_CODES = {torch.bfloat16: 3, torch.float32: 5}
+_MX = {"e4m3": 1, "e2m1x2": 2, "e5m2": 4}
 
 
 def _mx_kind(dtype, what: str):
     """Name and code of an MX type."""
     dtype = _dtype_name(dtype)
-    if dtype not in ("e4m3", "e5m2", "e2m1x2"):
-        raise ValueError(f"{what}={dtype!r}: one of e4m3, e5m2, e2m1x2 expected")
-    return dtype, mg.DTYPES[dtype]
+    return dtype, _code(_MX, dtype, what)
 
 
 def rms_norm(x, weight, *, residual=None, h=None, eps: float = 1e-6, dtype="bf16", copy=None,
@@ -434,45 +433,46 @@ def rms_norm(x, weight, *, residual=None, h=None, eps: float = 1e-6, dtype="bf16
     the residual itself, or a new tensor.  Returns y, or a tuple of y, the
     copy and h as far as they were asked for."""
     dev = _lead(x, "x", _STREAMS, 2)
-    rows, width = x.shape
+    shape = x.shape
+    rows, width = shape
     _fits(width)
     wp = _want(weight, "weight", torch.float32, (width,), dev)
-    kind = x.dtype
-    rp = hp = None
+    kind, layout = x.dtype, _code(mg.SF_LAYOUTS, sf_layout, "sf_layout")
+    code = stream_code = _TYPE_CODES[kind]
+    rp = hp = yp = cp = sp = None
     if residual is not None:
-        if _lead(residual, "residual", _STREAMS, 2) != dev:
-            _want(residual, "residual", residual.dtype, (rows, width), dev)
+        if not isinstance(residual, torch.Tensor) or residual.dtype not in _STREAMS:
+            _refuse(residual, "residual", _STREAMS, shape, dev)
         kind = residual.dtype
-        rp = _want(residual, "residual", kind, (rows, width), dev)
+        stream_code = _TYPE_CODES[kind]
+        rp = _want(residual, "residual", kind, shape, dev)
+        hp = None if h is None else _want(h, "h", kind, shape, dev)
     elif h is not None:
         raise ValueError("h: the sum with a residual, and none was given")
-    name, mx, layout = _row_kind(dtype, sf_layout)
-    bf16 = name == "bf16"
-    if bf16 and copy is not None:
-        name, mx = _mx_kind(copy, "copy")
+    name, mx = _dtype_name(dtype), 0
+    if name != "bf16":
+        if copy is not None:
+            raise ValueError("copy: for a bf16 y")
+        name, mx = _mx_kind(name, "dtype")
     elif copy is not None:
-        raise ValueError("copy: for a bf16 y")
-    elif bf16:
-        name, mx = None, 0
-    p = mg.moegg_norm_problem(rows, width, _TYPE_CODES[x.dtype], _TYPE_CODES[kind], mx, layout, eps)
+        name, mx = _mx_kind(copy, "copy")
+    p = mg.moegg_norm_problem(rows, width, code, stream_code, mx, layout, eps)
     s, guard = _on(dev, stream)
     try:
         out = []
-        y = codes = sf = None
-        if bf16:
-            y = x.new_empty((rows, width), dtype=torch.bfloat16)
+        if copy is not None or not mx:
+            y = torch.empty_like(x) if x.dtype is torch.bfloat16 else x.new_empty(shape, dtype=torch.bfloat16)
+            yp = y.data_ptr()
             out.append(y)
-        if name is not None:
+        if mx:
             codes, cp, sf, sp = _row_outputs(None, x, rows, width, name, sf_layout, dev)
             out.append((codes, sf))
-        else:
-            cp = sp = None
         if residual is not None:
-            h = residual.new_empty((rows, width)) if h is None else h
-            hp = _want(h, "h", kind, (rows, width), dev)
+            if hp is None:
+                h = torch.empty_like(residual)
+                hp = h.data_ptr()
             out.append(h)
-        a = mg.moegg_norm_args(x.data_ptr(), rp, wp, hp, None if y is None else y.data_ptr(), cp, sp)
-        _done(mg._load().moegg_rms_norm(p, a, s))
+        _done(mg._load().moegg_rms_norm(p, mg.moegg_norm_args(x.data_ptr(), rp, wp, hp, yp, cp, sp), s))
     finally:
         if guard is not None:
             guard.close()
@@ -500,11 +500,17 @@ def rms_norm_backward(dy, h, weight, *, dh=None, eps: float = 1e-6, need=("dx", 
     size = lib.moegg_rms_norm_backward_workspace(p) if "dw" in need else 0     # -1: an invalid problem, which the call refuses
     s, guard = _on(dev, stream)
     try:
-        dx = torch.empty_like(h) if "dx" in need else None
-        dw = weight.new_empty((width,)) if "dw" in need else None
-        ws = h.new_empty(size, dtype=torch.uint8) if size > 0 else None
-        a = mg.moegg_norm_args(None, None, wp, h.data_ptr(), None, None, None, dp, gp, None if dx is None else dx.data_ptr(),
-                               None if dw is None else dw.data_ptr(), None if ws is None else ws.data_ptr(), size)
+        dx = dw = dxp = dwp = wsp = None
+        if "dx" in need:
+            dx = torch.empty_like(h)
+            dxp = dx.data_ptr()
+        if "dw" in need:
+            dw = torch.empty_like(weight)
+            dwp = dw.data_ptr()
+        if size > 0:
+            ws = h.new_empty(size, dtype=torch.uint8)
+            wsp = ws.data_ptr()
+        a = mg.moegg_norm_args(None, None, wp, h.data_ptr(), None, None, None, dp, gp, dxp, dwp, wsp, size)
         _done(lib.moegg_rms_norm_backward(p, a, s))
     finally:
         if guard is not None:
@@ -515,6 +521,7 @@ def rms_norm_backward(dy, h, weight, *, dh=None, eps: float = 1e-6, need=("dx", 
 # ---- rows kept in 8 bits -------------------------------------------------------------
 
 _KEPT = {"e4m3": 1, "e5m2": 4}
+_KEPT_OR_NOT = {"bf16": 3, **_KEPT}
 
 
 def _pair(t, name: str, rows: int, width: int, sf_layout: str, dev: int):
@@ -651,9 +658,8 @@ def linear_backward(dy, x, w, *, c=None, act: str = "none", offsets=None, need=(
     x8, c8 = x_dtype != "bf16", c is not None and c_dtype != "bf16"
     keep = None
     if x8 or c8:
-        codes = {"bf16": 3, **_KEPT}
-        keep = mg.moegg_linear_saved(_code(codes, x_dtype, "x_dtype"), _code(mg.SF_LAYOUTS, sf_layout, "sf_layout"),
-                                     _code(codes, c_dtype if c8 else "bf16", "c_dtype"))
+        keep = mg.moegg_linear_saved(_code(_KEPT_OR_NOT, x_dtype, "x_dtype"), _code(mg.SF_LAYOUTS, sf_layout, "sf_layout"),
+                                     _code(_KEPT_OR_NOT, c_dtype, "c_dtype") if c8 else 3)
     if x8 and (not isinstance(x, (tuple, list)) or len(x) != 2):
         raise TypeError("x: a pair (codes, scales) expected")
     dev, p, lead, xp, wp, op = _linear_problem(x[0] if x8 else x, w, act, dw_dtype, offsets,
@@ -675,12 +681,19 @@ def linear_backward(dy, x, w, *, c=None, act: str = "none", offsets=None, need=(
         else lib.moegg_linear_saved_backward_workspace(p, keep, want)
     s, guard = _on(dev, stream)
     try:
-        ws = w.new_empty(size, dtype=torch.uint8) if size > 0 else None
-        dx = w.new_empty((m, k)) if "dx" in need else None
-        dw = w.new_empty((*lead, n, k), dtype=torch.float32 if dw_dtype == "f32" else torch.bfloat16) \
-            if "dw" in need else None
-        db = w.new_empty((*lead, n), dtype=torch.float32) if "db" in need else None
-        dxp, dwp, dbp, wsp = (None if t is None else t.data_ptr() for t in (dx, dw, db, ws))
+        dx = dw = db = dxp = dwp = dbp = wsp = None
+        if size > 0:
+            ws = w.new_empty(size, dtype=torch.uint8)
+            wsp = ws.data_ptr()
+        if want & 1:
+            dx = w.new_empty((m, k)) if x8 else torch.empty_like(x)
+            dxp = dx.data_ptr()
+        if want & 2:
+            dw = torch.empty_like(w, dtype=torch.float32) if dw_dtype == "f32" else torch.empty_like(w)
+            dwp = dw.data_ptr()
+        if want & 4:
+            db = w.new_empty((*lead, n), dtype=torch.float32)
+            dbp = db.data_ptr()
         a = mg.moegg_linear_args(xp, wp, None, None, op, None, cp, dp, dxp, dwp, dbp, wsp, size)
         _done(lib.moegg_linear_backward(p, a, s) if keep is None else lib.moegg_linear_saved_backward(p, a, keep, s))
     finally:
