@@ -616,8 +616,8 @@ def linear(x, w, *, bias=None, act: str = "none", residual=None, offsets=None, s
     rp = None if residual is None else _want(residual, "residual", torch.bfloat16, shape, dev)
     lib = mg._load()
     keep = None
-    if save_c is not False and save_c is not True:
-        keep = mg.moegg_linear_saved(3, 0, _code(_KEPT, _dtype_name(save_c), "save_c"))
+    if isinstance(save_c, str):
+        keep = mg.moegg_linear_saved(3, 0, _code(_KEPT, save_c, "save_c"))
     # (-1: an invalid problem, which the call refuses)
     need = lib.moegg_linear_workspace(p) if keep is None else lib.moegg_linear_saving_workspace(p, keep)
     s, guard = _on(dev, stream)
