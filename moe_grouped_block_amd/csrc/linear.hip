@@ -536,6 +536,18 @@ hipError_t launch_tiles(const LinearArgs& a, const Plan& p, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(p.workgroups));
   switch (p.shape) {
     case SHAPE_256:
+      if constexpr (MODE == MODE_DW) {
+        if (a.x8.kind == ROW_E4M3) {
+          hipLaunchKernelGGL((linear_pingpong_kernel<MODE, ROW_E4M3>), grid, dim3(512), 0, s, a, t);
+          launch_join<MODE, 256, 256>(a, p, s);
+          break;
+        }
+        if (a.x8.kind == ROW_E5M2) {
+          hipLaunchKernelGGL((linear_pingpong_kernel<MODE, ROW_E5M2>), grid, dim3(512), 0, s, a, t);
+          launch_join<MODE, 256, 256>(a, p, s);
+          break;
+        }
+      }
       hipLaunchKernelGGL((linear_pingpong_kernel<MODE>), grid, dim3(512), 0, s, a, t);
       launch_join<MODE, 256, 256>(a, p, s);
       break;
@@ -576,7 +588,11 @@ hipError_t launch_both(const LinearArgs& a, const Plan& dx, const Plan& dw, cons
   p.dw_eights = static_cast<int>(div_up(dw.workgroups, 8));
   const dim3 grid(static_cast<unsigned>(8 * (p.db_eights + p.dw_eights) + dx.workgroups)), block(512);
   if (dx.shape == SHAPE_256) {
-    hipLaunchKernelGGL(linear_both_kernel, grid, block, 0, s, a, p);
+    switch (a.x8.kind) {
+      case ROW_E4M3: hipLaunchKernelGGL((linear_both_kernel<ROW_E4M3>), grid, block, 0, s, a, p); break;
+      case ROW_E5M2: hipLaunchKernelGGL((linear_both_kernel<ROW_E5M2>), grid, block, 0, s, a, p); break;
+      default: hipLaunchKernelGGL((linear_both_kernel<ROW_BF16>), grid, block, 0, s, a, p); break;
+    }
     launch_join<MODE_DX, 256, 256>(a, dx, s);
     launch_join<MODE_DW, 256, 256>(a, dw, s);
   } else {
@@ -586,6 +602,12 @@ hipError_t launch_both(const LinearArgs& a, const Plan& dx, const Plan& dw, cons
   }
   return hipGetLastError();
 }
+
+// Whether an x in 8 bits is brought to BF16 in the workspace: the 256 x 256 tile
+// of dw reads the codes itself (64 groups of 1408 x 2048, 24571 rows: 454 -> 434
+// to 440 us, 16384 x 2816 x 2048 378 -> 376, and no copy of x in memory); the
+// others are fed by direct loads alone.
+bool x_by_workspace(const LinearArgs& a) { return a.x8.kind != ROW_BF16 && plan_dw(a).shape != SHAPE_256; }
 
 // Workspace of the backward: dz, the column sums of the row tiles, the parts
 // of dx and of dw, and x in BF16 where it is kept in 8 bits.
@@ -604,7 +626,7 @@ BackwardWorkspace backward_workspace(const LinearArgs& a, bool dx, bool dw, bool
   w.sums = take(db ? row_tiles(a, dz_rows(a)) * a.n * 4 : 0);
   w.dx = take(dx && a.m ? plan_rows(a, MODE_DX).partial_bytes : 0);
   w.dw = take(dw ? plan_dw(a).partial_bytes : 0);
-  w.x = take(dw && a.x8.kind != ROW_BF16 ? a.m * a.k * 2 : 0);
+  w.x = take(dw && x_by_workspace(a) ? a.m * a.k * 2 : 0);
   w.total = at;
   return w;
 }
@@ -679,7 +701,7 @@ hipError_t launch_linear_backward(const LinearArgs& args, hipStream_t s) {
   const BackwardWorkspace w = backward_workspace(a, a.dx, a.dw, a.db);
   uint8_t* const ws = static_cast<uint8_t*>(a.workspace);
   const bool make_dz = a.act != LIN_NONE && (a.dx || a.dw) && a.m;
-  const bool x8 = a.dw && a.x8.kind != ROW_BF16;
+  const bool x8 = a.dw && x_by_workspace(a);
   uint16_t* const dz = make_dz ? reinterpret_cast<uint16_t*>(ws + w.dz) : nullptr;
   float* const sums = a.db ? reinterpret_cast<float*>(ws + w.sums) : nullptr;
   uint16_t* const x = x8 ? reinterpret_cast<uint16_t*>(ws + w.x) : nullptr;
@@ -702,7 +724,10 @@ hipError_t launch_linear_backward(const LinearArgs& args, hipStream_t s) {
   } else if (x8 && a.m && (e = launch_dequantise(a.x8, x, false, a.m, a.k, s)) != hipSuccess) {
     return e;
   }
-  if (x8) a.x = x;
+  if (x8) {
+    a.x = x;
+    a.x8.kind = ROW_BF16;
+  }
   // db by few row tiles a group: few threads a column, or most of them only wait
   // (64 groups of 2048 columns, 4 tiles each: 15 us with 16 threads, 5 with 2)
   DbPlan db{};

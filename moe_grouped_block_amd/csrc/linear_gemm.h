@@ -890,6 +890,47 @@ __global__ __launch_bounds__(512, 2) void linear_narrow_kernel(LinearArgs a, Til
   narrow_tile<MODE>(a, plan, blockIdx.x, sP0, sP1, sQ0, sQ1);
 }
 
+// x in 8 bits as the Q operand of dw's 256 x 256 tile: a thread loads 16 codes of
+// a row (a stage's 32 rows of 256 columns are 512 threads' worth) with their
+// scale byte into registers, two stages in flight, and writes them as BF16 into
+// the image that the transposing reads expect.
+template <int KIND>
+struct SavedTile {
+  const uint8_t *codes, *scales;       // the next stage's, per lane
+  int64_t codes_step, scales_step;
+  int line;                            // of the stage
+  uint32_t at;                         // where the lane's 32 bytes go
+  v4u code[2];
+  uint32_t byte[2];
+  __device__ __forceinline__ void init(const LinearArgs& a, int col0, int64_t r0) {
+    line = threadIdx.x >> 4;
+    const int c = threadIdx.x & 15, col = min(col0 + 16 * c, a.k - 16);
+    codes = a.x8.codes + (r0 + line) * a.k + col;
+    scales = a.x8.scales + scale_at(a.x8, a.m, a.k, r0 + line, col >> 5);
+    codes_step = int64_t{kRingR} * a.k;
+    scales_step = a.x8.kplanes ? kRingR * 4 : a.k;
+    at = line * 512 + ((2 * c) ^ line_swizzle<32>(line)) * 16;
+  }
+  // The next stage into set `i`; `left`: of its rows exist (ANY), the others are zeros.
+  template <bool ANY>
+  __device__ __forceinline__ void load(int i, int left) {
+    const uint8_t* const zeros = reinterpret_cast<const uint8_t*>(kZeros);
+    const bool there = !ANY || line < left;
+    code[i] = *reinterpret_cast<const v4u*>(there ? codes : zeros);
+    byte[i] = *(there ? scales : zeros);
+    codes += codes_step;
+    scales += scales_step;
+  }
+  // Half h of set `i` to the image.  (The byte is looked at here and no earlier:
+  // the compiler would do it where it was loaded, and wait for it there.)
+  __device__ __forceinline__ void store(int i, int h, uint8_t* lds) {
+    asm volatile("" : "+v"(byte[i]));
+    const float f = mx_scale_value(byte[i]);
+    const v2u lo = mx_four_bf16<KIND>(code[i][2 * h], f), hi = mx_four_bf16<KIND>(code[i][2 * h + 1], f);
+    *reinterpret_cast<v4u*>(lds + at + 16 * h) = v4u{lo.x, lo.y, hi.x, hi.y};
+  }
+};
+
 // The 256 x 256 tile: 8 waves, 2 along p x 4 along q, each 128 x 64, on the
 // ping-pong schedule of the grouped product.  A step of 32 r is two clusters:
 // M reads the step's 12 fragments from LDS, C runs its 16 MFMAs.  The two
@@ -899,8 +940,11 @@ __global__ __launch_bounds__(512, 2) void linear_narrow_kernel(LinearArgs a, Til
 // read by then, and is waited for at the end of M(s + 2), four clusters later.
 // Steps past the last read zeros, so the steps go in fours with one exit and
 // every wave has the same loads in flight.
+// With dw's x in 8 bits (XK) the Q operand comes by way of registers: what was
+// loaded during C(s - 2) is written for stage s + 2 during C(s), between its
+// MFMAs, and the registers take stage s + 4; both groups read it from M(s + 2) on.
 constexpr int kRingBytes = 256 * kRingR * 2;      // one operand, one stage
-template <int MODE>
+template <int MODE, int XK = ROW_BF16>
 __device__ __forceinline__ void pingpong_tile(const LinearArgs& a, const TilePlan& plan, int w, uint8_t* const (&sp)[4],
                                               uint8_t* const (&sq)[4]) {
   constexpr int R = kRingR;
@@ -919,7 +963,11 @@ __device__ __forceinline__ void pingpong_tile(const LinearArgs& a, const TilePla
   TQ q;
   p.init(MODE == MODE_FORWARD ? a.x : a.dz, MODE == MODE_FORWARD ? a.k : a.n, t.row0, MODE == MODE_DW ? a.n : t.row_end, t.r0,
          wave, lane);
-  q.init(MODE == MODE_DW ? a.x : a.w + wg, a.k, t.col0, MODE == MODE_FORWARD ? a.n : a.k, t.r0, wave, lane);
+  constexpr bool X8 = XK != ROW_BF16;
+  static_assert(!X8 || MODE == MODE_DW, "x in 8 bits is an operand of dw");
+  SavedTile<X8 ? XK : ROW_E4M3> q8;
+  if constexpr (X8) q8.init(a, t.col0, t.r0);
+  else q.init(MODE == MODE_DW ? a.x : a.w + wg, a.k, t.col0, MODE == MODE_FORWARD ? a.n : a.k, t.r0, wave, lane);
   typename TP::template Frags<4> ap;
   typename TQ::template Frags<2> aq;
   ap.init(wp * 128, lane);
@@ -945,7 +993,7 @@ __device__ __forceinline__ void pingpong_tile(const LinearArgs& a, const TilePla
       if constexpr (decltype(any)::value) p.load_tail(d.p, wave, lane, j, span - s * R);
       else p.load(d.p, wave, j);
       if (j == TP::NI - 1) p.base += p.advance;
-    } else {
+    } else if constexpr (!X8) {
       if constexpr (decltype(any)::value) q.load_tail(d.q, wave, lane, j - TP::NI, span - s * R);
       else q.load(d.q, wave, j - TP::NI);
       if (j == N - 1) q.base += q.advance;
@@ -956,7 +1004,8 @@ __device__ __forceinline__ void pingpong_tile(const LinearArgs& a, const TilePla
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
   };
-  auto step = [&](auto any, int s, const Stage& now, const Stage& next3) __attribute__((always_inline)) {
+  auto step = [&](auto any, int s, const Stage& now, const Stage& next2, const Stage& next3, auto set)
+      __attribute__((always_inline)) {
     v4u fq[2][2], fp[4][2];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
@@ -985,12 +1034,25 @@ __device__ __forceinline__ void pingpong_tile(const LinearArgs& a, const TilePla
                                                               __builtin_bit_cast(v8bf, fp[i][k]), acc[i][j], 0, 0, 0);
           const int m = k * 8 + i * 2 + j;
           if (m % 4 == 0) issue(any, s + 3, next3, m / 4);
+          if constexpr (X8) {
+            if (m == 1 || m == 5) q8.store(set, m / 4, next2.q);
+            if (m == 9) q8.template load<decltype(any)::value>(set, span - (s + 4) * R);
+          }
         }
+    // a few of the conversions behind every MFMA, which hides them
+    if constexpr (X8) {
+#pragma unroll
+      for (int m = 0; m < 16; ++m) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);       // MFMA
+        __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);       // VALU
+      }
+    }
     // the MFMAs stay in their cluster
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) asm volatile("" : "+v"(acc[i][j]));
+    if constexpr (X8) __builtin_amdgcn_s_waitcnt(0xC07F);       // stage s + 2 written
     sync();
   };
   if (span > 0) {
@@ -1000,18 +1062,32 @@ __device__ __forceinline__ void pingpong_tile(const LinearArgs& a, const TilePla
     for (int s = 0; s < 3; ++s)
 #pragma unroll
       for (int j = 0; j < N; ++j) issue(any, s, st[s], j);
-    wait_vmcnt<2 * N>();
+    if constexpr (X8) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) q8.template load<true>(s, span - s * R);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        q8.store(s, 0, st[s].q);
+        q8.store(s, 1, st[s].q);
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s) q8.template load<true>(s, span - (s + 2) * R);
+      __builtin_amdgcn_s_waitcnt(0xC07F);
+    }
+    wait_vmcnt<X8 ? 4 : 2 * N>();
     sync();
     if (wp) sync();
     int s = 0;
-    for (; s + 6 < full; s += 4) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) step(plain, s + i, st[i], st[(i + 3) & 3]);
-    }
-    for (; s * R < span; s += 4) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) step(any, s + i, st[i], st[(i + 3) & 3]);
-    }
+    const std::integral_constant<int, 0> set0{};
+    const std::integral_constant<int, 1> set1{};
+    auto four = [&](auto any, int s) __attribute__((always_inline)) {
+      step(any, s, st[0], st[2], st[3], set0);
+      step(any, s + 1, st[1], st[3], st[0], set1);
+      step(any, s + 2, st[2], st[0], st[1], set0);
+      step(any, s + 3, st[3], st[1], st[2], set1);
+    };
+    for (; s + (X8 ? 7 : 6) < full; s += 4) four(plain, s);
+    for (; s * R < span; s += 4) four(any, s);
     wait_vmcnt<0>();
     if (!wp) sync();
     sync();
@@ -1028,10 +1104,10 @@ __device__ __forceinline__ void pingpong_tile(const LinearArgs& a, const TilePla
   uint8_t* const sp[4] = {sP0, sP1, sP2, sP3};                                                                \
   uint8_t* const sq[4] = {sQ0, sQ1, sQ2, sQ3}
 
-template <int MODE>
+template <int MODE, int XK = ROW_BF16>
 __global__ __launch_bounds__(512, 1) void linear_pingpong_kernel(LinearArgs a, TilePlan plan) {
   MOEGG_RING_STAGES;
-  pingpong_tile<MODE>(a, plan, blockIdx.x, sp, sq);
+  pingpong_tile<MODE, XK>(a, plan, blockIdx.x, sp, sq);
 }
 
 // db, the tiles of dw and then those of dx in one launch.  The workgroups of
@@ -1050,12 +1126,13 @@ __device__ __forceinline__ int both_part(const BothPlan& p, int& w) {
   w -= 8 * p.dw_eights;
   return p.dx.tiles < 0 || w < p.dx.first + (p.dx.tiles - p.dx.first) * p.dx.parts ? 2 : 3;
 }
+template <int XK>
 __global__ __launch_bounds__(512, 1) void linear_both_kernel(LinearArgs a, BothPlan p) {
   MOEGG_RING_STAGES;
   int w;
   const int part = both_part(p, w);
   if (part == 0) db_workgroup(a, p.db, w, reinterpret_cast<float*>(sP0));
-  else if (part == 1) pingpong_tile<MODE_DW>(a, p.dw, w, sp, sq);
+  else if (part == 1) pingpong_tile<MODE_DW, XK>(a, p.dw, w, sp, sq);
   else if (part == 2) pingpong_tile<MODE_DX>(a, p.dx, w, sp, sq);
 }
 __global__ __launch_bounds__(512, 2) void linear_narrow_both_kernel(LinearArgs a, BothPlan p) {

@@ -191,6 +191,18 @@ __device__ __forceinline__ void mx_four(uint32_t codes, float f, float* v) {
   v[3] = b.y * f;
 }
 
+// Four codes -> what they stand for in BF16, rounded to nearest even (the
+// conversion unit multiplies by the power of two; a NaN scale gives NaN).
+template <int KIND>
+__device__ __forceinline__ v2u mx_four_bf16(uint32_t codes, float f) {
+  if constexpr (KIND == ROW_E4M3)
+    return v2u{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, f, false)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, f, true))};
+  else
+    return v2u{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(codes, f, false)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(codes, f, true))};
+}
+
 // Elements of a workgroup of 4 waves that brings rows to 8 bits or back.
 constexpr int kSavedChunk = 4096;
 
@@ -206,25 +218,21 @@ __device__ __forceinline__ void dequantise_chunk(const SavedRows& s, void* out, 
     at = scale_at(s, rows, width, r, static_cast<int>(i - r * width) >> 5);
   }
   const float f = mx_scale_value(s.scales[at]);
-  float v[16];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) mx_four<KIND>(q[j], f, v + 4 * j);
   if constexpr (F32) {
     typedef float v4f __attribute__((ext_vector_type(4)));
     v4f* const p = reinterpret_cast<v4f*>(static_cast<float*>(out) + i);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) p[j] = v4f{v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]};
+    for (int j = 0; j < 4; ++j) {
+      float v[4];
+      mx_four<KIND>(q[j], f, v);
+      p[j] = v4f{v[0], v[1], v[2], v[3]};
+    }
   } else {
-    typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
-    typedef float f2 __attribute__((ext_vector_type(2)));
     v4u* const p = reinterpret_cast<v4u*>(static_cast<uint16_t*>(out) + i);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      v4u o;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        o[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{v[8 * j + 2 * e], v[8 * j + 2 * e + 1]}, bf2));
-      p[j] = o;
+      const v2u lo = mx_four_bf16<KIND>(q[2 * j], f), hi = mx_four_bf16<KIND>(q[2 * j + 1], f);
+      p[j] = v4u{lo.x, lo.y, hi.x, hi.y};
     }
   }
 }

@@ -309,6 +309,35 @@ def test_backward_large(m, n, k):
     assert all(torch.equal(a, b) for a, b in zip(got, same))
 
 
+@pytest.mark.parametrize("m,n,k,groups,fmt,layout", [
+    (6000, 2048, 1408, 12, "e4m3", "kplanes"), (3001, 1408, 2048, 16, "e5m2", "row_major"), (24571, 1408, 2048, 64, "e4m3", "kplanes"),
+    (700, 2816, 2080, 9, "e4m3", "row_major"), (4099, 2080, 2144, 0, "e5m2", "row_major"), (40, 2048, 2048, 32, "e4m3", "kplanes"),
+    (2500, 1056, 1120, 4, "e4m3", "row_major")])
+@pytest.mark.parametrize("need", [("dx", "dw", "db"), ("dw",)])
+def test_backward_large_grouped(m, n, k, groups, fmt, layout, need):
+    """Ragged and empty groups, widths that end inside a tile, rows that end inside a step: bit for bit as from BF16,
+    with NaN scales among the rows of other groups."""
+    gen = torch.Generator(device="cuda").manual_seed(m)
+    x8 = mg.quantise(torch.randn(m, k, generator=gen, device="cuda"), dtype=fmt, sf_layout=layout)
+    c8 = mg.quantise(torch.randn(m, n, generator=gen, device="cuda"), dtype=fmt)
+    w = (torch.randn(*((groups, n, k) if groups else (n, k)), generator=gen, device="cuda") / math.sqrt(k)).to(BF)
+    dy = torch.randn(m, n, generator=gen, device="cuda").to(BF)
+    off = None
+    if groups:
+        cut = torch.sort(torch.randint(0, m - 6, (groups,), generator=gen, device="cuda")).values
+        cut[1], cut[-1] = cut[0], m - 7                    # an empty group, and rows behind the last
+        off = torch.sort(cut).values.to(torch.int32)
+        (x8[1][:, -7:] if layout == "kplanes" else x8[1][-7:]).fill_(255)
+    print(f"[gpu-case] linear backward from {fmt} large m={m} n={n} k={k} groups={groups} {layout} {need}", flush=True)
+    got = mg.linear_backward(dy, x8, w, c=c8, act="gelu", offsets=off, need=need, x_dtype=fmt, c_dtype=fmt, sf_layout=layout)
+    x, c = mg.dequantise(x8, dtype=fmt, sf_layout=layout), mg.dequantise(c8, dtype=fmt)
+    same = mg.linear_backward(dy, x, w, c=c, act="gelu", offsets=off, need=need)
+    for a, b in zip(got, same):
+        if a is not None and a.shape == (m, k) and groups:
+            a, b = a[:m - 7], b[:m - 7]
+        assert (a is None) == (b is None) and (a is None or (torch.equal(a, b) and not torch.isnan(a).any()))
+
+
 def test_scale_bytes_of_not_numbers():
     """A scale byte of 255 in x or c: NaN in the gradients that read it, and in no other."""
     gen = torch.Generator().manual_seed(2)

@@ -245,7 +245,7 @@ def test_saved_backward_refusals(prob, saved, ptr, want):
 
 
 def test_saved_workspaces():
-    """x's BF16 form is part of the workspace only where dw reads an x in 8 bits."""
+    """x's BF16 form is part of the workspace only where dw needs one of an x in 8 bits."""
     lib, p = mg._load(), mg.moegg_linear_problem(3000, 256, 512, 1, 7, 3)
     plain, x8 = mg.moegg_linear_saved(3, 0, 3), mg.moegg_linear_saved(1, 0, 3)
     for want in range(1, 8):
@@ -253,6 +253,9 @@ def test_saved_workspaces():
         assert lib.moegg_linear_saved_backward_workspace(p, plain, want) == base
         more = lib.moegg_linear_saved_backward_workspace(p, x8, want) - base
         assert more >= 3000 * 512 * 2 if want & 2 else more == 0
+    # the largest tiles of dw read the codes themselves
+    big = mg.moegg_linear_problem(16384, 2816, 2048, 1, 1, 3)
+    assert lib.moegg_linear_saved_backward_workspace(big, x8, 7) == lib.moegg_linear_backward_workspace(big, 7)
     assert lib.moegg_linear_saving_workspace(p, plain) == lib.moegg_linear_workspace(p)
     assert lib.moegg_linear_saving_workspace(p, mg.moegg_linear_saved(3, 0, 2)) == -1
     assert lib.moegg_linear_saved_backward_workspace(p, mg.moegg_linear_saved(1, 0, 3, 5), 7) == -1
