@@ -192,7 +192,7 @@ __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp
 // clear gap are put into the order of their keys in 64 bits, one key a lane;
 // where no gap follows, the wave's tokens are chosen again with all keys in 64
 // bits.  Measured, 16381 tokens, 256 experts, sigmoid: 64 bits for every token
-// 30 us, this form 17 us.
+// 30 us, this form 14 us.
 constexpr int kSpare = 2;
 constexpr int kSlots = kMaxTopK + kSpare;
 
@@ -233,10 +233,10 @@ __device__ __forceinline__ void take(float& b0, float& b1, float v) {
 // theirs again in 64 bits.  (It is rare, but among 16381 tokens there always are
 // such, and their waves are the last to end.)
 // Measured, 16381 tokens, top 8 of 4 of 8 groups of 32 by their two best,
-// sigmoid, without a bias (with one): 14.0 (18.3) us, where groups by their best
-// logit take 12.1 and no groups 9.5 (16.1); with 64 bits for all experts of a
-// wave in doubt 20.6 (22 to 24); with all groups through LDS besides, three
-// workgroups to a compute unit, (24 to 28).
+// sigmoid, without a bias (with one): 14.0 (16.5) us, where groups by their best
+// logit take 12.1 and no groups 9.5 (14.0); with 64 bits for all experts of a
+// wave in doubt 6.6 (4 to 6) more; with all groups through LDS besides, three
+// workgroups to a compute unit, (another 2 to 4).
 template <typename R, int LPT, int EPL>
 __device__ __forceinline__ uint32_t closed_groups(const RouteArgs& a, GroupScratch<LPT, EPL>& lds, const float* x, const float* score,
                                                   bool sums, bool logits, float top, int64_t row, int lane) {
@@ -599,6 +599,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
 #pragma unroll
           for (int i = 0; i < N; ++i) {
             rank[i] = 0;
+            if (!__any(id[i] >= 0)) continue;        // (the waves in doubt are the last to end)
             for (int j = 0; j < m; ++j) {
               const double o = s_exact[slot][j];
               const int oid = s_id[slot][j];
