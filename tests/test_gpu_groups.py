@@ -102,6 +102,7 @@ def test_masked_experts(score, best, with_bias):
     x[40:60, ::2] = -INF
     x[60:70, 3] = INF
     x[70:80, 16:24] = -1e30
+    x[80:90, :48] = torch.finfo(torch.float32).min      # the lowest number is one that can be chosen
     bias = torch.randn(64, generator=gen) * 0.1 if with_bias else None
     if with_bias:
         bias[5], bias[9], bias[17] = math.nan, -INF, 30.0
@@ -135,6 +136,34 @@ def test_all_groups_are_no_choice():
 def test_large_batch():
     x, gen = logits(5003, 256, 2, torch.bfloat16)
     check(x, 8, 8, 4, 2, "sigmoid", torch.randn(256, generator=gen) * 0.1)
+
+
+@pytest.mark.parametrize("t", [2048, 2049])
+@pytest.mark.parametrize("e,groups,top", [(72, 8, 3), (128, 8, 4), (160, 8, 3), (256, 16, 5), (256, 2, 1)])
+@pytest.mark.parametrize("score,best,with_bias", [("softmax", 1, False), ("softmax", 2, True), ("sigmoid", 2, False)])
+def test_few_tokens_and_many(t, e, groups, top, score, best, with_bias):
+    """Up to 2048 tokens of up to 256 experts go a wave a token, more by four to a wave."""
+    x, gen = logits(t, e, t + e, torch.bfloat16)
+    x[::5, ::3] = -INF
+    check(x, 5, groups, top, best, score, torch.randn(e, generator=gen) * 0.1 if with_bias else None)
+
+
+@pytest.mark.parametrize("t", [2048, 2049])
+@pytest.mark.parametrize("e", [65, 96, 128, 200, 256])
+@pytest.mark.parametrize("score,with_bias", [("softmax", False), ("softmax", True), ("sigmoid", True)])
+@pytest.mark.parametrize("renormalise", [False, True])
+def test_without_groups_few_tokens_and_many(t, e, score, with_bias, renormalise):
+    x, gen = logits(t, e, t + e)
+    bias = torch.randn(e, generator=gen) * 0.1 if with_bias else None
+    print(f"[gpu-case] route {t}x{e} {score} bias={with_bias} renormalise={renormalise}", flush=True)
+    ids, w = mg.route(x.cuda(), 7, score=score, bias=None if bias is None else bias.cuda(), renormalise=renormalise)
+    want, ww, _ = layer_ref.route(x, 7, score, bias, renormalise)
+    assert torch.equal(ids.cpu().long(), want)
+    assert ((w.cpu().double() - ww).abs() <= 64 * ref.F32 * (1.0 + x.abs().amax()) * ww.abs()).all()
+    g = torch.randn(t, 7, generator=gen)
+    d = mg.route_backward(x.cuda(), ids, g.cuda(), score=score, renormalise=renormalise).cpu().double()
+    dd = layer_ref.route_backward(x, want, g, score, renormalise)
+    assert ((d - dd).abs() <= ref.F32 * dd.abs() + 256 * ref.F32 * g.abs().sum(1, keepdim=True).double()).all()
 
 
 def test_no_tokens_and_graph():
