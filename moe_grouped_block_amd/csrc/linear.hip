@@ -573,7 +573,10 @@ hipError_t launch_tiles(const LinearArgs& a, const Plan& p, hipStream_t s) {
 // few workgroups are beside them.  Measured against launches of their own: 64
 // groups of 2048 x 1408, 24571 rows, 565 -> 514 us (fp32 dw), 456 -> 422 (BF16
 // dw); dense 16384 x 2816 x 2048 and 4096^3, 1 to 2 % less.  (The tiles of the
-// two spread over each other took 546 instead of 516 us in the first case.)
+// two spread over each other took 546 instead of 516 us in the first case.  256
+// workgroups that take tile after tile from counters, with the next tile's loads
+// ahead of this one's stores, took 465 instead of 436 us, 64 groups of 1408 x
+// 2048 from 8 bits: the registers do not hold both tiles.)
 // 129 rows of 512 x 512 from 8 bits: 25 -> 17 us.
 bool both(const LinearArgs& a, const Plan& dx, const Plan& dw) {
   return a.m && dx.shape == dw.shape && dx.shape != SHAPE_128 &&
