@@ -10,8 +10,8 @@
 //   dw = sum over rows of dy xh
 //
 // Both are bound by HBM: every value is read once and stays in registers until
-// its row's sums are known.  A row belongs to one wave (up to 2048 columns) or
-// to several of a workgroup, whose sums meet in LDS.
+// its row's sums are known.  A row belongs to one wave (up to 1024 columns), to a
+// part of one, or to several of a workgroup, whose sums meet in LDS.
 //
 // Squares and products are summed in 64 bits: no h in range overflows or
 // vanishes in them, and the rate of 64-bit operations is far from being needed.
@@ -80,13 +80,28 @@ __device__ __forceinline__ void inverse_root(double v, float& a, float& b) {
   b = __builtin_amdgcn_rsqf(static_cast<float>(ldexp(v, -e)));                              // of [1, 4)
 }
 
-// The sum over a row's lanes, the same in all of them: `waves` waves from the
-// team's first on.  Every thread of the workgroup calls it (`turn`: another
-// one from call to call, two sums' places take turns).
+// Who has a row: LPR lanes (64, or fewer of narrow rows, of which a wave then
+// has several), of `waves` waves.
+template <int LPR>
+struct Team {
+  int lane, wave, w, teams, team;
+  __device__ __forceinline__ Team(int waves) {
+    const int whole = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    lane = threadIdx.x & (LPR - 1);
+    wave = whole;
+    w = whole & (waves - 1);
+    teams = static_cast<int>(blockDim.x >> 6) / waves * (64 / LPR);
+    team = whole / waves * (64 / LPR) + (threadIdx.x & 63) / LPR;
+  }
+};
+
+// The sums over a row's lanes, the same in all of them (`two`: of s and t).
+// Every thread of the workgroup calls it; a second call needs another place.
+template <int LPR>
 __device__ __forceinline__ void row_sums(double& s, double& t, int waves, int wave, double (*place)[2], bool two) {
-  s = lanes_sum<64>(s);
-  if (two) t = lanes_sum<64>(t);
-  if (waves == 1) return;
+  s = lanes_sum<LPR>(s);
+  if (two) t = lanes_sum<LPR>(t);
+  if (LPR < 64 || waves == 1) return;
   if ((threadIdx.x & 63) == 0) {
     place[wave][0] = s;
     place[wave][1] = t;
@@ -109,16 +124,17 @@ __device__ __forceinline__ void row_sums(double& s, double& t, int waves, int wa
 // that every access of a wave is one run: with 16 columns a lane (as dispatch has
 // them for MX rows) 16381 x 2048 with an fp32 stream took 102 us, 4999 x 4096
 // with E4M3 rows 33.
-template <bool XF32, bool SF32, int KIND, int P>
+template <bool XF32, bool SF32, int KIND, int P, int LPR>
 __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a, int waves) {
   constexpr int U = SF32 ? 4 : 8;
+  static_assert(LPR == 64 || (P == 1 && (KIND == ROW_BF16 || LPR * U >= 128)), "narrow rows; a scale word is one row's");
   __shared__ double place[16][2];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int teams = (blockDim.x >> 6) / waves, team = wave / waves, w = wave & (waves - 1);
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * teams + team;
+  const Team<LPR> me(waves);
+  const int lane = me.lane;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * me.teams + me.team;
   const bool live = row < a.rows;
   const int64_t first = (live ? row : 0) * a.width;
-  const int col0 = (w * 64 + lane) * U, step = waves * 64 * U;
+  const int col0 = (me.w * 64 + lane) * U, step = waves * 64 * U;
   Unit<XF32, U> x[P];
   Unit<SF32, U> r[P];
 #pragma unroll
@@ -149,7 +165,7 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a, int waves) {
 #pragma unroll
     for (int i = 0; i < U; ++i) sum = fma(static_cast<double>(h[p][i]), static_cast<double>(h[p][i]), sum);
   }
-  row_sums(sum, none, waves, wave, place, false);
+  row_sums<LPR>(sum, none, waves, me.wave, place, false);
   float ra, rb;
   inverse_root(sum * a.inverse_width + a.eps, ra, rb);
 #pragma unroll
@@ -189,79 +205,98 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a, int waves) {
 // backward
 // ---------------------------------------------------------------------------
 
-// (Beyond 16384 columns the 128 registers of 16 waves do not hold a lane's part of
-// a row with its weights and sums: some of them go through memory.)
+// Beyond 16384 columns the 128 registers of 16 waves do not hold a lane's part of
+// a row with its weights, its sums and dh: weights and dh are read when they are
+// wanted (kept all the same, they spilled: 1024 x 32768 178 us instead of 93;
+// 2048 x 16384 46).
 // A workgroup's teams take rows in turn and add up their part of dw in
 // registers; the teams' parts meet in LDS, the workgroups' in norm_dw_kernel,
 // in a fixed order.
-template <bool SF32, int P, int THREADS>
+template <bool SF32, int P, int THREADS, int LPR>
 __global__ __launch_bounds__(THREADS) void rms_norm_backward_kernel(NormArgs a, int waves) {
+  constexpr bool KEPT = P < 4;
   __shared__ double place[2][16][2];
   __shared__ v4f part[4][P * 2][64];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int teams = (blockDim.x >> 6) / waves, team = wave / waves, w = wave & (waves - 1);
+  const Team<LPR> me(waves);
+  const int lane = threadIdx.x & 63, wave = me.wave, w = me.w, teams = me.teams;
   int col[P];
-  float weight[P][8], acc[P][8];
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    col[p] = ((p * waves + w) * 64 + lane) * 8;
+  float kept[KEPT ? P : 1][8], acc[P][8];
+  auto load_weights = [&](int p, float* f) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < 8; i += 4) {
       v4f v{};
       if (col[p] < a.width) v = *reinterpret_cast<const v4f_any*>(a.weight + col[p] + i);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        weight[p][i + q] = v[q];
-        acc[p][i + q] = 0.0f;
-      }
+      for (int q = 0; q < 4; ++q) f[i + q] = v[q];
     }
+  };
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    col[p] = ((p * waves + w) * 64 + me.lane) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[p][i] = 0.0f;
+    if constexpr (KEPT) load_weights(p, kept[p]);
   }
+  auto weights = [&](int p, float* f) __attribute__((always_inline)) {
+    if constexpr (KEPT) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = kept[p][i];
+    } else {
+      load_weights(p, f);
+    }
+  };
   int turn = 0;
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * teams; base < a.rows;
        base += static_cast<int64_t>(gridDim.x) * teams, turn ^= 1) {
-    const int64_t row = base + team;
+    const int64_t row = base + me.team;
     const bool live = row < a.rows;
     const int64_t first = (live ? row : 0) * a.width;
     Unit<false, 8> dy[P];
-    Unit<SF32, 8> h[P], dh[P];
+    Unit<SF32, 8> h[P], dh[KEPT ? P : 1];
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       dy[p].clear();
       h[p].clear();
-      dh[p].clear();
+      if constexpr (KEPT) dh[p].clear();
       if (live && col[p] < a.width) {
         dy[p].load(a.dy, first + col[p]);
         h[p].load(a.stored, first + col[p]);
-        if (a.dh) dh[p].load(a.dh, first + col[p]);
+        if (KEPT && a.dh) dh[p].load(a.dh, first + col[p]);
       }
     }
     double sq = 0.0, dot = 0.0;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      float d[8], v[8];
+      float d[8], v[8], wt[8];
       dy[p].get(d);
       h[p].get(v);
+      weights(p, wt);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         sq = fma(static_cast<double>(v[i]), static_cast<double>(v[i]), sq);
-        dot = fma(static_cast<double>(d[i] * weight[p][i]), static_cast<double>(v[i]), dot);
+        dot = fma(static_cast<double>(d[i] * wt[i]), static_cast<double>(v[i]), dot);
       }
     }
-    row_sums(sq, dot, waves, wave, place[turn], true);
+    row_sums<LPR>(sq, dot, waves, wave, place[turn], true);
     float ra, rb;
     inverse_root(sq * a.inverse_width + a.eps, ra, rb);
     const float mean = static_cast<float>(dot * a.inverse_width * ra * rb);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      float d[8], v[8], g[8];
+      float d[8], v[8], g[8], wt[8];
       dy[p].get(d);
       h[p].get(v);
-      dh[p].get(g);
+      if constexpr (!KEPT) {
+        dh[0].clear();
+        if (a.dh && live && col[p] < a.width) dh[0].load(a.dh, first + col[p]);
+      }
+      dh[KEPT ? p : 0].get(g);
+      weights(p, wt);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float xh = v[i] * ra * rb;
         acc[p][i] = fmaf(d[i], xh, acc[p][i]);
-        v[i] = fmaf((d[i] * weight[p][i] - xh * mean) * ra, rb, g[i]);
+        v[i] = fmaf((d[i] * wt[i] - xh * mean) * ra, rb, g[i]);
       }
       if (a.dx && live && col[p] < a.width) {
         h[p].set(v);
@@ -270,8 +305,13 @@ __global__ __launch_bounds__(THREADS) void rms_norm_backward_kernel(NormArgs a, 
     }
   }
   if (!a.partial) return;
-  if (teams > 1) {
-    // (waves of a workgroup with several teams: 4)
+  // the rows of a wave, then the waves with the same columns (4, where there are several)
+#pragma unroll
+  for (int d = LPR; d < 64; d <<= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[0][i] += __shfl_xor(acc[0][i], d);
+  const int team = wave / waves, same = static_cast<int>(blockDim.x >> 6) / waves;
+  if (same > 1) {
     if (team > 0) {
 #pragma unroll
       for (int p = 0; p < P; ++p)
@@ -281,7 +321,7 @@ __global__ __launch_bounds__(THREADS) void rms_norm_backward_kernel(NormArgs a, 
     }
     __syncthreads();
     if (team > 0) return;
-    for (int t = 1; t < teams; ++t)
+    for (int t = 1; t < same; ++t)
 #pragma unroll
       for (int p = 0; p < P; ++p)
 #pragma unroll
@@ -291,6 +331,7 @@ __global__ __launch_bounds__(THREADS) void rms_norm_backward_kernel(NormArgs a, 
           for (int i = 0; i < 4; ++i) acc[p][4 * q + i] += v[i];
         }
   }
+  if (LPR < 64 && lane >= LPR) return;
 #pragma unroll
   for (int p = 0; p < P; ++p)
     if (col[p] < a.width) {
@@ -323,22 +364,29 @@ __global__ __launch_bounds__(256) void norm_dw_kernel(const float* partial, floa
 // choices
 // ---------------------------------------------------------------------------
 
-// Pieces a lane and waves a row, both powers of two, for rows in pieces of
-// `piece` columns of a wave: 1024 columns a wave, 2048 where 16 waves would not
-// hold the row otherwise.  Measured against 2048 a wave (and 512), 2048 columns:
-// forward with an fp32 stream 78.6 us against 85.6 (77.2), backward 49.7 against
-// 50.8 (61); 4096 columns with E4M3 rows 28.3 against 29.1 (29.5).
+// Pieces a lane, waves a row and lanes a row, all powers of two, for `unit`
+// columns a lane and piece: 1024 columns a wave, 2048 where 16 waves would not
+// hold the row otherwise, and several narrow rows a wave.  Measured against 2048
+// a wave (and 512), 2048 columns: forward with an fp32 stream 78.6 us against 85.6
+// (77.2), backward 49.7 against 50.8 (61); 4096 columns with E4M3 rows 28.3
+// against 29.1 (29.5).  524288 x 64 with residual: eight rows a wave 45 us forward
+// and 48 backward, a row a wave 151 and 280.
 struct Shape {
-  int p, waves;
+  int p, waves, lanes;
 };
-Shape shape_of(int width, int piece) {
-  Shape s{1, 1};
-  const int pieces = (width + piece - 1) / piece, most = (width <= 16384 ? 1024 : 2048) / piece;
+Shape shape_of(int width, int unit, int least_lanes) {
+  Shape s{1, 1, 64};
+  const int pieces = (width + 64 * unit - 1) / (64 * unit), most = (width <= 16384 ? 1024 : 2048) / (64 * unit);
   while (s.p < most && s.p < pieces) s.p *= 2;
   while (s.p * s.waves < pieces) s.waves *= 2;
+  while (s.lanes > least_lanes && s.lanes / 2 * unit >= width) s.lanes /= 2;
   return s;
 }
 int threads_of(const Shape& s) { return s.waves > 4 ? 64 * s.waves : 256; }
+int64_t blocks_of(const Shape& s, int64_t rows) {
+  const int teams = threads_of(s) / 64 / s.waves * (64 / s.lanes);
+  return (rows + teams - 1) / teams;
+}
 
 template <typename F>
 hipError_t by_pieces(int p, F&& f) {
@@ -350,16 +398,23 @@ hipError_t by_pieces(int p, F&& f) {
   }
 }
 
+template <bool XF32, bool SF32, int KIND, int P, int LPR>
+hipError_t launch_norm_kernel(const NormArgs& a, const Shape& sh, hipStream_t s) {
+  hipLaunchKernelGGL((rms_norm_kernel<XF32, SF32, KIND, P, LPR>), dim3(static_cast<unsigned>(blocks_of(sh, a.rows))),
+                     dim3(threads_of(sh)), 0, s, a, sh.waves);
+  return hipGetLastError();
+}
 template <bool XF32, bool SF32, int KIND>
 hipError_t launch_norm_kind(const NormArgs& a, hipStream_t s) {
-  constexpr int kPiece = SF32 ? 256 : 512;
-  const Shape sh = shape_of(a.width, kPiece);
+  constexpr int U = SF32 ? 4 : 8, kMost = 2048 / (64 * U), kLeast = KIND == ROW_BF16 ? 8 : 128 / U;
+  const Shape sh = shape_of(a.width, U, kLeast);
+  if constexpr (kLeast <= 8)
+    if (sh.lanes == 8) return launch_norm_kernel<XF32, SF32, KIND, 1, 8>(a, sh, s);
+  if constexpr (kLeast <= 16)
+    if (sh.lanes == 16) return launch_norm_kernel<XF32, SF32, KIND, 1, 16>(a, sh, s);
+  if (sh.lanes == 32) return launch_norm_kernel<XF32, SF32, KIND, 1, 32>(a, sh, s);
   return by_pieces(sh.p, [&](auto p) {
-    constexpr int P = decltype(p)::value < 2048 / kPiece ? decltype(p)::value : 2048 / kPiece;
-    const int threads = threads_of(sh), teams = threads / 64 / sh.waves;
-    const unsigned blocks = static_cast<unsigned>((a.rows + teams - 1) / teams);
-    hipLaunchKernelGGL((rms_norm_kernel<XF32, SF32, KIND, P>), dim3(blocks), dim3(threads), 0, s, a, sh.waves);
-    return hipGetLastError();
+    return launch_norm_kernel<XF32, SF32, KIND, decltype(p)::value < kMost ? decltype(p)::value : kMost, 64>(a, sh, s);
   });
 }
 template <bool XF32, bool SF32>
@@ -372,22 +427,20 @@ hipError_t launch_norm_types(const NormArgs& a, hipStream_t s) {
   }
 }
 
-Shape backward_shape(int width) { return shape_of(width, 512); }
+Shape backward_shape(int width) { return shape_of(width, 8, 8); }
 
 // Workgroups of the backward: two of four waves to a compute unit (1024 of them:
 // 53.6 us instead of 49.7, their parts of dw are twice as many).
 int64_t backward_blocks(int64_t rows, int width) {
-  const Shape sh = backward_shape(width);
-  const int teams = threads_of(sh) / 64 / sh.waves;
-  const int64_t all = (rows + teams - 1) / teams;
+  const int64_t all = blocks_of(backward_shape(width), rows);
   return all < 512 ? all : 512;
 }
 
-template <int P, int THREADS>
+template <int P, int THREADS, int LPR = 64>
 void launch_backward_kernel(const NormArgs& a, dim3 grid, int waves, hipStream_t s) {
   const dim3 block(waves > 4 ? 64 * waves : 256);
-  if (a.stream_f32) hipLaunchKernelGGL((rms_norm_backward_kernel<true, P, THREADS>), grid, block, 0, s, a, waves);
-  else hipLaunchKernelGGL((rms_norm_backward_kernel<false, P, THREADS>), grid, block, 0, s, a, waves);
+  if (a.stream_f32) hipLaunchKernelGGL((rms_norm_backward_kernel<true, P, THREADS, LPR>), grid, block, 0, s, a, waves);
+  else hipLaunchKernelGGL((rms_norm_backward_kernel<false, P, THREADS, LPR>), grid, block, 0, s, a, waves);
 }
 
 }  // namespace
@@ -407,6 +460,12 @@ hipError_t launch_rms_norm_backward(const NormArgs& a, hipStream_t s) {
     const dim3 grid(static_cast<unsigned>(blocks));
     const hipError_t e = by_pieces(sh.p, [&](auto p) {
       constexpr int P = decltype(p)::value < 4 ? decltype(p)::value : 4;
+      if constexpr (P == 1) {
+        if (sh.lanes == 8) launch_backward_kernel<P, 256, 8>(a, grid, sh.waves, s);
+        else if (sh.lanes == 16) launch_backward_kernel<P, 256, 16>(a, grid, sh.waves, s);
+        else if (sh.lanes == 32) launch_backward_kernel<P, 256, 32>(a, grid, sh.waves, s);
+        if (sh.lanes < 64) return hipGetLastError();
+      }
       // (more than one wave takes two pieces a lane, more than 16384 columns four)
       if constexpr (P == 4) launch_backward_kernel<P, 1024>(a, grid, sh.waves, s);
       else if (sh.waves <= 4) launch_backward_kernel<P, 256>(a, grid, sh.waves, s);

@@ -72,6 +72,21 @@ def test_forward_mx_odd_widths(h):
         check_forward(9, h, dtype=dtype, layout="kplanes")
 
 
+@pytest.mark.parametrize("h", [8, 16, 24, 56, 64, 72, 120, 128, 136, 248, 256, 264, 504])
+@pytest.mark.parametrize("t", [1, 7, 33, 301, 4099])
+@pytest.mark.parametrize("kind", [BF, F32])
+def test_narrow_rows(t, h, kind):
+    """Several rows a wave."""
+    check_forward(t, h, BF, kind, True, seed=t + h)
+    check_backward(t, h, kind, seed=t + h)
+    if h % 128 == 0:
+        for layout in ("row_major", "kplanes"):
+            check_forward(t, h, BF, kind, True, dtype="e4m3", layout=layout, seed=t)
+            check_forward(t, h, BF, kind, True, copy="e5m2", layout=layout, seed=t)
+    if h % 256 == 0:
+        check_forward(t, h, kind, kind, False, dtype="e2m1x2", layout="kplanes", seed=t)
+
+
 def test_the_copy_is_the_output():
     """The MX copy beside a BF16 y, the MX y alone, and both y's: the same numbers."""
     x, r, w, _ = make(77, 1024, BF, BF, True)
