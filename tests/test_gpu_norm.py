@@ -182,6 +182,23 @@ def test_in_place():
     assert torch.equal(dh, dx)
 
 
+def test_vectors_at_any_multiple_of_4_bytes():
+    x, r, w, gen = make(40, 1032, BF, BF, True)
+    wide = torch.zeros(1032 + 5, device="cuda")
+    want = mg.rms_norm(x.cuda(), w.cuda(), residual=r.cuda())
+    dy = torch.randn(40, 1032, generator=gen).to(BF).cuda()
+    grads = mg.rms_norm_backward(dy, want[1], w.cuda())
+    for shift in (1, 2, 3):
+        view = wide[shift:shift + 1032]
+        view.copy_(w)
+        got = mg.rms_norm(x.cuda(), view, residual=r.cuda())
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        g = mg.rms_norm_backward(dy, want[1], view)
+        assert torch.equal(g[0], grads[0]) and torch.equal(g[1], grads[1])
+    with pytest.raises(mg.MoeggError, match="aligned"):
+        mg.rms_norm(torch.zeros(9 * 1032 + 4, dtype=BF, device="cuda")[4:].view(9, 1032), w.cuda())
+
+
 def test_no_rows():
     w = torch.ones(256, device="cuda")
     e = torch.empty(0, 256, dtype=BF, device="cuda")

@@ -202,6 +202,50 @@ def test_forward_large(m, n, k):
     assert ((y.double() - y0.double()).abs().cpu() <= 2 * bound).all()
 
 
+def check_on_gpu(m, n, k, act, groups, fmt):
+    """c against float64 products on the GPU."""
+    gen = torch.Generator(device="cuda").manual_seed(m + n)
+    x = torch.randn(m, k, generator=gen, device="cuda").to(BF)
+    w = (torch.randn(max(groups, 1), n, k, generator=gen, device="cuda") / math.sqrt(k)).to(BF)
+    b = torch.randn(max(groups, 1), n, generator=gen, device="cuda") * 0.3
+    ends = [m]
+    if groups:
+        ends = torch.sort(torch.randint(0, m + 1, (groups - 1,), generator=gen, device="cuda")).values.tolist() + [m]
+    off = torch.tensor(ends, dtype=torch.int32, device="cuda") if groups else None
+    print(f"[gpu-case] linear keeps {fmt} m={m} n={n} k={k} {act} groups={groups}", flush=True)
+    if groups:
+        y, (codes, sf) = mg.linear(x, w, bias=b, act=act, offsets=off, save_c=fmt)
+        y0, _ = mg.linear(x, w, bias=b, act=act, offsets=off, save_c=True)
+    else:
+        y, (codes, sf) = mg.linear(x, w[0], bias=b[0], act=act, save_c=fmt)
+        y0, _ = mg.linear(x, w[0], bias=b[0], act=act, save_c=True)
+    z, mag, at = torch.empty(m, n, dtype=torch.float64), torch.empty(m, n, dtype=torch.float64), 0
+    for g, end in enumerate(ends):
+        xs, ws = x[at:end].double(), w[g].double()
+        z[at:end] = (xs @ ws.t() + b[g].double()).cpu()
+        mag[at:end] = (xs.abs() @ ws.abs().t() + b[g].double().abs()).cpu()
+        at = end
+    ref.check_mx(codes, sf, fmt, z, (k + 8) * ref.F32 * mag)
+    bound = layer_ref.linear_bound(z, mag, k, act, None, ref.BF16)
+    assert ((y.cpu().double() - y0.cpu().double()).abs() <= 2 * bound).all()
+
+
+@pytest.mark.parametrize("m,n,k,act,fmt", [(300, 160, 4096, "none", "e5m2"), (600, 1056, 8192, "gelu", "e4m3"),
+                                           (300, 2048, 8192, "swiglu", "e4m3"), (2500, 2048, 8192, "swiglu", "e5m2"),
+                                           (700, 512, 16384, "srelu", "e4m3")])
+def test_forward_parts_of_r(m, n, k, act, fmt):
+    """Sums split among workgroups: the join keeps c."""
+    code = {"none": 0, "swiglu": 1, "srelu": 2, "gelu": 7}[act]
+    assert mg._load().moegg_linear_saving_workspace(mg.moegg_linear_problem(m, n, k, 1, code, 3), mg.moegg_linear_saved(3, 0, 1)) > 0
+    check_on_gpu(m, n, k, act, 0, fmt)
+
+
+@pytest.mark.parametrize("m,n,k,act,groups,fmt", [(5000, 2048, 520, "swiglu", 6, "e4m3"), (3001, 1056, 2048, "gelu", 20, "e5m2"),
+                                                  (777, 2816, 264, "srelu", 64, "e4m3")])
+def test_forward_large_grouped(m, n, k, act, groups, fmt):
+    check_on_gpu(m, n, k, act, groups, fmt)
+
+
 def test_rows_behind_the_last_group_are_left():
     x, w, b, _, _, _ = make(300, 128, 64, "gelu", 3, 1)
     off = torch.tensor([100, 100, 170], dtype=torch.int32).cuda()
