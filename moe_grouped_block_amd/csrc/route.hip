@@ -154,8 +154,9 @@ __device__ __forceinline__ void chosen_weights(const RouteArgs& a, float top, fl
 // six, and 16381 tokens of 256 experts took 17.6 us instead of 16.8.)
 __device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
 __device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
+// Lane's keys are of experts first, first + 1, ...
 template <int LPT, int EPL, typename Key>
-__device__ __forceinline__ void choose(Key* key, int rounds, int lane, int* ids, Key* keys) {
+__device__ __forceinline__ void choose(Key* key, int rounds, int lane, int first, int* ids, Key* keys) {
   constexpr Key none = -static_cast<Key>(__builtin_inff());
   for (int j = 0; j < rounds; ++j) {
     Key mine = key[0];
@@ -175,7 +176,7 @@ __device__ __forceinline__ void choose(Key* key, int rounds, int lane, int* ids,
         key[q] = hit ? none : key[q];
         at = hit ? q : at;
       }
-      ids[j] = best > none ? lane * EPL + at : -1;
+      ids[j] = best > none ? first + at : -1;
       if (keys) keys[j] = best;
     }
   }
@@ -206,7 +207,7 @@ constexpr float kKeyP = 50.0f * 5.9604645e-8f, kKeySum = 2.4e-7f;
 // bits; its groups' scores; the last group in and the first one out.  Four
 // workgroups fit a compute unit.
 template <int LPT, int EPL>
-struct GroupScratch {
+struct alignas(16) GroupScratch {
   union {
     float score[LPT * (EPL + 1)];
     double exact[kMaxGroups];
@@ -431,6 +432,38 @@ __device__ __forceinline__ uint32_t closed_groups(const RouteArgs& a, GroupScrat
   return closed;
 }
 
+// The best keys of the token's experts as choose() has them, and the best that
+// is left.  Where the open groups are whole lanes and at most half of them, the
+// closed ones take half of their keys each: a round then looks at half as many
+// (16381 tokens, 4 of 8 groups of 32, a bias: 16.5 -> 14.6 us, 128 experts 12.2
+// -> 11.4).
+template <int LPT, int EPL>
+__device__ __forceinline__ float choose_open(const RouteArgs& a, GroupScratch<LPT, EPL>& lds, float* key, bool open, int rounds,
+                                             int lane, int* ids, float* keys) {
+  constexpr int H = EPL / 2, ROW = EPL + 4;       // (a row's 16 bytes more: its lanes meet no bank twice)
+  static_assert(LPT / 2 * ROW <= LPT * (EPL + 1) && LPT / 2 <= kMaxGroups, "rows of the open lanes");
+  const int count = a.top_groups * a.group_lanes;
+  const uint64_t all = __ballot(open) >> (threadIdx.x & 63 & ~(LPT - 1));
+  wave_sync();
+  if (open) {
+    const int r = __builtin_popcountll(all & ((1ull << lane) - 1));
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) lds.score[r * ROW + j] = key[j];
+    lds.group[r] = __int_as_float(lane * EPL);
+  }
+  wave_sync();
+  const int r = lane >> 1, half = (lane & 1) * H;
+  float mine[H];
+#pragma unroll
+  for (int j = 0; j < H; ++j) mine[j] = r < count ? lds.score[r * ROW + half + j] : kNegInf;
+  const int first = r < count ? __float_as_int(lds.group[r]) + half : 0;
+  choose<LPT, H, float>(mine, rounds, lane, first, ids, keys);
+  float rest = mine[0];
+#pragma unroll
+  for (int j = 1; j < H; ++j) rest = fmaxf(rest, mine[j]);
+  return lanes_max<LPT>(rest);
+}
+
 template <bool BF16, int LPT, int EPL, int V, bool BIAS, bool GROUPS>
 __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
   using R = Row<BF16, LPT, EPL, V>;
@@ -463,11 +496,23 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
   }
 
   float key[EPL];
+  // the `rounds` best, and the best that is left
+  auto best_of = [&](auto& scratch, int rounds, float* keys) __attribute__((always_inline)) {
+    if constexpr (GROUPS && EPL >= 8) {
+      if (a.group_lanes && 2 * a.top_groups * a.group_lanes <= LPT)
+        return choose_open<LPT, EPL>(a, scratch[slot], key, !closed, rounds, lane, s_id[slot], keys);
+    }
+    choose<LPT, EPL, float>(key, rounds, lane, lane * EPL, s_id[slot], keys);
+    float rest = key[0];
+#pragma unroll
+    for (int q = 1; q < EPL; ++q) rest = fmaxf(rest, key[q]);
+    return lanes_max<LPT>(rest);
+  };
+  __shared__ GroupScratch<LPT, GROUPS ? EPL : 1> scratch[GROUPS ? TPB : 1];
   if constexpr (!BIAS) {
 #pragma unroll
     for (int j = 0; j < EPL; ++j) key[j] = x[j] > kNegInf ? x[j] : kNegInf;
     if constexpr (GROUPS) {
-      __shared__ GroupScratch<LPT, EPL> scratch[TPB];
       float score[EPL];
       float valid = total;
       if (a.softmax && __any(!(total == total))) {     // (a NaN leaves the choice among the others)
@@ -486,7 +531,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
 #pragma unroll
       for (int j = 0; j < EPL; ++j) key[j] = closed >> j & 1 ? kNegInf : key[j];
     }
-    choose<LPT, EPL, float>(key, k, lane, s_id[slot], s_logit[slot]);   // (the keys are the logits)
+    best_of(scratch, k, s_logit[slot]);            // (the keys are the logits)
     wave_sync();
   } else {
     // a NaN in the softmax's sum leaves the choice among the others
@@ -513,17 +558,12 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
       }
     }
     if constexpr (GROUPS) {
-      __shared__ GroupScratch<LPT, EPL> scratch[TPB];
       closed = closed_groups<R>(a, scratch[slot], x, key, a.group_sums, false, top, row, lane);
 #pragma unroll
       for (int j = 0; j < EPL; ++j) key[j] = closed >> j & 1 ? kNegInf : key[j];
     }
     const int cand = min(k + kSpare, a.experts);
-    choose<LPT, EPL, float>(key, cand, lane, s_id[slot], s_key[slot]);
-    float rest = key[0];
-#pragma unroll
-    for (int q = 1; q < EPL; ++q) rest = fmaxf(rest, key[q]);
-    rest = lanes_max<LPT>(rest);                   // the best that is left
+    const float rest = best_of(scratch, cand, s_key[slot]);
     wave_sync();
     auto fetch_logits = [&](int n) __attribute__((always_inline)) {
       for (int j = lane; j < n; j += LPT) {
@@ -575,7 +615,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
             const double q = exact[j] * dt + a.bias[e < a.experts ? e : 0];
             exact[j] = x[j] > kNegInf && !(closed >> j & 1) && q > -__builtin_inf() ? q : -__builtin_inf();
           }
-          choose<LPT, EPL, double>(exact, k, lane, s_id[slot], nullptr);
+          choose<LPT, EPL, double>(exact, k, lane, lane * EPL, s_id[slot], nullptr);
           wave_sync();
           fetch_logits(k);
         } else {
