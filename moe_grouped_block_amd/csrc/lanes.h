@@ -11,9 +11,11 @@ namespace {
 
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
+// (the bound control lets the compiler put the exchange into the instruction that
+// uses it; every source lane exists)
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_u(uint32_t x) {
-  return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), CTRL, 0xF, 0xF, false));
+  return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), CTRL, 0xF, 0xF, true));
 }
 
 // STEP 0..3 pair lanes inside a 16-lane row (1, 2 apart, mirrored halves,
@@ -35,6 +37,10 @@ __device__ __forceinline__ uint32_t partner(uint32_t x) {
 template <int STEP>
 __device__ __forceinline__ float partner(float x) {
   return __uint_as_float(partner<STEP>(__float_as_uint(x)));
+}
+template <int STEP>
+__device__ __forceinline__ int32_t partner(int32_t x) {
+  return static_cast<int32_t>(partner<STEP>(static_cast<uint32_t>(x)));
 }
 template <int STEP>
 __device__ __forceinline__ double partner(double x) {
