@@ -102,6 +102,13 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// The bits of a token's lanes.
+template <int LPT>
+__device__ __forceinline__ uint64_t token_ballot(bool b) {
+  const uint64_t all = __ballot(b);
+  return LPT == 64 ? all : (all >> (threadIdx.x & 63 & ~(LPT - 1))) & ((1ull << (LPT & 63)) - 1);
+}
+
 // Choices j = lane, lane + LPT, ... are a lane's own: at most JPL of them.
 template <int LPT>
 constexpr int kJpl = (kMaxTopK + LPT - 1) / LPT;
@@ -211,6 +218,7 @@ __device__ __forceinline__ Key choose(const Key* key, int rounds, int lane, int 
 
 // e^x by the exponential unit, for sums and keys with bounds of their own.
 __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.4426950408889634f); }
+__device__ __forceinline__ float fast_sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + fast_exp(-x)); }
 
 // With a bias the keys are sums of two numbers of different size, whose
 // order can hang on bits that fp32 does not have.  They are formed in fp32
@@ -249,9 +257,9 @@ __device__ __forceinline__ void take(float& b0, float& b1, float v) {
   b0 = fmaxf(b0, v);
 }
 
-// Bits of the lane's EPL experts that are in no chosen group.  `score`: what
-// the groups' scores are made of (-inf: not there); `sums`: the two largest
-// added, else the largest; `logits`: they are exact.  A group that is whole
+// Bits of the lane's EPL experts that are in no chosen group.  `score`: the
+// experts' keys (-inf: not there), or with LOGITS their logits, which are exact
+// and of whose largest p_of() makes a group's sum.  A group that is whole
 // lanes, a power of two of them (256 experts in 8 groups: 2), is reduced in
 // registers; of others lane g scans group g's experts through LDS (rows of a
 // lane's EPL scores and a word more, so that neither side of the exchange meets
@@ -265,20 +273,25 @@ __device__ __forceinline__ void take(float& b0, float& b1, float v) {
 // logit take 12.1 and no groups 9.5 (14.0); with 64 bits for all experts of a
 // wave in doubt 6.6 (4 to 6) more; with all groups through LDS besides, three
 // workgroups to a compute unit, (another 2 to 4).
-template <typename R, int LPT, int EPL>
+template <typename R, bool LOGITS, int LPT, int EPL, typename P>
 __device__ __forceinline__ uint32_t closed_groups(const RouteArgs& a, GroupScratch<LPT, EPL>& lds, const float* x, const float* score,
-                                                  bool sums, bool logits, float top, int64_t row, int lane) {
+                                                  P&& p_of, float top, int64_t row, int lane) {
   constexpr int N = kMaxGroups / LPT;            // groups of a lane
   constexpr double kNone = -__builtin_inf();
   const int groups = a.groups, size = a.experts / groups;
+  const bool sums = a.group_sums, sharp = LOGITS && !sums;
   float mine[N], off[N];
   float low0[N], low1[N], g0 = kNegInf, g1 = kNegInf;     // the groups' two largest: of lane g's, of the lane's own
   auto set = [&](int i, float b0, float b1) __attribute__((always_inline)) {
     low0[i] = b0;
     low1[i] = b1;
     const bool two = sums && b1 > kNegInf;
+    if (LOGITS && sums) {
+      b0 = b0 > kNegInf ? p_of(b0) : kNegInf;
+      b1 = p_of(b1);
+    }
     mine[i] = two ? b0 + b1 : b0;
-    off[i] = logits ? 0.0f : two ? 2.0f * kKeyP + kKeySum * (fabsf(b0) + fabsf(b1)) : kKeyP + kKeySum * fabsf(b0);
+    off[i] = sharp ? 0.0f : two ? 2.0f * kKeyP + kKeySum * (fabsf(b0) + fabsf(b1)) : b0 > kNegInf ? kKeyP + kKeySum * fabsf(b0) : 0.0f;
   };
   if (a.group_lanes) {
 #pragma unroll
@@ -332,15 +345,12 @@ __device__ __forceinline__ uint32_t closed_groups(const RouteArgs& a, GroupScrat
     for (int o = 0; o < groups; o += 4) {
       const v4f q = *reinterpret_cast<const v4f*>(&lds.group[o]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) rank += q[e] > v || (q[e] == v && o + e < g);
+      for (int e = 0; e < 4; ++e) rank += (q[e] > v) | ((q[e] == v) & (o + e < g));     // (no branches)
     }
     return rank;
   };
   uint64_t mask = 0;                             // the token's open groups
-  auto add = [&](int i, bool open) __attribute__((always_inline)) {
-    const uint64_t all = __ballot(open);
-    mask |= (LPT == 64 ? all : (all >> (threadIdx.x & 63 & ~(LPT - 1))) & ((1ull << (LPT & 63)) - 1)) << (i * LPT);
-  };
+  auto add = [&](int i, bool open) __attribute__((always_inline)) { mask |= token_ballot<LPT>(open) << (i * LPT); };
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     if (i * LPT >= groups) break;
@@ -348,7 +358,7 @@ __device__ __forceinline__ uint32_t closed_groups(const RouteArgs& a, GroupScrat
     add(i, rank < a.top_groups);
     if (rank == a.top_groups - 1 || rank == a.top_groups) lds.edge[rank == a.top_groups] = mine[i];
   }
-  if (!logits) {
+  if (!sharp) {
     wave_sync();
     float most = 0.0f;                           // what any of the token's groups may be off by
 #pragma unroll
@@ -380,7 +390,7 @@ __device__ __forceinline__ uint32_t closed_groups(const RouteArgs& a, GroupScrat
       };
       auto near = [&](float v, float b0, float b1) __attribute__((always_inline)) {
         const float least = sums && b1 > kNegInf ? b1 : b0;
-        return v > kNegInf && !(least - v > 2.0f * (kKeyP + kKeySum * fabsf(least)));
+        return v > kNegInf && !(least - v > (LOGITS ? 0.0f : 2.0f * (kKeyP + kKeySum * fabsf(least))));
       };
       double again[N];
       if (a.group_lanes) {
@@ -442,7 +452,10 @@ __device__ __forceinline__ uint32_t closed_groups(const RouteArgs& a, GroupScrat
         int rank = kMaxGroups;
         if (g < groups) {
           rank = 0;
-          for (int o = 0; o < groups; ++o) rank += lds.exact[o] > again[i] || (lds.exact[o] == again[i] && o < g);
+          for (int o = 0; o < groups; ++o) {
+            const double v = lds.exact[o];
+            rank += (v > again[i]) | ((v == again[i]) & (o < g));
+          }
         }
         add(i, rank < a.top_groups);
       }
@@ -470,7 +483,7 @@ __device__ __forceinline__ float choose_open(const RouteArgs& a, GroupScratch<LP
   constexpr int H = EPL / 2, ROW = EPL + 4;       // (a row's 16 bytes more: its lanes meet no bank twice)
   static_assert(LPT / 2 * ROW <= LPT * (EPL + 1) && LPT / 2 <= kMaxGroups, "rows of the open lanes");
   const int count = a.top_groups * a.group_lanes;
-  const uint64_t all = __ballot(open) >> (threadIdx.x & 63 & ~(LPT - 1));
+  const uint64_t all = token_ballot<LPT>(open);
   wave_sync();
   if (open) {
     const int r = __builtin_popcountll(all & ((1ull << lane) - 1));
@@ -495,7 +508,6 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
   __shared__ float s_logit[TPB][kSlots];
   __shared__ int s_id[TPB][kSlots];
   __shared__ float s_key[BIAS ? TPB : 1][kSlots];
-  __shared__ int s_flag[BIAS ? TPB : 1][kSlots];
   __shared__ double s_exact[BIAS ? TPB : 1][kSlots];
   const int lane = threadIdx.x % LPT, slot = threadIdx.x / LPT;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * TPB + slot;
@@ -518,6 +530,17 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     total = lanes_sum<LPT>(total);
   }
 
+  // (a NaN in the softmax's sum leaves the choice among the others)
+  float valid = total;
+  if ((BIAS || GROUPS) && a.softmax && __any(!(total == total))) {
+    valid = 0.0f;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) valid += x[j] == x[j] ? fast_exp(x[j] - top) : 0.0f;
+    valid = lanes_sum<LPT>(valid);
+  }
+  const float rt = 1.0f / valid;
+  auto score_of = [&](float l) __attribute__((always_inline)) { return a.softmax ? fast_exp(l - top) * rt : fast_sigmoid(l); };
+
   float key[EPL];
   // the `rounds` best, and the best that is left
   auto best_of = [&](auto& scratch, int rounds, float* keys) __attribute__((always_inline)) {
@@ -532,52 +555,33 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
 #pragma unroll
     for (int j = 0; j < EPL; ++j) key[j] = x[j] > kNegInf ? x[j] : kNegInf;
     if constexpr (GROUPS) {
-      float score[EPL];
-      float valid = total;
-      if (a.softmax && __any(!(total == total))) {     // (a NaN leaves the choice among the others)
-        valid = 0.0f;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) valid += x[j] == x[j] ? fast_exp(x[j] - top) : 0.0f;
-        valid = lanes_sum<LPT>(valid);
-      }
-      const float rt = 1.0f / valid;
-#pragma unroll
-      for (int j = 0; j < EPL; ++j) {
-        const float p = a.softmax ? fast_exp(key[j] - top) * rt : __builtin_amdgcn_rcpf(1.0f + fast_exp(-key[j]));
-        score[j] = a.group_sums && key[j] > kNegInf ? p : key[j];
-      }
-      closed = closed_groups<R>(a, scratch[slot], x, score, a.group_sums, !a.group_sums, top, row, lane);
+      closed = closed_groups<R, true>(a, scratch[slot], x, key, score_of, top, row, lane);
 #pragma unroll
       for (int j = 0; j < EPL; ++j) key[j] = closed >> j & 1 ? kNegInf : key[j];
     }
     best_of(scratch, k, s_logit[slot]);            // (the keys are the logits)
     wave_sync();
   } else {
-    // a NaN in the softmax's sum leaves the choice among the others
-    float valid = total;
-    if (a.softmax && __any(!(total == total))) {
-      valid = 0.0f;
+    // (the score's choice outside of the loop: inside it every key waits for the one
+    // before; fmaf by name, since equal numbers have to give equal keys and the
+    // compiler by itself fuses the sums of some of them)
+    auto keys_of = [&](auto plus) __attribute__((always_inline)) {
 #pragma unroll
-      for (int j = 0; j < EPL; ++j) valid += x[j] == x[j] ? fast_exp(x[j] - top) : 0.0f;
-      valid = lanes_sum<LPT>(valid);
-    }
-    const float rt = 1.0f / valid;
+      for (int i = 0; i < R::NI; ++i) {
+        typedef float vec __attribute__((ext_vector_type(V), aligned(4)));
+        const int e = R::expert(lane, i, 0);
+        const vec bv = *reinterpret_cast<const vec*>(a.bias + (e < a.experts ? e : 0));   // (whole groups of V exist)
 #pragma unroll
-    for (int i = 0; i < R::NI; ++i) {
-      typedef float vec __attribute__((ext_vector_type(V), aligned(4)));
-      const int e = R::expert(lane, i, 0);
-      const vec bv = *reinterpret_cast<const vec*>(a.bias + (e < a.experts ? e : 0));   // (whole groups of V exist)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int j = i * V + v;
-        const float b = bv[v];
-        const float p = a.softmax ? fast_exp(x[j] - top) * rt : __builtin_amdgcn_rcpf(1.0f + fast_exp(-x[j]));
-        const float q = p + b;
-        key[j] = x[j] > kNegInf && q > kNegInf ? q : kNegInf;    // NaN: false
+        for (int v = 0; v < V; ++v) {
+          const int j = i * V + v;
+          key[j] = x[j] == kNegInf ? kNegInf : fmaxf(plus(x[j], bv[v]), kNegInf);    // (NaN: -inf)
+        }
       }
-    }
+    };
+    if (a.softmax) keys_of([&](float l, float b) __attribute__((always_inline)) { return fmaf(fast_exp(l - top), rt, b); });
+    else keys_of([&](float l, float b) __attribute__((always_inline)) { return fast_sigmoid(l) + b; });
     if constexpr (GROUPS) {
-      closed = closed_groups<R>(a, scratch[slot], x, key, a.group_sums, false, top, row, lane);
+      closed = closed_groups<R, false>(a, scratch[slot], x, key, score_of, top, row, lane);
 #pragma unroll
       for (int j = 0; j < EPL; ++j) key[j] = closed >> j & 1 ? kNegInf : key[j];
     }
@@ -592,28 +596,30 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
       wave_sync();
     };
     fetch_logits(cand);
-    // Choice j against the next: 0 clear, 1 the same numbers, 2 in doubt.
+    // Choice j against the next: clear, of the same numbers (`same`), in doubt
+    // (`near`): a bit each.
     constexpr float kP = 2.0f * kKeyP, kSum = kKeySum;
-    bool maybe = false;
-    for (int j = lane; j < cand; j += LPT) {
-      const float k0 = s_key[slot][j], k1 = j + 1 < cand ? s_key[slot][j + 1] : rest;
-      int f = 0;
-      if (k1 > kNegInf && !(k0 - k1 > kP + kSum * (fabsf(k0) + fabsf(k1)))) {
-        f = 2;
-        if (j + 1 < cand && s_logit[slot][j] == s_logit[slot][j + 1] &&
-            a.bias[s_id[slot][j]] == a.bias[s_id[slot][j + 1]])
-          f = 1;
+    uint64_t near = 0, same = 0;
+    for (int j0 = 0; j0 < cand; j0 += LPT) {
+      const int j = j0 + lane;
+      bool n = false, e = false;
+      if (j < cand) {
+        const float k0 = s_key[slot][j], k1 = j + 1 < cand ? s_key[slot][j + 1] : rest;
+        n = k1 > kNegInf && !(k0 - k1 > kP + kSum * (fabsf(k0) + fabsf(k1)));
+        if (n && j + 1 < cand && s_logit[slot][j] == s_logit[slot][j + 1] &&
+            a.bias[s_id[slot][j]] == a.bias[s_id[slot][j + 1]]) {
+          n = false;
+          e = true;
+        }
       }
-      s_flag[slot][j] = f;
-      maybe |= f && j < k;
+      near |= token_ballot<LPT>(n) << j0;
+      same |= token_ballot<LPT>(e) << j0;
     }
-    wave_sync();
-    if (__any(maybe)) {
-      int m = k;                                   // choices up to the next clear gap
-      while (m < cand && s_flag[slot][m - 1]) ++m;
-      const bool open = s_flag[slot][m - 1] != 0;
-      bool doubt = false;
-      for (int j = 0; j < m; ++j) doubt |= s_flag[slot][j] == 2;
+    const uint64_t tied = near | same;
+    if (__any((tied & ((1ull << k) - 1)) != 0)) {
+      const int m = min(cand, k + __builtin_ctzll(~(tied >> (k - 1))));      // choices up to the next clear gap
+      const bool open = tied >> (m - 1) & 1;
+      const bool doubt = (near & ((1ull << m) - 1)) != 0;
       if (__any(doubt)) {
         const bool all = __any(doubt && open);
         double exact[EPL];
@@ -659,10 +665,11 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
           for (int i = 0; i < N; ++i) {
             rank[i] = 0;
             if (!__any(id[i] >= 0)) continue;        // (the waves in doubt are the last to end)
+#pragma unroll 4
             for (int j = 0; j < m; ++j) {
               const double o = s_exact[slot][j];
               const int oid = s_id[slot][j];
-              if (oid >= 0 && (o > mine[i] || (o == mine[i] && oid < id[i]))) ++rank[i];
+              rank[i] += (oid >= 0) & ((o > mine[i]) | ((o == mine[i]) & (oid < id[i])));
             }
           }
           wave_sync();
