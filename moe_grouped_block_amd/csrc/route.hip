@@ -158,8 +158,8 @@ __device__ __forceinline__ void chosen_weights(const RouteArgs& a, float top, fl
 // which is taken out.  A lane keeps its keys in ordered pairs: a round looks at
 // the larger ones, and where one is taken the smaller moves up.  (The first of a
 // lane's equal keys is singled out in the masks of the comparisons, by scalar
-// instructions.  16381 tokens of 256 experts: 8.3 us, without pairs 9.4; with a
-// bias 12.1 and 14.0.)
+// instructions.  16381 tokens of 256 experts: 8.2 us, without pairs 1.0 more; with a
+// bias 11.0 and 1.5 more.)
 __device__ __forceinline__ int32_t larger(int32_t a, int32_t b) { return max(a, b); }
 __device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
 // fp32 keys are compared as integers of the same order (-0 is 0): a step of a
@@ -228,14 +228,19 @@ __device__ __forceinline__ float fast_sigmoid(float x) { return __builtin_amdgcn
 // clear gap are put into the order of their keys in 64 bits, one key a lane;
 // where no gap follows, the wave's tokens are chosen again with all keys in 64
 // bits.  Measured, 16381 tokens, 256 experts, sigmoid: 64 bits for every token
-// 30 us, this form 14 us.
+// 30 us, this form 11 us.
 constexpr int kSpare = 2;
 constexpr int kSlots = kMaxTopK + kSpare;
 
-// What a key p + bias is off by, formed in fp32: a rounding of its sum and p's
-// error: p <= 1, its exponential's argument (p |x| < 0.4), the unit's last
-// places and a sum of up to 16 + 6 terms, below 50 2^-24.
-constexpr float kKeyP = 50.0f * 5.9604645e-8f, kKeySum = 2.4e-7f;
+// What a key p + bias is off by, formed in fp32: a rounding of its sum (u = 2^-24
+// of it, four are counted) and p's error.  e^x: 1.22 |x| u by its argument and 2 u by
+// the unit.  Sigmoid: p (1 - p) of that (|x| p (1 - p) < 0.23), the sum's u and
+// the reciprocal's 2 u, below 4 u; softmax: p |x| < 0.4, and a sum of up to 16 + 6
+// terms with errors of their own, below 50 u.  The sigmoid's is taken twice: what
+// counts is how few tokens are in doubt, whose waves end last (16381 x 256, 4 of 8
+// groups with a bias, with 50 u for both 12.5 instead of 11.9 us).
+constexpr float kUnit = 5.9604645e-8f, kKeySum = 4.0f * kUnit;
+__device__ __forceinline__ float key_p(const RouteArgs& a) { return (a.softmax ? 50.0f : 8.0f) * kUnit; }
 
 // LDS of the choice of groups for a token (its lanes' own: nothing of it is
 // another wave's): its scores, then in their place its groups' scores in 64
@@ -269,10 +274,9 @@ __device__ __forceinline__ void take(float& b0, float& b1, float v) {
 // theirs again in 64 bits.  (It is rare, but among 16381 tokens there always are
 // such, and their waves are the last to end.)
 // Measured, 16381 tokens, top 8 of 4 of 8 groups of 32 by their two best,
-// sigmoid, without a bias (with one): 14.0 (16.5) us, where groups by their best
-// logit take 12.1 and no groups 9.5 (14.0); with 64 bits for all experts of a
-// wave in doubt 6.6 (4 to 6) more; with all groups through LDS besides, three
-// workgroups to a compute unit, (another 2 to 4).
+// sigmoid, without a bias (with one): 10.6 (11.9) us, where groups by their best
+// logit take 8.7 and no groups 8.2 (11.0); 64 bits for all experts of a wave in
+// doubt 6.6 (4 to 6) more.
 template <typename R, bool LOGITS, int LPT, int EPL, typename P>
 __device__ __forceinline__ uint32_t closed_groups(const RouteArgs& a, GroupScratch<LPT, EPL>& lds, const float* x, const float* score,
                                                   P&& p_of, float top, int64_t row, int lane) {
@@ -280,6 +284,7 @@ __device__ __forceinline__ uint32_t closed_groups(const RouteArgs& a, GroupScrat
   constexpr double kNone = -__builtin_inf();
   const int groups = a.groups, size = a.experts / groups;
   const bool sums = a.group_sums, sharp = LOGITS && !sums;
+  const float kp = key_p(a);
   float mine[N], off[N];
   float low0[N], low1[N], g0 = kNegInf, g1 = kNegInf;     // the groups' two largest: of lane g's, of the lane's own
   auto set = [&](int i, float b0, float b1) __attribute__((always_inline)) {
@@ -291,7 +296,7 @@ __device__ __forceinline__ uint32_t closed_groups(const RouteArgs& a, GroupScrat
       b1 = p_of(b1);
     }
     mine[i] = two ? b0 + b1 : b0;
-    off[i] = sharp ? 0.0f : two ? 2.0f * kKeyP + kKeySum * (fabsf(b0) + fabsf(b1)) : b0 > kNegInf ? kKeyP + kKeySum * fabsf(b0) : 0.0f;
+    off[i] = sharp || !(b0 > kNegInf) ? 0.0f : two ? 2.0f * kp + kKeySum * (fabsf(b0) + fabsf(b1)) : kp + kKeySum * fabsf(b0);
   };
   if (a.group_lanes) {
 #pragma unroll
@@ -390,19 +395,27 @@ __device__ __forceinline__ uint32_t closed_groups(const RouteArgs& a, GroupScrat
       };
       auto near = [&](float v, float b0, float b1) __attribute__((always_inline)) {
         const float least = sums && b1 > kNegInf ? b1 : b0;
-        return v > kNegInf && !(least - v > (LOGITS ? 0.0f : 2.0f * (kKeyP + kKeySum * fabsf(least))));
+        return v > kNegInf && !(least - v > (LOGITS ? 0.0f : 2.0f * (kp + kKeySum * fabsf(least))));
       };
       double again[N];
       if (a.group_lanes) {
         const float own = lds.group[lane / a.group_lanes & (kMaxGroups - 1)];
         const bool hot = doubt && lane / a.group_lanes < groups && sure(own) == 0.0;
         double b0 = kNone, b1 = kNone;
+        uint32_t want = 0;
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-          const bool want = hot && near(score[j], g0, g1);
-          if (!__any(want)) continue;
-          const double v = exact(x[j], min(lane * EPL + j, a.experts - 1));
+        for (int j = 0; j < EPL; ++j) want |= hot && near(score[j], g0, g1) ? 1u << j : 0u;
+        while (__any(want != 0)) {                // (the lanes' next experts together: the exponentials are what takes long)
+          const int at = want ? __builtin_ctz(want) : 0;
+          float l = x[0];
+#pragma unroll
+          for (int j = 1; j < EPL; ++j) {
+            l = at == j ? x[j] : l;
+            asm("" : "+v"(l));                    // (or the compiler makes it an access to memory)
+          }
+          const double v = exact(l, min(lane * EPL + at, a.experts - 1));
           if (want) take2(b0, b1, v);
+          want &= want - 1;
         }
         steps<LPT>([&](auto c) {
           constexpr int S = decltype(c)::value;
@@ -423,16 +436,20 @@ __device__ __forceinline__ uint32_t closed_groups(const RouteArgs& a, GroupScrat
           if (i * LPT >= groups) break;
           const int g = lane + i * LPT;
           again[i] = g < groups ? sure(mine[i]) : kNone;
-          int e = doubt && again[i] == 0.0 ? g * size : a.experts;
-          const int end = e + size;
+          const bool hot = doubt && again[i] == 0.0;
           double b0 = kNone, b1 = kNone;
-          while (true) {                          // (the lanes' next experts are found first, then formed together)
-            while (e < min(end, a.experts) && !near(lds.score[e + e / EPL], low0[i], low1[i])) ++e;
-            const bool some = e < min(end, a.experts);
-            if (!__any(some)) break;
-            if (some) {
-              take2(b0, b1, exact(R::one(a.logits, row, a.experts, e), e));
-              ++e;
+          for (int e0 = 0; e0 < size; e0 += 32) {
+            uint32_t want = 0;
+#pragma unroll 4
+            for (int e = e0; e < min(size, e0 + 32); ++e) {
+              const int at = hot ? g * size + e : 0;
+              want |= hot && near(lds.score[at + at / EPL], low0[i], low1[i]) ? 1u << (e - e0) : 0u;
+            }
+            while (__any(want != 0)) {
+              const int e = want ? g * size + e0 + __builtin_ctz(want) : 0;
+              const double v = exact(R::one(a.logits, row, a.experts, e), e);
+              if (want) take2(b0, b1, v);
+              want &= want - 1;
             }
           }
           if (again[i] == 0.0) again[i] = sums && b1 > kNone ? b0 + b1 : b0;
@@ -452,6 +469,7 @@ __device__ __forceinline__ uint32_t closed_groups(const RouteArgs& a, GroupScrat
         int rank = kMaxGroups;
         if (g < groups) {
           rank = 0;
+#pragma unroll 4
           for (int o = 0; o < groups; ++o) {
             const double v = lds.exact[o];
             rank += (v > again[i]) | ((v == again[i]) & (o < g));
@@ -475,8 +493,7 @@ __device__ __forceinline__ uint32_t closed_groups(const RouteArgs& a, GroupScrat
 // The best keys of the token's experts as choose() has them, and the best that
 // is left.  Where the open groups are whole lanes and at most half of them, the
 // closed ones take half of their keys each: a round then looks at half as many
-// (16381 tokens, 4 of 8 groups of 32, a bias: 16.5 -> 14.6 us, 128 experts 12.2
-// -> 11.4).
+// (16381 tokens, 4 of 8 groups of 32, a bias: 1.9 us less; of 128 experts 0.8).
 template <int LPT, int EPL>
 __device__ __forceinline__ float choose_open(const RouteArgs& a, GroupScratch<LPT, EPL>& lds, float* key, bool open, int rounds,
                                              int lane, int* ids, float* keys) {
@@ -598,14 +615,14 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     fetch_logits(cand);
     // Choice j against the next: clear, of the same numbers (`same`), in doubt
     // (`near`): a bit each.
-    constexpr float kP = 2.0f * kKeyP, kSum = kKeySum;
+    const float kp = 2.0f * key_p(a);
     uint64_t near = 0, same = 0;
     for (int j0 = 0; j0 < cand; j0 += LPT) {
       const int j = j0 + lane;
       bool n = false, e = false;
       if (j < cand) {
         const float k0 = s_key[slot][j], k1 = j + 1 < cand ? s_key[slot][j + 1] : rest;
-        n = k1 > kNegInf && !(k0 - k1 > kP + kSum * (fabsf(k0) + fabsf(k1)));
+        n = k1 > kNegInf && !(k0 - k1 > kp + kKeySum * (fabsf(k0) + fabsf(k1)));
         if (n && j + 1 < cand && s_logit[slot][j] == s_logit[slot][j + 1] &&
             a.bias[s_id[slot][j]] == a.bias[s_id[slot][j + 1]]) {
           n = false;
@@ -819,9 +836,9 @@ template <bool BF16>
 hipError_t launch_size(const RouteArgs& a, bool backward, hipStream_t s) {
   if (a.experts <= 64) return launch_width<BF16, 16, 4>(a, backward, s);
   // Few tokens leave most of the chip empty: a wave a token then, whose keys are
-  // a quarter as many a lane.  256 experts, top 8, 1 / 1024 / 4096 tokens: 4.0 /
-  // 4.5 / 6.3 us against 6.4 / 6.8 / 6.5, groups with a bias 6.0 / 8.0 / 10.8
-  // against 9.7 / 11.9 / 11.8; 128 experts, 4096 tokens: 5.7 against 4.9.
+  // a quarter as many a lane.  256 experts, top 8, 1 / 1024 / 4096 tokens: 3.8 /
+  // 4.1 / 5.6 us against 5.4 / 5.6 / 5.4, groups with a bias 5.8 / 6.2 / 8.4
+  // against 6.9 / 7.3 / 8.3; 128 experts, 4096 tokens: 5.7 against 4.3.
   if (a.experts <= 256 && a.tokens <= 2048) return launch_width<BF16, 64, 4>(a, backward, s);
   if (a.experts <= 128) return launch_width<BF16, 16, 8>(a, backward, s);
   if (a.experts <= 256) return launch_width<BF16, 16, 16>(a, backward, s);
