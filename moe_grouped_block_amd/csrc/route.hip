@@ -793,11 +793,45 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteArgs a) {
   float out[EPL];
 #pragma unroll
   for (int q = 0; q < EPL; ++q) out[q] = 0.0f;
-  for (int j = 0; j < k; ++j) {
-    const int e = s_id[slot][j];
-    const float d = s_d[slot][j];
+  // The choices go to their experts' places by LDS, unless two of them are one
+  // expert's, which shows where each has written its number: those are added in
+  // their order.  (Every lane looking at every choice took 7.0 instead of 5.4 us,
+  // 16381 x 256, and 4.7 instead of 4.4 of 64 experts.)
+  constexpr int PITCH = EPL + 4;                  // (16 bytes more: a row's lanes meet no bank twice)
+  typedef float v4f __attribute__((ext_vector_type(4)));
+  __shared__ __attribute__((aligned(16))) float s_row[TPB][LPT * PITCH];
+  float* const own = s_row[slot] + lane * PITCH;
 #pragma unroll
-    for (int q = 0; q < EPL; ++q) out[q] += R::expert(lane, q / V, q % V) == e ? d : 0.0f;
+  for (int q = 0; q < EPL; q += 4) *reinterpret_cast<v4f*>(own + q) = v4f{};
+  wave_sync();
+  auto place = [&](int e) __attribute__((always_inline)) { return s_row[slot] + e / EPL * PITCH + e % EPL; };
+#pragma unroll
+  for (int i = 0; i < JPL; ++i)
+    if (id[i] >= 0) *place(id[i]) = __int_as_float(lane + i * LPT);
+  wave_sync();
+  bool twice = false;
+#pragma unroll
+  for (int i = 0; i < JPL; ++i)
+    if (id[i] >= 0) twice |= __float_as_int(*place(id[i])) != lane + i * LPT;
+  wave_sync();
+  if (!__any(twice)) {
+#pragma unroll
+    for (int i = 0; i < JPL; ++i)
+      if (id[i] >= 0) *place(id[i]) = s_d[slot][lane + i * LPT] + 0.0f;
+    wave_sync();
+#pragma unroll
+    for (int q = 0; q < EPL; q += 4) {
+      const v4f v = *reinterpret_cast<const v4f*>(own + q);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out[q + e] = v[e];
+    }
+  } else {
+    for (int j = 0; j < k; ++j) {
+      const int e = s_id[slot][j];
+      const float d = s_d[slot][j];
+#pragma unroll
+      for (int q = 0; q < EPL; ++q) out[q] += R::expert(lane, q / V, q % V) == e ? d : 0.0f;
+    }
   }
   if (full) {
     const float r = total > 0.0f ? 1.0f / total : (total == 0.0f ? 0.0f : total);   // NaN stays

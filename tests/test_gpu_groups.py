@@ -166,6 +166,42 @@ def test_without_groups_few_tokens_and_many(t, e, score, with_bias, renormalise)
     assert ((d - dd).abs() <= ref.F32 * dd.abs() + 256 * ref.F32 * g.abs().sum(1, keepdim=True).double()).all()
 
 
+@pytest.mark.parametrize("t", [37, 2051])
+@pytest.mark.parametrize("e,groups,top", [(256, 8, 1), (256, 8, 4), (256, 16, 8), (128, 8, 2), (1024, 16, 8), (512, 8, 3)])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_keys_of_few_groups(t, e, groups, top, with_bias):
+    """Open groups that are at most half of the lanes, whose keys are dealt out: equal and masked
+    experts, more choices than experts that are left, the last expert of a lane."""
+    gen = torch.Generator().manual_seed(t + e + top)
+    x = torch.randint(-3, 4, (t, e), generator=gen).float() * 0.5
+    x[::4] = torch.randn((t + 3) // 4, e, generator=gen)
+    x[1::4, ::2] = -INF
+    x[2::4] = torch.where(torch.rand(x[2::4].shape, generator=gen) < 0.95, -INF, x[2::4])
+    x[3::8] = 0.0
+    x[7::8, ::3] = -0.0                                 # (0 and -0 are one number)
+    bias = torch.randint(-1, 2, (e,), generator=gen).float() * 0.25 if with_bias else None
+    for k in (1, 8, 16, 31):
+        if k <= top * (e // groups):
+            check(x, k, groups, top, 2, "sigmoid", bias, grad=False)
+
+
+@pytest.mark.parametrize("t", [5, 2100])
+@pytest.mark.parametrize("e", [40, 70, 128, 256, 600])
+@pytest.mark.parametrize("k", [4, 20])
+@pytest.mark.parametrize("renormalise", [False, True])
+def test_gradient_of_an_expert_chosen_twice(t, e, k, renormalise):
+    """Ids that a caller has changed: the gradients of equal ones are added, those out of range have none."""
+    x, gen = logits(t, e, t + e + k)
+    ids = torch.randint(-1, e + 1, (t, k), generator=gen, dtype=torch.int32)
+    ids[::3, 1] = ids[::3, 0]
+    ids[1::3] = torch.stack([torch.randperm(e, generator=gen)[:k] for _ in range(ids[1::3].shape[0])]).int()
+    g = torch.randn(t, k, generator=gen)
+    for score in ("softmax", "sigmoid"):
+        d = mg.route_backward(x.cuda(), ids.cuda(), g.cuda(), score=score, renormalise=renormalise).cpu().double()
+        dd = layer_ref.route_backward(x, ids, g, score, renormalise)
+        assert ((d - dd).abs() <= ref.F32 * dd.abs() + 256 * ref.F32 * g.abs().sum(1, keepdim=True).double()).all()
+
+
 def test_no_tokens_and_graph():
     ids, w = mg.route(torch.empty(0, 64, device="cuda"), 4, num_groups=8, top_groups=2)
     assert ids.shape == (0, 4) and w.shape == (0, 4)
