@@ -123,6 +123,7 @@ constexpr int kJpl = (kMaxTopK + LPT - 1) / LPT;
 template <int LPT>
 __device__ __forceinline__ void chosen_weights(const RouteArgs& a, float top, float total, const float* l, float* w) {
   constexpr int JPL = kJpl<LPT>;
+  const int k = a.top_k;
   if (a.renormalise) {
     float m = l[0];
 #pragma unroll
@@ -133,6 +134,8 @@ __device__ __forceinline__ void chosen_weights(const RouteArgs& a, float top, fl
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < JPL; ++i) {
+      w[i] = 0.0f;
+      if (i * LPT >= k) continue;                // (the same for all)
       const float e = a.softmax ? expf(l[i] - mm) : 1.0f / (em + expf(mm - l[i]));
       w[i] = l[i] == kNegInf ? 0.0f : e;
       sum += w[i];
@@ -144,6 +147,8 @@ __device__ __forceinline__ void chosen_weights(const RouteArgs& a, float top, fl
   } else {
 #pragma unroll
     for (int i = 0; i < JPL; ++i) {
+      w[i] = 0.0f;
+      if (i * LPT >= k) continue;
       const float p = a.softmax ? expf(l[i] - top) / total : sigmoid(l[i]);
       w[i] = l[i] == kNegInf ? 0.0f : a.scale * p;
     }
@@ -159,7 +164,7 @@ __device__ __forceinline__ void chosen_weights(const RouteArgs& a, float top, fl
 // the larger ones, and where one is taken the smaller moves up.  (The first of a
 // lane's equal keys is singled out in the masks of the comparisons, by scalar
 // instructions.  16381 tokens of 256 experts: 8.2 us, without pairs 1.0 more; with a
-// bias 11.0 and 1.5 more.)
+// bias 10.9 and 1.5 more.)
 __device__ __forceinline__ int32_t larger(int32_t a, int32_t b) { return max(a, b); }
 __device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
 // fp32 keys are compared as integers of the same order (-0 is 0): a step of a
@@ -228,7 +233,7 @@ __device__ __forceinline__ float fast_sigmoid(float x) { return __builtin_amdgcn
 // clear gap are put into the order of their keys in 64 bits, one key a lane;
 // where no gap follows, the wave's tokens are chosen again with all keys in 64
 // bits.  Measured, 16381 tokens, 256 experts, sigmoid: 64 bits for every token
-// 30 us, this form 11 us.
+// 30 us, this form 10.9 us.
 constexpr int kSpare = 2;
 constexpr int kSlots = kMaxTopK + kSpare;
 
@@ -238,7 +243,7 @@ constexpr int kSlots = kMaxTopK + kSpare;
 // the reciprocal's 2 u, below 4 u; softmax: p |x| < 0.4, and a sum of up to 16 + 6
 // terms with errors of their own, below 50 u.  The sigmoid's is taken twice: what
 // counts is how few tokens are in doubt, whose waves end last (16381 x 256, 4 of 8
-// groups with a bias, with 50 u for both 12.5 instead of 11.9 us).
+// groups with a bias, with 50 u for both 0.6 us more).
 constexpr float kUnit = 5.9604645e-8f, kKeySum = 4.0f * kUnit;
 __device__ __forceinline__ float key_p(const RouteArgs& a) { return (a.softmax ? 50.0f : 8.0f) * kUnit; }
 
@@ -256,9 +261,9 @@ struct alignas(16) GroupScratch {
   float edge[4];
 };
 
-// The two largest of a set, one more value or another set's two taken in.
+// The two largest of a set, one more value taken in.
 __device__ __forceinline__ void take(float& b0, float& b1, float v) {
-  b1 = fmaxf(b1, fminf(b0, v));
+  b1 = __builtin_amdgcn_fmed3f(b0, b1, v);
   b0 = fmaxf(b0, v);
 }
 
@@ -274,8 +279,8 @@ __device__ __forceinline__ void take(float& b0, float& b1, float v) {
 // theirs again in 64 bits.  (It is rare, but among 16381 tokens there always are
 // such, and their waves are the last to end.)
 // Measured, 16381 tokens, top 8 of 4 of 8 groups of 32 by their two best,
-// sigmoid, without a bias (with one): 10.6 (11.9) us, where groups by their best
-// logit take 8.7 and no groups 8.2 (11.0); 64 bits for all experts of a wave in
+// sigmoid, without a bias (with one): 10.2 (11.3) us, where groups by their best
+// logit take 8.2 and no groups 8.2 (10.9); 64 bits for all experts of a wave in
 // doubt 6.6 (4 to 6) more.
 template <typename R, bool LOGITS, int LPT, int EPL, typename P>
 __device__ __forceinline__ uint32_t closed_groups(const RouteArgs& a, GroupScratch<LPT, EPL>& lds, const float* x, const float* score,
@@ -565,6 +570,10 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
       if (a.group_lanes && 2 * a.top_groups * a.group_lanes <= LPT)
         return choose_open<LPT, EPL>(a, scratch[slot], key, !closed, rounds, lane, s_id[slot], keys);
     }
+    if constexpr (GROUPS) {
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) key[j] = closed >> j & 1 ? kNegInf : key[j];
+    }
     return lanes_max<LPT>(choose<LPT, EPL, float>(key, rounds, lane, lane * EPL, s_id[slot], keys));
   };
   __shared__ GroupScratch<LPT, GROUPS ? EPL : 1> scratch[GROUPS ? TPB : 1];
@@ -573,8 +582,6 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     for (int j = 0; j < EPL; ++j) key[j] = x[j] > kNegInf ? x[j] : kNegInf;
     if constexpr (GROUPS) {
       closed = closed_groups<R, true>(a, scratch[slot], x, key, score_of, top, row, lane);
-#pragma unroll
-      for (int j = 0; j < EPL; ++j) key[j] = closed >> j & 1 ? kNegInf : key[j];
     }
     best_of(scratch, k, s_logit[slot]);            // (the keys are the logits)
     wave_sync();
@@ -599,8 +606,6 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     else keys_of([&](float l, float b) __attribute__((always_inline)) { return fast_sigmoid(l) + b; });
     if constexpr (GROUPS) {
       closed = closed_groups<R, false>(a, scratch[slot], x, key, score_of, top, row, lane);
-#pragma unroll
-      for (int j = 0; j < EPL; ++j) key[j] = closed >> j & 1 ? kNegInf : key[j];
     }
     const int cand = min(k + kSpare, a.experts);
     const float rest = best_of(scratch, cand, s_key[slot]);
@@ -795,8 +800,8 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteArgs a) {
   for (int q = 0; q < EPL; ++q) out[q] = 0.0f;
   // The choices go to their experts' places by LDS, unless two of them are one
   // expert's, which shows where each has written its number: those are added in
-  // their order.  (Every lane looking at every choice took 7.0 instead of 5.4 us,
-  // 16381 x 256, and 4.7 instead of 4.4 of 64 experts.)
+  // their order.  (Every lane looking at every choice took 7.0 instead of 5.3 us,
+  // 16381 x 256, and 4.7 instead of 4.3 of 64 experts.)
   constexpr int PITCH = EPL + 4;                  // (16 bytes more: a row's lanes meet no bank twice)
   typedef float v4f __attribute__((ext_vector_type(4)));
   __shared__ __attribute__((aligned(16))) float s_row[TPB][LPT * PITCH];
