@@ -378,7 +378,8 @@ moegg_status run_linear(const moegg_linear_problem* problem, const moegg_linear_
   if (a.x8.kind != moegg::ROW_BF16) return set_error(MOEGG_ERROR_NOT_SUPPORTED, "x_dtype: the forward reads a BF16 x");
   if (any && a.c_kind != moegg::ROW_BF16 && (!a.c || !a.c_sf))
     return set_error(MOEGG_ERROR_INVALID_VALUE, "c and c_sf are required with c_dtype");
-  const int64_t workspace = moegg::linear_workspace(a);
+  const moegg::LinearPlan plan = moegg::plan_linear(a);
+  const int64_t workspace = plan.workspace;
   st = check_linear_pointers(p, *args, saved, workspace);
   if (st != MOEGG_OK) return st;
   const int64_t n_out = p.act == MOEGG_ACT_SWIGLU ? p.n / 2 : p.n;
@@ -395,7 +396,7 @@ moegg_status run_linear(const moegg_linear_problem* problem, const moegg_linear_
   if (overlap(a.residual, p.m * n_out * 2, a.y, y_bytes) && (a.out_f32 || static_cast<const void*>(a.residual) != a.y))
     return set_error(MOEGG_ERROR_INVALID_VALUE, "residual and y overlap without being the same BF16 tensor");
   if (!any) return launched(hipSuccess, "linear");
-  return launched(moegg::launch_linear(a, static_cast<hipStream_t>(stream)), "linear kernel");
+  return launched(moegg::launch_linear(a, plan, static_cast<hipStream_t>(stream)), "linear kernel");
 }
 
 moegg_status run_linear_backward(const moegg_linear_problem* problem, const moegg_linear_args* args,
@@ -419,7 +420,8 @@ moegg_status run_linear_backward(const moegg_linear_problem* problem, const moeg
   if (any && a.c && a.c_kind != moegg::ROW_BF16 && !a.c_sf) return set_error(MOEGG_ERROR_INVALID_VALUE, "c in 8 bits needs c_sf");
   if (any && a.dw && a.x8.kind != moegg::ROW_BF16 && !a.x8.scales)
     return set_error(MOEGG_ERROR_INVALID_VALUE, "x in 8 bits needs x_sf");
-  const int64_t workspace = moegg::linear_backward_workspace(a, a.dx, a.dw, a.db);
+  const moegg::LinearPlan plan = moegg::plan_linear_backward(a, a.dx, a.dw, a.db);
+  const int64_t workspace = plan.workspace;
   st = check_linear_pointers(p, *args, saved, workspace);
   if (st != MOEGG_OK) return st;
   const int64_t n_out = p.act == MOEGG_ACT_SWIGLU ? p.n / 2 : p.n;
@@ -430,7 +432,7 @@ moegg_status run_linear_backward(const moegg_linear_problem* problem, const moeg
                       {"db", a.db, int64_t{p.num_groups} * p.n * 4}, {"workspace", a.workspace, workspace}};
   if ((st = check_apart(in, out)) != MOEGG_OK) return st;
   if (none) return launched(hipSuccess, "linear backward");
-  return launched(moegg::launch_linear_backward(a, static_cast<hipStream_t>(stream)), "linear backward kernel");
+  return launched(moegg::launch_linear_backward(a, plan, static_cast<hipStream_t>(stream)), "linear backward kernel");
 }
 
 // ---- norm, rows kept in 8 bits -----------------------------------------------------
@@ -709,23 +711,23 @@ moegg_status moegg_unsort(const float* rows_values, const int32_t* row_of, float
 
 int64_t moegg_linear_workspace(const moegg_linear_problem* problem) {
   if (check_linear(problem) != MOEGG_OK) return -1;
-  return moegg::linear_workspace(linear_args(*problem, nullptr));
+  return moegg::plan_linear(linear_args(*problem, nullptr)).workspace;
 }
 
 int64_t moegg_linear_backward_workspace(const moegg_linear_problem* problem, int32_t want) {
   if (check_linear(problem) != MOEGG_OK) return -1;
-  return moegg::linear_backward_workspace(linear_args(*problem, nullptr), want & 1, want & 2, want & 4);
+  return moegg::plan_linear_backward(linear_args(*problem, nullptr), want & 1, want & 2, want & 4).workspace;
 }
 
 int64_t moegg_linear_saving_workspace(const moegg_linear_problem* problem, const moegg_linear_saved* saved) {
   if (check_linear(problem) != MOEGG_OK || (saved && check_saved(*problem, *saved) != MOEGG_OK)) return -1;
-  return moegg::linear_workspace(linear_args(*problem, nullptr, saved));
+  return moegg::plan_linear(linear_args(*problem, nullptr, saved)).workspace;
 }
 
 int64_t moegg_linear_saved_backward_workspace(const moegg_linear_problem* problem, const moegg_linear_saved* saved,
                                               int32_t want) {
   if (check_linear(problem) != MOEGG_OK || (saved && check_saved(*problem, *saved) != MOEGG_OK)) return -1;
-  return moegg::linear_backward_workspace(linear_args(*problem, nullptr, saved), want & 1, want & 2, want & 4);
+  return moegg::plan_linear_backward(linear_args(*problem, nullptr, saved), want & 1, want & 2, want & 4).workspace;
 }
 
 moegg_status moegg_linear(const moegg_linear_problem* problem, const moegg_linear_args* args, void* stream) {

@@ -192,9 +192,15 @@ struct LinearArgs {
   SavedRows x8;             // x in 8 bits (kind ROW_BF16: none)    [backward]
 };
 // Bytes of workspace (pointers in `a` only say what is asked for).
-int64_t linear_workspace(const LinearArgs& a);
-int64_t linear_backward_workspace(const LinearArgs& a, bool dx, bool dw, bool db);
-hipError_t launch_linear(const LinearArgs& a, hipStream_t s);
-hipError_t launch_linear_backward(const LinearArgs& a, hipStream_t s);
+// A call's workspace in bytes, and its tiles in linear.hip's own form: made once
+// for the check of the workspace and the launch (a plan is 0.3 us, a small call 8).
+struct LinearPlan {
+  int64_t workspace;
+  int64_t detail[20];
+};
+LinearPlan plan_linear(const LinearArgs& a);
+LinearPlan plan_linear_backward(const LinearArgs& a, bool dx, bool dw, bool db);
+hipError_t launch_linear(const LinearArgs& a, const LinearPlan& plan, hipStream_t s);
+hipError_t launch_linear_backward(const LinearArgs& a, const LinearPlan& plan, hipStream_t s);
 
 }  // namespace moegg

@@ -8,6 +8,9 @@
 //
 // Group g owns rows [offsets[g-1], offsets[g]) (any numbers, no alignment);
 // without offsets there is one group of all rows.
+#include <cstring>
+#include <type_traits>
+
 #include "linear_gemm.h"
 
 namespace moegg {
@@ -505,9 +508,10 @@ bool few_rows(const LinearArgs& a) {
 // 8200 x 4096 x 4096 244 -> 230, 16390 x 64 x 2048 28.4 -> 24.0.
 struct ForwardPlan {
   Plan tiles;
-  int64_t few;
+  int64_t few;                // all of them: no tiles
 };
 ForwardPlan plan_forward(const LinearArgs& a) {
+  if (a.m == 0 || few_rows(a)) return {Plan{}, a.m};
   ForwardPlan f{plan_rows(a, MODE_FORWARD), 0};
   const int64_t few = a.m % 128;
   if (a.c_kind == ROW_BF16 && a.groups == 1 && !a.offsets && few && few <= kFewRows && few < a.m) {
@@ -610,38 +614,57 @@ hipError_t launch_both(const LinearArgs& a, const Plan& dx, const Plan& dw, cons
 // of dw reads the codes itself (64 groups of 1408 x 2048, 24571 rows: 454 -> 434
 // to 440 us, 16384 x 2816 x 2048 378 -> 376, and no copy of x in memory); the
 // others are fed by direct loads alone.
-bool x_by_workspace(const LinearArgs& a) { return a.x8.kind != ROW_BF16 && plan_dw(a).shape != SHAPE_256; }
+bool x_by_workspace(const LinearArgs& a, const Plan& dw) { return a.x8.kind != ROW_BF16 && dw.shape != SHAPE_256; }
 
-// Workspace of the backward: dz, the column sums of the row tiles, the parts
-// of dx and of dw, and x in BF16 where it is kept in 8 bits.
-struct BackwardWorkspace {
-  int64_t dz, sums, dx, dw, x, total;
+// The backward's tiles, and the places in its workspace of dz, the column sums
+// of the row tiles, the parts of dx and of dw, and x in BF16 where it is kept in 8
+// bits.
+struct BackwardPlan {
+  Plan dx, dw;
+  int64_t dz_at, sums_at, dx_at, dw_at, x_at, total;
 };
-BackwardWorkspace backward_workspace(const LinearArgs& a, bool dx, bool dw, bool db) {
-  BackwardWorkspace w{};
+BackwardPlan plan_backward(const LinearArgs& a, bool dx, bool dw, bool db) {
+  BackwardPlan p{};
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t here = at;
     at += round_up(bytes, 256);
     return here;
   };
-  w.dz = take(a.act != LIN_NONE && (dx || dw) ? a.m * a.n * 2 : 0);
-  w.sums = take(db ? row_tiles(a, dz_rows(a)) * a.n * 4 : 0);
-  w.dx = take(dx && a.m ? plan_rows(a, MODE_DX).partial_bytes : 0);
-  w.dw = take(dw ? plan_dw(a).partial_bytes : 0);
-  w.x = take(dw && x_by_workspace(a) ? a.m * a.k * 2 : 0);
-  w.total = at;
-  return w;
+  if (dx && a.m) p.dx = plan_rows(a, MODE_DX);
+  if (dw) p.dw = plan_dw(a);
+  p.dz_at = take(a.act != LIN_NONE && (dx || dw) ? a.m * a.n * 2 : 0);
+  p.sums_at = take(db ? row_tiles(a, dz_rows(a)) * a.n * 4 : 0);
+  p.dx_at = take(p.dx.partial_bytes);
+  p.dw_at = take(p.dw.partial_bytes);
+  p.x_at = take(dw && x_by_workspace(a, p.dw) ? a.m * a.k * 2 : 0);
+  p.total = at;
+  return p;
+}
+
+template <typename T>
+LinearPlan packed(const T& t, int64_t workspace) {
+  static_assert(sizeof(T) <= sizeof(LinearPlan::detail) && std::is_trivially_copyable_v<T>, "the form that callers pass on");
+  LinearPlan p{workspace, {}};
+  memcpy(p.detail, &t, sizeof(T));
+  return p;
+}
+template <typename T>
+T unpacked(const LinearPlan& p) {
+  T t;
+  memcpy(&t, p.detail, sizeof(T));
+  return t;
 }
 
 }  // namespace
 
-int64_t linear_workspace(const LinearArgs& a) {
-  if (a.m == 0 || few_rows(a)) return 0;
-  return plan_forward(a).tiles.partial_bytes;
+LinearPlan plan_linear(const LinearArgs& a) {
+  const ForwardPlan f = plan_forward(a);
+  return packed(f, f.tiles.partial_bytes);
 }
-int64_t linear_backward_workspace(const LinearArgs& a, bool dx, bool dw, bool db) {
-  return backward_workspace(a, dx, dw, db).total;
+LinearPlan plan_linear_backward(const LinearArgs& a, bool dx, bool dw, bool db) {
+  const BackwardPlan p = plan_backward(a, dx, dw, db);
+  return packed(p, p.total);
 }
 
 // Many workgroups (groups): small ones of 4 waves and 32 columns, four to a
@@ -661,12 +684,12 @@ hipError_t launch_few_rows(const LinearArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_linear(const LinearArgs& args, hipStream_t s) {
+hipError_t launch_linear(const LinearArgs& args, const LinearPlan& plan, hipStream_t s) {
   LinearArgs a = args;
+  const ForwardPlan p = unpacked<ForwardPlan>(plan);
   if (a.m == 0) return hipSuccess;
-  if (few_rows(a)) return launch_few_rows(a, s);
+  if (p.few == a.m) return launch_few_rows(a, s);
   a.dx_partial = static_cast<float*>(a.workspace);
-  const ForwardPlan p = plan_forward(a);
   a.m -= p.few;
   const hipError_t e = launch_tiles<MODE_FORWARD>(a, p.tiles, s);
   if (e != hipSuccess || !p.few) return e;
@@ -699,19 +722,19 @@ void launch_dz_kind(const LinearArgs& a, const DzPlan& p, dim3 grid, hipStream_t
 }
 }  // namespace
 
-hipError_t launch_linear_backward(const LinearArgs& args, hipStream_t s) {
+hipError_t launch_linear_backward(const LinearArgs& args, const LinearPlan& plan, hipStream_t s) {
   LinearArgs a = args;
-  const BackwardWorkspace w = backward_workspace(a, a.dx, a.dw, a.db);
+  const BackwardPlan w = unpacked<BackwardPlan>(plan);
   uint8_t* const ws = static_cast<uint8_t*>(a.workspace);
   const bool make_dz = a.act != LIN_NONE && (a.dx || a.dw) && a.m;
-  const bool x8 = a.dw && x_by_workspace(a);
-  uint16_t* const dz = make_dz ? reinterpret_cast<uint16_t*>(ws + w.dz) : nullptr;
-  float* const sums = a.db ? reinterpret_cast<float*>(ws + w.sums) : nullptr;
-  uint16_t* const x = x8 ? reinterpret_cast<uint16_t*>(ws + w.x) : nullptr;
+  const bool x8 = a.dw && x_by_workspace(a, w.dw);
+  uint16_t* const dz = make_dz ? reinterpret_cast<uint16_t*>(ws + w.dz_at) : nullptr;
+  float* const sums = a.db ? reinterpret_cast<float*>(ws + w.sums_at) : nullptr;
+  uint16_t* const x = x8 ? reinterpret_cast<uint16_t*>(ws + w.x_at) : nullptr;
   const int rows = dz_rows(a);
   a.dz = make_dz ? dz : a.dy;
-  a.dx_partial = reinterpret_cast<float*>(ws + w.dx);
-  a.dw_partial = reinterpret_cast<float*>(ws + w.dw);
+  a.dx_partial = reinterpret_cast<float*>(ws + w.dx_at);
+  a.dw_partial = reinterpret_cast<float*>(ws + w.dw_at);
   hipError_t e = hipSuccess;
   if ((make_dz || a.db) && a.m) {
     const int64_t tiles = row_tiles(a, rows);
@@ -738,16 +761,15 @@ hipError_t launch_linear_backward(const LinearArgs& args, hipStream_t s) {
     const int q = row_tiles(a, rows) <= 16 * static_cast<int64_t>(a.groups) ? 2 : 16;
     db = {sums, rows, q, static_cast<int>(div_up(a.n, 512 / q)), a.groups};
   }
-  const Plan pdx = plan_rows(a, MODE_DX), pdw = plan_dw(a);
-  if (a.dx && a.dw && both(a, pdx, pdw)) return launch_both(a, pdx, pdw, db, s);
+  if (a.dx && a.dw && both(a, w.dx, w.dw)) return launch_both(a, w.dx, w.dw, db, s);
   if (a.db) {
     const dim3 grid(static_cast<unsigned>(db.cols), static_cast<unsigned>(db.groups));
     if (db.q == 2) hipLaunchKernelGGL((linear_db_kernel<2>), grid, dim3(512), 0, s, a, db);
     else hipLaunchKernelGGL((linear_db_kernel<16>), grid, dim3(512), 0, s, a, db);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  if (a.dx && a.m && (e = launch_tiles<MODE_DX>(a, pdx, s)) != hipSuccess) return e;
-  if (a.dw && (e = launch_tiles<MODE_DW>(a, pdw, s)) != hipSuccess) return e;
+  if (a.dx && a.m && (e = launch_tiles<MODE_DX>(a, w.dx, s)) != hipSuccess) return e;
+  if (a.dw && (e = launch_tiles<MODE_DW>(a, w.dw, s)) != hipSuccess) return e;
   return e;
 }
 

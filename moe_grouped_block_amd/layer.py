@@ -524,13 +524,14 @@ _KEPT = {"e4m3": 1, "e5m2": 4}
 _KEPT_OR_NOT = {"bf16": 3, **_KEPT}
 
 
-def _pair(t, name: str, rows: int, width: int, sf_layout: str, dev: int):
-    """Addresses of the codes (rows, width) and scales of rows kept in 8 bits."""
+def _is_pair(t, name: str) -> None:
     if not isinstance(t, (tuple, list)) or len(t) != 2:
         raise TypeError(f"{name}: a pair (codes, scales) expected")
-    shape = (width // 128, rows, 4) if sf_layout == "kplanes" else (rows, width // 32)
-    return (_want(t[0], f"{name}[0]", torch.uint8, (rows, width), dev),
-            _want(t[1], f"{name}[1]", torch.uint8, shape, dev))
+
+
+def _scales(t, name: str, rows: int, width: int, sf_layout: str, dev: int) -> int:
+    """Address of the scales of rows kept in 8 bits (one of the pair's tensors)."""
+    return _want(t, name, torch.uint8, (width // 128, rows, 4) if sf_layout == "kplanes" else (rows, width // 32), dev)
 
 
 def quantise(x, *, dtype="e4m3", sf_layout: str = "row_major", out=None, stream=None):
@@ -554,15 +555,14 @@ def quantise(x, *, dtype="e4m3", sf_layout: str = "row_major", out=None, stream=
 
 def dequantise(rows, *, dtype="e4m3", sf_layout: str = "row_major", to="bf16", stream=None):
     """x (T, H) in bf16 or fp32 (``to``) of its (codes, scales)."""
-    if not isinstance(rows, (tuple, list)) or len(rows) != 2:
-        raise TypeError("rows: a pair (codes, scales) expected")
+    _is_pair(rows, "rows")
     dev = _lead(rows[0], "rows[0]", (torch.uint8,), 2)
     n, width = rows[0].shape
     _fits(width)
     kind, layout = _code(_KEPT, _dtype_name(dtype), "dtype"), _code(mg.SF_LAYOUTS, sf_layout, "sf_layout")
     to = _dtype_name(to)
     code = _code(_LINEAR_DTYPES, to, "to")
-    cp, sp = _pair(rows, "rows", n, width, sf_layout, dev)
+    cp, sp = rows[0].data_ptr(), _scales(rows[1], "rows[1]", n, width, sf_layout, dev)
     s, guard = _on(dev, stream)
     try:
         x = rows[0].new_empty((n, width), dtype=torch.float32 if to == "f32" else torch.bfloat16)
@@ -660,17 +660,18 @@ def linear_backward(dy, x, w, *, c=None, act: str = "none", offsets=None, need=(
     if x8 or c8:
         keep = mg.moegg_linear_saved(_code(_KEPT_OR_NOT, x_dtype, "x_dtype"), _code(mg.SF_LAYOUTS, sf_layout, "sf_layout"),
                                      _code(_KEPT_OR_NOT, c_dtype, "c_dtype") if c8 else 3)
-    if x8 and (not isinstance(x, (tuple, list)) or len(x) != 2):
-        raise TypeError("x: a pair (codes, scales) expected")
+    if x8:
+        _is_pair(x, "x")
     dev, p, lead, xp, wp, op = _linear_problem(x[0] if x8 else x, w, act, dw_dtype, offsets,
                                                torch.uint8 if x8 else torch.bfloat16)
     m, n, k = p.m, p.n, p.k
     if x8:
-        _, keep.x_sf = _pair(x, "x", m, k, sf_layout, dev)
+        keep.x_sf = _scales(x[1], "x[1]", m, k, sf_layout, dev)
     dp = _want(dy, "dy", torch.bfloat16, (m, n // 2 if act == "swiglu" else n), dev)
     cp = None
     if c is not None and c8:
-        cp, keep.c_sf = _pair(c, "c", m, n, "row_major", dev)
+        _is_pair(c, "c")
+        cp, keep.c_sf = _want(c[0], "c[0]", torch.uint8, (m, n), dev), _scales(c[1], "c[1]", m, n, "row_major", dev)
     elif c is not None:
         cp = _want(c, "c", torch.bfloat16, (m, n), dev)
     elif act != "none":
