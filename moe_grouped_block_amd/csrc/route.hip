@@ -645,7 +645,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
       if (__any(doubt)) {
         const bool all = __any(doubt && open);
         double exact[EPL];
-        double dt = 1.0;
+        double dt = 1.0;                           // (and fma by name, as for the keys in fp32)
         if (a.softmax || all) {
           double sum = 0.0;
 #pragma unroll
@@ -659,7 +659,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
 #pragma unroll
           for (int j = 0; j < EPL; ++j) {
             const int e = R::expert(lane, j / V, j % V);
-            const double q = exact[j] * dt + a.bias[e < a.experts ? e : 0];
+            const double q = fma(exact[j], dt, static_cast<double>(a.bias[e < a.experts ? e : 0]));
             exact[j] = x[j] > kNegInf && !(closed >> j & 1) && q > -__builtin_inf() ? q : -__builtin_inf();
           }
           choose<LPT, EPL, double>(exact, k, lane, lane * EPL, s_id[slot], nullptr);
@@ -678,7 +678,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
             mine[i] = 0.0;
             if (id[i] >= 0) {
               const double l = lg[i];
-              mine[i] = (a.softmax ? exp(l - top) * dt : 1.0 / (1.0 + exp(-l))) + a.bias[id[i]];
+              mine[i] = fma(a.softmax ? exp(l - top) : 1.0 / (1.0 + exp(-l)), dt, static_cast<double>(a.bias[id[i]]));
               s_exact[slot][j] = mine[i];
             }
           }

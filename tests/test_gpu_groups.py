@@ -1,5 +1,6 @@
 """GPU tests of the router that chooses groups of experts first, against the
 float64 reference: the choice exactly, weights and gradient as route()'s."""
+import itertools
 import math
 
 import pytest
@@ -42,6 +43,49 @@ def check(x, k, groups, top, best, score="softmax", bias=None, renormalise=True,
         most = (g.abs().sum(1, keepdim=True) * abs(scale)).double()
         assert ((d - dd).abs() <= eps * dd.abs() + 256 * ref.F32 * most + 1e-37).all()
     return ids, w
+
+
+def check_up_to_64_bits(x, k, groups, top, best, score, bias):
+    """As check() of the ids, where scores may be nearer than 64 bits tell.  With v = 2^-53: a score is an
+    exponential (2 v of it), a sum and a quotient (v each; the softmax's sum of at most 1024 terms, by
+    partial sums of at most 16 + 6, 24 v), so p is off by at most 30 v in either order of the operations, p +
+    bias by 2 v more (|p + bias| < 2), and a sum of two keys by 2 * 32 v + 2 v: numbers nearer than twice that,
+    132 v < 2^-45, can stand in either order.  Logits are exact.  Such a row's choice has to be one that
+    some order of such numbers gives."""
+    t, e = x.shape
+    size, near = e // groups, 2.0 ** -45
+    print(f"[gpu-case] route {t}x{e} top {k} of {top}/{groups} groups best={best} {score} bias={bias is not None}", flush=True)
+    ids, _ = mg.route(x.cuda(), k, score=score, bias=None if bias is None else bias.cuda(), num_groups=groups,
+                      top_groups=top, group_best=best)
+    ids = ids.cpu().long()
+    want = ref.route_grouped(x, k, groups, top, best, score, bias)
+    for i in (ids != want).any(1).nonzero().flatten().tolist():
+        l = x[i].double()
+        p = torch.where(l > -INF, torch.softmax(l, 0) if score == "softmax" else torch.sigmoid(l), 0.0)
+        key = torch.where(l > -INF, l if bias is None else p + bias.double(), -INF)
+        base = key if bias is not None or best == 1 else torch.where(l > -INF, p, -INF)
+        two = base.reshape(groups, size).topk(best, 1).values
+        g = torch.where(two[:, -1] > -INF, two.sum(1), two[:, 0])
+        edge = g.sort(descending=True).values[top - 1]
+        sharp = bias is None and best == 1
+        assert not sharp, i
+        sure = [q for q in range(groups) if g[q] > edge + near]
+        maybe = [q for q in range(groups) if abs(g[q] - edge) <= near]
+        fits = False
+        for some in itertools.combinations(maybe, top - len(sure)):
+            open_ = torch.zeros(groups, dtype=torch.bool)
+            open_[list(sure) + list(some)] = True
+            kk = torch.where(open_.repeat_interleave(size), key, -INF)
+            if bias is None:
+                order = sorted((j for j in range(e) if kk[j] > -INF), key=lambda j: (-kk[j].item(), j))[:k]
+                fits |= ids[i].tolist() == order + [-1] * (k - len(order))
+            else:
+                got = [j for j in ids[i].tolist() if j >= 0]
+                v, left = kk[got], kk.clone()
+                left[got] = -INF
+                fits |= len(set(got)) == len(got) == min(k, int((kk > -INF).sum())) and bool(
+                    (v > -INF).all() and (v[1:] <= v[:-1] + near).all() and (len(got) == 0 or left.max() <= v[-1] + near))
+        assert fits, (i, ids[i].tolist(), want[i].tolist())
 
 
 def logits(t, e, seed, dtype=torch.float32, spread=1.5):
@@ -89,6 +133,24 @@ def test_scores_next_to_each_other(score):
     check(x, 4, 8, 3, 1, score, bias)
     # pairs that swap their members' bits between them: sums equal in exact numbers
     check(torch.cat([x[:, :32], x[:, :32].flip(1)], 1), 4, 8, 3, 2, score)
+
+
+@pytest.mark.parametrize("t,e,groups,top", [(300, 60, 5, 2), (200, 1000, 8, 3), (200, 640, 5, 2), (2100, 256, 8, 4), (300, 256, 8, 4),
+                                            (2100, 160, 8, 3), (2100, 120, 10, 4), (100, 1024, 16, 7)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_scores_next_to_each_other_of_all_shapes(t, e, groups, top, score, with_bias):
+    """The same for groups of whole lanes, of parts of them and of more than 32 experts: all of a token's
+    experts within a few steps of fp32, empty groups among them."""
+    gen = torch.Generator().manual_seed(e + t)
+    x = torch.randn(t, 1, generator=gen).expand(t, e).contiguous()
+    x = x * (1.0 + torch.randint(-3, 4, (t, e), generator=gen) * 2.0 ** -22)
+    x[1::4] = torch.where(torch.rand(x[1::4].shape, generator=gen) < 0.9, -INF, x[1::4])
+    x[2::4, :e // groups] = -INF
+    x[3::4] += torch.rand(x[3::4].shape, generator=gen) * 1e-5
+    bias = 0.25 + torch.randint(-4, 5, (e,), generator=gen) * 2.0 ** -24 if with_bias else None
+    for best in (1, 2):
+        check_up_to_64_bits(x, 6, groups, top, best, score, bias)
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
