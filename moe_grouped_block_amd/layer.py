@@ -603,8 +603,8 @@ def linear(x, w, *, bias=None, act: str = "none", residual=None, offsets=None, s
     """y = act(x w^T + bias) + residual: x (M, K) bf16, w (N, K) bf16, or with
     ``offsets`` (L, int32 ends of the groups' rows) w (L, N, K) and bias
     (L, N).  ``dtype`` of y: bf16 or f32.  With ``save_c`` returns (y, c), c
-    the pre-activation that linear_backward() takes: in bf16 (True), or kept in
-    8 bits ("e4m3" or "e5m2") as (codes, scales (M, N / 32)).  Rows behind the
+    the pre-activation that linear_backward() takes: in bf16 (True or "bf16"), or
+    kept in 8 bits ("e4m3" or "e5m2") as (codes, scales (M, N / 32)).  Rows behind the
     last group are not written: `out` keeps them, new tensors (c too) hold
     anything there."""
     dtype = _dtype_name(dtype)
@@ -616,8 +616,10 @@ def linear(x, w, *, bias=None, act: str = "none", residual=None, offsets=None, s
     rp = None if residual is None else _want(residual, "residual", torch.bfloat16, shape, dev)
     lib = mg._load()
     keep = None
-    if isinstance(save_c, str):
-        keep = mg.moegg_linear_saved(3, 0, _code(_KEPT, save_c, "save_c"))
+    if isinstance(save_c, (str, torch.dtype)):
+        kept = _code(_KEPT_OR_NOT, _dtype_name(save_c), "save_c")
+        if kept != _KEPT_OR_NOT["bf16"]:
+            keep = mg.moegg_linear_saved(3, 0, kept)
     # (-1: an invalid problem, which the call refuses)
     need = lib.moegg_linear_workspace(p) if keep is None else lib.moegg_linear_saving_workspace(p, keep)
     s, guard = _on(dev, stream)
