@@ -437,6 +437,8 @@ moegg_status run_linear_backward(const moegg_linear_problem* problem, const moeg
 
 // ---- norm, rows kept in 8 bits -----------------------------------------------------
 
+int norm_kind(const moegg_norm_problem& p) { return p.mx_dtype == MOEGG_DT_NONE ? moegg::ROW_BF16 : row_kind(p.mx_dtype); }
+
 moegg_status check_norm(const moegg_norm_problem* pp, bool backward) {
   if (!pp) return set_error(MOEGG_ERROR_INVALID_VALUE, "problem must be non-NULL");
   const moegg_norm_problem& p = *pp;
@@ -461,9 +463,8 @@ moegg_status check_norm(const moegg_norm_problem* pp, bool backward) {
     return set_error(MOEGG_ERROR_NOT_SUPPORTED, "width=%d: a positive multiple of %d needed", p.width, step);
   if (p.width > moegg::kMaxNormWidth)
     return set_error(MOEGG_ERROR_NOT_SUPPORTED, "width=%d above %d", p.width, moegg::kMaxNormWidth);
-  // (a power of two of waves, below twice the pieces of 1024 columns; the backward's grid is bounded)
-  const int64_t waves = (p.width + 1023) / 1024 * 2;
-  if (!backward && (p.rows + 4) * waves * 64 > moegg::kLaunchThreads)
+  // (the backward's grid is bounded)
+  if (!backward && moegg::rms_norm_threads(p.rows, p.width, p.stream_dtype == MOEGG_DT_F32, norm_kind(p)) > moegg::kLaunchThreads)
     return set_error(MOEGG_ERROR_NOT_SUPPORTED, "rows=%lld width=%d: more threads than a launch holds", (long long)p.rows, p.width);
   return MOEGG_OK;
 }
@@ -485,7 +486,7 @@ moegg::NormArgs norm_args(const moegg_norm_problem& p, const moegg_norm_args& q,
     a.y = static_cast<uint16_t*>(q.y);
     a.codes = q.codes;
     a.scales = q.sf;
-    a.kind = p.mx_dtype == MOEGG_DT_NONE ? moegg::ROW_BF16 : row_kind(p.mx_dtype);
+    a.kind = norm_kind(p);
     a.x_f32 = p.x_dtype == MOEGG_DT_F32;
     a.kplanes = p.sf_layout == MOEGG_SF_KPLANES;
   }

@@ -143,6 +143,7 @@ struct NormArgs {
   double eps;
   double inverse_width;
 };
+int64_t rms_norm_threads(int64_t rows, int32_t width, bool stream_f32, int kind);
 hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s);
 int64_t rms_norm_backward_workspace(int64_t rows, int32_t width);
 hipError_t launch_rms_norm_backward(const NormArgs& a, hipStream_t s);

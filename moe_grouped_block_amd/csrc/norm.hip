@@ -398,6 +398,11 @@ hipError_t by_pieces(int p, F&& f) {
   }
 }
 
+// Columns a lane and piece of the forward, and the least lanes a row: what a
+// scale word's 128 columns take, or 8.
+constexpr int forward_unit(bool stream_f32) { return stream_f32 ? 4 : 8; }
+constexpr int forward_lanes(bool stream_f32, int kind) { return kind == ROW_BF16 ? 8 : 128 / forward_unit(stream_f32); }
+
 template <bool XF32, bool SF32, int KIND, int P, int LPR>
 hipError_t launch_norm_kernel(const NormArgs& a, const Shape& sh, hipStream_t s) {
   hipLaunchKernelGGL((rms_norm_kernel<XF32, SF32, KIND, P, LPR>), dim3(static_cast<unsigned>(blocks_of(sh, a.rows))),
@@ -406,7 +411,7 @@ hipError_t launch_norm_kernel(const NormArgs& a, const Shape& sh, hipStream_t s)
 }
 template <bool XF32, bool SF32, int KIND>
 hipError_t launch_norm_kind(const NormArgs& a, hipStream_t s) {
-  constexpr int U = SF32 ? 4 : 8, kMost = 2048 / (64 * U), kLeast = KIND == ROW_BF16 ? 8 : 128 / U;
+  constexpr int U = forward_unit(SF32), kMost = 2048 / (64 * U), kLeast = forward_lanes(SF32, KIND);
   const Shape sh = shape_of(a.width, U, kLeast);
   if constexpr (kLeast <= 8)
     if (sh.lanes == 8) return launch_norm_kernel<XF32, SF32, KIND, 1, 8>(a, sh, s);
@@ -444,6 +449,11 @@ void launch_backward_kernel(const NormArgs& a, dim3 grid, int waves, hipStream_t
 }
 
 }  // namespace
+
+int64_t rms_norm_threads(int64_t rows, int32_t width, bool stream_f32, int kind) {
+  const Shape sh = shape_of(width, forward_unit(stream_f32), forward_lanes(stream_f32, kind));
+  return blocks_of(sh, rows) * threads_of(sh);
+}
 
 hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s) {
   if (a.rows == 0) return hipSuccess;
