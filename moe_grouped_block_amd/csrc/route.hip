@@ -875,10 +875,18 @@ template <bool BF16>
 hipError_t launch_size(const RouteArgs& a, bool backward, hipStream_t s) {
   if (a.experts <= 64) return launch_width<BF16, 16, 4>(a, backward, s);
   // Few tokens leave most of the chip empty: a wave a token then, whose keys are
-  // a quarter as many a lane.  256 experts, top 8, 1 / 1024 / 4096 tokens: 3.8 /
-  // 4.1 / 5.6 us against 5.4 / 5.6 / 5.4, groups with a bias 5.8 / 6.2 / 8.4
-  // against 6.9 / 7.3 / 8.3; 128 experts, 4096 tokens: 5.7 against 4.3.
-  if (a.experts <= 256 && a.tokens <= 2048) return launch_width<BF16, 64, 4>(a, backward, s);
+  // half or a quarter as many a lane.  us by a wave a token / by 16 lanes, BF16, top
+  // 8, without a bias, and of the gradient:
+  //   128 experts,    1 token    3.6 / 3.9    2.6 / 2.7
+  //                1024 tokens   4.0 / 4.25   3.0 / 3.0
+  //                1536          4.4 / 4.2    3.2 / 3.0
+  //                2048          4.4 / 4.2    3.2 / 3.1
+  //   256 experts,    1          3.7 / 5.5    2.6 / 2.8
+  //                1024          4.0 / 5.8    2.9 / 3.2
+  //                2048          4.4 / 5.6    3.3 / 3.25
+  //                4096          5.6 / 5.6    3.5 / 3.5
+  // (96 experts are as 128, 160 as 256.)
+  if (a.experts <= 256 && a.tokens <= (a.experts <= 128 ? 1024 : 2048)) return launch_width<BF16, 64, 4>(a, backward, s);
   if (a.experts <= 128) return launch_width<BF16, 16, 8>(a, backward, s);
   if (a.experts <= 256) return launch_width<BF16, 16, 16>(a, backward, s);
   return launch_width<BF16, 64, 16>(a, backward, s);

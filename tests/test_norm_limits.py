@@ -61,12 +61,12 @@ def test_rows_up_to_what_a_launch_holds(width, stream, mx):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("stream", ["bf16", "f32"])
-def test_many_narrow_rows(stream):
+@pytest.mark.parametrize("stream,h", [("bf16", 8), ("f32", 8), ("bf16", 64)])
+def test_many_narrow_rows(stream, h):
     """2^25 rows and more (a thread count of 2^32 if each had a wave and its place)."""
     torch = pytest.importorskip("torch")
     import more_ref as ref
-    t, h = (1 << 26) + 5, 8
+    t = (1 << 26) + 5
     kind = torch.bfloat16 if stream == "bf16" else torch.float32
     x = torch.zeros(t, h, dtype=torch.bfloat16, device="cuda")
     r = torch.zeros(t, h, dtype=kind, device="cuda")
