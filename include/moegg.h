@@ -481,8 +481,10 @@ moegg_status moegg_dequantise(const uint8_t* codes, const uint8_t* sf, int64_t r
  * over each row of `width` columns, the norm of the h that is stored.  y comes
  * as BF16, as MX rows (codes with scales, scaled and rounded from the unrounded
  * y as in moegg_dispatch: moegg_run's A and SFA) or as both.  Sums are held in
- * 64 bits: no finite h overflows or vanishes in them.  A NaN or an infinity in a
- * row is one of that row alone. */
+ * 64 bits: no finite h overflows or vanishes in them.  The factors of one value, (h /
+ * sqrt(...)) weight and in the gradient dy weight, are multiplied in fp32: a product
+ * beyond its range is infinite (and its row's dx NaN), one below it 0.  A NaN or an
+ * infinity in a row is one of that row alone. */
 typedef struct moegg_norm_problem {
   int64_t rows;         /* 0..2^31-1                                           */
   int32_t width;        /* multiple of 8 (128 for MX rows, 256 for E2M1X2), <= 32768 */

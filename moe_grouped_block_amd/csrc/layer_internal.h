@@ -192,13 +192,13 @@ struct LinearArgs {
   uint8_t* c_sf;            // scales of an 8-bit c, (M, N / 32)
   SavedRows x8;             // x in 8 bits (kind ROW_BF16: none)    [backward]
 };
-// Bytes of workspace (pointers in `a` only say what is asked for).
 // A call's workspace in bytes, and its tiles in linear.hip's own form: made once
 // for the check of the workspace and the launch (a plan is 0.3 us, a small call 8).
 struct LinearPlan {
   int64_t workspace;
   int64_t detail[20];
 };
+// They read the sizes, the types and whether there are offsets; no pointer is followed.
 LinearPlan plan_linear(const LinearArgs& a);
 LinearPlan plan_linear_backward(const LinearArgs& a, bool dx, bool dw, bool db);
 hipError_t launch_linear(const LinearArgs& a, const LinearPlan& plan, hipStream_t s);
