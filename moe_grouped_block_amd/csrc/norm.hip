@@ -15,7 +15,7 @@
 //
 // Squares and products are summed in 64 bits: no h in range overflows or
 // vanishes in them, and the rate of 64-bit operations is far from being needed.
-// r is kept as a power of two a and a factor b in (0.5, 2): (h a) b does not
+// r is kept as a power of two a and a factor b in [0.5, 1]: (h a) b does not
 // leave the range of fp32 where the result does not.
 #include "mx_rows.h"
 
@@ -73,7 +73,7 @@ struct Unit {
   }
 };
 
-// 1 / sqrt(v) = a b for v > 0 (NaN: b is NaN; +inf: b is 0): a a power of two, b in (0.5, 2].
+// 1 / sqrt(v) = a b for v > 0 (NaN: b is NaN; +inf: b is 0): a a power of two, b in [0.5, 1].
 // b is what the unit gives of the rounded argument, without a step of Newton's: with
 // one in 64 bits 7 instead of 8 of 8388608 E4M3 codes (4096 x 2048) were others
 // than those of the 64-bit values, which lie on a rounding's edge.
