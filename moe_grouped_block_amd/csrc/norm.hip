@@ -74,9 +74,10 @@ struct Unit {
 };
 
 // 1 / sqrt(v) = a b for v > 0 (NaN: b is NaN; +inf: b is 0): a a power of two, b in [0.5, 1].
-// b is what the unit gives of the rounded argument, without a step of Newton's: with
-// one in 64 bits 7 instead of 8 of 8388608 E4M3 codes (4096 x 2048) were others
-// than those of the 64-bit values, which lie on a rounding's edge.
+// b is what the unit gives of the rounded argument, without a step of Newton's: one
+// in 64 bits brought no more E4M3 codes onto those of the 64-bit values (8 instead
+// of 7 of 8388608 differ, 4096 x 2048: on a rounding's edge, where the fp32
+// products by r and the weight decide).
 __device__ __forceinline__ void inverse_root(double v, float& a, float& b) {
   const int e = (static_cast<int>(__builtin_bit_cast(uint64_t, v) >> 52) - 1023) & ~1;      // even, so that its half is whole
   a = ldexpf(1.0f, -e / 2);
